@@ -325,6 +325,147 @@ TGEMM_API int tgemm_validate_rope_region(const void* q, int64_t ldq, int64_t P, 
                                          const float* inv_freq, const void* cos_out,
                                          const void* sin_out, int64_t ldc, const float* q_out);
 
+/*
+ * ---- The feed-forward block: gated products, 8-bit products, norms ------
+ *
+ * What a gated feed-forward block adds around its down projection, as it is
+ * trained (bf16 operands, with the gradient) and as it is served (8-bit
+ * integer operands).  Storage, layout flags, asynchrony, streams, threads,
+ * workspace and errors as for tgemm_run.
+ */
+
+/* Activations of the gated products (fp32 arithmetic). */
+typedef enum {
+  TGEMM_ACT_SILU = 0,     /* g / (1 + exp(-g))                                         */
+  TGEMM_ACT_GELU_TANH = 1 /* g/2 * (1 + tanh(sqrt(2/pi) * (g + 0.044715 * g^3)))       */
+} tgemm_activation;
+
+/*
+ * RMS norm of rows, with the residual's addition, to 8-bit codes with one
+ * scale per row.  Per row of K elements:
+ *   h     = bf16(fp32(x + residual)), written to `sum` (h = x without a
+ *           residual)
+ *   t     = h * weight, T = max |t|
+ *   scale = T / (127 * sqrt(mean(h^2) + eps))                       fp32
+ *   q     = 127 * t / T rounded to the nearest integer, ties to even
+ * so scale * q is the normed row h * weight / sqrt(mean(h^2) + eps) in 255
+ * levels (q in [-127, 127]).  The codes are the exact quotients' roundings:
+ * the same row always gives the same codes.  A row with T = 0 gets scale 0
+ * and codes 0; a row in which some t is NaN or infinite (in fp32) gets scale
+ * NaN and codes 0.  Products t below fp32's normal range lose bits.
+ *
+ *   x, residual, sum  bf16 [M, K], row strides ldx, ldr, lds >= K (elements).
+ *                     residual and sum are both given or both NULL; sum may
+ *                     be x or residual itself (same address and stride).
+ *   weight            bf16 [K].      eps  finite and >= 0.
+ *   q                 int8 [M, K], row stride ldq >= K.
+ *   scale             fp32 [M].
+ * Rows may start at any element: no alignment is asked for.  No workspace.
+ */
+TGEMM_API int tgemm_rms_norm_i8(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                                const void* weight, float eps, int64_t M, int64_t K, void* sum,
+                                int64_t lds, int8_t* q, int64_t ldq, float* scale, void* stream);
+
+/* Host-only argument check of tgemm_rms_norm_i8 (no GPU access). */
+TGEMM_API int tgemm_validate_rms_norm_i8(const void* x, int64_t ldx, const void* residual,
+                                         int64_t ldr, const void* weight, float eps, int64_t M,
+                                         int64_t K, const void* sum, int64_t lds, const int8_t* q,
+                                         int64_t ldq, const float* scale);
+
+/*
+ * Rows of x (bf16 [M, K]) to 8-bit codes with one scale per row: as above
+ * with t = x and scale = T / 127.
+ */
+TGEMM_API int tgemm_quantize_i8(const void* x, int64_t ldx, int64_t M, int64_t K, int8_t* q,
+                                int64_t ldq, float* scale, void* stream);
+
+/* Host-only argument check of tgemm_quantize_i8 (no GPU access). */
+TGEMM_API int tgemm_validate_quantize_i8(const void* x, int64_t ldx, int64_t M, int64_t K,
+                                         const int8_t* q, int64_t ldq, const float* scale);
+
+/*
+ * Product of 8-bit integers with a scale for each row (token) of op(A) and
+ * each column (channel) of op(B):
+ *   C[m,n] = scale_a[m] * scale_b[n] * sum_k op(A)[m,k] * op(B)[k,n]
+ * The sum is exact (int32; K <= 131071, else TGEMM_ERR_UNSUPPORTED); it is
+ * converted to fp32 and multiplied by scale_a, then scale_b.
+ *
+ *   A, B      int8, in any layout (row strides lda, ldb in elements).
+ *   scale_a   fp32 [M], scale_b fp32 [N].
+ *   C         bf16 (TGEMM_EPI_STORE_BF16) or fp32 (TGEMM_EPI_STORE_F32).
+ *
+ * A 'N' and B 'T' with 16-byte aligned bases and lda, ldb and K multiples of
+ * 16 are read in place; other operands are first copied, K-contiguous, into
+ * the workspace.  Up to 64 rows of op(A) run on a kernel that streams B once.
+ */
+TGEMM_API int tgemm_run_i8(char transA, char transB, int64_t M, int64_t N, int64_t K,
+                           const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb,
+                           const float* scale_a, const float* scale_b, void* C, int64_t ldc,
+                           int epilogue, void* stream);
+
+/* Host-only argument check of tgemm_run_i8 (no GPU access). */
+TGEMM_API int tgemm_validate_i8(char transA, char transB, int64_t M, int64_t N, int64_t K,
+                                const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb,
+                                const float* scale_a, const float* scale_b, const void* C,
+                                int64_t ldc, int epilogue);
+
+/*
+ * Gate and up projections, the activation and their product in one call:
+ *   [g | u] = op(A) . op(B)   op(B) is [K, 2F]: columns 0 .. F-1 give g,
+ *                             F .. 2F-1 give u (fp32 sums)
+ *   H       = bf16(act(g) * u)                              [M, F]
+ * g and u are not written unless GU is given: bf16 [M, 2F] (row stride ldgu
+ * >= 2F), g in the first F columns and u in the last, for tgemm_gated_grad.
+ * H is computed from the fp32 sums either way.
+ *
+ * A 'N' and B 'T' with 16-byte aligned bases and lda, ldb and K multiples of
+ * 8 run on kernels of their own (up to 64 rows: one that streams B once);
+ * others take the GEMM of tgemm_run into an fp32 [M, 2F] workspace and a
+ * second pass.
+ */
+TGEMM_API int tgemm_run_gated(char transA, char transB, int64_t M, int64_t F, int64_t K,
+                              const void* A, int64_t lda, const void* B, int64_t ldb,
+                              int activation, void* H, int64_t ldh, void* GU, int64_t ldgu,
+                              void* stream);
+
+/* Host-only argument check of tgemm_run_gated (no GPU access). */
+TGEMM_API int tgemm_validate_gated(char transA, char transB, int64_t M, int64_t F, int64_t K,
+                                   const void* A, int64_t lda, const void* B, int64_t ldb,
+                                   int activation, const void* H, int64_t ldh, const void* GU,
+                                   int64_t ldgu);
+
+/*
+ * The gated product from 8-bit operands: g and u as tgemm_run_i8 computes
+ * them (scale_b has 2F entries), H = bf16(act(g) * u).
+ */
+TGEMM_API int tgemm_run_gated_i8(char transA, char transB, int64_t M, int64_t F, int64_t K,
+                                 const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb,
+                                 const float* scale_a, const float* scale_b, int activation,
+                                 void* H, int64_t ldh, void* stream);
+
+/* Host-only argument check of tgemm_run_gated_i8 (no GPU access). */
+TGEMM_API int tgemm_validate_gated_i8(char transA, char transB, int64_t M, int64_t F, int64_t K,
+                                      const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb,
+                                      const float* scale_a, const float* scale_b, int activation,
+                                      const void* H, int64_t ldh);
+
+/*
+ * Gradient of H = act(g) * u with respect to g and u:
+ *   dGU[:, :F] = bf16(dH * u * act'(g)),  dGU[:, F:] = bf16(dH * act(g))
+ * dH bf16 [M, F], GU bf16 [M, 2F] as tgemm_run_gated left it, dGU bf16
+ * [M, 2F].  The operands' gradients are products of dGU: dOp(A) = dGU .
+ * op(B)^T and dOp(B) = op(A)^T . dGU (tgemm_run reads every transpose in
+ * place).  No workspace.
+ */
+TGEMM_API int tgemm_gated_grad(int64_t M, int64_t F, const void* dH, int64_t lddh, const void* GU,
+                               int64_t ldgu, int activation, void* dGU, int64_t lddgu,
+                               void* stream);
+
+/* Host-only argument check of tgemm_gated_grad (no GPU access). */
+TGEMM_API int tgemm_validate_gated_grad(int64_t M, int64_t F, const void* dH, int64_t lddh,
+                                        const void* GU, int64_t ldgu, int activation,
+                                        const void* dGU, int64_t lddgu);
+
 /* Human-readable name of a status code (static string, never NULL). */
 TGEMM_API const char* tgemm_status_string(int status);
 

@@ -10,9 +10,15 @@ from . import tgemm  # noqa: F401
 from .tgemm import (  # noqa: F401
     TgemmError,
     cross_entropy,
+    gated_backward,
+    gated_matmul,
+    gated_matmul_i8,
     layout_of,
     matmul,
+    matmul_i8,
     outer_f32,
+    quantize_i8,
+    rms_norm_i8,
     rope_cos_sin,
     run,
     set_tile_config,

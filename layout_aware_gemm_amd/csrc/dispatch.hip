@@ -28,10 +28,7 @@ int g_fp8_cast_once = 1;  // tgemm_set_fp8_cast_once
 
 inline bool is_n(char t) { return t == 'N' || t == 'n'; }
 
-inline int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
-
-// A dispatch packet's grid is at most 2^32 - 1 work-items.
-constexpr int64_t kMaxWorkgroups = (int64_t(1) << 24) - 1;
+}  // namespace
 
 bool verbose() {
   static int v = -1;
@@ -41,6 +38,8 @@ bool verbose() {
   }
   return v == 1;
 }
+
+namespace {
 
 // Tile choice.
 //  - 256x256 tiles when they alone give most of the 256 compute units a
@@ -118,12 +117,6 @@ int status_of(hipError_t e) { return e == hipSuccess ? TGEMM_OK : TGEMM_ERR_HIP;
 // tgemm_run_noalloc: the fixed device array `scratch` below, one per
 // device, found once per device with hipGetSymbolAddress; no allocation.
 // ----------------------------------------------------------------------
-struct Workspace {
-  void* ptr = nullptr;
-  bool owned = false;                 // free in stream order at the end of this call
-  std::unique_lock<std::mutex> hold;  // the cache entry, until the last launch is enqueued
-};
-
 struct WsEntry {
   int dev;
   hipStream_t stream;
@@ -134,8 +127,6 @@ struct WsEntry {
 
 std::mutex g_ws_mu;                               // guards the list itself
 std::vector<std::unique_ptr<WsEntry>> g_ws;       // entries never move or go away
-
-enum WsMode : int { kWsCached = 0, kWsScratch = 1 };
 
 // (the array `scratch` is defined at file scope, below the anonymous
 // namespace)
@@ -163,6 +154,8 @@ int scratch_address(void** out) {
   *out = g_scratch_ptr[dev];
   return TGEMM_OK;
 }
+
+}  // namespace
 
 // Returns TGEMM_OK with w->ptr set, TGEMM_ERR_NO_MEMORY (allocation
 // failed), TGEMM_ERR_WORKSPACE_LIMIT (scratch too small) or TGEMM_ERR_HIP.
@@ -232,7 +225,6 @@ hipError_t launch_gemm(char ta, char tb, int cfg, int epi, const GemmParams& p, 
   return launch_gemm_tt(cfg, epi, p, s);
 }
 
-}  // namespace
 }  // namespace tgemm
 
 using namespace tgemm;

@@ -1,0 +1,140 @@
+// Shared by the feed-forward operators' translation units: the 8-bit and
+// gated products (rows_gemm.hip, rows_skinny.hip, rows_finish.hip), the row
+// quantiser (row_quant.hip) and their host entries (ffn.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "tgemm_internal.h"
+
+namespace tgemm {
+
+// Operand element types of the row products.
+enum RowsType : int { kRowsI8 = 0, kRowsBf16 = 1 };
+
+// What a row product does with its sums.
+//   kRowsStoreBf16 / F32  C[m][n] = sum * scale_a[m] * scale_b[n]   (int8)
+//   kRowsGated            C[m][f] = bf16(act(g) * u), g = column f of the
+//                         product, u = column F + f (int8: after the
+//                         scales; bf16: optionally g, u kept as bf16)
+//   kRowsPart             the raw sums (int32 or fp32) of one K chunk, into
+//                         slice `chunk` of the partial buffer [split][M][N]
+enum RowsEpi : int { kRowsStoreBf16 = 0, kRowsStoreF32 = 1, kRowsGated = 2, kRowsPart = 3 };
+
+// A product of two row-major, K-contiguous operands: A [M][K], B [N][K]
+// (gated: N = 2F, rows 0..F-1 the gate, F..2F-1 the up projection).  Row
+// strides and K are in BYTES.  The direct-copy kernels need both bases and
+// every stride and K to be multiples of 16 bytes (rows_aligned).
+struct RowsParams {
+  const char* A;
+  const char* B;
+  int64_t lda, ldb;  // bytes
+  int M, N, K;       // rows of A, rows of B, bytes of K
+  int F;             // gated: N / 2
+  int act;           // gated: tgemm_activation
+  const float* scale_a;  // int8: [M]
+  const float* scale_b;  // int8: [N]
+  void* C;
+  int64_t ldc;       // elements
+  uint16_t* gu;      // bf16 gated: optional [M][ldgu], g then u
+  int64_t ldgu;
+  void* part;        // kRowsPart: [split][M][N] int32 / fp32
+  int tilesM, tilesN, groupM;
+  int split, kchunk; // K chunks and bytes per chunk (a multiple of 128)
+};
+
+inline bool rows_aligned(const void* p, int64_t ld_bytes, int64_t k_bytes) {
+  return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)ld_bytes | (uintptr_t)k_bytes) & 15) == 0;
+}
+
+// Output tile shapes of the large-product kernel.
+enum RowsTile : int { kRows256 = 0, kRows128 = 1 };
+inline int rows_tile(int t) { return t == kRows256 ? 256 : 128; }
+
+// Large products (rows_gemm.hip).  `gate`: B's rows are interleaved in the
+// tile (kRowsGated, or kRowsPart of a gated product).
+hipError_t launch_rows_gemm(int type, int tile, int epi, bool gate, const RowsParams& p,
+                            hipStream_t s);
+
+// Products of at most kSkinnyRows rows of A (rows_skinny.hip).
+constexpr int kSkinnyRows = 64;
+hipError_t launch_rows_skinny(int type, int epi, bool gate, const RowsParams& p, hipStream_t s);
+// The K chunks the kernel above should be split into (1: no partials).
+int rows_skinny_split(const RowsParams& p, bool gate);
+
+// Sum the partial products over the K chunks and apply `epi` (one of
+// kRowsStoreBf16, kRowsStoreF32, kRowsGated) (rows_finish.hip).
+hipError_t launch_rows_finish(int type, int epi, const RowsParams& p, hipStream_t s);
+
+// Copy an int8 operand of any layout into K-contiguous rows [R][Kp], zero
+// past K: X [R][K] (k_contiguous) or [K][R], row stride ld bytes; Kp a
+// multiple of 16 (rows_finish.hip).
+hipError_t launch_pack_i8(const int8_t* X, int64_t ld, bool k_contiguous, int R, int K,
+                          int8_t* out, int Kp, hipStream_t s);
+
+// dgu = [dh * u * act'(g) | dh * act(g)] (rows_finish.hip).
+hipError_t launch_gated_grad(const uint16_t* dh, int64_t lddh, const uint16_t* gu, int64_t ldgu,
+                             int M, int64_t F, int act, uint16_t* dgu, int64_t lddgu,
+                             hipStream_t s);
+
+// Rows to 8-bit codes with one scale each (row_quant.hip).  weight null:
+// codes of x itself; else of the RMS norm of x (+ residual, whose bf16 sum
+// goes to sum).
+struct RowQuantParams {
+  const uint16_t* x;
+  int64_t ldx;
+  const uint16_t* residual;
+  int64_t ldr;
+  const uint16_t* weight;
+  float eps;
+  uint16_t* sum;
+  int64_t lds;
+  int8_t* q;
+  int64_t ldq;
+  float* scale;
+  int M;
+  int64_t K;
+};
+hipError_t launch_row_quant(const RowQuantParams& p, hipStream_t s);
+
+// ----------------------------------------------------------------------
+// Activations.  Both are g * sigmoid(s(g)): silu with s = g; the tanh form
+// of gelu, g/2 (1 + tanh z) with z = sqrt(2/pi)(g + 0.044715 g^3), with
+// s = 2z, since (1 + tanh z)/2 = sigmoid(2z).  fp32 throughout, on the
+// hardware exp2 and reciprocal (1 ulp each): the error of the exponent's
+// argument, |s| 2^-24 relative in the result, stays far below the bf16
+// rounding of every output for |s| up to 100, and past that the sigmoid
+// has saturated.
+// ----------------------------------------------------------------------
+constexpr float kGeluC2 = 1.5957691216057308f;  // 2 sqrt(2/pi)
+constexpr float kGeluK = 0.044715f;
+
+__device__ __forceinline__ float act_sigmoid(float g, int act) {
+  const float s = act == 0 ? g : kGeluC2 * (g + kGeluK * g * g * g);
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * s));
+}
+
+__device__ __forceinline__ float act_value(float g, int act) { return g * act_sigmoid(g, act); }
+
+// act(g) and its derivative p + g p (1 - p) s'(g); the second term is 0
+// where the sigmoid has saturated (s' may be infinite there).
+__device__ __forceinline__ void act_value_grad(float g, int act, float& a, float& d) {
+  const float p = act_sigmoid(g, act);
+  const float t = p * (1.f - p);
+  const float ds = act == 0 ? 1.f : kGeluC2 * (1.f + 3.f * kGeluK * g * g);
+  a = g * p;
+  d = t > 0.f ? fmaf(a * (1.f - p), ds, p) : p;
+}
+
+// 16-byte and 8-byte vectors at any element alignment: the hardware takes
+// unaligned vector accesses to global memory, so rows of odd length cost no
+// variant of their own.
+struct __attribute__((packed, aligned(2))) u16x8_any {
+  uint32_t w[4];
+};
+struct __attribute__((packed, aligned(1))) u8x8_any {
+  uint32_t w[2];
+};
+
+}  // namespace tgemm

@@ -1,0 +1,310 @@
+// Host entries of the feed-forward operators: 8-bit products, gated
+// products and their gradient, the row quantiser.  Validation (validate.cpp),
+// choice of kernel, workspace, launches.
+#include "ffn.h"
+
+#include <stdio.h>
+
+#include "tgemm.h"
+
+using namespace tgemm;
+
+namespace tgemm {
+namespace {
+
+inline bool is_n(char t) { return t == 'N' || t == 'n'; }
+
+// hipErrorInvalidValue is what the launchers here return for a grid past
+// the dispatch limit.
+int status_of(hipError_t e) {
+  return e == hipSuccess ? TGEMM_OK : e == hipErrorInvalidValue ? TGEMM_ERR_UNSUPPORTED
+                                                                : TGEMM_ERR_HIP;
+}
+
+constexpr size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+// The copy offsets of a tile (at most 256 rows) stay below 2^31 bytes.
+inline bool stride_fits(int64_t ld_bytes) { return ld_bytes < (int64_t(1) << 23); }
+
+// Kernel, tile and K chunks of a product whose operands are aligned.
+struct RowsPlan {
+  bool skinny;
+  int tile;
+};
+
+RowsPlan plan_rows(RowsParams* p, bool gate) {
+  RowsPlan r = {p->M <= kSkinnyRows, kRows256};
+  p->split = 1;
+  if (r.skinny) {
+    p->split = rows_skinny_split(*p, gate);
+  } else {
+    const int64_t t256 = (int64_t)ceil_div(p->M, 256) * ceil_div(p->N, 256);
+    r.tile = t256 >= 128 ? kRows256 : kRows128;
+    const int b = rows_tile(r.tile);
+    p->tilesM = ceil_div(p->M, b);
+    p->tilesN = gate ? ceil_div(p->F, b / 2) : ceil_div(p->N, b);
+    p->groupM = p->tilesM < 4 ? p->tilesM : (p->tilesM <= 8 ? p->tilesM : 4);
+    if (r.tile == kRows128) {
+      const int64_t t = (int64_t)p->tilesM * p->tilesN;
+      const int64_t fill = 512 / t, by_k = p->K / 2048;
+      const int64_t n = fill < by_k ? fill : by_k;
+      p->split = n < 1 ? 1 : (int)n;
+    }
+  }
+  p->kchunk = ceil_div(ceil_div(p->K, p->split), 128) * 128;
+  p->split = ceil_div(p->K, p->kchunk);  // no empty chunks
+  return r;
+}
+
+bool grid_fits(const RowsParams& p, const RowsPlan& r, bool gate) {
+  const int64_t tiles = r.skinny ? ceil_div(gate ? p.F : p.N, 16) : (int64_t)p.tilesM * p.tilesN;
+  return tiles * p.split <= kMaxWorkgroups;
+}
+
+hipError_t launch_rows(int type, const RowsParams& p, const RowsPlan& r, int epi, bool gate,
+                       hipStream_t s) {
+  const int e = p.split > 1 ? (int)kRowsPart : epi;
+  const hipError_t h = r.skinny ? launch_rows_skinny(type, e, gate, p, s)
+                                : launch_rows_gemm(type, r.tile, e, gate, p, s);
+  return h != hipSuccess || p.split == 1 ? h : launch_rows_finish(type, epi, p, s);
+}
+
+void say_rows(const char* what, const RowsParams& p, const RowsPlan& r) {
+  if (verbose())
+    fprintf(stderr, "tgemm: %s M=%d N=%d K=%d bytes %s tile=%d split=%d\n", what, p.M, p.N, p.K,
+            r.skinny ? "skinny" : "tiles", r.skinny ? 16 : rows_tile(r.tile), p.split);
+}
+
+// p holds everything but the operands' final addresses.  Operands that the
+// direct-copy kernels cannot read in place -- not K-contiguous, or with
+// rows off 16-byte boundaries -- are copied into the workspace first.
+int run_i8(char ta, char tb, const void* A, int64_t lda, const void* B, int64_t ldb, RowsParams p,
+           int epi, bool gate, hipStream_t s) {
+  const int K = p.K;
+  const int Kp = ceil_div(K, 16) * 16;
+  // (the stride of a single row is never used)
+  if (is_n(ta) && p.M == 1) lda = Kp;
+  if (!is_n(tb) && p.N == 1) ldb = Kp;
+  const bool packA = !is_n(ta) || !rows_aligned(A, lda, K) || !stride_fits(lda);
+  const bool packB = is_n(tb) || !rows_aligned(B, ldb, K) || !stride_fits(ldb);
+  p.K = packA || packB ? Kp : K;
+  const RowsPlan r = plan_rows(&p, gate);
+  if (!grid_fits(p, r, gate)) return TGEMM_ERR_UNSUPPORTED;
+  const size_t bytesA = packA ? round256((size_t)p.M * Kp) : 0;
+  const size_t bytesB = packB ? round256((size_t)p.N * Kp) : 0;
+  const size_t bytesP = p.split > 1 ? (size_t)p.split * p.M * p.N * sizeof(int) : 0;
+  say_rows(gate ? "gated i8" : "i8", p, r);
+  Workspace w;
+  const bool need = bytesA + bytesB + bytesP != 0;
+  if (need) {
+    const int st = get_workspace(kWsCached, s, bytesA + bytesB + bytesP, &w);
+    if (st != TGEMM_OK) return st;
+  }
+  char* ws = static_cast<char*>(w.ptr);
+  p.A = static_cast<const char*>(A);
+  p.B = static_cast<const char*>(B);
+  p.lda = lda;
+  p.ldb = ldb;
+  hipError_t e = hipSuccess;
+  if (packA) {
+    int8_t* o = reinterpret_cast<int8_t*>(ws);
+    e = launch_pack_i8(static_cast<const int8_t*>(A), lda, is_n(ta), p.M, K, o, Kp, s);
+    p.A = reinterpret_cast<const char*>(o);
+    p.lda = Kp;
+  }
+  if (packB && e == hipSuccess) {
+    int8_t* o = reinterpret_cast<int8_t*>(ws + bytesA);
+    e = launch_pack_i8(static_cast<const int8_t*>(B), ldb, !is_n(tb), p.N, K, o, Kp, s);
+    p.B = reinterpret_cast<const char*>(o);
+    p.ldb = Kp;
+  }
+  if (bytesP) p.part = ws + bytesA + bytesB;
+  if (e == hipSuccess) e = launch_rows(kRowsI8, p, r, epi, gate, s);
+  if (need) {
+    const hipError_t f = release_workspace(w, s);
+    if (e == hipSuccess) e = f;
+  }
+  return status_of(e);
+}
+
+// bf16 gated product.  K-contiguous operands with 16-byte rows run on the
+// gated kernels; any other layout or alignment as the library's GEMM into
+// an fp32 [M][2F] workspace and a pass that gates it.
+int run_gated(char ta, char tb, int64_t M, int64_t F, int64_t K, const void* A, int64_t lda,
+              const void* B, int64_t ldb, int act, void* H, int64_t ldh, void* GU, int64_t ldgu,
+              hipStream_t s) {
+  RowsParams p = {};
+  p.M = (int)M;
+  p.N = (int)(2 * F);
+  p.F = (int)F;
+  p.act = act;
+  p.C = H;
+  p.ldc = ldh;
+  p.gu = static_cast<uint16_t*>(GU);
+  p.ldgu = ldgu;
+  const int64_t ldx = is_n(ta) && M == 1 ? K : lda;
+  const bool direct = is_n(ta) && !is_n(tb) && rows_aligned(A, 2 * ldx, 2 * K) &&
+                      rows_aligned(B, 2 * ldb, 2 * K) && stride_fits(2 * ldx) &&
+                      stride_fits(2 * ldb) && K < (int64_t(1) << 30);
+  Workspace w;
+  hipError_t e;
+  if (direct) {
+    p.A = static_cast<const char*>(A);
+    p.B = static_cast<const char*>(B);
+    p.lda = 2 * ldx;
+    p.ldb = 2 * ldb;
+    p.K = (int)(2 * K);
+    const RowsPlan r = plan_rows(&p, true);
+    if (!grid_fits(p, r, true)) return TGEMM_ERR_UNSUPPORTED;
+    say_rows("gated bf16", p, r);
+    if (p.split > 1) {
+      const int st =
+          get_workspace(kWsCached, s, (size_t)p.split * p.M * p.N * sizeof(float), &w);
+      if (st != TGEMM_OK) return st;
+      p.part = w.ptr;
+    }
+    e = launch_rows(kRowsBf16, p, r, kRowsGated, true, s);
+  } else {
+    GemmParams g = {};
+    const int64_t t256 = (int64_t)ceil_div(M, 256) * ceil_div(p.N, 256);
+    const int cfg = t256 >= 144 ? kTile256 : kTile128;
+    g.A = static_cast<const uint16_t*>(A);
+    g.B = static_cast<const uint16_t*>(B);
+    g.lda = lda;
+    g.ldb = ldb;
+    g.ldc = p.N;
+    g.M = p.M;
+    g.N = p.N;
+    g.K = (int)K;
+    g.tilesM = ceil_div(M, tile_rows(cfg));
+    g.tilesN = ceil_div(p.N, tile_cols(cfg));
+    g.splitk = 1;
+    g.kchunk = (int)K;
+    if ((int64_t)g.tilesM * g.tilesN > kMaxWorkgroups) return TGEMM_ERR_UNSUPPORTED;
+    g.groupM = g.tilesM < 4 ? g.tilesM : (g.tilesM <= 8 ? g.tilesM : 4);
+    g.aligned = rows_aligned(A, 2 * lda, 0) && rows_aligned(B, 2 * ldb, 0);
+    if (verbose())
+      fprintf(stderr, "tgemm: gated bf16 %c%c M=%d F=%d K=%d through fp32 [M][2F]\n", ta, tb, p.M,
+              p.F, g.K);
+    const int st = get_workspace(kWsCached, s, (size_t)p.M * p.N * sizeof(float), &w);
+    if (st != TGEMM_OK) return st;
+    g.C = w.ptr;
+    e = launch_gemm(ta, tb, cfg, kEpiStoreF32, g, s);
+    p.part = w.ptr;
+    p.split = 1;
+    if (e == hipSuccess) e = launch_rows_finish(kRowsBf16, kRowsGated, p, s);
+  }
+  const hipError_t f = release_workspace(w, s);
+  return status_of(e != hipSuccess ? e : f);
+}
+
+// The workspace list allocates host memory; no exception leaves the library.
+template <class Fn>
+int no_throw(Fn&& fn) {
+  try {
+    return fn();
+  } catch (...) {
+    return TGEMM_ERR_NO_MEMORY;
+  }
+}
+
+}  // namespace
+}  // namespace tgemm
+
+extern "C" int tgemm_run_i8(char transA, char transB, int64_t M, int64_t N, int64_t K,
+                            const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb,
+                            const float* scale_a, const float* scale_b, void* C, int64_t ldc,
+                            int epilogue, void* stream) {
+  const int st = tgemm_validate_i8(transA, transB, M, N, K, A, lda, B, ldb, scale_a, scale_b, C,
+                                   ldc, epilogue);
+  if (st != TGEMM_OK) return st;
+  RowsParams p = {};
+  p.M = (int)M;
+  p.N = (int)N;
+  p.K = (int)K;
+  p.scale_a = scale_a;
+  p.scale_b = scale_b;
+  p.C = C;
+  p.ldc = ldc;
+  return no_throw([&] {
+    return run_i8(transA, transB, A, lda, B, ldb, p,
+                  epilogue == TGEMM_EPI_STORE_BF16 ? kRowsStoreBf16 : kRowsStoreF32, false,
+                  reinterpret_cast<hipStream_t>(stream));
+  });
+}
+
+extern "C" int tgemm_run_gated_i8(char transA, char transB, int64_t M, int64_t F, int64_t K,
+                                  const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb,
+                                  const float* scale_a, const float* scale_b, int activation,
+                                  void* H, int64_t ldh, void* stream) {
+  const int st = tgemm_validate_gated_i8(transA, transB, M, F, K, A, lda, B, ldb, scale_a, scale_b,
+                                         activation, H, ldh);
+  if (st != TGEMM_OK) return st;
+  RowsParams p = {};
+  p.M = (int)M;
+  p.N = (int)(2 * F);
+  p.F = (int)F;
+  p.K = (int)K;
+  p.act = activation;
+  p.scale_a = scale_a;
+  p.scale_b = scale_b;
+  p.C = H;
+  p.ldc = ldh;
+  return no_throw([&] {
+    return run_i8(transA, transB, A, lda, B, ldb, p, kRowsGated, true,
+                  reinterpret_cast<hipStream_t>(stream));
+  });
+}
+
+extern "C" int tgemm_run_gated(char transA, char transB, int64_t M, int64_t F, int64_t K,
+                               const void* A, int64_t lda, const void* B, int64_t ldb,
+                               int activation, void* H, int64_t ldh, void* GU, int64_t ldgu,
+                               void* stream) {
+  const int st =
+      tgemm_validate_gated(transA, transB, M, F, K, A, lda, B, ldb, activation, H, ldh, GU, ldgu);
+  if (st != TGEMM_OK) return st;
+  return no_throw([&] {
+    return run_gated(transA, transB, M, F, K, A, lda, B, ldb, activation, H, ldh, GU, ldgu,
+                     reinterpret_cast<hipStream_t>(stream));
+  });
+}
+
+extern "C" int tgemm_gated_grad(int64_t M, int64_t F, const void* dH, int64_t lddh, const void* GU,
+                                int64_t ldgu, int activation, void* dGU, int64_t lddgu,
+                                void* stream) {
+  const int st = tgemm_validate_gated_grad(M, F, dH, lddh, GU, ldgu, activation, dGU, lddgu);
+  if (st != TGEMM_OK) return st;
+  if (verbose())
+    fprintf(stderr, "tgemm: gated grad M=%lld F=%lld\n", (long long)M, (long long)F);
+  return status_of(launch_gated_grad(static_cast<const uint16_t*>(dH), lddh,
+                                     static_cast<const uint16_t*>(GU), ldgu, (int)M, F, activation,
+                                     static_cast<uint16_t*>(dGU), lddgu,
+                                     reinterpret_cast<hipStream_t>(stream)));
+}
+
+extern "C" int tgemm_rms_norm_i8(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                                 const void* weight, float eps, int64_t M, int64_t K, void* sum,
+                                 int64_t lds, int8_t* q, int64_t ldq, float* scale, void* stream) {
+  const int st = tgemm_validate_rms_norm_i8(x, ldx, residual, ldr, weight, eps, M, K, sum, lds, q,
+                                            ldq, scale);
+  if (st != TGEMM_OK) return st;
+  if (verbose())
+    fprintf(stderr, "tgemm: rms norm i8 M=%lld K=%lld residual=%d\n", (long long)M, (long long)K,
+            residual != nullptr);
+  const RowQuantParams p = {static_cast<const uint16_t*>(x), ldx,
+                            static_cast<const uint16_t*>(residual), ldr,
+                            static_cast<const uint16_t*>(weight), eps,
+                            static_cast<uint16_t*>(sum), lds, q, ldq, scale, (int)M, K};
+  return status_of(launch_row_quant(p, reinterpret_cast<hipStream_t>(stream)));
+}
+
+extern "C" int tgemm_quantize_i8(const void* x, int64_t ldx, int64_t M, int64_t K, int8_t* q,
+                                 int64_t ldq, float* scale, void* stream) {
+  const int st = tgemm_validate_quantize_i8(x, ldx, M, K, q, ldq, scale);
+  if (st != TGEMM_OK) return st;
+  if (verbose())
+    fprintf(stderr, "tgemm: quantize i8 M=%lld K=%lld\n", (long long)M, (long long)K);
+  const RowQuantParams p = {static_cast<const uint16_t*>(x), ldx, nullptr, 0, nullptr, 0.f,
+                            nullptr, 0, q, ldq, scale, (int)M, K};
+  return status_of(launch_row_quant(p, reinterpret_cast<hipStream_t>(stream)));
+}

@@ -1,0 +1,375 @@
+// Large products of two K-contiguous operands on the matrix cores, int8
+// (scaled, or gated) and bf16 (gated): out = epilogue(A . B^T), A [M][K],
+// B [N][K].
+//
+// The LDS image, copy schedule and tile shapes are those of the bf16 NT
+// kernel: a k-step is 128 bytes of every row (128 int8 or 64 bf16), copied
+// straight from global memory into swizzled LDS rows, two A and three B
+// panels in flight, one barrier per k-step.  A 16-byte chunk per lane feeds
+// one matrix instruction of either type (32x32x32 int8, 32x32x16 bf16), so
+// one loop serves both: an int8 k-step does twice the products in the same
+// cycles, and the sums of int8 are exact in int32.
+//
+// Edges need no other loop.  Each panel is read through a buffer whose
+// range ends with the operand's last row, so rows past it read as zero, and
+// in the last k-step the lanes whose chunk starts at or past K take an
+// offset outside the range.
+//
+// Gated products (B holds F gate rows, then F up rows) interleave the two
+// halves in groups of 32 tile rows: accumulator blocks 2j and 2j + 1 of a
+// lane are gate and up of the same output columns, so act(g) * u is formed
+// in registers and the [M][2F] product never reaches memory.
+#include "ffn.h"
+#include "gemm_kernel.h"
+
+namespace tgemm {
+namespace {
+
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x16_t __attribute__((ext_vector_type(16)));
+
+struct OpI8 {
+  typedef i32x4_t frag;
+  typedef i32x16_t acc;
+  static __device__ __forceinline__ acc mma(const frag& a, const frag& b, const acc& c) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
+#else
+    return c;
+#endif
+  }
+};
+struct OpBf16 {
+  typedef bf16x8_t frag;
+  typedef f32x16_t acc;
+  static __device__ __forceinline__ acc mma(const frag& a, const frag& b, const acc& c) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+#else
+    return c;
+#endif
+  }
+};
+
+constexpr int kRowBytes = 128;  // bytes of K per k-step (one LDS row)
+
+// This wave's share of one panel's copies: R tile rows, 1 KB (8 rows) per
+// copy.  Tile row r is row r of the operand, or with GATE row
+// (r >> 6) * 32 + (r & 31) of its gate (r & 32 == 0) or up half.
+template <int R, bool GATE>
+struct RowsPanel {
+  static constexpr int PER_WAVE = R / 32;
+  static_assert(PER_WAVE == 4 || PER_WAVE == 8, "panels of 128 or 256 rows");
+  uint32_t e[2];   // lane's byte offset in even / odd 8-row blocks
+  uint32_t et[2];  // the same in a last, partial k-step: outside the range past K
+  uint32_t row8;   // 8 rows in bytes
+#if defined(__HIP_DEVICE_COMPILE__)
+  __amdgpu_buffer_rsrc_t rs[GATE ? 2 : 1];
+#endif
+
+  static __device__ __forceinline__ uint64_t uniform(const char* p) {
+    const uint64_t b = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)b);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
+    return ((uint64_t)hi << 32) | lo;
+  }
+
+  // X: the operand; rows: its row count (GATE: of each half, which start
+  // at X and X + rows * ld); r0: first row of this tile (of each half);
+  // [kb, kend): the bytes of K to read.
+  __device__ __forceinline__ void init(const char* X, int64_t ld, int rows, int r0, int kb,
+                                       int kend, int wave_u, int lane) {
+    // first operand row of the wave's block 0
+    const int w0 = GATE ? (PER_WAVE == 8 ? wave_u * 32 : (wave_u >> 1) * 32)
+                        : wave_u * PER_WAVE * 8;
+    const int last = ((kend - kb - 1) & (kRowBytes - 1)) >> 4;  // last chunk of the last k-step
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      // (the swizzle of tile row 8 * block + lane / 8 depends on the block
+      // only through its parity)
+      const int c = (lane & 7) ^ swz((lane >> 3) + 8 * q);
+      e[q] = (uint32_t)((w0 + (lane >> 3)) * ld + c * 16);
+      et[q] = c <= last ? e[q] : 0x80000000u;
+    }
+    row8 = (uint32_t)(ld * 8);
+    const int valid = min(R / (GATE ? 2 : 1), rows - r0);
+    const int bytes = (int)((valid - 1) * ld + (kend - kb));
+#if defined(__HIP_DEVICE_COMPILE__)
+    const char* o = X + (int64_t)r0 * ld + kb;
+    // word 3 = 0x00020000: 32-bit data format, the raw-buffer setting
+    if constexpr (!GATE) {
+      rs[0] = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(uniform(o)), (short)0,
+                                                __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
+    } else {
+      // 256 rows: a wave's blocks 0-3 are gate rows, 4-7 up rows; 128 rows:
+      // even waves hold gate rows, odd waves up rows
+      const char* u = o + (int64_t)rows * ld;
+      const char* o0 = PER_WAVE == 8 ? o : ((wave_u & 1) ? u : o);
+      const char* o1 = PER_WAVE == 8 ? u : o0;
+      rs[0] = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(uniform(o0)), (short)0,
+                                                __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
+      rs[1] = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(uniform(o1)), (short)0,
+                                                __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
+    }
+#else
+    (void)X, (void)bytes;
+#endif
+  }
+
+  // Copy block j of the k-step at byte kofs; tail: it is a partial one.
+  // The whole offset sits in the lane's register (the range check takes
+  // the scalar offset off the range, which must not pass below zero).
+  __device__ __forceinline__ void issue_one(uint16_t* panel, int wave_u, int j, uint32_t kofs,
+                                            bool tail) const {
+    const int blk = wave_u * PER_WAVE + j;
+    const int jj = GATE && PER_WAVE == 8 ? (j & 3) : j;
+    const uint32_t off = (tail ? et[j & 1] : e[j & 1]) + (jj * row8 + kofs);
+#if defined(__HIP_DEVICE_COMPILE__)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rs[GATE && PER_WAVE == 8 ? (j >> 2) : 0],
+        (__attribute__((address_space(3))) void*)(panel + blk * 512), 16, (int)off, 0, 0, 0);
+#else
+    (void)panel, (void)blk, (void)off;
+#endif
+  }
+
+  __device__ __forceinline__ void issue(uint16_t* panel, int wave_u, uint32_t kofs,
+                                        bool tail) const {
+#pragma unroll
+    for (int j = 0; j < PER_WAVE; ++j) issue_one(panel, wave_u, j, kofs, tail);
+  }
+};
+
+// One substep (16 bytes of K per lane): MFMA q, then one fragment read of
+// the next substep and, with CP, this wave's copies of one panel, both
+// spread over the slots.
+template <class Op, int FM, int FN, bool CP, class Panel>
+__device__ __forceinline__ void rows_substep(typename Op::acc (&acc)[FM][FN],
+                                             const typename Op::frag* fa,
+                                             const typename Op::frag* fb,
+                                             typename Op::frag* na, typename Op::frag* nb,
+                                             const uint16_t* pa, const uint16_t* pb,
+                                             const Panel& d, uint16_t* dst, int wave_u,
+                                             uint32_t kofs, bool tail) {
+  constexpr int SL = FM * FN;
+#pragma unroll
+  for (int q = 0; q < SL; ++q) {
+    acc[q / FN][q % FN] = Op::mma(fa[q / FN], fb[q % FN], acc[q / FN][q % FN]);
+    if (q < FM)
+      na[q] = *reinterpret_cast<const typename Op::frag*>(pa + q * 32 * kBK);
+    else if (q < FM + FN)
+      nb[q - FM] = *reinterpret_cast<const typename Op::frag*>(pb + (q - FM) * 32 * kBK);
+    if constexpr (CP) {
+#pragma unroll
+      for (int c = 0; c < Panel::PER_WAVE; ++c)
+        if ((c * SL) / Panel::PER_WAVE == q) d.issue_one(dst, wave_u, c, kofs, tail);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+template <class Op, int BM, int BN, bool GATE, int EPI>
+__global__ void __launch_bounds__(kThreads, BM == 256 ? 1 : 2) rows_kernel(RowsParams p) {
+  constexpr bool I8 = std::is_same<Op, OpI8>::value;
+  constexpr int FM = BM / 64, FN = BN / 64;
+  constexpr int SA = BM * kBK, SB = BN * kBK;  // panel sizes in 16-bit units
+  static_assert(FM + FN <= FM * FN && FN % 2 == 0, "slots for the fragment reads, gate pairs");
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * SA + 3 * SB];
+
+  const int lane = threadIdx.x & 63;
+  const int wave_u = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int wm = wave_u >> 1, wn = wave_u & 1;
+  const int h = lane >> 5, lc = lane & 31;
+  int tile, ks, tm, tn;
+  xcd_remap(blockIdx.x, p.tilesM * p.tilesN * p.split, p.split, tile, ks);
+  tile_coords(tile, p.tilesM, p.tilesN, p.groupM, tm, tn);
+  const int m0 = tm * BM, n0 = tn * (GATE ? BN / 2 : BN);
+  const int kb = ks * p.kchunk, kend = min(p.K, kb + p.kchunk);
+  const int nk = (kend - kb + kRowBytes - 1) / kRowBytes;
+  const bool partial = ((kend - kb) & (kRowBytes - 1)) != 0;
+
+  typename Op::acc acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+
+  RowsPanel<BM, false> da;
+  RowsPanel<BN, GATE> db;
+  da.init(p.A, p.lda, p.M, m0, kb, kend, wave_u, lane);
+  db.init(p.B, p.ldb, GATE ? p.F : p.N, n0, kb, kend, wave_u, lane);
+
+  uint16_t* const abuf = lds;           // two A panels
+  uint16_t* const bbuf = lds + 2 * SA;  // three B panels
+  const int a_base = (wm * (BM / 2) + lc) * kBK;
+  const int b_base = (wn * (BN / 2) + lc) * kBK;
+  int xo[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) xo[s] = ((2 * s + h) ^ swz(lc)) << 3;
+
+  // k-steps past the end re-read k-step 0 into a buffer that is never
+  // multiplied, which keeps the copy counts, and so the waits, uniform
+  auto kof = [nk](int t) { return (uint32_t)((t < nk ? t : 0) * kRowBytes); };
+  auto tail = [nk, partial](int t) { return partial && (t == nk - 1 || (t > nk - 1 && nk == 1)); };
+  da.issue(abuf, wave_u, kof(0), tail(0));
+  db.issue(bbuf, wave_u, kof(0), tail(0));
+  db.issue(bbuf + SB, wave_u, kof(1), tail(1));
+  da.issue(abuf + SA, wave_u, kof(1), tail(1));
+  constexpr int NA = RowsPanel<BM, false>::PER_WAVE, NB = RowsPanel<BN, GATE>::PER_WAVE;
+  // k-step 0 landed (own copies; other waves': the barrier)
+  __builtin_amdgcn_s_waitcnt(waitcnt_imm(NA + NB, 0));
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  typename Op::frag fa[2][FM], fb[2][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+    fa[0][i] = *reinterpret_cast<const typename Op::frag*>(abuf + a_base + xo[0] + i * 32 * kBK);
+#pragma unroll
+  for (int j = 0; j < FN; ++j)
+    fb[0][j] = *reinterpret_cast<const typename Op::frag*>(bbuf + b_base + xo[0] + j * 32 * kBK);
+  int b3 = 0;  // kt % 3
+  for (int kt = 0; kt < nk; ++kt) {
+    const int b3n = b3 == 2 ? 0 : b3 + 1;  // (kt + 1) % 3
+    const int b3p = b3 == 0 ? 2 : b3 - 1;  // (kt + 2) % 3, the buffer k-step kt-1 used
+    const uint16_t* ac = abuf + (kt & 1) * SA + a_base;
+    const uint16_t* bc = bbuf + b3 * SB + b_base;
+    const uint16_t* an = abuf + ((kt + 1) & 1) * SA + a_base;
+    const uint16_t* bn = bbuf + b3n * SB + b_base;
+    const uint32_t k2 = kof(kt + 2);
+    const bool t2 = tail(kt + 2);
+    __builtin_amdgcn_sched_barrier(0);
+    rows_substep<Op, FM, FN, true>(acc, fa[0], fb[0], fa[1], fb[1], ac + xo[1], bc + xo[1], db,
+                                   bbuf + b3p * SB, wave_u, k2, t2);
+    rows_substep<Op, FM, FN, false>(acc, fa[1], fb[1], fa[0], fb[0], ac + xo[2], bc + xo[2], db,
+                                    bbuf, wave_u, k2, t2);
+    rows_substep<Op, FM, FN, false>(acc, fa[0], fb[0], fa[1], fb[1], ac + xo[3], bc + xo[3], db,
+                                    bbuf, wave_u, k2, t2);
+    // A(kt+1) and B(kt+1) landed (own copies: all but the NB just issued;
+    // other waves': the barrier) and this wave's reads of k-step kt are
+    // done, so after the barrier A(kt)'s buffer is free for A(kt+2)
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(NB, 0));
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    rows_substep<Op, FM, FN, true>(acc, fa[1], fb[1], fa[0], fb[0], an + xo[0], bn + xo[0], da,
+                                   abuf + (kt & 1) * SA, wave_u, k2, t2);
+    b3 = b3n;
+  }
+  // the trailing re-reads must land before the LDS is released
+  wait_dma();
+  __syncthreads();
+
+  // Epilogue: lane l, register r of block (i, j) is row 8*(r/4) + 4*(l/32)
+  // + r%4 and column l%32 of the block.
+  const int row0 = m0 + wm * (BM / 2) + 4 * h;
+  if constexpr (GATE) {
+    // blocks 2j, 2j + 1: gate and up of output columns c0 + 32j
+    const int c0 = n0 + wn * (BN / 4) + lc;
+    float sg[FN / 2], su[FN / 2];
+    if constexpr (I8 && EPI == kRowsGated) {
+#pragma unroll
+      for (int j = 0; j < FN / 2; ++j) {
+        const int c = min(c0 + 32 * j, p.F - 1);
+        sg[j] = p.scale_b[c];
+        su[j] = p.scale_b[p.F + c];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int row = row0 + i * 32 + 8 * (r >> 2) + (r & 3);
+        if (row >= p.M) continue;
+        float sa = 1.f;
+        if constexpr (I8 && EPI == kRowsGated) sa = p.scale_a[row];
+#pragma unroll
+        for (int j = 0; j < FN / 2; ++j) {
+          const int c = c0 + 32 * j;
+          if (c >= p.F) continue;
+          if constexpr (EPI == kRowsPart) {
+            auto* o = static_cast<std::conditional_t<I8, int, float>*>(p.part) +
+                      ((int64_t)ks * p.M + row) * p.N;
+            o[c] = acc[i][2 * j][r];
+            o[p.F + c] = acc[i][2 * j + 1][r];
+          } else {
+            float g = (float)acc[i][2 * j][r], u = (float)acc[i][2 * j + 1][r];
+            if constexpr (I8) {
+              g = g * sa * sg[j];
+              u = u * sa * su[j];
+            }
+            static_cast<uint16_t*>(p.C)[(int64_t)row * p.ldc + c] =
+                to_bf16(act_value(g, p.act) * u);
+            if constexpr (!I8) {
+              if (p.gu != nullptr) {
+                p.gu[(int64_t)row * p.ldgu + c] = to_bf16(g);
+                p.gu[(int64_t)row * p.ldgu + p.F + c] = to_bf16(u);
+              }
+            }
+          }
+        }
+      }
+  } else {
+    const int c0 = n0 + wn * (BN / 2) + lc;
+    float sb[FN];
+    if constexpr (EPI != kRowsPart) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j) sb[j] = p.scale_b[min(c0 + 32 * j, p.N - 1)];
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int row = row0 + i * 32 + 8 * (r >> 2) + (r & 3);
+        if (row >= p.M) continue;
+        float sa = 1.f;
+        if constexpr (EPI != kRowsPart) sa = p.scale_a[row];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          const int c = c0 + 32 * j;
+          if (c >= p.N) continue;
+          if constexpr (EPI == kRowsPart) {
+            static_cast<int*>(p.part)[((int64_t)ks * p.M + row) * p.N + c] = acc[i][j][r];
+          } else {
+            const float v = (float)acc[i][j][r] * sa * sb[j];
+            if constexpr (EPI == kRowsStoreBf16)
+              static_cast<uint16_t*>(p.C)[(int64_t)row * p.ldc + c] = to_bf16(v);
+            else
+              static_cast<float*>(p.C)[(int64_t)row * p.ldc + c] = v;
+          }
+        }
+      }
+  }
+}
+
+template <class Op, int B, bool GATE, int EPI>
+hipError_t launch_one(const RowsParams& p, hipStream_t s) {
+  const dim3 grid(p.tilesM * p.tilesN * p.split), block(kThreads);
+  hipLaunchKernelGGL((rows_kernel<Op, B, B, GATE, EPI>), grid, block, 0, s, p);
+  return hipGetLastError();
+}
+
+template <int B>
+hipError_t launch_tile(int type, int epi, bool gate, const RowsParams& p, hipStream_t s) {
+  if (type == kRowsI8) {
+    if (gate && epi == kRowsGated) return launch_one<OpI8, B, true, kRowsGated>(p, s);
+    if (gate && epi == kRowsPart) return launch_one<OpI8, B, true, kRowsPart>(p, s);
+    if (!gate && epi == kRowsStoreBf16) return launch_one<OpI8, B, false, kRowsStoreBf16>(p, s);
+    if (!gate && epi == kRowsStoreF32) return launch_one<OpI8, B, false, kRowsStoreF32>(p, s);
+    if (!gate && epi == kRowsPart) return launch_one<OpI8, B, false, kRowsPart>(p, s);
+  } else if (gate) {
+    if (epi == kRowsGated) return launch_one<OpBf16, B, true, kRowsGated>(p, s);
+    if (epi == kRowsPart) return launch_one<OpBf16, B, true, kRowsPart>(p, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+hipError_t launch_rows_gemm(int type, int tile, int epi, bool gate, const RowsParams& p,
+                            hipStream_t s) {
+  if (tile == kRows256) return launch_tile<256>(type, epi, gate, p, s);
+  return launch_tile<128>(type, epi, gate, p, s);
+}
+
+}  // namespace tgemm

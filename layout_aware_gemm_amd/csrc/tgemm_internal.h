@@ -3,9 +3,37 @@
 #pragma once
 
 #include <hip/hip_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
+#include <mutex>
+
 namespace tgemm {
+
+// ----------------------------------------------------------------------
+// Per-call workspace (dispatch.hip): the cached buffer of (device, stream)
+// or, for the no-allocation calls, the library's fixed device array.
+// get_workspace returns TGEMM_OK with ptr set, TGEMM_ERR_NO_MEMORY,
+// TGEMM_ERR_WORKSPACE_LIMIT or TGEMM_ERR_HIP; a call takes at most one
+// workspace and releases it after its last launch.
+// ----------------------------------------------------------------------
+struct Workspace {
+  void* ptr = nullptr;
+  bool owned = false;                 // free in stream order at the end of this call
+  std::unique_lock<std::mutex> hold;  // the cache entry, until the last launch is enqueued
+};
+enum WsMode : int { kWsCached = 0, kWsScratch = 1 };
+int get_workspace(WsMode mode, hipStream_t s, size_t bytes, Workspace* w);
+hipError_t release_workspace(Workspace& w, hipStream_t s);
+
+// TGEMM_VERBOSE is set: each call prints the path it takes.
+bool verbose();
+
+// Most workgroups of one launch (a dispatch packet's grid is at most
+// 2^32 - 1 work-items).
+constexpr int64_t kMaxWorkgroups = (int64_t(1) << 24) - 1;
+
+inline int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 // Epilogue variants of the matrix-core GEMM kernel.  The Q8 stores take
 // operands cast to e4m3fn on load (scale, clamp, round) and multiply the
@@ -69,6 +97,9 @@ hipError_t launch_gemm_nn(int cfg, int epi, const GemmParams& p, hipStream_t s);
 hipError_t launch_gemm_nt(int cfg, int epi, const GemmParams& p, hipStream_t s);
 hipError_t launch_gemm_tn(int cfg, int epi, const GemmParams& p, hipStream_t s);
 hipError_t launch_gemm_tt(int cfg, int epi, const GemmParams& p, hipStream_t s);
+
+// The one of them for the layout flags (dispatch.hip).
+hipError_t launch_gemm(char ta, char tb, int cfg, int epi, const GemmParams& p, hipStream_t s);
 
 // Split-K: C = sum over chunks q = 0, 1, ..., split-1 (in that order) of
 // the fp32 partial products ws[q][M][N] (defined in splitk.hip).

@@ -86,6 +86,92 @@ extern "C" int tgemm_validate_rope_region(const void* q, int64_t ldq, int64_t P,
   return TGEMM_OK;
 }
 
+namespace {
+
+// Products summed in int32: K codes of magnitude at most 128 each.
+constexpr int64_t kMaxK8 = 131071;
+
+// rows x cols elements with row stride ld, and offsets that fit 64 bits
+inline int check_rows(const void* p, int64_t rows, int64_t cols, int64_t ld) {
+  if (p == nullptr || ld < cols) return TGEMM_ERR_INVALID_ARG;
+  return ld > INT64_MAX / 4 / rows ? TGEMM_ERR_UNSUPPORTED : TGEMM_OK;
+}
+
+inline bool act_ok(int a) { return a == TGEMM_ACT_SILU || a == TGEMM_ACT_GELU_TANH; }
+
+}  // namespace
+
+extern "C" int tgemm_validate_i8(char transA, char transB, int64_t M, int64_t N, int64_t K,
+                                 const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb,
+                                 const float* scale_a, const float* scale_b, const void* C,
+                                 int64_t ldc, int epilogue) {
+  if (epilogue != TGEMM_EPI_STORE_BF16 && epilogue != TGEMM_EPI_STORE_F32)
+    return TGEMM_ERR_INVALID_ARG;
+  if (scale_a == nullptr || scale_b == nullptr) return TGEMM_ERR_INVALID_ARG;
+  const int st = tgemm_validate(transA, transB, M, N, K, A, lda, B, ldb, C, ldc, epilogue, nullptr,
+                                nullptr, nullptr);
+  if (st != TGEMM_OK) return st;
+  return K > kMaxK8 ? TGEMM_ERR_UNSUPPORTED : TGEMM_OK;
+}
+
+extern "C" int tgemm_validate_gated(char transA, char transB, int64_t M, int64_t F, int64_t K,
+                                    const void* A, int64_t lda, const void* B, int64_t ldb,
+                                    int activation, const void* H, int64_t ldh, const void* GU,
+                                    int64_t ldgu) {
+  if (!act_ok(activation)) return TGEMM_ERR_INVALID_ARG;
+  if (F > kMaxDim / 2) return TGEMM_ERR_UNSUPPORTED;
+  if (H == nullptr || M < 1 || F < 1 || ldh < F) return TGEMM_ERR_INVALID_ARG;
+  // (the product itself has 2F columns; its C is H here, checked above)
+  const int st = tgemm_validate(transA, transB, M, 2 * F, K, A, lda, B, ldb, H, 2 * F,
+                                TGEMM_EPI_STORE_BF16, nullptr, nullptr, nullptr);
+  if (st != TGEMM_OK) return st;
+  if (check_rows(H, M, F, ldh) != TGEMM_OK) return TGEMM_ERR_UNSUPPORTED;
+  return GU == nullptr ? TGEMM_OK : check_rows(GU, M, 2 * F, ldgu);
+}
+
+extern "C" int tgemm_validate_gated_i8(char transA, char transB, int64_t M, int64_t F, int64_t K,
+                                       const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb,
+                                       const float* scale_a, const float* scale_b, int activation,
+                                       const void* H, int64_t ldh) {
+  if (scale_a == nullptr || scale_b == nullptr) return TGEMM_ERR_INVALID_ARG;
+  const int st = tgemm_validate_gated(transA, transB, M, F, K, A, lda, B, ldb, activation, H, ldh,
+                                      nullptr, 0);
+  if (st != TGEMM_OK) return st;
+  return K > kMaxK8 ? TGEMM_ERR_UNSUPPORTED : TGEMM_OK;
+}
+
+extern "C" int tgemm_validate_gated_grad(int64_t M, int64_t F, const void* dH, int64_t lddh,
+                                         const void* GU, int64_t ldgu, int activation,
+                                         const void* dGU, int64_t lddgu) {
+  if (!act_ok(activation) || M < 1 || F < 1) return TGEMM_ERR_INVALID_ARG;
+  if (M > kMaxDim || F > kMaxDim / 2) return TGEMM_ERR_UNSUPPORTED;
+  int st = check_rows(dH, M, F, lddh);
+  if (st == TGEMM_OK) st = check_rows(GU, M, 2 * F, ldgu);
+  if (st == TGEMM_OK) st = check_rows(dGU, M, 2 * F, lddgu);
+  return st;
+}
+
+extern "C" int tgemm_validate_rms_norm_i8(const void* x, int64_t ldx, const void* residual,
+                                          int64_t ldr, const void* weight, float eps, int64_t M,
+                                          int64_t K, const void* sum, int64_t lds, const int8_t* q,
+                                          int64_t ldq, const float* scale) {
+  if (weight == nullptr || (residual == nullptr) != (sum == nullptr)) return TGEMM_ERR_INVALID_ARG;
+  // (a negative or NaN eps could make the root's argument negative)
+  if (!(eps >= 0.f) || eps > 3.402823466e38f) return TGEMM_ERR_INVALID_ARG;
+  int st = tgemm_validate_quantize_i8(x, ldx, M, K, q, ldq, scale);
+  if (st == TGEMM_OK && residual != nullptr) st = check_rows(residual, M, K, ldr);
+  if (st == TGEMM_OK && sum != nullptr) st = check_rows(sum, M, K, lds);
+  return st;
+}
+
+extern "C" int tgemm_validate_quantize_i8(const void* x, int64_t ldx, int64_t M, int64_t K,
+                                          const int8_t* q, int64_t ldq, const float* scale) {
+  if (M < 1 || K < 1 || scale == nullptr) return TGEMM_ERR_INVALID_ARG;
+  if (M > kMaxDim || K > kMaxDim) return TGEMM_ERR_UNSUPPORTED;
+  const int st = check_rows(x, M, K, ldx);
+  return st == TGEMM_OK ? check_rows(q, M, K, ldq) : st;
+}
+
 extern "C" const char* tgemm_status_string(int status) {
   switch (status) {
     case TGEMM_OK: return "TGEMM_OK";
@@ -98,4 +184,4 @@ extern "C" const char* tgemm_status_string(int status) {
   }
 }
 
-extern "C" int tgemm_version(void) { return 200; }
+extern "C" int tgemm_version(void) { return 300; }

@@ -35,7 +35,15 @@ EXPORTS = ("tgemm_run", "tgemm_run_fp8", "tgemm_validate", "tgemm_validate_fp8",
            "tgemm_set_fp8_cast_once", "tgemm_clock_probe", "tgemm_version",
            "tgemm_release_workspace", "tgemm_run_noalloc", "tgemm_noalloc_scratch_bytes",
            "tgemm_rope_region", "tgemm_validate_rope_region", "tgemm_run_ce_deferred",
-           "tgemm_run_ce_grad", "tgemm_mfma_ceiling")
+           "tgemm_run_ce_grad", "tgemm_mfma_ceiling", "tgemm_rms_norm_i8",
+           "tgemm_validate_rms_norm_i8", "tgemm_quantize_i8", "tgemm_validate_quantize_i8",
+           "tgemm_run_i8", "tgemm_validate_i8", "tgemm_run_gated", "tgemm_validate_gated",
+           "tgemm_run_gated_i8", "tgemm_validate_gated_i8", "tgemm_gated_grad",
+           "tgemm_validate_gated_grad")
+
+ACT_SILU = 0
+ACT_GELU_TANH = 1
+_ACTS = {"silu": ACT_SILU, "gelu_tanh": ACT_GELU_TANH}
 
 
 class TgemmError(RuntimeError):
@@ -101,6 +109,20 @@ def lib():
         L.tgemm_validate_rope_region.argtypes = [vp, i64, i64, i64, i64, vp, i64, vp, vp, vp, i64,
                                                  vp]
         L.tgemm_validate_rope_region.restype = ctypes.c_int
+        # the feed-forward operators: a validator takes its call's arguments
+        # without the stream
+        ch, ci, cf = ctypes.c_char, ctypes.c_int, ctypes.c_float
+        for name, args in (
+                ("rms_norm_i8", [vp, i64, vp, i64, vp, cf, i64, i64, vp, i64, vp, i64, vp]),
+                ("quantize_i8", [vp, i64, i64, i64, vp, i64, vp]),
+                ("run_i8", [ch, ch, i64, i64, i64, vp, i64, vp, i64, vp, vp, vp, i64, ci]),
+                ("run_gated", [ch, ch, i64, i64, i64, vp, i64, vp, i64, ci, vp, i64, vp, i64]),
+                ("run_gated_i8", [ch, ch, i64, i64, i64, vp, i64, vp, i64, vp, vp, ci, vp, i64]),
+                ("gated_grad", [i64, i64, vp, i64, vp, i64, ci, vp, i64])):
+            call = getattr(L, "tgemm_" + name)
+            call.argtypes, call.restype = args + [vp], ci
+            check = getattr(L, "tgemm_validate_" + name.replace("run_", ""))
+            check.argtypes, check.restype = args, ci
         _lib = L
     return _lib
 
@@ -505,6 +527,236 @@ def rope_region(q, pos, inv_freq, heads, stream=None):
     run_rope_region(q, q.stride(0), P, heads, D, pos, pos.stride(0), inv_freq, cos, sin, D, q_out,
                     stream=stream)
     return q_out, cos, sin
+
+
+# ---- the feed-forward block --------------------------------------------------
+
+
+def _act(act):
+    if isinstance(act, str):
+        if act not in _ACTS:
+            raise ValueError(f"unknown activation {act!r}: one of {sorted(_ACTS)}")
+        return _ACTS[act]
+    return int(act)
+
+
+def _same_device(*ts):
+    """The one CUDA device every given tensor is on."""
+    ts = [t for t in ts if t is not None]
+    _check_dev(*ts)
+    dev = ts[0].device
+    for t in ts[1:]:
+        if t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+    return dev
+
+
+class _On:
+    """The operands' device and the given stream made current, so that the
+    outputs and temporaries of a helper are allocated for the stream its
+    kernels run on (a stream handle or torch stream; None: the current one)."""
+
+    def __init__(self, dev, stream):
+        self._ctx = []
+        if dev.index is not None and torch.cuda.current_device() != dev.index:
+            self._ctx.append(torch.cuda.device(dev))
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = (torch.cuda.ExternalStream(int(stream), device=dev) if int(stream)
+                          else torch.cuda.default_stream(dev))
+            self._ctx.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self._ctx:
+            c.__enter__()
+
+    def __exit__(self, *exc):
+        for c in reversed(self._ctx):
+            c.__exit__(*exc)
+
+
+def _call(name, *args):
+    st = getattr(lib(), name)(*args, torch.cuda.current_stream().cuda_stream)
+    if st != TGEMM_OK:
+        raise TgemmError(st, name)
+
+
+def _rows(x, what, dtype):
+    """[..., K] -> ([rows, K] view, row stride): any row stride, unit last
+    stride."""
+    if x.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}")
+    if x.dim() < 1:
+        raise ValueError(f"{what} must have at least one dimension")
+    if x.dim() != 2:
+        if x.stride(-1) != 1 and x.shape[-1] != 1:
+            raise ValueError(f"{what} needs a contiguous last dimension")
+        x = x.view(-1, x.shape[-1])
+    if x.shape[1] != 1 and x.stride(1) != 1:
+        raise ValueError(f"{what} needs a contiguous last dimension")
+    ld = x.shape[1] if x.shape[0] == 1 else x.stride(0)
+    if ld < x.shape[1]:
+        raise ValueError(f"{what}: rows overlap (stride {ld} of {x.shape[1]} elements)")
+    return x, ld
+
+
+def _vector(x, n, what, dtype):
+    if x.dtype != dtype or x.shape != (n,) or not x.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} [{n}] tensor")
+    return x
+
+
+def _row_scales(x, lead, what):
+    """One fp32 per row, in the shape of the rows or flat."""
+    n = 1
+    for d in lead:
+        n *= d
+    if x.dtype != torch.float32 or x.numel() != n or not x.is_contiguous() or \
+            (x.dim() != 1 and x.shape != lead):
+        raise ValueError(f"{what} must be a contiguous fp32 tensor with one value per row")
+    return x
+
+
+def _product(a, b, dtype, what):
+    """Shapes, flags and strides of a [..., K] @ [K, N]."""
+    if a.dtype != dtype or b.dtype != dtype:
+        raise TypeError(f"{what} expects {dtype} operands")
+    if b.dim() != 2 or a.dim() < 1:
+        raise ValueError(f"{what} expects a [..., K] and a 2-D [K, N] operand")
+    a2 = a.view(1, -1) if a.dim() == 1 else _flatten_rows(a)
+    if a2.shape[1] != b.shape[0]:
+        raise ValueError(f"inner dimensions differ: {a2.shape[1]} vs {b.shape[0]}")
+    return (a2,) + layout_of(a2) + layout_of(b)
+
+
+def rms_norm_i8(x, weight, eps=1e-6, residual=None, out_residual=None, stream=None):
+    """RMS norm of the rows of ``x`` (plus ``residual``) to 8-bit codes.
+
+    ``x``, ``residual`` bf16 [..., K] with any row stride, ``weight`` bf16
+    [K].  Returns (q int8 [..., K], scale fp32 [...]); with a residual also
+    the bf16 sum x + residual, written to ``out_residual`` if given (which
+    may be ``residual`` or ``x`` itself).  ``q * scale[..., None]`` is the
+    normed row.
+    """
+    if residual is None and out_residual is not None:
+        raise ValueError("out_residual needs a residual")
+    x2, ldx = _rows(x, "x", torch.bfloat16)
+    M, K = x2.shape
+    _vector(weight, K, "weight", torch.bfloat16)
+    ldr = lds = 0
+    if residual is not None:
+        if residual.shape != x.shape:
+            raise ValueError("x and residual differ in shape")
+        r2, ldr = _rows(residual, "residual", torch.bfloat16)
+    with _On(_same_device(x, weight, residual, out_residual), stream):
+        q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        s2 = None
+        if residual is not None:
+            if out_residual is None:
+                out_residual = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+            if out_residual.shape != x.shape:
+                raise ValueError("x and out_residual differ in shape")
+            s2, lds = _rows(out_residual, "out_residual", torch.bfloat16)
+        _call("tgemm_rms_norm_i8", _ptr(x2), ldx, _ptr(r2) if residual is not None else None, ldr,
+              _ptr(weight), float(eps), M, K, _ptr(s2), lds, _ptr(q), K, _ptr(scale))
+    return (q, scale) if residual is None else (q, scale, out_residual)
+
+
+def quantize_i8(x, stream=None):
+    """Rows of bf16 ``x`` [..., K] to (q int8 [..., K], scale fp32 [...]):
+    ``q * scale[..., None]`` is x in 255 levels of its row's largest value."""
+    x2, ldx = _rows(x, "x", torch.bfloat16)
+    M, K = x2.shape
+    with _On(_same_device(x), stream):
+        q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        _call("tgemm_quantize_i8", _ptr(x2), ldx, M, K, _ptr(q), K, _ptr(scale))
+    return q, scale
+
+
+def matmul_i8(a, b, scale_a, scale_b, out_dtype=torch.bfloat16, stream=None):
+    """scale_a[..., None] * scale_b * (a @ b) for int8 a [..., K] and b [K, N]
+    (any row/column-major view, usually ``w.t()`` of a weight stored [N, K]);
+    exact integer sums.  ``scale_a`` fp32, one per row of a; ``scale_b`` fp32
+    [N].  ``out_dtype`` is torch.bfloat16 or torch.float32."""
+    a2, ta, lda, tb, ldb = _product(a, b, torch.int8, "matmul_i8")
+    (M, K), N = a2.shape, b.shape[1]
+    sa = _row_scales(scale_a, a.shape[:-1], "scale_a")
+    _vector(scale_b, N, "scale_b", torch.float32)
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out_dtype must be bf16 or fp32")
+    with _On(_same_device(a, b, sa, scale_b), stream):
+        out = torch.empty(a.shape[:-1] + (N,), dtype=out_dtype, device=a.device)
+        _call("tgemm_run_i8", _flag(ta), _flag(tb), M, N, K, _ptr(a2), lda, _ptr(b), ldb, _ptr(sa),
+              _ptr(scale_b), _ptr(out), N,
+              EPI_STORE_BF16 if out_dtype == torch.bfloat16 else EPI_STORE_F32)
+    return out
+
+
+def _gate_width(w):
+    if w.dim() != 2 or w.shape[1] % 2 or w.shape[1] == 0:
+        raise ValueError("the gated weight is [K, 2F]: F gate columns, then F up columns")
+    return w.shape[1] // 2
+
+
+def gated_matmul_i8(a, b, scale_a, scale_b, act="silu", stream=None):
+    """act(g) * u as bf16 [..., F], [g | u] = ``matmul_i8(a, b, ...)`` with b
+    int8 [K, 2F] (g first) and ``scale_b`` fp32 [2F]; g and u stay in fp32
+    registers."""
+    F = _gate_width(b)
+    a2, ta, lda, tb, ldb = _product(a, b, torch.int8, "gated_matmul_i8")
+    M, K = a2.shape
+    sa = _row_scales(scale_a, a.shape[:-1], "scale_a")
+    _vector(scale_b, 2 * F, "scale_b", torch.float32)
+    with _On(_same_device(a, b, sa, scale_b), stream):
+        h = torch.empty(a.shape[:-1] + (F,), dtype=torch.bfloat16, device=a.device)
+        _call("tgemm_run_gated_i8", _flag(ta), _flag(tb), M, F, K, _ptr(a2), lda, _ptr(b), ldb,
+              _ptr(sa), _ptr(scale_b), _act(act), _ptr(h), F)
+    return h
+
+
+def gated_matmul(x, w, act="silu", save=False, stream=None):
+    """The gated projections of a feed-forward block: h = act(g) * u, bf16
+    [..., F], with [g | u] = x @ w for bf16 x [..., K] and w [K, 2F] (any
+    row/column-major view, usually ``W.t()`` of a weight stored [2F, K] with
+    the gate rows first).  ``act``: "silu" or "gelu_tanh".  ``save``: also
+    return gu, bf16 [..., 2F], which ``gated_backward`` reads."""
+    F = _gate_width(w)
+    x2, ta, lda, tb, ldb = _product(x, w, torch.bfloat16, "gated_matmul")
+    M, K = x2.shape
+    with _On(_same_device(x, w), stream):
+        h = torch.empty(x.shape[:-1] + (F,), dtype=torch.bfloat16, device=x.device)
+        gu = (torch.empty(x.shape[:-1] + (2 * F,), dtype=torch.bfloat16, device=x.device)
+              if save else None)
+        _call("tgemm_run_gated", _flag(ta), _flag(tb), M, F, K, _ptr(x2), lda, _ptr(w), ldb,
+              _act(act), _ptr(h), F, _ptr(gu), 2 * F)
+    return (h, gu) if save else h
+
+
+def gated_backward(dh, gu, x, w, act="silu", dw_dtype=torch.bfloat16, stream=None):
+    """Gradients (dx [..., K] bf16, dw [K, 2F]) of ``gated_matmul`` for the
+    gradient ``dh`` bf16 [..., F] of h; ``gu`` as the forward saved it, ``x``
+    and ``w`` its operands.  dw has w's layout (for ``W.t()``, dw.t() is the
+    contiguous [2F, K] gradient of W) and ``dw_dtype`` (bf16 or fp32)."""
+    F = _gate_width(w)
+    x2, _, _, tb, _ = _product(x, w, torch.bfloat16, "gated_backward")
+    M, K = x2.shape
+    if dh.shape != x.shape[:-1] + (F,) or gu.shape != x.shape[:-1] + (2 * F,):
+        raise ValueError("dh must be [..., F] and gu [..., 2F] for x [..., K]")
+    if dw_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("dw_dtype must be bf16 or fp32")
+    d2, ldd = _rows(dh, "dh", torch.bfloat16)
+    g2, ldg = _rows(gu, "gu", torch.bfloat16)
+    with _On(_same_device(dh, gu, x, w), stream):
+        dgu = torch.empty(M, 2 * F, dtype=torch.bfloat16, device=x.device)
+        _call("tgemm_gated_grad", M, F, _ptr(d2), ldd, _ptr(g2), ldg, _act(act), _ptr(dgu), 2 * F)
+        dx = matmul(dgu, w.t())
+        if tb == "T":
+            dw = matmul(dgu.t(), x2, out_dtype=dw_dtype).t()
+        else:
+            dw = matmul(x2.t(), dgu, out_dtype=dw_dtype)
+    return dx.view(x.shape), dw
 
 
 def outer_f32(a, b, stream=None):

@@ -31,6 +31,9 @@ Everything is computed from the plain definitions in fp64 with NumPy:
                      for the pattern of output1 = pointwise(input); output2 =
                      transpose(output1)" (the example: scale, clamp, cast to
                      e4m3fn) applied to both operands of the GEMM.
+* ``ffn``         -- the feed-forward block around the down projection: row
+                     quantiser with and without RMS norm, 8-bit products,
+                     gated projections and their gradient.
 
 Parity pins: every function is pinned in ``tests/test_oracle.py`` against
 brute force, closed forms, identities or library routines.  The exact bf16
@@ -43,6 +46,7 @@ from .gemm import op_matrix, gemm
 from .xent import cross_entropy, logsumexp_rows, tile_partials, merge_partials, merge_pair
 from .rope import k1_outer, rope_angles, rope_tables, rope_region
 from .fp8 import E4M3_MAX, e4m3_round, quantize, gemm_fp8
+from . import ffn
 
 __all__ = [
     "bf16_bits_to_f64",
@@ -62,4 +66,5 @@ __all__ = [
     "e4m3_round",
     "quantize",
     "gemm_fp8",
+    "ffn",
 ]
