@@ -59,9 +59,7 @@ hipError_t launch_rows_gemm(int type, int tile, int epi, bool gate, const RowsPa
 
 // Products of at most kSkinnyRows rows of A (rows_skinny.hip).
 constexpr int kSkinnyRows = 64;
-hipError_t launch_rows_skinny(int type, int epi, bool gate, const RowsParams& p, hipStream_t s);
-// The K chunks the kernel above should be split into (1: no partials).
-int rows_skinny_split(const RowsParams& p, bool gate);
+hipError_t launch_rows_skinny(int type, int epi, const RowsParams& p, hipStream_t s);
 
 // Sum the partial products over the K chunks and apply `epi` (one of
 // kRowsStoreBf16, kRowsStoreF32, kRowsGated) (rows_finish.hip).

@@ -35,9 +35,7 @@ struct RowsPlan {
 RowsPlan plan_rows(RowsParams* p, bool gate) {
   RowsPlan r = {p->M <= kSkinnyRows, kRows256};
   p->split = 1;
-  if (r.skinny) {
-    p->split = rows_skinny_split(*p, gate);
-  } else {
+  if (!r.skinny) {
     const int64_t t256 = (int64_t)ceil_div(p->M, 256) * ceil_div(p->N, 256);
     r.tile = t256 >= 128 ? kRows256 : kRows128;
     const int b = rows_tile(r.tile);
@@ -64,7 +62,7 @@ bool grid_fits(const RowsParams& p, const RowsPlan& r, bool gate) {
 hipError_t launch_rows(int type, const RowsParams& p, const RowsPlan& r, int epi, bool gate,
                        hipStream_t s) {
   const int e = p.split > 1 ? (int)kRowsPart : epi;
-  const hipError_t h = r.skinny ? launch_rows_skinny(type, e, gate, p, s)
+  const hipError_t h = r.skinny ? launch_rows_skinny(type, e, p, s)
                                 : launch_rows_gemm(type, r.tile, e, gate, p, s);
   return h != hipSuccess || p.split == 1 ? h : launch_rows_finish(type, epi, p, s);
 }

@@ -168,10 +168,91 @@ __device__ __forceinline__ void rows_substep(typename Op::acc (&acc)[FM][FN],
   }
 }
 
+// Lane l, register r of accumulator block (i, j) is row 8*(r/4) + 4*(l/32)
+// + r%4 and column l%32 of the block.  scl: the tile's scales in LDS (loaded
+// at the kernel's start, one per thread: fetched from memory between the
+// stores they cost 28 us per 256x256 tile, half of a K = 4096 main loop).
+template <class Op, int BM, int BN, bool GATE, int EPI, bool FULL>
+__device__ __forceinline__ void rows_epilogue(const RowsParams& p,
+                                              typename Op::acc (&acc)[BM / 64][BN / 64],
+                                              const float* scl, int m0, int n0, int wm, int wn,
+                                              int lane, int ks) {
+  constexpr bool I8 = std::is_same<Op, OpI8>::value;
+  constexpr bool SCALED = I8 && EPI != kRowsPart;
+  constexpr int FM = BM / 64, FN = BN / 64;
+  const int h = lane >> 5, lc = lane & 31;
+  const int rl = wm * (BM / 2) + 4 * h;   // lane's first row in the tile
+  const int cl = wn * (BN / 2) + lc;      // lane's first tile column
+  const int nout = GATE ? p.F : p.N;
+  // lane's first output column
+  const int c0 = n0 + (GATE ? wn * (BN / 4) + lc : cl);
+  float sb[FN];
+  if constexpr (SCALED) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j) sb[j] = scl[BM + cl + 32 * j];
+  }
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float4 sa = make_float4(1.f, 1.f, 1.f, 1.f);
+      if constexpr (SCALED)
+        sa = *reinterpret_cast<const float4*>(scl + rl + i * 32 + 8 * q);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = 4 * q + e;
+        const int row = m0 + rl + i * 32 + 8 * q + e;
+        if (!FULL && row >= p.M) continue;
+        const float s = e == 0 ? sa.x : e == 1 ? sa.y : e == 2 ? sa.z : sa.w;
+        if constexpr (EPI == kRowsPart) {
+          auto* o = static_cast<std::conditional_t<I8, int, float>*>(p.part) +
+                    ((int64_t)ks * p.M + row) * p.N;
+#pragma unroll
+          for (int j = 0; j < FN; ++j) {
+            const int c = c0 + 32 * (GATE ? j / 2 : j);
+            if (FULL || c < nout) o[(GATE && (j & 1) ? p.F : 0) + c] = acc[i][j][r];
+          }
+        } else if constexpr (GATE) {
+          uint16_t* const o = static_cast<uint16_t*>(p.C) + (int64_t)row * p.ldc;
+#pragma unroll
+          for (int j = 0; j < FN / 2; ++j) {
+            const int c = c0 + 32 * j;
+            float g = (float)acc[i][2 * j][r], u = (float)acc[i][2 * j + 1][r];
+            if constexpr (I8) {
+              g = g * s * sb[2 * j];
+              u = u * s * sb[2 * j + 1];
+            }
+            if (!FULL && c >= nout) continue;
+            o[c] = to_bf16(act_value(g, p.act) * u);
+            if constexpr (!I8) {
+              if (p.gu != nullptr) {
+                uint16_t* const w = p.gu + (int64_t)row * p.ldgu;
+                w[c] = to_bf16(g);
+                w[p.F + c] = to_bf16(u);
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < FN; ++j) {
+            const int c = c0 + 32 * j;
+            const float v = (float)acc[i][j][r] * s * sb[j];
+            if (!FULL && c >= nout) continue;
+            if constexpr (EPI == kRowsStoreBf16)
+              static_cast<uint16_t*>(p.C)[(int64_t)row * p.ldc + c] = to_bf16(v);
+            else
+              static_cast<float*>(p.C)[(int64_t)row * p.ldc + c] = v;
+          }
+        }
+      }
+    }
+}
+
 template <class Op, int BM, int BN, bool GATE, int EPI>
 __global__ void __launch_bounds__(kThreads, BM == 256 ? 1 : 2) rows_kernel(RowsParams p) {
-  constexpr bool I8 = std::is_same<Op, OpI8>::value;
+  constexpr bool SCALED = std::is_same<Op, OpI8>::value && EPI != kRowsPart;
   constexpr int FM = BM / 64, FN = BN / 64;
+  constexpr int NT = GATE ? BN / 2 : BN;       // output columns per tile
   constexpr int SA = BM * kBK, SB = BN * kBK;  // panel sizes in 16-bit units
   static_assert(FM + FN <= FM * FN && FN % 2 == 0, "slots for the fragment reads, gate pairs");
   __shared__ __attribute__((aligned(16))) uint16_t lds[2 * SA + 3 * SB];
@@ -183,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, BM == 256 ? 1 : 2) rows_kernel(RowsP
   int tile, ks, tm, tn;
   xcd_remap(blockIdx.x, p.tilesM * p.tilesN * p.split, p.split, tile, ks);
   tile_coords(tile, p.tilesM, p.tilesN, p.groupM, tm, tn);
-  const int m0 = tm * BM, n0 = tn * (GATE ? BN / 2 : BN);
+  const int m0 = tm * BM, n0 = tn * NT;
   const int kb = ks * p.kchunk, kend = min(p.K, kb + p.kchunk);
   const int nk = (kend - kb + kRowBytes - 1) / kRowBytes;
   const bool partial = ((kend - kb) & (kRowBytes - 1)) != 0;
@@ -200,6 +281,17 @@ __global__ void __launch_bounds__(kThreads, BM == 256 ? 1 : 2) rows_kernel(RowsP
   RowsPanel<BN, GATE> db;
   da.init(p.A, p.lda, p.M, m0, kb, kend, wave_u, lane);
   db.init(p.B, p.ldb, GATE ? p.F : p.N, n0, kb, kend, wave_u, lane);
+
+  // the scales of tile row and tile column threadIdx.x, for the epilogue
+  float sa_t = 0.f, sb_t = 0.f;
+  if constexpr (SCALED) {
+    const int t = threadIdx.x;
+    sa_t = p.scale_a[min(m0 + t, p.M - 1)];
+    if constexpr (GATE)
+      sb_t = p.scale_b[((t & 32) ? p.F : 0) + min(n0 + (t >> 6) * 32 + (t & 31), p.F - 1)];
+    else
+      sb_t = p.scale_b[min(n0 + t, p.N - 1)];
+  }
 
   uint16_t* const abuf = lds;           // two A panels
   uint16_t* const bbuf = lds + 2 * SA;  // three B panels
@@ -256,90 +348,21 @@ __global__ void __launch_bounds__(kThreads, BM == 256 ? 1 : 2) rows_kernel(RowsP
                                    abuf + (kt & 1) * SA, wave_u, k2, t2);
     b3 = b3n;
   }
-  // the trailing re-reads must land before the LDS is released
+  // the trailing re-reads must land before the LDS is reused or released
   wait_dma();
   __syncthreads();
-
-  // Epilogue: lane l, register r of block (i, j) is row 8*(r/4) + 4*(l/32)
-  // + r%4 and column l%32 of the block.
-  const int row0 = m0 + wm * (BM / 2) + 4 * h;
-  if constexpr (GATE) {
-    // blocks 2j, 2j + 1: gate and up of output columns c0 + 32j
-    const int c0 = n0 + wn * (BN / 4) + lc;
-    float sg[FN / 2], su[FN / 2];
-    if constexpr (I8 && EPI == kRowsGated) {
-#pragma unroll
-      for (int j = 0; j < FN / 2; ++j) {
-        const int c = min(c0 + 32 * j, p.F - 1);
-        sg[j] = p.scale_b[c];
-        su[j] = p.scale_b[p.F + c];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int row = row0 + i * 32 + 8 * (r >> 2) + (r & 3);
-        if (row >= p.M) continue;
-        float sa = 1.f;
-        if constexpr (I8 && EPI == kRowsGated) sa = p.scale_a[row];
-#pragma unroll
-        for (int j = 0; j < FN / 2; ++j) {
-          const int c = c0 + 32 * j;
-          if (c >= p.F) continue;
-          if constexpr (EPI == kRowsPart) {
-            auto* o = static_cast<std::conditional_t<I8, int, float>*>(p.part) +
-                      ((int64_t)ks * p.M + row) * p.N;
-            o[c] = acc[i][2 * j][r];
-            o[p.F + c] = acc[i][2 * j + 1][r];
-          } else {
-            float g = (float)acc[i][2 * j][r], u = (float)acc[i][2 * j + 1][r];
-            if constexpr (I8) {
-              g = g * sa * sg[j];
-              u = u * sa * su[j];
-            }
-            static_cast<uint16_t*>(p.C)[(int64_t)row * p.ldc + c] =
-                to_bf16(act_value(g, p.act) * u);
-            if constexpr (!I8) {
-              if (p.gu != nullptr) {
-                p.gu[(int64_t)row * p.ldgu + c] = to_bf16(g);
-                p.gu[(int64_t)row * p.ldgu + p.F + c] = to_bf16(u);
-              }
-            }
-          }
-        }
-      }
-  } else {
-    const int c0 = n0 + wn * (BN / 2) + lc;
-    float sb[FN];
-    if constexpr (EPI != kRowsPart) {
-#pragma unroll
-      for (int j = 0; j < FN; ++j) sb[j] = p.scale_b[min(c0 + 32 * j, p.N - 1)];
-    }
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int row = row0 + i * 32 + 8 * (r >> 2) + (r & 3);
-        if (row >= p.M) continue;
-        float sa = 1.f;
-        if constexpr (EPI != kRowsPart) sa = p.scale_a[row];
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          const int c = c0 + 32 * j;
-          if (c >= p.N) continue;
-          if constexpr (EPI == kRowsPart) {
-            static_cast<int*>(p.part)[((int64_t)ks * p.M + row) * p.N + c] = acc[i][j][r];
-          } else {
-            const float v = (float)acc[i][j][r] * sa * sb[j];
-            if constexpr (EPI == kRowsStoreBf16)
-              static_cast<uint16_t*>(p.C)[(int64_t)row * p.ldc + c] = to_bf16(v);
-            else
-              static_cast<float*>(p.C)[(int64_t)row * p.ldc + c] = v;
-          }
-        }
-      }
+  float* const scl = reinterpret_cast<float*>(lds);  // BM row scales, BN column scales
+  if constexpr (SCALED) {
+    if ((int)threadIdx.x < BM) scl[threadIdx.x] = sa_t;
+    if ((int)threadIdx.x < BN) scl[BM + threadIdx.x] = sb_t;
+    __syncthreads();
   }
+  // A wave whose whole block lies inside the output stores without tests.
+  const bool full = m0 + BM <= p.M && n0 + NT <= (GATE ? p.F : p.N);
+  if (full)
+    rows_epilogue<Op, BM, BN, GATE, EPI, true>(p, acc, scl, m0, n0, wm, wn, lane, ks);
+  else
+    rows_epilogue<Op, BM, BN, GATE, EPI, false>(p, acc, scl, m0, n0, wm, wn, lane, ks);
 }
 
 template <class Op, int B, bool GATE, int EPI>

@@ -3,17 +3,21 @@
 // kernel streams B from HBM once, at full width, and nothing else matters.
 //
 // The weight's rows take the matrix instruction's row side (16x16x64 int8,
-// 16x16x32 bf16) and the tokens its column side: a lane loads 16 bytes of
-// row l%16 at chunk l/16 of a 64-byte step straight into the operand
-// register, with no LDS in between, since no other wave needs them.  The
-// tokens' operand has the same shape and comes from L2.  Tokens past M
-// repeat the last one (their columns are not stored), weight rows past N
-// the last row.
+// 16x16x32 bf16) and the tokens its column side.  Its operand layout has
+// consecutive lanes on different rows, and loading it that way from memory
+// takes one request per lane (measured: 4.6 TB/s at best, bound by the
+// address units).  So a wave loads whole 128-byte runs of its rows into
+// registers and turns them around through LDS words of its own: no barrier,
+// and the registers keep the next step's loads in flight meanwhile.
 //
-// A workgroup's W waves share one block of weight rows and split K; their
-// sums meet in LDS, in wave order, so the result does not depend on timing.
-// Where the blocks alone leave compute units without work, K is split over
-// workgroups too and rows_finish adds the chunks.
+// A workgroup's W waves share one block of weight rows and take its 128-byte
+// steps of K in turn, so together they read consecutive memory; their sums
+// meet in LDS, in wave order, so the result does not depend on timing.  K is
+// never split over workgroups: the second pass costs more than the idle
+// compute units of a small weight (2048 x 8192: 6 us in all).
+//
+// Measured (MI355X, HBM-resident weights): 5.2 to 5.7 TB/s of weight for up
+// to 16 tokens, where a large copy reaches 4.7.
 #include "ffn.h"
 #include "gemm_kernel.h"
 
@@ -25,7 +29,6 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 struct SkI8 {
   typedef i32x4_t acc;
-  typedef int elem;
   static __device__ __forceinline__ acc mma(const i32x4_t& a, const i32x4_t& b, const acc& c) {
 #if defined(__HIP_DEVICE_COMPILE__)
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
@@ -36,7 +39,6 @@ struct SkI8 {
 };
 struct SkBf16 {
   typedef f32x4_t acc;
-  typedef float elem;
   static __device__ __forceinline__ acc mma(const i32x4_t& a, const i32x4_t& b, const acc& c) {
 #if defined(__HIP_DEVICE_COMPILE__)
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
@@ -47,43 +49,26 @@ struct SkBf16 {
   }
 };
 
-constexpr int kStep = 64;  // bytes of K per row and matrix instruction
+constexpr int kStep = 128;  // bytes of K per row and step
 
-// MB blocks of 16 tokens, NB blocks of 16 weight rows per wave (GATE: the
+// TB groups of 8 tokens, NB blocks of 16 weight rows per wave (GATE: the
 // first half gate rows, the second half the up rows of the same outputs),
 // W waves.
-template <class Op, int MB, int NB, int W, bool GATE, int EPI>
+template <class Op, int TB, int NB, int W, bool GATE, int EPI>
 __global__ void __launch_bounds__(W * 64) skinny_kernel(RowsParams p) {
   constexpr bool I8 = std::is_same<Op, SkI8>::value;
   constexpr int NO = GATE ? NB / 2 : NB;  // blocks of 16 outputs
-  constexpr int U = NB * MB >= 8 ? 2 : (NB + MB > 4 ? 4 : 8);  // steps in flight
-  __shared__ typename Op::acc red[W][NB * MB][64];
+  constexpr int MB = (TB + 1) / 2;        // blocks of 16 tokens
+  // a wave's staged rows, 16-byte units: weight rows, then tokens
+  constexpr int ROWS = NB * 16 + TB * 8, STAGE = ROWS * 8;
+  constexpr int RED = NB * MB * 64;
+  __shared__ i32x4_t lds[W * (STAGE > RED ? STAGE : RED)];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int r = lane & 15, g = lane >> 4;
   const int nout = GATE ? p.F : p.N;
-  const int nblk = (nout + 16 * NO - 1) / (16 * NO);
-  const int blk = blockIdx.x % nblk, ks = blockIdx.x / nblk;
-  const int n0 = blk * 16 * NO;
-  // this wave's bytes of K: whole steps, except the last wave of the last
-  // chunk
-  const int cb = ks * p.kchunk, ce = min(p.K, cb + p.kchunk);
-  const int steps = (ce - cb + kStep - 1) / kStep;
-  const int per = (steps + W - 1) / W;
-  const int s0 = min(steps, wave * per), s1 = min(steps, s0 + per);
-  const int kb = cb + s0 * kStep, ke = min(ce, cb + s1 * kStep);
-
-  const char* bp[NB];
-#pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    const int o = min(n0 + (GATE ? b % NO : b) * 16 + r, nout - 1);
-    const int64_t row = GATE && b >= NO ? (int64_t)p.F + o : o;
-    bp[b] = p.B + row * p.ldb + g * 16;
-  }
-  const char* ap[MB];
-#pragma unroll
-  for (int m = 0; m < MB; ++m) ap[m] = p.A + (int64_t)min(m * 16 + r, p.M - 1) * p.lda + g * 16;
+  const int n0 = blockIdx.x * 16 * NO;
+  const int steps = (p.K + kStep - 1) / kStep;
 
   typename Op::acc acc[MB][NB];
 #pragma unroll
@@ -91,48 +76,87 @@ __global__ void __launch_bounds__(W * 64) skinny_kernel(RowsParams p) {
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[m][b] = typename Op::acc{0, 0, 0, 0};
 
-  int k = kb;
-  for (; k + U * kStep <= ke; k += U * kStep) {
-    i32x4_t wv[U][NB], av[U][MB];
+#if defined(__HIP_DEVICE_COMPILE__)
+  // Loads: lane l takes row l/8, chunk l%8 of each group of 8 rows.  Weight
+  // rows past the last repeat it, tokens past M the last one (neither is
+  // stored).  The buffers' range is 2^31 - 1 bytes, which no row passes
+  // (the host checks the strides); a chunk at or past the end of K takes an
+  // offset past it and reads as zero.
+  const int lc = lane & 7, lr = lane >> 3;
+  uint32_t woff[2 * NO], aoff[TB];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+  for (int b = 0; b < 2 * NO; ++b)
+    woff[b] = (uint32_t)((min(n0 + b * 8 + lr, nout - 1) - n0) * (int)p.ldb);
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
-        wv[u][b] = *reinterpret_cast<const i32x4_t*>(bp[b] + k + u * kStep);
+  for (int t = 0; t < TB; ++t) aoff[t] = (uint32_t)(min(t * 8 + lr, p.M - 1) * (int)p.lda);
+  __amdgpu_buffer_rsrc_t rw[GATE ? 2 : 1], ra;
+  ra = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p.A), (short)0, 0x7fffffff,
+                                         0x00020000);
+  rw[0] = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p.B + (int64_t)n0 * p.ldb),
+                                            (short)0, 0x7fffffff, 0x00020000);
+  if constexpr (GATE)
+    rw[1] = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(p.B + ((int64_t)p.F + n0) * p.ldb), (short)0, 0x7fffffff,
+        0x00020000);
+  i32x4_t wv[2 * NB], av[TB];
+  auto load = [&](int s) __attribute__((always_inline)) {
+    const int k = s * kStep + lc * 16;
+    const uint32_t ko = k < p.K ? (uint32_t)k : 0x80000000u;
 #pragma unroll
-      for (int m = 0; m < MB; ++m)
-        av[u][m] = *reinterpret_cast<const i32x4_t*>(ap[m] + k + u * kStep);
-    }
+    for (int b = 0; b < 2 * NB; ++b)
+      wv[b] = __builtin_bit_cast(
+          i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rw[GATE ? b / (2 * NO) : 0],
+                                                         (int)(woff[b % (2 * NO)] + ko), 0, 0));
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int t = 0; t < TB; ++t)
+      av[t] = __builtin_bit_cast(
+          i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ra, (int)(aoff[t] + ko), 0, 0));
+  };
+  // Staged row R holds its chunk c at c ^ swz(R), as in the tiled kernels:
+  // neither the writes nor the operand reads conflict.
+  i32x4_t* const st = lds + wave * STAGE;
+  int wr[2];  // even / odd groups of 8 rows
 #pragma unroll
-      for (int m = 0; m < MB; ++m)
+  for (int q = 0; q < 2; ++q) wr[q] = lr * 8 + (lc ^ swz(8 * q + lr));
+  const int r = lane & 15, g = lane >> 4;
+  const int ar = TB == 1 ? (r & 7) : r;  // (8 tokens: columns 8-15 repeat them)
+  int fo[2], ao[2];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) acc[m][b] = Op::mma(wv[u][b], av[u][m], acc[m][b]);
-  }
-  for (; k < ke; k += kStep) {
-    i32x4_t wv[NB], av[MB];
-    const bool in = k + g * 16 < ke;  // (K is a multiple of 16 bytes)
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      wv[b] = i32x4_t{0, 0, 0, 0};
-      if (in) wv[b] = *reinterpret_cast<const i32x4_t*>(bp[b] + k);
-    }
-#pragma unroll
-    for (int m = 0; m < MB; ++m) {
-      av[m] = i32x4_t{0, 0, 0, 0};
-      if (in) av[m] = *reinterpret_cast<const i32x4_t*>(ap[m] + k);
-    }
-#pragma unroll
-    for (int m = 0; m < MB; ++m)
-#pragma unroll
-      for (int b = 0; b < NB; ++b) acc[m][b] = Op::mma(wv[b], av[m], acc[m][b]);
+  for (int s = 0; s < 2; ++s) {
+    fo[s] = r * 8 + ((4 * s + g) ^ swz(r));
+    ao[s] = NB * 128 + ar * 8 + ((4 * s + g) ^ swz(ar));
   }
 
+  if (wave < steps) load(wave);
+  for (int s = wave; s < steps; s += W) {
+#pragma unroll
+    for (int b = 0; b < 2 * NB; ++b) st[b * 64 + wr[b & 1]] = wv[b];
+#pragma unroll
+    for (int t = 0; t < TB; ++t) st[NB * 128 + t * 64 + wr[t & 1]] = av[t];
+    if (s + W < steps) load(s + W);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      i32x4_t wf[NB], af[MB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) wf[b] = st[b * 128 + fo[q]];
+#pragma unroll
+      for (int m = 0; m < MB; ++m) af[m] = st[m * 128 + ao[q]];
+#pragma unroll
+      for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) acc[m][b] = Op::mma(wf[b], af[m], acc[m][b]);
+    }
+  }
+#else
+  (void)steps, (void)n0;
+#endif
+
+  __syncthreads();  // the staged rows become the sums' buffer
+  typename Op::acc* const red = reinterpret_cast<typename Op::acc*>(lds);
 #pragma unroll
   for (int m = 0; m < MB; ++m)
 #pragma unroll
-    for (int b = 0; b < NB; ++b) red[wave][m * NB + b][lane] = acc[m][b];
+    for (int b = 0; b < NB; ++b) red[wave * RED + (m * NB + b) * 64 + lane] = acc[m][b];
   __syncthreads();
 
   // One thread per (token, 4 consecutive outputs): lane l of a block holds
@@ -143,23 +167,19 @@ __global__ void __launch_bounds__(W * 64) skinny_kernel(RowsParams p) {
     const int row = m * 16 + (l & 15);
     const int c0 = n0 + b * 16 + 4 * (l >> 4);
     if (row >= p.M) continue;
-    typename Op::acc a = red[0][m * NB + b][l], a2 = a;
+    typename Op::acc a = red[(m * NB + b) * 64 + l], a2 = a;
 #pragma unroll
-    for (int w = 1; w < W; ++w) a += red[w][m * NB + b][l];
+    for (int w = 1; w < W; ++w) a += red[w * RED + (m * NB + b) * 64 + l];
     if constexpr (GATE) {
-      a2 = red[0][m * NB + NO + b][l];
+      a2 = red[(m * NB + NO + b) * 64 + l];
 #pragma unroll
-      for (int w = 1; w < W; ++w) a2 += red[w][m * NB + NO + b][l];
+      for (int w = 1; w < W; ++w) a2 += red[w * RED + (m * NB + NO + b) * 64 + l];
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int c = c0 + e;
       if (c >= nout) continue;
-      if constexpr (EPI == kRowsPart) {
-        auto* o = static_cast<typename Op::elem*>(p.part) + ((int64_t)ks * p.M + row) * p.N;
-        o[c] = a[e];
-        if constexpr (GATE) o[p.F + c] = a2[e];
-      } else if constexpr (GATE) {
+      if constexpr (GATE) {
         float gv = (float)a[e], uv = (float)a2[e];
         if constexpr (I8) {
           const float sa = p.scale_a[row];
@@ -184,46 +204,57 @@ __global__ void __launch_bounds__(W * 64) skinny_kernel(RowsParams p) {
   }
 }
 
-template <class Op, int MB, int NB, int W, bool GATE, int EPI>
+template <class Op, int TB, int NB, int W, bool GATE, int EPI>
 hipError_t launch_one(const RowsParams& p, hipStream_t s) {
   constexpr int NO = GATE ? NB / 2 : NB;
   const int nblk = ceil_div(GATE ? p.F : p.N, 16 * NO);
-  hipLaunchKernelGGL((skinny_kernel<Op, MB, NB, W, GATE, EPI>), dim3(nblk * p.split), dim3(W * 64),
-                     0, s, p);
+  hipLaunchKernelGGL((skinny_kernel<Op, TB, NB, W, GATE, EPI>), dim3(nblk), dim3(W * 64), 0, s,
+                     p);
   return hipGetLastError();
 }
 
-// Waves per workgroup: 8 for gated blocks (two weight rows streams per
-// wave), 16 for plain ones, 8 once the tokens' sums fill the LDS.
+template <class Op, int NB, int W, bool GATE, int EPI>
+hipError_t launch_nb(const RowsParams& p, hipStream_t s) {
+  if (p.M <= 8) return launch_one<Op, 1, NB, W, GATE, EPI>(p, s);
+  if (p.M <= 16) return launch_one<Op, 2, NB, W, GATE, EPI>(p, s);
+  if (p.M <= 32) return launch_one<Op, 4, NB, W, GATE, EPI>(p, s);
+  return launch_one<Op, 8, NB, W, GATE, EPI>(p, s);
+}
+
+// Blocks of weight rows per wave and waves per workgroup, by the number of
+// tokens and of blocks (us on MI355X; int8, N x K = 5120 x 13824 / 32000 x
+// 4096, then gated 13824 x 5120 int8 / bf16):
+//   one token    two blocks (gated four), 8 waves   12.4  27.9  28.6  52.3
+//                half the blocks                    12.9  26.9  29.6  54.5
+//                half the waves                     14.4  31.0  28.9  52.2
+//   32 tokens    two (four), 8 waves                14.3  32.9  37.0  63.1
+//                half the blocks                    19.5  38.6  38.6  67.6
+//   64 tokens    two (four), 8 waves                19.7  44.9  42.1  73.1
+//                the same, 4 waves                  20.1  43.0  40.5  71.5
+//                four, 4 waves                      27.4  36.9
+// Fewer than 128 such blocks leave compute units idle, and half the blocks
+// win (2048 x 4096: 4.6 against 4.9; 1024 x 16384: 8.6 against 9.6).
 template <class Op, bool GATE, int EPI>
-hipError_t launch_mb(const RowsParams& p, hipStream_t s) {
-  constexpr int NB = GATE ? 2 : 1;
-  if (p.M <= 16) return launch_one<Op, 1, NB, 8, GATE, EPI>(p, s);
-  if (p.M <= 32) return launch_one<Op, 2, NB, 8, GATE, EPI>(p, s);
-  return launch_one<Op, 4, NB, 8, GATE, EPI>(p, s);
+hipError_t launch_blocks(const RowsParams& p, hipStream_t s) {
+  constexpr int NB = GATE ? 4 : 2;
+  const int nout = GATE ? p.F : p.N;
+  if (ceil_div(nout, 32) < 128) return launch_nb<Op, NB / 2, 8, GATE, EPI>(p, s);
+  if (p.M <= 32) return launch_nb<Op, NB, 8, GATE, EPI>(p, s);
+  if constexpr (!GATE) {
+    if (ceil_div(nout, 64) >= 256) return launch_one<Op, 8, 4, 4, GATE, EPI>(p, s);
+  }
+  return launch_one<Op, 8, NB, 4, GATE, EPI>(p, s);
 }
 
 }  // namespace
 
-int rows_skinny_split(const RowsParams& p, bool gate) {
-  const int nblk = ceil_div(gate ? p.F : p.N, 16);
-  const int fill = 256 / nblk, by_k = p.K / 4096;
-  const int n = fill < by_k ? fill : by_k;
-  return n < 1 ? 1 : n;
-}
-
-hipError_t launch_rows_skinny(int type, int epi, bool gate, const RowsParams& p, hipStream_t s) {
+hipError_t launch_rows_skinny(int type, int epi, const RowsParams& p, hipStream_t s) {
   if (p.M > kSkinnyRows) return hipErrorInvalidValue;
-  if (type == kRowsI8) {
-    if (gate && epi == kRowsGated) return launch_mb<SkI8, true, kRowsGated>(p, s);
-    if (gate && epi == kRowsPart) return launch_mb<SkI8, true, kRowsPart>(p, s);
-    if (!gate && epi == kRowsStoreBf16) return launch_mb<SkI8, false, kRowsStoreBf16>(p, s);
-    if (!gate && epi == kRowsStoreF32) return launch_mb<SkI8, false, kRowsStoreF32>(p, s);
-    if (!gate && epi == kRowsPart) return launch_mb<SkI8, false, kRowsPart>(p, s);
-  } else if (gate) {
-    if (epi == kRowsGated) return launch_mb<SkBf16, true, kRowsGated>(p, s);
-    if (epi == kRowsPart) return launch_mb<SkBf16, true, kRowsPart>(p, s);
-  }
+  if (type == kRowsBf16)
+    return epi == kRowsGated ? launch_blocks<SkBf16, true, kRowsGated>(p, s) : hipErrorInvalidValue;
+  if (epi == kRowsGated) return launch_blocks<SkI8, true, kRowsGated>(p, s);
+  if (epi == kRowsStoreBf16) return launch_blocks<SkI8, false, kRowsStoreBf16>(p, s);
+  if (epi == kRowsStoreF32) return launch_blocks<SkI8, false, kRowsStoreF32>(p, s);
   return hipErrorInvalidValue;
 }
 
