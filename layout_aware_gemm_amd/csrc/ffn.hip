@@ -32,19 +32,44 @@ struct RowsPlan {
   int tile;
 };
 
+void set_tile(RowsParams* p, bool gate, int tile) {
+  p->tilesM = ceil_div(p->M, rows_tile_m(tile));
+  p->tilesN = gate ? ceil_div(p->F, rows_tile_n(tile) / 2) : ceil_div(p->N, rows_tile_n(tile));
+  p->groupM = p->tilesM < 4 ? p->tilesM : (p->tilesM <= 8 ? p->tilesM : 4);
+}
+
 RowsPlan plan_rows(RowsParams* p, bool gate) {
-  RowsPlan r = {p->M <= kSkinnyRows, kRows256};
+  // Few rows of A: the kernel that streams B.  From 17 rows on a gated
+  // weight wide enough to fill the chip with 128x128 tiles is as fast or
+  // faster there (13824 x 5120, us tiles / streaming, int8 then bf16: 16 rows
+  // 30.6 / 29.4, 50.8 / 53.5; 24 rows 31.3 / 33.2, 52.0 / 56.6; 64 rows 37.0
+  // / 38.9, 58.9 / 67.1), a plain one is not (32000 x 4096: 64 rows 35.9 /
+  // 34.6), nor a small one (4096 x 1024 bf16: 64 rows 12.6 / 8.3).
+  RowsPlan r = {p->M <= 16 || (p->M <= kSkinnyRows && !(gate && p->F >= 192 * 64)), kRows256};
   p->split = 1;
   if (!r.skinny) {
-    const int64_t t256 = (int64_t)ceil_div(p->M, 256) * ceil_div(p->N, 256);
-    r.tile = t256 >= 128 ? kRows256 : kRows128;
-    const int b = rows_tile(r.tile);
-    p->tilesM = ceil_div(p->M, b);
-    p->tilesN = gate ? ceil_div(p->F, b / 2) : ceil_div(p->N, b);
-    p->groupM = p->tilesM < 4 ? p->tilesM : (p->tilesM <= 8 ? p->tilesM : 4);
+    // The tile whose rounds of 256 workgroups (one per compute unit) cost
+    // least.  Relative cost of a round, from int8 and bf16 products of 128 to
+    // 768 rows (gated 13824 x 5120, us for 128x128 / 128x256 / 256x256 tiles:
+    // 256 rows 66.9 / 51.4 / 65.0 int8, 114 / 89 / 121 bf16; 512 rows 123 /
+    // 92 / 70 and 211 / 158 / 125).
+    const double cost[3] = {1.95, 1.33, 1.0};
+    double best = 0.0;
+    for (int t = kRows256; t <= kRows128; ++t) {
+      set_tile(p, gate, t);
+      const double c = (double)(((int64_t)p->tilesM * p->tilesN + 255) / 256) * cost[t];
+      if (t == kRows256 || c < best) {
+        best = c;
+        r.tile = t;
+      }
+    }
+    set_tile(p, gate, r.tile);
+    // Few 128x128 tiles: split K to give every compute unit a workgroup, in
+    // chunks of at least 2048 bytes (128 x 5120 x 13824 int8: 45.0 us whole,
+    // 22.2 in 6 chunks with the second pass; 384 rows: 49.8 whole, 42.1 in 2).
     if (r.tile == kRows128) {
       const int64_t t = (int64_t)p->tilesM * p->tilesN;
-      const int64_t fill = 512 / t, by_k = p->K / 2048;
+      const int64_t fill = 256 / t, by_k = p->K / 2048;
       const int64_t n = fill < by_k ? fill : by_k;
       p->split = n < 1 ? 1 : (int)n;
     }
@@ -70,7 +95,7 @@ hipError_t launch_rows(int type, const RowsParams& p, const RowsPlan& r, int epi
 void say_rows(const char* what, const RowsParams& p, const RowsPlan& r) {
   if (verbose())
     fprintf(stderr, "tgemm: %s M=%d N=%d K=%d bytes %s tile=%d split=%d\n", what, p.M, p.N, p.K,
-            r.skinny ? "skinny" : "tiles", r.skinny ? 16 : rows_tile(r.tile), p.split);
+            r.skinny ? "skinny" : "tiles", r.skinny ? 0 : rows_tile_m(r.tile) * 1000 + rows_tile_n(r.tile), p.split);
 }
 
 // p holds everything but the operands' final addresses.  Operands that the

@@ -10,42 +10,86 @@ namespace {
 
 constexpr int kThr = 256;
 
-// out = epilogue(sum over chunks, in ascending order), one thread per
-// output.  Partials [split][M][N] (gated: N = 2F, outputs [M][F]).
+template <class T>
+struct __attribute__((packed, aligned(4))) x4_any {
+  T v[4];
+};
+struct __attribute__((packed, aligned(2))) u16x4_any {
+  uint32_t w[2];
+};
+
+// n (1 to 4) values as bf16 / fp32 at any element alignment.
+__device__ __forceinline__ void put4(uint16_t* o, const float* v, int n) {
+  if (n == 4) {
+    u16x4_any w;
+    w.w[0] = pack_bf16x2(v[0], v[1]);
+    w.w[1] = pack_bf16x2(v[2], v[3]);
+    *reinterpret_cast<u16x4_any*>(o) = w;
+  } else {
+    for (int i = 0; i < n; ++i) o[i] = to_bf16(v[i]);
+  }
+}
+__device__ __forceinline__ void put4(float* o, const float* v, int n) {
+  if (n == 4) {
+    *reinterpret_cast<x4_any<float>*>(o) = x4_any<float>{{v[0], v[1], v[2], v[3]}};
+  } else {
+    for (int i = 0; i < n; ++i) o[i] = v[i];
+  }
+}
+template <class T>
+__device__ __forceinline__ void add4(T* a, const T* p, int n) {
+  if (n == 4) {
+    const x4_any<T> t = *reinterpret_cast<const x4_any<T>*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] += t.v[i];
+  } else {
+    for (int i = 0; i < n; ++i) a[i] += p[i];
+  }
+}
+
+// out = epilogue(sum over chunks, in ascending order), four consecutive
+// outputs per thread.  Partials [split][M][N] (gated: N = 2F, outputs
+// [M][F]).
 template <class T, int EPI>
 __global__ void __launch_bounds__(kThr) finish_kernel(RowsParams p) {
   constexpr bool I8 = std::is_same<T, int>::value;
   constexpr bool GATE = EPI == kRowsGated;
   const int nout = GATE ? p.F : p.N;
-  const int64_t per_row = (nout + kThr - 1) / kThr;
+  const int per_row = (nout + 4 * kThr - 1) / (4 * kThr);
   const int row = (int)(blockIdx.x / per_row);
-  const int c = (int)(blockIdx.x % per_row) * kThr + (int)threadIdx.x;
+  const int c = ((int)(blockIdx.x % per_row) * kThr + (int)threadIdx.x) * 4;
   if (c >= nout) return;
+  const int n = min(4, nout - c);
   const T* part = static_cast<const T*>(p.part) + (int64_t)row * p.N + c;
   const int64_t slice = (int64_t)p.M * p.N;
-  T a = part[0], a2 = GATE ? part[p.F] : T(0);
-  for (int q = 1; q < p.split; ++q) {
-    a += part[q * slice];
-    if constexpr (GATE) a2 += part[q * slice + p.F];
+  T a[4] = {0, 0, 0, 0}, a2[4] = {0, 0, 0, 0};
+  for (int q = 0; q < p.split; ++q) {
+    add4(a, part + q * slice, n);
+    if constexpr (GATE) add4(a2, part + q * slice + p.F, n);
   }
-  float v = (float)a, u = (float)a2;
-  if constexpr (I8) {
-    const float sa = p.scale_a[row];
-    v = v * sa * p.scale_b[c];
-    if constexpr (GATE) u = u * sa * p.scale_b[p.F + c];
+  float v[4], u[4], h[4];
+  const float sa = I8 ? p.scale_a[row] : 1.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = (float)a[i];
+    u[i] = (float)a2[i];
+    if constexpr (I8) {
+      const int ci = min(c + i, nout - 1);
+      v[i] = v[i] * sa * p.scale_b[ci];
+      if constexpr (GATE) u[i] = u[i] * sa * p.scale_b[p.F + ci];
+    }
+    h[i] = GATE ? act_value(v[i], p.act) * u[i] : v[i];
   }
   const int64_t o = (int64_t)row * p.ldc + c;
-  if constexpr (EPI == kRowsStoreF32) {
-    static_cast<float*>(p.C)[o] = v;
-  } else if constexpr (EPI == kRowsStoreBf16) {
-    static_cast<uint16_t*>(p.C)[o] = to_bf16(v);
-  } else {
-    static_cast<uint16_t*>(p.C)[o] = to_bf16(act_value(v, p.act) * u);
-    if constexpr (!I8) {
-      if (p.gu != nullptr) {
-        p.gu[(int64_t)row * p.ldgu + c] = to_bf16(v);
-        p.gu[(int64_t)row * p.ldgu + p.F + c] = to_bf16(u);
-      }
+  if constexpr (EPI == kRowsStoreF32)
+    put4(static_cast<float*>(p.C) + o, h, n);
+  else
+    put4(static_cast<uint16_t*>(p.C) + o, h, n);
+  if constexpr (GATE && !I8) {
+    if (p.gu != nullptr) {
+      uint16_t* const w = p.gu + (int64_t)row * p.ldgu + c;
+      put4(w, v, n);
+      put4(w + p.F, u, n);
     }
   }
 }
@@ -128,7 +172,7 @@ __global__ void __launch_bounds__(kThr) gated_grad_kernel(
 
 template <class T, int EPI>
 hipError_t finish_one(const RowsParams& p, hipStream_t s) {
-  const int64_t blocks = (int64_t)p.M * ceil_div(EPI == kRowsGated ? p.F : p.N, kThr);
+  const int64_t blocks = (int64_t)p.M * ceil_div(EPI == kRowsGated ? p.F : p.N, 4 * kThr);
   if (blocks > kMaxWorkgroups) return hipErrorInvalidValue;
   hipLaunchKernelGGL((finish_kernel<T, EPI>), dim3((unsigned)blocks), dim3(kThr), 0, s, p);
   return hipGetLastError();

@@ -51,6 +51,11 @@ struct OpBf16 {
   }
 };
 
+// Stages of the ring of 128-row tiles (an A and a B panel each).
+template <int BN>
+constexpr int ring_rows() {
+  return BN == 128 ? 5 : 3;  // 160 KB, 144 KB
+}
 constexpr int kRowBytes = 128;  // bytes of K per k-step (one LDS row)
 
 // This wave's share of one panel's copies: R tile rows, 1 KB (8 rows) per
@@ -168,6 +173,38 @@ __device__ __forceinline__ void rows_substep(typename Op::acc (&acc)[FM][FN],
   }
 }
 
+// One substep of the ring loop: as above, with quarter X of the copies of
+// one whole stage (A's NA blocks, then B's) spread over the slots.
+template <class Op, int FM, int FN, int X, class PA, class PB>
+__device__ __forceinline__ void ring_rows_substep(typename Op::acc (&acc)[FM][FN],
+                                                  const typename Op::frag* fa,
+                                                  const typename Op::frag* fb,
+                                                  typename Op::frag* na, typename Op::frag* nb,
+                                                  const uint16_t* pa, const uint16_t* pb,
+                                                  const PA& da, const PB& db, uint16_t* da_dst,
+                                                  uint16_t* db_dst, int wave_u, uint32_t kofs,
+                                                  bool tail) {
+  constexpr int SL = FM * FN, CN = (PA::PER_WAVE + PB::PER_WAVE) / 4;
+#pragma unroll
+  for (int q = 0; q < SL; ++q) {
+    acc[q / FN][q % FN] = Op::mma(fa[q / FN], fb[q % FN], acc[q / FN][q % FN]);
+    if (q < FM)
+      na[q] = *reinterpret_cast<const typename Op::frag*>(pa + q * 32 * kBK);
+    else if (q < FM + FN)
+      nb[q - FM] = *reinterpret_cast<const typename Op::frag*>(pb + (q - FM) * 32 * kBK);
+#pragma unroll
+    for (int c = 0; c < CN; ++c) {
+      if ((c * SL) / CN != q) continue;
+      const int b = X * CN + c;
+      if (b < PA::PER_WAVE)
+        da.issue_one(da_dst, wave_u, b, kofs, tail);
+      else
+        db.issue_one(db_dst, wave_u, b - PA::PER_WAVE, kofs, tail);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
 // Lane l, register r of accumulator block (i, j) is row 8*(r/4) + 4*(l/32)
 // + r%4 and column l%32 of the block.  scl: the tile's scales in LDS (loaded
 // at the kernel's start, one per thread: fetched from memory between the
@@ -249,13 +286,16 @@ __device__ __forceinline__ void rows_epilogue(const RowsParams& p,
 }
 
 template <class Op, int BM, int BN, bool GATE, int EPI>
-__global__ void __launch_bounds__(kThreads, BM == 256 ? 1 : 2) rows_kernel(RowsParams p) {
+__global__ void __launch_bounds__(kThreads, 1) rows_kernel(RowsParams p) {
   constexpr bool SCALED = std::is_same<Op, OpI8>::value && EPI != kRowsPart;
   constexpr int FM = BM / 64, FN = BN / 64;
   constexpr int NT = GATE ? BN / 2 : BN;       // output columns per tile
   constexpr int SA = BM * kBK, SB = BN * kBK;  // panel sizes in 16-bit units
   static_assert(FM + FN <= FM * FN && FN % 2 == 0, "slots for the fragment reads, gate pairs");
-  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * SA + 3 * SB];
+  static_assert((BM == 256 && BN == 256) || BM == 128, "one of the two schedules");
+  // two A and three B panels, or the ring
+  __shared__ __attribute__((aligned(16)))
+  uint16_t lds[BM == 128 ? ring_rows<BN>() * (SA + SB) : 2 * SA + 3 * SB];
 
   const int lane = threadIdx.x & 63;
   const int wave_u = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -293,8 +333,6 @@ __global__ void __launch_bounds__(kThreads, BM == 256 ? 1 : 2) rows_kernel(RowsP
       sb_t = p.scale_b[min(n0 + t, p.N - 1)];
   }
 
-  uint16_t* const abuf = lds;           // two A panels
-  uint16_t* const bbuf = lds + 2 * SA;  // three B panels
   const int a_base = (wm * (BM / 2) + lc) * kBK;
   const int b_base = (wn * (BN / 2) + lc) * kBK;
   int xo[4];
@@ -305,48 +343,103 @@ __global__ void __launch_bounds__(kThreads, BM == 256 ? 1 : 2) rows_kernel(RowsP
   // multiplied, which keeps the copy counts, and so the waits, uniform
   auto kof = [nk](int t) { return (uint32_t)((t < nk ? t : 0) * kRowBytes); };
   auto tail = [nk, partial](int t) { return partial && (t == nk - 1 || (t > nk - 1 && nk == 1)); };
-  da.issue(abuf, wave_u, kof(0), tail(0));
-  db.issue(bbuf, wave_u, kof(0), tail(0));
-  db.issue(bbuf + SB, wave_u, kof(1), tail(1));
-  da.issue(abuf + SA, wave_u, kof(1), tail(1));
   constexpr int NA = RowsPanel<BM, false>::PER_WAVE, NB = RowsPanel<BN, GATE>::PER_WAVE;
-  // k-step 0 landed (own copies; other waves': the barrier)
-  __builtin_amdgcn_s_waitcnt(waitcnt_imm(NA + NB, 0));
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_sched_barrier(0);
   typename Op::frag fa[2][FM], fb[2][FN];
+  // fragments of substep 0 of the first k-step
+  auto read_first = [&](const uint16_t* a, const uint16_t* b) __attribute__((always_inline)) {
 #pragma unroll
-  for (int i = 0; i < FM; ++i)
-    fa[0][i] = *reinterpret_cast<const typename Op::frag*>(abuf + a_base + xo[0] + i * 32 * kBK);
+    for (int i = 0; i < FM; ++i)
+      fa[0][i] = *reinterpret_cast<const typename Op::frag*>(a + a_base + xo[0] + i * 32 * kBK);
 #pragma unroll
-  for (int j = 0; j < FN; ++j)
-    fb[0][j] = *reinterpret_cast<const typename Op::frag*>(bbuf + b_base + xo[0] + j * 32 * kBK);
-  int b3 = 0;  // kt % 3
-  for (int kt = 0; kt < nk; ++kt) {
-    const int b3n = b3 == 2 ? 0 : b3 + 1;  // (kt + 1) % 3
-    const int b3p = b3 == 0 ? 2 : b3 - 1;  // (kt + 2) % 3, the buffer k-step kt-1 used
-    const uint16_t* ac = abuf + (kt & 1) * SA + a_base;
-    const uint16_t* bc = bbuf + b3 * SB + b_base;
-    const uint16_t* an = abuf + ((kt + 1) & 1) * SA + a_base;
-    const uint16_t* bn = bbuf + b3n * SB + b_base;
-    const uint32_t k2 = kof(kt + 2);
-    const bool t2 = tail(kt + 2);
-    __builtin_amdgcn_sched_barrier(0);
-    rows_substep<Op, FM, FN, true>(acc, fa[0], fb[0], fa[1], fb[1], ac + xo[1], bc + xo[1], db,
-                                   bbuf + b3p * SB, wave_u, k2, t2);
-    rows_substep<Op, FM, FN, false>(acc, fa[1], fb[1], fa[0], fb[0], ac + xo[2], bc + xo[2], db,
-                                    bbuf, wave_u, k2, t2);
-    rows_substep<Op, FM, FN, false>(acc, fa[0], fb[0], fa[1], fb[1], ac + xo[3], bc + xo[3], db,
-                                    bbuf, wave_u, k2, t2);
-    // A(kt+1) and B(kt+1) landed (own copies: all but the NB just issued;
-    // other waves': the barrier) and this wave's reads of k-step kt are
-    // done, so after the barrier A(kt)'s buffer is free for A(kt+2)
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(NB, 0));
+    for (int j = 0; j < FN; ++j)
+      fb[0][j] = *reinterpret_cast<const typename Op::frag*>(b + b_base + xo[0] + j * 32 * kBK);
+  };
+  if constexpr (BM == 128) {
+    // Ring of S stages: after the barrier of k-step kt its stage is free,
+    // and the copies of k-step kt + S go there, a quarter in each of the next
+    // four substeps.  A small tile's k-step is short (4 or 8 matrix
+    // instructions per substep), so it takes several in flight to cover the
+    // memory's latency.
+    constexpr int S = ring_rows<BN>(), CN = NA + NB;
+    auto stA = [&](int g) { return lds + g * (SA + SB); };
+#pragma unroll
+    for (int g = 0; g < S - 1; ++g) {
+      da.issue(stA(g), wave_u, kof(g), tail(g));
+      db.issue(stA(g) + SA, wave_u, kof(g), tail(g));
+    }
+#pragma unroll
+    for (int c = 0; c < CN / 4; ++c) da.issue_one(stA(S - 1), wave_u, c, kof(S - 1), tail(S - 1));
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm((S - 2) * CN + CN / 4, 0));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    rows_substep<Op, FM, FN, true>(acc, fa[1], fb[1], fa[0], fb[0], an + xo[0], bn + xo[0], da,
-                                   abuf + (kt & 1) * SA, wave_u, k2, t2);
-    b3 = b3n;
+    read_first(lds, lds + SA);
+    int cur = 0;  // kt % S
+    for (int kt = 0; kt < nk; ++kt) {
+      const int nxt = cur + 1 == S ? 0 : cur + 1, prv = cur == 0 ? S - 1 : cur - 1;
+      const uint16_t* ac = stA(cur) + a_base;
+      const uint16_t* bc = stA(cur) + SA + b_base;
+      const uint16_t* an = stA(nxt) + a_base;
+      const uint16_t* bn = stA(nxt) + SA + b_base;
+      uint16_t* dp = stA(prv);
+      const uint32_t kp = kof(kt - 1 + S), kn = kof(kt + S);
+      const bool tp = tail(kt - 1 + S), tn2 = tail(kt + S);
+      __builtin_amdgcn_sched_barrier(0);
+      ring_rows_substep<Op, FM, FN, 1>(acc, fa[0], fb[0], fa[1], fb[1], ac + xo[1], bc + xo[1], da,
+                                       db, dp, dp + SA, wave_u, kp, tp);
+      ring_rows_substep<Op, FM, FN, 2>(acc, fa[1], fb[1], fa[0], fb[0], ac + xo[2], bc + xo[2], da,
+                                       db, dp, dp + SA, wave_u, kp, tp);
+      ring_rows_substep<Op, FM, FN, 3>(acc, fa[0], fb[0], fa[1], fb[1], ac + xo[3], bc + xo[3], da,
+                                       db, dp, dp + SA, wave_u, kp, tp);
+      // k-step kt+1 landed (own copies: all but the S-2 stages after it;
+      // other waves': the barrier) and this wave's reads of k-step kt are
+      // done, so after the barrier its stage is free
+      __builtin_amdgcn_s_waitcnt(waitcnt_imm((S - 2) * CN, 0));
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      uint16_t* dc = stA(cur);
+      ring_rows_substep<Op, FM, FN, 0>(acc, fa[1], fb[1], fa[0], fb[0], an + xo[0], bn + xo[0], da,
+                                       db, dc, dc + SA, wave_u, kn, tn2);
+      cur = nxt;
+    }
+  } else {
+    uint16_t* const abuf = lds;           // two A panels
+    uint16_t* const bbuf = lds + 2 * SA;  // three B panels
+    da.issue(abuf, wave_u, kof(0), tail(0));
+    db.issue(bbuf, wave_u, kof(0), tail(0));
+    db.issue(bbuf + SB, wave_u, kof(1), tail(1));
+    da.issue(abuf + SA, wave_u, kof(1), tail(1));
+    // k-step 0 landed (own copies; other waves': the barrier)
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(NA + NB, 0));
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    read_first(abuf, bbuf);
+    int b3 = 0;  // kt % 3
+    for (int kt = 0; kt < nk; ++kt) {
+      const int b3n = b3 == 2 ? 0 : b3 + 1;  // (kt + 1) % 3
+      const int b3p = b3 == 0 ? 2 : b3 - 1;  // (kt + 2) % 3, the buffer k-step kt-1 used
+      const uint16_t* ac = abuf + (kt & 1) * SA + a_base;
+      const uint16_t* bc = bbuf + b3 * SB + b_base;
+      const uint16_t* an = abuf + ((kt + 1) & 1) * SA + a_base;
+      const uint16_t* bn = bbuf + b3n * SB + b_base;
+      const uint32_t k2 = kof(kt + 2);
+      const bool t2 = tail(kt + 2);
+      __builtin_amdgcn_sched_barrier(0);
+      rows_substep<Op, FM, FN, true>(acc, fa[0], fb[0], fa[1], fb[1], ac + xo[1], bc + xo[1], db,
+                                     bbuf + b3p * SB, wave_u, k2, t2);
+      rows_substep<Op, FM, FN, false>(acc, fa[1], fb[1], fa[0], fb[0], ac + xo[2], bc + xo[2], db,
+                                      bbuf, wave_u, k2, t2);
+      rows_substep<Op, FM, FN, false>(acc, fa[0], fb[0], fa[1], fb[1], ac + xo[3], bc + xo[3], db,
+                                      bbuf, wave_u, k2, t2);
+      // A(kt+1) and B(kt+1) landed (own copies: all but the NB just issued;
+      // other waves': the barrier) and this wave's reads of k-step kt are
+      // done, so after the barrier A(kt)'s buffer is free for A(kt+2)
+      __builtin_amdgcn_s_waitcnt(waitcnt_imm(NB, 0));
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      rows_substep<Op, FM, FN, true>(acc, fa[1], fb[1], fa[0], fb[0], an + xo[0], bn + xo[0], da,
+                                     abuf + (kt & 1) * SA, wave_u, k2, t2);
+      b3 = b3n;
+    }
   }
   // the trailing re-reads must land before the LDS is reused or released
   wait_dma();
@@ -365,24 +458,24 @@ __global__ void __launch_bounds__(kThreads, BM == 256 ? 1 : 2) rows_kernel(RowsP
     rows_epilogue<Op, BM, BN, GATE, EPI, false>(p, acc, scl, m0, n0, wm, wn, lane, ks);
 }
 
-template <class Op, int B, bool GATE, int EPI>
+template <class Op, int BM, int BN, bool GATE, int EPI>
 hipError_t launch_one(const RowsParams& p, hipStream_t s) {
   const dim3 grid(p.tilesM * p.tilesN * p.split), block(kThreads);
-  hipLaunchKernelGGL((rows_kernel<Op, B, B, GATE, EPI>), grid, block, 0, s, p);
+  hipLaunchKernelGGL((rows_kernel<Op, BM, BN, GATE, EPI>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 
-template <int B>
+template <int BM, int BN>
 hipError_t launch_tile(int type, int epi, bool gate, const RowsParams& p, hipStream_t s) {
   if (type == kRowsI8) {
-    if (gate && epi == kRowsGated) return launch_one<OpI8, B, true, kRowsGated>(p, s);
-    if (gate && epi == kRowsPart) return launch_one<OpI8, B, true, kRowsPart>(p, s);
-    if (!gate && epi == kRowsStoreBf16) return launch_one<OpI8, B, false, kRowsStoreBf16>(p, s);
-    if (!gate && epi == kRowsStoreF32) return launch_one<OpI8, B, false, kRowsStoreF32>(p, s);
-    if (!gate && epi == kRowsPart) return launch_one<OpI8, B, false, kRowsPart>(p, s);
+    if (gate && epi == kRowsGated) return launch_one<OpI8, BM, BN, true, kRowsGated>(p, s);
+    if (gate && epi == kRowsPart) return launch_one<OpI8, BM, BN, true, kRowsPart>(p, s);
+    if (!gate && epi == kRowsStoreBf16) return launch_one<OpI8, BM, BN, false, kRowsStoreBf16>(p, s);
+    if (!gate && epi == kRowsStoreF32) return launch_one<OpI8, BM, BN, false, kRowsStoreF32>(p, s);
+    if (!gate && epi == kRowsPart) return launch_one<OpI8, BM, BN, false, kRowsPart>(p, s);
   } else if (gate) {
-    if (epi == kRowsGated) return launch_one<OpBf16, B, true, kRowsGated>(p, s);
-    if (epi == kRowsPart) return launch_one<OpBf16, B, true, kRowsPart>(p, s);
+    if (epi == kRowsGated) return launch_one<OpBf16, BM, BN, true, kRowsGated>(p, s);
+    if (epi == kRowsPart) return launch_one<OpBf16, BM, BN, true, kRowsPart>(p, s);
   }
   return hipErrorInvalidValue;
 }
@@ -391,8 +484,9 @@ hipError_t launch_tile(int type, int epi, bool gate, const RowsParams& p, hipStr
 
 hipError_t launch_rows_gemm(int type, int tile, int epi, bool gate, const RowsParams& p,
                             hipStream_t s) {
-  if (tile == kRows256) return launch_tile<256>(type, epi, gate, p, s);
-  return launch_tile<128>(type, epi, gate, p, s);
+  if (tile == kRows256) return launch_tile<256, 256>(type, epi, gate, p, s);
+  if (tile == kRows128x256) return launch_tile<128, 256>(type, epi, gate, p, s);
+  return launch_tile<128, 128>(type, epi, gate, p, s);
 }
 
 }  // namespace tgemm
