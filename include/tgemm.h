@@ -330,8 +330,22 @@ TGEMM_API int tgemm_validate_rope_region(const void* q, int64_t ldq, int64_t P, 
  *
  * What a gated feed-forward block adds around its down projection, as it is
  * trained (bf16 operands, with the gradient) and as it is served (8-bit
- * integer operands).  Storage, layout flags, asynchrony, streams, threads,
- * workspace and errors as for tgemm_run.
+ * integer operands).  Storage, layout flags, asynchrony, streams, threads
+ * and errors as for tgemm_run.
+ *
+ * Workspace: a call that needs scratch memory takes it from the caller's
+ * `workspace` (device memory, 16-byte aligned, workspace_bytes >= 0 bytes;
+ * the call's ..._workspace_bytes function says how many it needs, 0 for
+ * most; the buffer must not be used by anything else until the call's
+ * kernels have run) and fails with TGEMM_ERR_WORKSPACE_LIMIT, before anything
+ * is enqueued, if that is too small.  workspace_bytes = -1 (workspace is
+ * then ignored) takes the library's buffer of the stream, as tgemm_run does,
+ * except while the stream is being captured into a graph: then a call that
+ * needs workspace fails with TGEMM_ERR_WORKSPACE_LIMIT, and the caller has to
+ * bring its own, so that a replayed graph never allocates.  The
+ * ..._workspace_bytes functions return a negative tgemm_status for invalid
+ * arguments; they look at the operands' addresses, strides and layouts, not
+ * at their contents, and enqueue nothing.
  */
 
 /* Activations of the gated products (fp32 arithmetic). */
@@ -401,7 +415,10 @@ TGEMM_API int tgemm_validate_quantize_i8(const void* x, int64_t ldx, int64_t M, 
 TGEMM_API int tgemm_run_i8(char transA, char transB, int64_t M, int64_t N, int64_t K,
                            const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb,
                            const float* scale_a, const float* scale_b, void* C, int64_t ldc,
-                           int epilogue, void* stream);
+                           int epilogue, void* workspace, int64_t workspace_bytes, void* stream);
+TGEMM_API int64_t tgemm_i8_workspace_bytes(char transA, char transB, int64_t M, int64_t N,
+                                           int64_t K, const int8_t* A, int64_t lda,
+                                           const int8_t* B, int64_t ldb);
 
 /* Host-only argument check of tgemm_run_i8 (no GPU access). */
 TGEMM_API int tgemm_validate_i8(char transA, char transB, int64_t M, int64_t N, int64_t K,
@@ -426,7 +443,10 @@ TGEMM_API int tgemm_validate_i8(char transA, char transB, int64_t M, int64_t N, 
 TGEMM_API int tgemm_run_gated(char transA, char transB, int64_t M, int64_t F, int64_t K,
                               const void* A, int64_t lda, const void* B, int64_t ldb,
                               int activation, void* H, int64_t ldh, void* GU, int64_t ldgu,
-                              void* stream);
+                              void* workspace, int64_t workspace_bytes, void* stream);
+TGEMM_API int64_t tgemm_gated_workspace_bytes(char transA, char transB, int64_t M, int64_t F,
+                                              int64_t K, const void* A, int64_t lda,
+                                              const void* B, int64_t ldb);
 
 /* Host-only argument check of tgemm_run_gated (no GPU access). */
 TGEMM_API int tgemm_validate_gated(char transA, char transB, int64_t M, int64_t F, int64_t K,
@@ -441,7 +461,11 @@ TGEMM_API int tgemm_validate_gated(char transA, char transB, int64_t M, int64_t 
 TGEMM_API int tgemm_run_gated_i8(char transA, char transB, int64_t M, int64_t F, int64_t K,
                                  const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb,
                                  const float* scale_a, const float* scale_b, int activation,
-                                 void* H, int64_t ldh, void* stream);
+                                 void* H, int64_t ldh, void* workspace, int64_t workspace_bytes,
+                                 void* stream);
+TGEMM_API int64_t tgemm_gated_i8_workspace_bytes(char transA, char transB, int64_t M, int64_t F,
+                                                 int64_t K, const int8_t* A, int64_t lda,
+                                                 const int8_t* B, int64_t ldb);
 
 /* Host-only argument check of tgemm_run_gated_i8 (no GPU access). */
 TGEMM_API int tgemm_validate_gated_i8(char transA, char transB, int64_t M, int64_t F, int64_t K,
@@ -453,9 +477,7 @@ TGEMM_API int tgemm_validate_gated_i8(char transA, char transB, int64_t M, int64
  * Gradient of H = act(g) * u with respect to g and u:
  *   dGU[:, :F] = bf16(dH * u * act'(g)),  dGU[:, F:] = bf16(dH * act(g))
  * dH bf16 [M, F], GU bf16 [M, 2F] as tgemm_run_gated left it, dGU bf16
- * [M, 2F].  The operands' gradients are products of dGU: dOp(A) = dGU .
- * op(B)^T and dOp(B) = op(A)^T . dGU (tgemm_run reads every transpose in
- * place).  No workspace.
+ * [M, 2F].  No workspace.
  */
 TGEMM_API int tgemm_gated_grad(int64_t M, int64_t F, const void* dH, int64_t lddh, const void* GU,
                                int64_t ldgu, int activation, void* dGU, int64_t lddgu,
@@ -465,6 +487,37 @@ TGEMM_API int tgemm_gated_grad(int64_t M, int64_t F, const void* dH, int64_t ldd
 TGEMM_API int tgemm_validate_gated_grad(int64_t M, int64_t F, const void* dH, int64_t lddh,
                                         const void* GU, int64_t ldgu, int activation,
                                         const void* dGU, int64_t lddgu);
+
+/*
+ * The whole gradient of tgemm_run_gated: dGU = [dg | du] as tgemm_gated_grad
+ * (kept in the workspace, bf16), then
+ *   dA = dGU . op(B)^T    bf16 [M, K] (op(A)'s shape, row stride ldda >= K)
+ *   dB = op(A)^T . dGU    in B's layout: [2F, K] for transB 'T' (row stride
+ *                         lddb >= K), [K, 2F] for 'N' (lddb >= 2F); bf16
+ *                         (epilogue TGEMM_EPI_STORE_BF16) or fp32
+ *                         (TGEMM_EPI_STORE_F32)
+ * with fp32 sums.  A, B as in the forward call, dH bf16 [M, F], GU as the
+ * forward call left it.  A 'N' and B 'T' with 16-byte aligned bases and lda,
+ * ldb multiples of 8 run both products in one launch; other operands take
+ * two.  Workspace: 4 * M * F bytes and, for few tiles, fp32 partial products.
+ */
+TGEMM_API int tgemm_run_gated_backward(char transA, char transB, int64_t M, int64_t F, int64_t K,
+                                       const void* A, int64_t lda, const void* B, int64_t ldb,
+                                       const void* dH, int64_t lddh, const void* GU, int64_t ldgu,
+                                       int activation, void* dA, int64_t ldda, void* dB,
+                                       int64_t lddb, int epilogue, void* workspace,
+                                       int64_t workspace_bytes, void* stream);
+TGEMM_API int64_t tgemm_gated_backward_workspace_bytes(char transA, char transB, int64_t M,
+                                                       int64_t F, int64_t K, const void* A,
+                                                       int64_t lda, const void* B, int64_t ldb);
+
+/* Host-only argument check of tgemm_run_gated_backward (no GPU access). */
+TGEMM_API int tgemm_validate_gated_backward(char transA, char transB, int64_t M, int64_t F,
+                                            int64_t K, const void* A, int64_t lda, const void* B,
+                                            int64_t ldb, const void* dH, int64_t lddh,
+                                            const void* GU, int64_t ldgu, int activation,
+                                            const void* dA, int64_t ldda, const void* dB,
+                                            int64_t lddb, int epilogue);
 
 /* Human-readable name of a status code (static string, never NULL). */
 TGEMM_API const char* tgemm_status_string(int status);

@@ -72,10 +72,21 @@ hipError_t launch_rows_finish(int type, int epi, const RowsParams& p, hipStream_
 hipError_t launch_pack_i8(const int8_t* X, int64_t ld, bool k_contiguous, int R, int K,
                           int8_t* out, int Kp, hipStream_t s);
 
-// dgu = [dh * u * act'(g) | dh * act(g)] (rows_finish.hip).
+// dgu = [dh * u * act'(g) | dh * act(g)]; columns 2F .. cols - 1 and rows M
+// .. rows - 1 of dgu are set to zero (rows_finish.hip).
 hipError_t launch_gated_grad(const uint16_t* dh, int64_t lddh, const uint16_t* gu, int64_t ldgu,
-                             int M, int64_t F, int act, uint16_t* dgu, int64_t lddgu,
-                             hipStream_t s);
+                             int M, int64_t F, int act, uint16_t* dgu, int64_t lddgu, int rows,
+                             int64_t cols, hipStream_t s);
+
+// dX = G . W (px: A = G [M][K], B = W) and dW = G^T . X (pw: A = G stored
+// [K][M], B = X), both bf16, in one launch (gated_bwd.hip).  M, N, A, B, C,
+// strides, K (a multiple of 64, G zero-padded to it) and kvb (the rows B
+// holds) are set by the caller; the plan sets tiles and K chunks.  Outputs
+// are bf16, or fp32 where asked; the fp32 partials of a product with more
+// than one chunk go to its ws instead.
+void gated_bwd_plan(GemmParams* px, GemmParams* pw);
+hipError_t launch_gated_bwd(const GemmParams& px, const GemmParams& pw, bool f32x, bool f32w,
+                            hipStream_t s);
 
 // Rows to 8-bit codes with one scale each (row_quant.hip).  weight null:
 // codes of x itself; else of the RMS norm of x (+ residual, whose bf16 sum
@@ -126,11 +137,17 @@ __device__ __forceinline__ void act_value_grad(float g, int act, float& a, float
   d = t > 0.f ? fmaf(a * (1.f - p), ds, p) : p;
 }
 
-// 16-byte and 8-byte vectors at any element alignment: the hardware takes
+// Vectors at any element alignment: the hardware takes
 // unaligned vector accesses to global memory, so rows of odd length cost no
 // variant of their own.
 struct __attribute__((packed, aligned(2))) u16x8_any {
   uint32_t w[4];
+};
+struct __attribute__((packed, aligned(2))) u16x4_any {
+  uint32_t w[2];
+};
+struct __attribute__((packed, aligned(4))) f32x4_any {
+  float v[4];
 };
 struct __attribute__((packed, aligned(1))) u8x8_any {
   uint32_t w[2];

@@ -94,15 +94,49 @@ hipError_t launch_rows(int type, const RowsParams& p, const RowsPlan& r, int epi
 
 void say_rows(const char* what, const RowsParams& p, const RowsPlan& r) {
   if (verbose())
-    fprintf(stderr, "tgemm: %s M=%d N=%d K=%d bytes %s tile=%d split=%d\n", what, p.M, p.N, p.K,
-            r.skinny ? "skinny" : "tiles", r.skinny ? 0 : rows_tile_m(r.tile) * 1000 + rows_tile_n(r.tile), p.split);
+    fprintf(stderr, "tgemm: %s M=%d N=%d K=%d bytes tile=%dx%d split=%d\n", what, p.M, p.N, p.K,
+            r.skinny ? 0 : rows_tile_m(r.tile), r.skinny ? 0 : rows_tile_n(r.tile), p.split);
+}
+
+// ----------------------------------------------------------------------
+// Workspace of one call.  bytes >= 0: the caller's buffer of that size (a
+// call that needs more fails before anything is enqueued); bytes < 0: the
+// library's own per-stream buffer, which a stream under capture does not
+// get: its graph would have to allocate and free memory as it replays.
+// query set: report the need and launch nothing.
+// ----------------------------------------------------------------------
+struct CallSpace {
+  void* ptr;
+  int64_t bytes;
+  int64_t* query;
+};
+
+constexpr int kQueried = 1;  // take_workspace: the need was reported
+
+int take_workspace(const CallSpace& c, hipStream_t s, size_t need, Workspace* w) {
+  if (c.query != nullptr) {
+    *c.query = (int64_t)need;
+    return kQueried;
+  }
+  if (need == 0) return TGEMM_OK;
+  if (c.bytes >= 0) {
+    if (c.ptr == nullptr || (size_t)c.bytes < need) return TGEMM_ERR_WORKSPACE_LIMIT;
+    if ((reinterpret_cast<uintptr_t>(c.ptr) & 15) != 0) return TGEMM_ERR_INVALID_ARG;
+    w->ptr = c.ptr;
+    return TGEMM_OK;
+  }
+  hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
+  if (s != nullptr && hipStreamIsCapturing(s, &cs) == hipSuccess &&
+      cs != hipStreamCaptureStatusNone)
+    return TGEMM_ERR_WORKSPACE_LIMIT;
+  return get_workspace(kWsCached, s, need, w);
 }
 
 // p holds everything but the operands' final addresses.  Operands that the
 // direct-copy kernels cannot read in place -- not K-contiguous, or with
 // rows off 16-byte boundaries -- are copied into the workspace first.
 int run_i8(char ta, char tb, const void* A, int64_t lda, const void* B, int64_t ldb, RowsParams p,
-           int epi, bool gate, hipStream_t s) {
+           int epi, bool gate, const CallSpace& space, hipStream_t s) {
   const int K = p.K;
   const int Kp = ceil_div(K, 16) * 16;
   // (the stride of a single row is never used)
@@ -116,13 +150,10 @@ int run_i8(char ta, char tb, const void* A, int64_t lda, const void* B, int64_t 
   const size_t bytesA = packA ? round256((size_t)p.M * Kp) : 0;
   const size_t bytesB = packB ? round256((size_t)p.N * Kp) : 0;
   const size_t bytesP = p.split > 1 ? (size_t)p.split * p.M * p.N * sizeof(int) : 0;
-  say_rows(gate ? "gated i8" : "i8", p, r);
   Workspace w;
-  const bool need = bytesA + bytesB + bytesP != 0;
-  if (need) {
-    const int st = get_workspace(kWsCached, s, bytesA + bytesB + bytesP, &w);
-    if (st != TGEMM_OK) return st;
-  }
+  const int st = take_workspace(space, s, bytesA + bytesB + bytesP, &w);
+  if (st != TGEMM_OK) return st;
+  say_rows(gate ? "gated i8" : "i8", p, r);
   char* ws = static_cast<char*>(w.ptr);
   p.A = static_cast<const char*>(A);
   p.B = static_cast<const char*>(B);
@@ -143,11 +174,36 @@ int run_i8(char ta, char tb, const void* A, int64_t lda, const void* B, int64_t 
   }
   if (bytesP) p.part = ws + bytesA + bytesB;
   if (e == hipSuccess) e = launch_rows(kRowsI8, p, r, epi, gate, s);
-  if (need) {
-    const hipError_t f = release_workspace(w, s);
-    if (e == hipSuccess) e = f;
-  }
-  return status_of(e);
+  const hipError_t f = release_workspace(w, s);
+  return status_of(e != hipSuccess ? e : f);
+}
+
+inline int64_t round_up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
+
+// A GEMM of the library's own (no K split), for what the kernels
+// here do not take.
+hipError_t run_plain(char ta, char tb, int M, int N, int K, const void* A, int64_t lda,
+                     const void* B, int64_t ldb, void* C, int64_t ldc, bool f32, hipStream_t s) {
+  GemmParams g = {};
+  const int64_t t256 = (int64_t)ceil_div(M, 256) * ceil_div(N, 256);
+  const int cfg = t256 >= 144 ? kTile256 : kTile128;
+  g.A = static_cast<const uint16_t*>(A);
+  g.B = static_cast<const uint16_t*>(B);
+  g.C = C;
+  g.lda = lda;
+  g.ldb = ldb;
+  g.ldc = ldc;
+  g.M = M;
+  g.N = N;
+  g.K = K;
+  g.tilesM = ceil_div(M, tile_rows(cfg));
+  g.tilesN = ceil_div(N, tile_cols(cfg));
+  g.splitk = 1;
+  g.kchunk = K;
+  if ((int64_t)g.tilesM * g.tilesN > kMaxWorkgroups) return hipErrorInvalidValue;
+  g.groupM = g.tilesM < 4 ? g.tilesM : (g.tilesM <= 8 ? g.tilesM : 4);
+  g.aligned = rows_aligned(A, 2 * lda, 0) && rows_aligned(B, 2 * ldb, 0);
+  return launch_gemm(ta, tb, cfg, f32 ? kEpiStoreF32 : kEpiStoreBf16, g, s);
 }
 
 // bf16 gated product.  K-contiguous operands with 16-byte rows run on the
@@ -155,7 +211,7 @@ int run_i8(char ta, char tb, const void* A, int64_t lda, const void* B, int64_t 
 // an fp32 [M][2F] workspace and a pass that gates it.
 int run_gated(char ta, char tb, int64_t M, int64_t F, int64_t K, const void* A, int64_t lda,
               const void* B, int64_t ldb, int act, void* H, int64_t ldh, void* GU, int64_t ldgu,
-              hipStream_t s) {
+              const CallSpace& space, hipStream_t s) {
   RowsParams p = {};
   p.M = (int)M;
   p.N = (int)(2 * F);
@@ -179,43 +235,98 @@ int run_gated(char ta, char tb, int64_t M, int64_t F, int64_t K, const void* A, 
     p.K = (int)(2 * K);
     const RowsPlan r = plan_rows(&p, true);
     if (!grid_fits(p, r, true)) return TGEMM_ERR_UNSUPPORTED;
+    const int st = take_workspace(
+        space, s, p.split > 1 ? (size_t)p.split * p.M * p.N * sizeof(float) : 0, &w);
+    if (st != TGEMM_OK) return st;
+    p.part = w.ptr;
     say_rows("gated bf16", p, r);
-    if (p.split > 1) {
-      const int st =
-          get_workspace(kWsCached, s, (size_t)p.split * p.M * p.N * sizeof(float), &w);
-      if (st != TGEMM_OK) return st;
-      p.part = w.ptr;
-    }
     e = launch_rows(kRowsBf16, p, r, kRowsGated, true, s);
   } else {
-    GemmParams g = {};
-    const int64_t t256 = (int64_t)ceil_div(M, 256) * ceil_div(p.N, 256);
-    const int cfg = t256 >= 144 ? kTile256 : kTile128;
-    g.A = static_cast<const uint16_t*>(A);
-    g.B = static_cast<const uint16_t*>(B);
-    g.lda = lda;
-    g.ldb = ldb;
-    g.ldc = p.N;
-    g.M = p.M;
-    g.N = p.N;
-    g.K = (int)K;
-    g.tilesM = ceil_div(M, tile_rows(cfg));
-    g.tilesN = ceil_div(p.N, tile_cols(cfg));
-    g.splitk = 1;
-    g.kchunk = (int)K;
-    if ((int64_t)g.tilesM * g.tilesN > kMaxWorkgroups) return TGEMM_ERR_UNSUPPORTED;
-    g.groupM = g.tilesM < 4 ? g.tilesM : (g.tilesM <= 8 ? g.tilesM : 4);
-    g.aligned = rows_aligned(A, 2 * lda, 0) && rows_aligned(B, 2 * ldb, 0);
-    if (verbose())
-      fprintf(stderr, "tgemm: gated bf16 %c%c M=%d F=%d K=%d through fp32 [M][2F]\n", ta, tb, p.M,
-              p.F, g.K);
-    const int st = get_workspace(kWsCached, s, (size_t)p.M * p.N * sizeof(float), &w);
+    const int st = take_workspace(space, s, (size_t)p.M * p.N * sizeof(float), &w);
     if (st != TGEMM_OK) return st;
-    g.C = w.ptr;
-    e = launch_gemm(ta, tb, cfg, kEpiStoreF32, g, s);
+    if (verbose())
+      fprintf(stderr, "tgemm: gated bf16 %c%c M=%d F=%d K=%lld through fp32 [M][2F]\n", ta, tb, p.M,
+              p.F, (long long)K);
+    e = run_plain(ta, tb, p.M, p.N, (int)K, A, lda, B, ldb, w.ptr, p.N, true, s);
     p.part = w.ptr;
     p.split = 1;
     if (e == hipSuccess) e = launch_rows_finish(kRowsBf16, kRowsGated, p, s);
+  }
+  const hipError_t f = release_workspace(w, s);
+  return status_of(e != hipSuccess ? e : f);
+}
+
+// Gradient of the gated product: dGU into the workspace, then dA = dGU .
+// op(B)^T and dB.  A 'N' and B 'T' with 16-byte rows take the joint launch;
+// other operands two launches of the library's GEMM.
+int run_gated_backward(char ta, char tb, int64_t M, int64_t F, int64_t K, const void* A,
+                       int64_t lda, const void* B, int64_t ldb, const void* dH, int64_t lddh,
+                       const void* GU, int64_t ldgu, int act, void* dA, int64_t ldda, void* dB,
+                       int64_t lddb, bool f32, const CallSpace& space, hipStream_t s) {
+  const int64_t N2 = 2 * F;
+  const int64_t ldx = M == 1 ? round_up(K, 8) : lda;  // (a single row's stride is never used)
+  const bool joint = is_n(ta) && !is_n(tb) && rows_aligned(A, 2 * ldx, 0) &&
+                     rows_aligned(B, 2 * ldb, 0) && ldx < (1 << 23) && ldb < (1 << 23) &&
+                     N2 + 64 < (1 << 23);
+  const int64_t ldg = joint ? round_up(N2, 64) : N2;
+  const int64_t rows = joint ? round_up(M, 64) : M;
+  // joint: tiles of 256 rows read on past the padding
+  const size_t bytesG = round256((size_t)((joint ? round_up(M, 256) * ldg + 256 : M * ldg) * 2));
+  GemmParams px = {}, pw = {};
+  size_t bytesX = 0, bytesW = 0;
+  if (joint) {
+    px.M = (int)M;
+    px.N = (int)K;
+    px.K = (int)ldg;
+    px.kvb = (int)N2;
+    px.B = static_cast<const uint16_t*>(B);
+    px.ldb = ldb;
+    px.lda = ldg;
+    px.C = dA;
+    px.ldc = ldda;
+    pw.M = (int)N2;
+    pw.N = (int)K;
+    pw.K = (int)rows;
+    pw.kvb = (int)M;
+    pw.B = static_cast<const uint16_t*>(A);
+    pw.ldb = ldx;
+    pw.lda = ldg;
+    pw.C = dB;
+    pw.ldc = lddb;
+    gated_bwd_plan(&px, &pw);
+    if (px.splitk > 1) bytesX = round256((size_t)px.splitk * px.M * px.N * sizeof(float));
+    if (pw.splitk > 1) bytesW = (size_t)pw.splitk * pw.M * pw.N * sizeof(float);
+  }
+  Workspace w;
+  const int st = take_workspace(space, s, bytesG + bytesX + bytesW, &w);
+  if (st != TGEMM_OK) return st;
+  if (verbose())
+    fprintf(stderr, "tgemm: gated backward %c%c M=%lld F=%lld K=%lld joint=%d split=%d,%d\n", ta,
+            tb, (long long)M, (long long)F, (long long)K, joint, px.splitk, pw.splitk);
+  char* const ws = static_cast<char*>(w.ptr);
+  uint16_t* const G = reinterpret_cast<uint16_t*>(ws);
+  hipError_t e = launch_gated_grad(static_cast<const uint16_t*>(dH), lddh,
+                                   static_cast<const uint16_t*>(GU), ldgu, (int)M, F, act, G, ldg,
+                                   (int)rows, ldg, s);
+  if (e == hipSuccess && joint) {
+    px.A = pw.A = G;
+    px.ws = reinterpret_cast<float*>(ws + bytesG);
+    pw.ws = reinterpret_cast<float*>(ws + bytesG + bytesX);
+    e = launch_gated_bwd(px, pw, false, f32, s);
+    if (e == hipSuccess && px.splitk > 1)
+      e = launch_splitk_sum(px.ws, px.splitk, px.M, px.N, dA, ldda, false, s);
+    if (e == hipSuccess && pw.splitk > 1)
+      e = launch_splitk_sum(pw.ws, pw.splitk, pw.M, pw.N, dB, lddb, f32, s);
+  } else if (e == hipSuccess) {
+    // dA = G . op(B)^T: B stored [2F][K] ('T') is read as it lies
+    e = run_plain('N', is_n(tb) ? 'T' : 'N', (int)M, (int)K, (int)N2, G, ldg, B, ldb, dA, ldda,
+                  false, s);
+    // dB in B's layout: [2F][K] = G^T . op(A), or [K][2F] = op(A)^T . G
+    if (e == hipSuccess && !is_n(tb))
+      e = run_plain('T', ta, (int)N2, (int)K, (int)M, G, ldg, A, lda, dB, lddb, f32, s);
+    else if (e == hipSuccess)
+      e = run_plain(is_n(ta) ? 'T' : 'N', 'N', (int)K, (int)N2, (int)M, A, lda, G, ldg, dB, lddb,
+                    f32, s);
   }
   const hipError_t f = release_workspace(w, s);
   return status_of(e != hipSuccess ? e : f);
@@ -234,62 +345,110 @@ int no_throw(Fn&& fn) {
 }  // namespace
 }  // namespace tgemm
 
-extern "C" int tgemm_run_i8(char transA, char transB, int64_t M, int64_t N, int64_t K,
-                            const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb,
-                            const float* scale_a, const float* scale_b, void* C, int64_t ldc,
-                            int epilogue, void* stream) {
-  const int st = tgemm_validate_i8(transA, transB, M, N, K, A, lda, B, ldb, scale_a, scale_b, C,
-                                   ldc, epilogue);
-  if (st != TGEMM_OK) return st;
+namespace {
+
+// The operators' calls after validation, and their workspace queries.
+int call_i8(char ta, char tb, int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda,
+            const int8_t* B, int64_t ldb, const float* sa, const float* sb, void* C, int64_t ldc,
+            int epi, int act, const CallSpace& space, void* stream) {
+  const bool gate = epi == kRowsGated;
   RowsParams p = {};
   p.M = (int)M;
   p.N = (int)N;
+  p.F = gate ? (int)(N / 2) : 0;
   p.K = (int)K;
-  p.scale_a = scale_a;
-  p.scale_b = scale_b;
+  p.act = act;
+  p.scale_a = sa;
+  p.scale_b = sb;
   p.C = C;
   p.ldc = ldc;
   return no_throw([&] {
-    return run_i8(transA, transB, A, lda, B, ldb, p,
-                  epilogue == TGEMM_EPI_STORE_BF16 ? kRowsStoreBf16 : kRowsStoreF32, false,
+    return run_i8(ta, tb, A, lda, B, ldb, p, epi, gate, space,
                   reinterpret_cast<hipStream_t>(stream));
   });
+}
+
+// need, or the error that kept it from being found
+int64_t queried(int st, int64_t need) { return st == kQueried ? need : st; }
+
+// (a non-NULL address for the arguments a query does not take)
+float g_any[1];
+
+}  // namespace
+
+extern "C" int tgemm_run_i8(char transA, char transB, int64_t M, int64_t N, int64_t K,
+                            const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb,
+                            const float* scale_a, const float* scale_b, void* C, int64_t ldc,
+                            int epilogue, void* workspace, int64_t workspace_bytes, void* stream) {
+  const int st = tgemm_validate_i8(transA, transB, M, N, K, A, lda, B, ldb, scale_a, scale_b, C,
+                                   ldc, epilogue);
+  if (st != TGEMM_OK) return st;
+  return call_i8(transA, transB, M, N, K, A, lda, B, ldb, scale_a, scale_b, C, ldc,
+                 epilogue == TGEMM_EPI_STORE_BF16 ? kRowsStoreBf16 : kRowsStoreF32, 0,
+                 {workspace, workspace_bytes, nullptr}, stream);
+}
+
+extern "C" int64_t tgemm_i8_workspace_bytes(char transA, char transB, int64_t M, int64_t N,
+                                            int64_t K, const int8_t* A, int64_t lda,
+                                            const int8_t* B, int64_t ldb) {
+  const int st = tgemm_validate_i8(transA, transB, M, N, K, A, lda, B, ldb, g_any, g_any, g_any, N,
+                                   TGEMM_EPI_STORE_BF16);
+  if (st != TGEMM_OK) return st;
+  int64_t need = 0;
+  return queried(call_i8(transA, transB, M, N, K, A, lda, B, ldb, nullptr, nullptr, nullptr, N,
+                         kRowsStoreBf16, 0, {nullptr, 0, &need}, nullptr),
+                 need);
 }
 
 extern "C" int tgemm_run_gated_i8(char transA, char transB, int64_t M, int64_t F, int64_t K,
                                   const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb,
                                   const float* scale_a, const float* scale_b, int activation,
-                                  void* H, int64_t ldh, void* stream) {
+                                  void* H, int64_t ldh, void* workspace, int64_t workspace_bytes,
+                                  void* stream) {
   const int st = tgemm_validate_gated_i8(transA, transB, M, F, K, A, lda, B, ldb, scale_a, scale_b,
                                          activation, H, ldh);
   if (st != TGEMM_OK) return st;
-  RowsParams p = {};
-  p.M = (int)M;
-  p.N = (int)(2 * F);
-  p.F = (int)F;
-  p.K = (int)K;
-  p.act = activation;
-  p.scale_a = scale_a;
-  p.scale_b = scale_b;
-  p.C = H;
-  p.ldc = ldh;
-  return no_throw([&] {
-    return run_i8(transA, transB, A, lda, B, ldb, p, kRowsGated, true,
-                  reinterpret_cast<hipStream_t>(stream));
-  });
+  return call_i8(transA, transB, M, 2 * F, K, A, lda, B, ldb, scale_a, scale_b, H, ldh, kRowsGated,
+                 activation, {workspace, workspace_bytes, nullptr}, stream);
+}
+
+extern "C" int64_t tgemm_gated_i8_workspace_bytes(char transA, char transB, int64_t M, int64_t F,
+                                                  int64_t K, const int8_t* A, int64_t lda,
+                                                  const int8_t* B, int64_t ldb) {
+  const int st = tgemm_validate_gated_i8(transA, transB, M, F, K, A, lda, B, ldb, g_any, g_any,
+                                         TGEMM_ACT_SILU, g_any, F);
+  if (st != TGEMM_OK) return st;
+  int64_t need = 0;
+  return queried(call_i8(transA, transB, M, 2 * F, K, A, lda, B, ldb, nullptr, nullptr, nullptr, F,
+                         kRowsGated, 0, {nullptr, 0, &need}, nullptr),
+                 need);
 }
 
 extern "C" int tgemm_run_gated(char transA, char transB, int64_t M, int64_t F, int64_t K,
                                const void* A, int64_t lda, const void* B, int64_t ldb,
                                int activation, void* H, int64_t ldh, void* GU, int64_t ldgu,
-                               void* stream) {
+                               void* workspace, int64_t workspace_bytes, void* stream) {
   const int st =
       tgemm_validate_gated(transA, transB, M, F, K, A, lda, B, ldb, activation, H, ldh, GU, ldgu);
   if (st != TGEMM_OK) return st;
   return no_throw([&] {
     return run_gated(transA, transB, M, F, K, A, lda, B, ldb, activation, H, ldh, GU, ldgu,
-                     reinterpret_cast<hipStream_t>(stream));
+                     {workspace, workspace_bytes, nullptr}, reinterpret_cast<hipStream_t>(stream));
   });
+}
+
+extern "C" int64_t tgemm_gated_workspace_bytes(char transA, char transB, int64_t M, int64_t F,
+                                               int64_t K, const void* A, int64_t lda,
+                                               const void* B, int64_t ldb) {
+  const int st = tgemm_validate_gated(transA, transB, M, F, K, A, lda, B, ldb, TGEMM_ACT_SILU,
+                                      g_any, F, nullptr, 0);
+  if (st != TGEMM_OK) return st;
+  int64_t need = 0;
+  return queried(no_throw([&] {
+                   return run_gated(transA, transB, M, F, K, A, lda, B, ldb, 0, nullptr, F, nullptr,
+                                    0, {nullptr, 0, &need}, nullptr);
+                 }),
+                 need);
 }
 
 extern "C" int tgemm_gated_grad(int64_t M, int64_t F, const void* dH, int64_t lddh, const void* GU,
@@ -301,8 +460,42 @@ extern "C" int tgemm_gated_grad(int64_t M, int64_t F, const void* dH, int64_t ld
     fprintf(stderr, "tgemm: gated grad M=%lld F=%lld\n", (long long)M, (long long)F);
   return status_of(launch_gated_grad(static_cast<const uint16_t*>(dH), lddh,
                                      static_cast<const uint16_t*>(GU), ldgu, (int)M, F, activation,
-                                     static_cast<uint16_t*>(dGU), lddgu,
+                                     static_cast<uint16_t*>(dGU), lddgu, (int)M, 2 * F,
                                      reinterpret_cast<hipStream_t>(stream)));
+}
+
+extern "C" int tgemm_run_gated_backward(char transA, char transB, int64_t M, int64_t F, int64_t K,
+                                        const void* A, int64_t lda, const void* B, int64_t ldb,
+                                        const void* dH, int64_t lddh, const void* GU, int64_t ldgu,
+                                        int activation, void* dA, int64_t ldda, void* dB,
+                                        int64_t lddb, int epilogue, void* workspace,
+                                        int64_t workspace_bytes, void* stream) {
+  const int st = tgemm_validate_gated_backward(transA, transB, M, F, K, A, lda, B, ldb, dH, lddh,
+                                               GU, ldgu, activation, dA, ldda, dB, lddb, epilogue);
+  if (st != TGEMM_OK) return st;
+  return no_throw([&] {
+    return run_gated_backward(transA, transB, M, F, K, A, lda, B, ldb, dH, lddh, GU, ldgu,
+                              activation, dA, ldda, dB, lddb, epilogue == TGEMM_EPI_STORE_F32,
+                              {workspace, workspace_bytes, nullptr},
+                              reinterpret_cast<hipStream_t>(stream));
+  });
+}
+
+extern "C" int64_t tgemm_gated_backward_workspace_bytes(char transA, char transB, int64_t M,
+                                                        int64_t F, int64_t K, const void* A,
+                                                        int64_t lda, const void* B, int64_t ldb) {
+  const int64_t ldd = transB == 'N' || transB == 'n' ? 2 * F : K;
+  const int st =
+      tgemm_validate_gated_backward(transA, transB, M, F, K, A, lda, B, ldb, g_any, F, g_any, 2 * F,
+                                    TGEMM_ACT_SILU, g_any, K, g_any, ldd, TGEMM_EPI_STORE_BF16);
+  if (st != TGEMM_OK) return st;
+  int64_t need = 0;
+  return queried(no_throw([&] {
+                   return run_gated_backward(transA, transB, M, F, K, A, lda, B, ldb, nullptr, F,
+                                             nullptr, 2 * F, 0, nullptr, K, nullptr, ldd, false,
+                                             {nullptr, 0, &need}, nullptr);
+                 }),
+                 need);
 }
 
 extern "C" int tgemm_rms_norm_i8(const void* x, int64_t ldx, const void* residual, int64_t ldr,

@@ -1,0 +1,179 @@
+// The gated product's two gradient products in one launch:
+//   dX = G . W       [M][K],  G = dGU [M][2F], W [2F][K]     (NN)
+//   dW = G^T . X     [2F][K], X [M][K]                       (TN)
+// with 256x256 tiles on the library's NN and TN loops.
+//
+// Why one launch: dX has few, long tiles (K dimension 2F) and dW many short
+// ones (K dimension M).  Alone, dX's last round leaves most compute units
+// idle for a whole tile (4096 x 13824 x 5120: 320 tiles on 256 units, 1.38
+// ms where 1.25 rounds of work would take 0.86); launched together with the
+// longer tiles first, the short ones fill the gap.
+//
+// Edges need no loop of their own.  G lives in the workspace, padded: rows
+// M .. round64(M) - 1 and columns 2F .. round64(2F) - 1 are zero, so the K
+// dimension of either product is whole k-steps of G, and G's tiles may read
+// on to whole tiles.  W and X are read through buffers that end with them:
+// past their last row, the padded part of the K dimension, they read 0; past
+// a row's end they read on into the next row, which only reaches output
+// columns that are not stored.
+#include "ffn.h"
+#include "gemm_kernel.h"
+
+namespace tgemm {
+namespace {
+
+constexpr int kT = 256;
+
+// Store a wave's 128x128 block of a tile (accumulator layout as in the
+// GEMM's epilogues) through LDS words of its own, 32 rows at a time: rows
+// leave as 256 or 512 contiguous bytes, and each accumulator is used in one
+// place only.  (Stored from registers under the tests for the edge and the
+// type, they were copied out of the matrix cores' registers all at once, and
+// some of them through scratch.)  Rows of 136 words: the two halves of a
+// wave, four rows apart, write to different halves of the banks.
+constexpr int kOutRow = 136;
+
+__device__ __forceinline__ void store_block(const GemmParams& p, void* C, int64_t ldc, bool f32,
+                                            const f32x16_t (&acc)[4][4], float* st, int row0,
+                                            int col0, int lane) {
+  const int h = lane >> 5, lc = lane & 31;
+  const int c = col0 + 4 * lc;  // this lane's four columns on the way out
+  const int n = p.N - c;        // of which so many exist
+  // (the base and the stride keep 4-element vectors aligned or not: the
+  // hardware takes either)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        st[(8 * (r >> 2) + 4 * h + (r & 3)) * kOutRow + j * 32 + lc] = acc[i][j][r];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      const int rl = 2 * q + h, row = row0 + i * 32 + rl;
+      const float4 v = *reinterpret_cast<const float4*>(st + rl * kOutRow + 4 * lc);
+      if (row >= p.M || n <= 0) continue;
+      const float e[4] = {v.x, v.y, v.z, v.w};
+      const int64_t off = (int64_t)row * ldc + c;
+      if (f32) {
+        float* const o = static_cast<float*>(C) + off;
+        if (n >= 4)
+          *reinterpret_cast<f32x4_any*>(o) = f32x4_any{{e[0], e[1], e[2], e[3]}};
+        else
+          for (int k = 0; k < n; ++k) o[k] = e[k];
+      } else {
+        uint16_t* const o = static_cast<uint16_t*>(C) + off;
+        if (n >= 4)
+          *reinterpret_cast<u16x4_any*>(o) =
+              u16x4_any{{pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3])}};
+        else
+          for (int k = 0; k < n; ++k) o[k] = to_bf16(e[k]);
+      }
+    }
+  }
+}
+
+// One tile of one product: dX (NN) or dW (TN).
+template <bool DW>
+__device__ __forceinline__ void grad_tile(const GemmParams& p, int bid, bool f32, uint16_t* lds) {
+  constexpr int FM = kT / 64, FN = kT / 64, SA = kT * kBK;
+  const int tid = threadIdx.x;
+  const int lane = tid & 63, wave = tid >> 6;
+  const int wm = wave >> 1, wn = wave & 1;
+  const int h = lane >> 5, lc = lane & 31;
+  int tile, ks, tm, tn;
+  xcd_remap(bid, p.tilesM * p.tilesN * p.splitk, p.splitk, tile, ks);
+  tile_coords(tile, p.tilesM, p.tilesN, p.groupM, tm, tn);
+  const int m0 = tm * kT, n0 = tn * kT;
+  const int kbeg = ks * p.kchunk;
+  const int nk = (min(p.K, kbeg + p.kchunk) - kbeg) / kBK;
+  f32x16_t acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  const int a_base = (wm * (kT / 2) + lc) * kBK;
+  const int b_base = SA + (wn * (kT / 2) + lc) * kBK;
+  int xo[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) xo[s] = ((2 * s + h) ^ swz(lc)) << 3;
+  if constexpr (DW)
+    reg2_mainloop<kT, kT, FM, FN, false, false, false, true>(p, m0, n0, kbeg, nk, lds, nullptr,
+                                                             nullptr, nullptr, tid, a_base, b_base,
+                                                             xo, acc);
+  else
+    mix_mainloop<kT, kT, FM, FN, true, false, true>(p, m0, n0, kbeg, nk, lds, lds + 3 * SA, tid,
+                                                    wave, lane, a_base, b_base - SA, xo, acc);
+  void* C = p.C;
+  int64_t ldc = p.ldc;
+  if (p.splitk > 1) {
+    C = p.ws + (int64_t)ks * p.M * p.N;
+    ldc = p.N;
+    f32 = true;
+  }
+  __syncthreads();  // the stages become the rows' buffer
+  store_block(p, C, ldc, f32, acc, reinterpret_cast<float*>(lds) + wave * 32 * kOutRow,
+              m0 + wm * (kT / 2), n0 + wn * (kT / 2), lane);
+}
+
+// Workgroups 0 .. nfirst - 1 (a multiple of 8, so that a product's tiles
+// keep their XCDs) take the product with the longer tiles, dW if wfirst.
+// f32x, f32w: the output types (K chunks are fp32).
+__global__ void __launch_bounds__(kThreads, 1) gated_bwd_kernel(GemmParams px, GemmParams pw,
+                                                                int nfirst, int wfirst, int f32x,
+                                                                int f32w) {
+  __shared__ __attribute__((aligned(16))) uint16_t lds[5 * kT * kBK];
+  const int b = blockIdx.x;
+  const bool w = (b < nfirst) == (wfirst != 0);
+  const int l = b < nfirst ? b : b - nfirst;
+  // (workgroups past a product's last tile are the padding to a multiple of 8)
+  if (w) {
+    if (l < pw.tilesM * pw.tilesN * pw.splitk) grad_tile<true>(pw, l, f32w != 0, lds);
+  } else {
+    if (l < px.tilesM * px.tilesN * px.splitk) grad_tile<false>(px, l, f32x != 0, lds);
+  }
+}
+
+void set_split(GemmParams* p, int split) {
+  const int steps = p->K / kBK;
+  const int per = ceil_div(steps, split);
+  p->kchunk = per * kBK;
+  p->splitk = ceil_div(steps, per);
+}
+
+}  // namespace
+
+void gated_bwd_plan(GemmParams* px, GemmParams* pw) {
+  for (GemmParams* p : {px, pw}) {
+    p->tilesM = ceil_div(p->M, kT);
+    p->tilesN = ceil_div(p->N, kT);
+    p->groupM = p->tilesM < 4 ? p->tilesM : (p->tilesM <= 8 ? p->tilesM : 4);
+  }
+  // Split the K dimension of a product whose tiles are longer than an even
+  // share of all the work, in chunks of at least kMinSteps k-steps.
+  constexpr int kMinSteps = 4;
+  const double total = (double)px->tilesM * px->tilesN * (px->K / kBK) +
+                       (double)pw->tilesM * pw->tilesN * (pw->K / kBK);
+  const double share = total / 256 > kMinSteps ? total / 256 : kMinSteps;
+  for (GemmParams* p : {px, pw}) {
+    const double n = (p->K / kBK) / share;
+    set_split(p, n < 1.5 ? 1 : n > 64 ? 64 : (int)(n + 0.5));
+  }
+}
+
+hipError_t launch_gated_bwd(const GemmParams& px, const GemmParams& pw, bool f32x, bool f32w,
+                            hipStream_t s) {
+  const int64_t nx = (int64_t)px.tilesM * px.tilesN * px.splitk;
+  const int64_t nw = (int64_t)pw.tilesM * pw.tilesN * pw.splitk;
+  if (nx + nw + 8 > kMaxWorkgroups) return hipErrorInvalidValue;
+  const int wfirst = pw.kchunk > px.kchunk;
+  const int nfirst = (int)(((wfirst ? nw : nx) + 7) / 8 * 8);
+  const dim3 grid((unsigned)(nfirst + (wfirst ? nx : nw))), block(kThreads);
+  hipLaunchKernelGGL(gated_bwd_kernel, grid, block, 0, s, px, pw, nfirst, wfirst, f32x ? 1 : 0,
+                     f32w ? 1 : 0);
+  return hipGetLastError();
+}
+
+}  // namespace tgemm

@@ -309,10 +309,15 @@ struct LoaderKMajor {
 // Thread t owns k-group kb (L consecutive k) of mn-chunk mc (8 consecutive
 // rows of the panel); it loads L 16-byte vectors (one per k) and
 // transposes them into LDS rows.
-template <int R, int NTH = kThreads>
+// CLAMP: interior loads stop at the operand's end -- k rows at or past
+// kvalid and everything after the last stored element read as 0 -- so a
+// panel may reach past both edges (columns past an inner row's end read the
+// next row's).  Its row stride is below 2^23 elements (32-bit offsets).
+template <int R, int NTH = kThreads, bool CLAMP = false>
 struct LoaderMNMajor {
   static constexpr int L = R * 8 / NTH;  // k values per thread per k-step
   static constexpr int KBN = kBK / L; // k-groups per k-step
+  int kvalid, rvalid;  // CLAMP: the operand's k rows, the extent of its contiguous index
   uint4 v[L];
 
   // Thread -> (k-group, mn-chunk).  A load instruction covers whole
@@ -388,15 +393,24 @@ struct LoaderMNMajor {
   __device__ __forceinline__ void prep_interior(const uint16_t* X, int64_t ld, int r0, int k0,
                                                 bool zero = false) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    rs = panel_rsrc(X + (int64_t)k0 * ld + r0,
-                    zero ? 0u : (uint32_t)(((int64_t)(kBK - 1) * ld + R) * 2));
+    if constexpr (CLAMP) {
+      // (whole dwords: a range ending inside one would drop it)
+      const int k = min(kBK, kvalid - k0), r = min(R, rvalid - r0);
+      const uint32_t bytes = (uint32_t)(((int64_t)(k - 1) * ld + ((r + 1) & ~1)) * 2);
+      rs = panel_rsrc(X + (int64_t)k0 * ld + r0, zero || k <= 0 ? 0u : bytes);
+    } else {
+      rs = panel_rsrc(X + (int64_t)k0 * ld + r0,
+                      zero ? 0u : (uint32_t)(((int64_t)(kBK - 1) * ld + R) * 2));
+    }
 #else
     (void)X, (void)ld, (void)r0, (void)k0, (void)zero;
 #endif
   }
   __device__ __forceinline__ void load_unit(int j) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    v[j] = buf_load16(rs, voff, j * sstep);
+    // (the range check leaves the scalar offset out, so a clamped load puts
+    // its row there too)
+    v[j] = CLAMP ? buf_load16(rs, voff + j * sstep, 0) : buf_load16(rs, voff, j * sstep);
 #else
     (void)j;
 #endif
@@ -1437,7 +1451,8 @@ __device__ __forceinline__ void mix_substep(f32x16_t (&acc)[FM][FN], const bf16x
 }
 
 // k-steps [k0/64, k0/64 + nk); AK: A is the K-contiguous operand (else B).
-template <int BM, int BN, int FM, int FN, bool AK, bool SW>
+// CLAMP: G ends at k row p.kvb and row p.N (AK only; see LoaderMNMajor).
+template <int BM, int BN, int FM, int FN, bool AK, bool SW, bool CLAMP = false>
 __device__ __forceinline__ void mix_mainloop(const GemmParams& p, int m0, int n0, int k0, int nk,
                                              uint16_t* __restrict__ dbuf,
                                              uint16_t* __restrict__ gbuf, int tid, int wave,
@@ -1449,7 +1464,8 @@ __device__ __forceinline__ void mix_mainloop(const GemmParams& p, int m0, int n0
   static_assert(BM == BN, "one panel size for both operands");
   constexpr int SP = BM * kBK;
   constexpr int ND = DmaPanel<BM>::PER_WAVE;
-  using LG = LoaderMNMajor<BM>;
+  static_assert(AK || !CLAMP, "only B's end is clamped");
+  using LG = LoaderMNMajor<BM, kThreads, CLAMP>;
   const int wave_u = __builtin_amdgcn_readfirstlane(wave);
   DmaPanel<BM> dp;
   dp.init(AK ? p.lda : p.ldb, wave, lane);
@@ -1460,6 +1476,10 @@ __device__ __forceinline__ void mix_mainloop(const GemmParams& p, int m0, int n0
   LG g0, g1;
   g0.init_interior(ldg, tid);
   g1.init_interior(ldg, tid);
+  if constexpr (CLAMP) {
+    g0.kvalid = g1.kvalid = p.kvb;
+    g0.rvalid = g1.rvalid = p.N;
+  }
   // The loop runs an even number of k-steps, nke: with nk odd, k-step nk
   // is one of zeros (both operands' loads get an empty buffer range), which
   // adds exactly nothing to the sums.  A loop entered only from this
@@ -1566,7 +1586,9 @@ __device__ __forceinline__ void mix_mainloop(const GemmParams& p, int m0, int n0
 // the k-step that stores them, before their LDS stores.
 // ----------------------------------------------------------------------
 // k-steps [k0/64, k0/64 + nk).
-template <int BM, int BN, int FM, int FN, bool SW, bool AK = false, bool GA = false>
+// CLAMP: B ends at k row p.kvb and row p.N (see LoaderMNMajor).
+template <int BM, int BN, int FM, int FN, bool SW, bool AK = false, bool GA = false,
+          bool CLAMP = false>
 __device__ __forceinline__ void reg2_mainloop(const GemmParams& p, int m0, int n0, int k0, int nk,
                                               uint16_t* __restrict__ lds,
                                               uint32_t* __restrict__ gbuf0,
@@ -1575,7 +1597,7 @@ __device__ __forceinline__ void reg2_mainloop(const GemmParams& p, int m0, int n
                                               int b_base, const int* xo,
                                               f32x16_t (&acc)[FM][FN]) {
   using LA = typename LoaderSel<AK, BM>::type;
-  using LB = LoaderMNMajor<BN>;
+  using LB = LoaderMNMajor<BN, kThreads, CLAMP>;
   static_assert(!AK || GA, "K-contiguous A takes this loop only as a gradient");
   static_assert(!GA || LA::L == 8, "the gradient transform covers 8 vectors per thread");
   // LDS: stage s holds A at s*SSTR and B BOFF after it.  GA: A of stages
@@ -1593,6 +1615,10 @@ __device__ __forceinline__ void reg2_mainloop(const GemmParams& p, int m0, int n
   a1.init_interior(p.lda, tid);
   b0.init_interior(p.ldb, tid);
   b1.init_interior(p.ldb, tid);
+  if constexpr (CLAMP) {
+    b0.kvalid = b1.kvalid = p.kvb;
+    b0.rvalid = b1.rvalid = p.N;
+  }
   const int wave_u = __builtin_amdgcn_readfirstlane(tid >> 6);
   GaStage<AK> ga;
   // GA: this thread's first staged word; what its label offsets are

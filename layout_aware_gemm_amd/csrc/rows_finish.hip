@@ -14,9 +14,6 @@ template <class T>
 struct __attribute__((packed, aligned(4))) x4_any {
   T v[4];
 };
-struct __attribute__((packed, aligned(2))) u16x4_any {
-  uint32_t w[2];
-};
 
 // n (1 to 4) values as bf16 / fp32 at any element alignment.
 __device__ __forceinline__ void put4(uint16_t* o, const float* v, int n) {
@@ -141,16 +138,26 @@ __device__ __forceinline__ void grad_pair(uint32_t dh, uint32_t g, uint32_t u, i
 }
 
 // 8 outputs per thread; the arithmetic is fp32, dg and du are rounded once
-// to bf16, the type the gradient products read.
+// to bf16, the type the gradient products read.  The padding (columns 2F ..
+// cols - 1, rows past M) is written by the threads whose chunk lies past F
+// and by the workgroups of rows past M.
 __global__ void __launch_bounds__(kThr) gated_grad_kernel(
     const uint16_t* __restrict__ dh, int64_t lddh, const uint16_t* __restrict__ gu, int64_t ldgu,
-    int64_t F, int act, uint16_t* __restrict__ dgu, int64_t lddgu, int64_t per_row) {
+    int M, int64_t F, int act, uint16_t* __restrict__ dgu, int64_t lddgu, int64_t cols,
+    int64_t per_row) {
   const int64_t row = blockIdx.x / per_row;
   const int64_t c = ((int64_t)(blockIdx.x % per_row) * kThr + threadIdx.x) * 8;
+  uint16_t* const out = dgu + row * lddgu;
+  if (row >= M) {
+    for (int64_t i = c; i < c + 8 && i < F; ++i) out[i] = out[F + i] = 0;
+    for (int64_t i = 2 * F + c; i < 2 * F + c + 8 && i < cols; ++i) out[i] = 0;
+    return;
+  }
+  for (int64_t i = 2 * F + c; i < 2 * F + c + 8 && i < cols; ++i) out[i] = 0;
   if (c >= F) return;
   const uint16_t* ph = dh + row * lddh + c;
   const uint16_t* pg = gu + row * ldgu + c;
-  uint16_t* po = dgu + row * lddgu + c;
+  uint16_t* po = out + c;
   if (c + 8 <= F) {
     const u16x8_any h = *reinterpret_cast<const u16x8_any*>(ph);
     const u16x8_any g = *reinterpret_cast<const u16x8_any*>(pg);
@@ -206,12 +213,14 @@ hipError_t launch_pack_i8(const int8_t* X, int64_t ld, bool k_contiguous, int R,
 }
 
 hipError_t launch_gated_grad(const uint16_t* dh, int64_t lddh, const uint16_t* gu, int64_t ldgu,
-                             int M, int64_t F, int act, uint16_t* dgu, int64_t lddgu,
-                             hipStream_t s) {
-  const int64_t per_row = (F + 8 * kThr - 1) / (8 * kThr);
-  if (M * per_row > kMaxWorkgroups) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(gated_grad_kernel, dim3((unsigned)(M * per_row)), dim3(kThr), 0, s, dh, lddh,
-                     gu, ldgu, F, act, dgu, lddgu, per_row);
+                             int M, int64_t F, int act, uint16_t* dgu, int64_t lddgu, int rows,
+                             int64_t cols, hipStream_t s) {
+  // (the padding of a row, cols - 2F < 64 elements, needs at most 8 threads)
+  const int64_t chunks = (F + 7) / 8 > 8 ? (F + 7) / 8 : 8;
+  const int64_t per_row = (chunks + kThr - 1) / kThr;
+  if (rows * per_row > kMaxWorkgroups) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(gated_grad_kernel, dim3((unsigned)(rows * per_row)), dim3(kThr), 0, s, dh,
+                     lddh, gu, ldgu, M, F, act, dgu, lddgu, cols, per_row);
   return hipGetLastError();
 }
 

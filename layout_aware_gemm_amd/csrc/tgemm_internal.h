@@ -85,6 +85,8 @@ struct GemmParams {
   const float* gscale;
   const int32_t* glabels;
   int gtok, gvoc;
+  // clamped loops (gated_bwd.hip): the k rows B holds; K may reach past them
+  int kvb;
 };
 
 // Width (in columns) of the per-row partial blocks the CE epilogue writes.

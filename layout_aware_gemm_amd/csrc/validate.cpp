@@ -151,6 +151,25 @@ extern "C" int tgemm_validate_gated_grad(int64_t M, int64_t F, const void* dH, i
   return st;
 }
 
+extern "C" int tgemm_validate_gated_backward(char transA, char transB, int64_t M, int64_t F,
+                                             int64_t K, const void* A, int64_t lda, const void* B,
+                                             int64_t ldb, const void* dH, int64_t lddh,
+                                             const void* GU, int64_t ldgu, int activation,
+                                             const void* dA, int64_t ldda, const void* dB,
+                                             int64_t lddb, int epilogue) {
+  if (epilogue != TGEMM_EPI_STORE_BF16 && epilogue != TGEMM_EPI_STORE_F32)
+    return TGEMM_ERR_INVALID_ARG;
+  if (GU == nullptr) return TGEMM_ERR_INVALID_ARG;
+  int st = tgemm_validate_gated(transA, transB, M, F, K, A, lda, B, ldb, activation, dH, lddh, GU,
+                                ldgu);
+  if (st == TGEMM_OK) st = check_rows(dA, M, K, ldda);
+  if (st == TGEMM_OK)
+    st = is_n(transB) ? check_rows(dB, K, 2 * F, lddb) : check_rows(dB, 2 * F, K, lddb);
+  // (the products' K dimensions, padded, are ints)
+  if (st == TGEMM_OK && (M > kMaxDim - 256 || 2 * F > kMaxDim - 256)) st = TGEMM_ERR_UNSUPPORTED;
+  return st;
+}
+
 extern "C" int tgemm_validate_rms_norm_i8(const void* x, int64_t ldx, const void* residual,
                                           int64_t ldr, const void* weight, float eps, int64_t M,
                                           int64_t K, const void* sum, int64_t lds, const int8_t* q,

@@ -39,7 +39,10 @@ EXPORTS = ("tgemm_run", "tgemm_run_fp8", "tgemm_validate", "tgemm_validate_fp8",
            "tgemm_validate_rms_norm_i8", "tgemm_quantize_i8", "tgemm_validate_quantize_i8",
            "tgemm_run_i8", "tgemm_validate_i8", "tgemm_run_gated", "tgemm_validate_gated",
            "tgemm_run_gated_i8", "tgemm_validate_gated_i8", "tgemm_gated_grad",
-           "tgemm_validate_gated_grad")
+           "tgemm_validate_gated_grad", "tgemm_run_gated_backward",
+           "tgemm_validate_gated_backward", "tgemm_i8_workspace_bytes",
+           "tgemm_gated_workspace_bytes", "tgemm_gated_i8_workspace_bytes",
+           "tgemm_gated_backward_workspace_bytes")
 
 ACT_SILU = 0
 ACT_GELU_TANH = 1
@@ -110,19 +113,26 @@ def lib():
                                                  vp]
         L.tgemm_validate_rope_region.restype = ctypes.c_int
         # the feed-forward operators: a validator takes its call's arguments
-        # without the stream
+        # without workspace and stream
         ch, ci, cf = ctypes.c_char, ctypes.c_int, ctypes.c_float
-        for name, args in (
-                ("rms_norm_i8", [vp, i64, vp, i64, vp, cf, i64, i64, vp, i64, vp, i64, vp]),
-                ("quantize_i8", [vp, i64, i64, i64, vp, i64, vp]),
-                ("run_i8", [ch, ch, i64, i64, i64, vp, i64, vp, i64, vp, vp, vp, i64, ci]),
-                ("run_gated", [ch, ch, i64, i64, i64, vp, i64, vp, i64, ci, vp, i64, vp, i64]),
-                ("run_gated_i8", [ch, ch, i64, i64, i64, vp, i64, vp, i64, vp, vp, ci, vp, i64]),
-                ("gated_grad", [i64, i64, vp, i64, vp, i64, ci, vp, i64])):
+        product = [ch, ch, i64, i64, i64, vp, i64, vp, i64]
+        for name, args, ws in (
+                ("rms_norm_i8", [vp, i64, vp, i64, vp, cf, i64, i64, vp, i64, vp, i64, vp], False),
+                ("quantize_i8", [vp, i64, i64, i64, vp, i64, vp], False),
+                ("run_i8", product + [vp, vp, vp, i64, ci], True),
+                ("run_gated", product + [ci, vp, i64, vp, i64], True),
+                ("run_gated_i8", product + [vp, vp, ci, vp, i64], True),
+                ("gated_grad", [i64, i64, vp, i64, vp, i64, ci, vp, i64], False),
+                ("run_gated_backward", product + [vp, i64, vp, i64, ci, vp, i64, vp, i64, ci],
+                 True)):
+            bare = name.replace("run_", "")
             call = getattr(L, "tgemm_" + name)
-            call.argtypes, call.restype = args + [vp], ci
-            check = getattr(L, "tgemm_validate_" + name.replace("run_", ""))
+            call.argtypes, call.restype = args + ([vp, i64, vp] if ws else [vp]), ci
+            check = getattr(L, "tgemm_validate_" + bare)
             check.argtypes, check.restype = args, ci
+            if ws:
+                need = getattr(L, f"tgemm_{bare}_workspace_bytes")
+                need.argtypes, need.restype = product, i64
         _lib = L
     return _lib
 
@@ -581,6 +591,21 @@ def _call(name, *args):
         raise TgemmError(st, name)
 
 
+def _call_ws(name, device, *args):
+    """As ``_call`` for a call with workspace (its first nine arguments are
+    the product's), which is a torch allocation: most calls need none, and
+    one that does says so before it enqueues anything."""
+    fn, stream = getattr(lib(), name), torch.cuda.current_stream().cuda_stream
+    st = fn(*args, None, 0, stream)
+    if st == TGEMM_ERR_WORKSPACE_LIMIT:
+        need = getattr(lib(), name.replace("run_", "") + "_workspace_bytes")(*args[:9])
+        if need > 0:
+            ws = torch.empty(need, dtype=torch.uint8, device=device)
+            st = fn(*args, ws.data_ptr(), need, stream)
+    if st != TGEMM_OK:
+        raise TgemmError(st, name)
+
+
 def _rows(x, what, dtype):
     """[..., K] -> ([rows, K] view, row stride): any row stride, unit last
     stride."""
@@ -688,9 +713,9 @@ def matmul_i8(a, b, scale_a, scale_b, out_dtype=torch.bfloat16, stream=None):
         raise TypeError("out_dtype must be bf16 or fp32")
     with _On(_same_device(a, b, sa, scale_b), stream):
         out = torch.empty(a.shape[:-1] + (N,), dtype=out_dtype, device=a.device)
-        _call("tgemm_run_i8", _flag(ta), _flag(tb), M, N, K, _ptr(a2), lda, _ptr(b), ldb, _ptr(sa),
-              _ptr(scale_b), _ptr(out), N,
-              EPI_STORE_BF16 if out_dtype == torch.bfloat16 else EPI_STORE_F32)
+        _call_ws("tgemm_run_i8", a.device, _flag(ta), _flag(tb), M, N, K, _ptr(a2), lda, _ptr(b),
+                 ldb, _ptr(sa), _ptr(scale_b), _ptr(out), N,
+                 EPI_STORE_BF16 if out_dtype == torch.bfloat16 else EPI_STORE_F32)
     return out
 
 
@@ -711,8 +736,8 @@ def gated_matmul_i8(a, b, scale_a, scale_b, act="silu", stream=None):
     _vector(scale_b, 2 * F, "scale_b", torch.float32)
     with _On(_same_device(a, b, sa, scale_b), stream):
         h = torch.empty(a.shape[:-1] + (F,), dtype=torch.bfloat16, device=a.device)
-        _call("tgemm_run_gated_i8", _flag(ta), _flag(tb), M, F, K, _ptr(a2), lda, _ptr(b), ldb,
-              _ptr(sa), _ptr(scale_b), _act(act), _ptr(h), F)
+        _call_ws("tgemm_run_gated_i8", a.device, _flag(ta), _flag(tb), M, F, K, _ptr(a2), lda,
+                 _ptr(b), ldb, _ptr(sa), _ptr(scale_b), _act(act), _ptr(h), F)
     return h
 
 
@@ -729,8 +754,8 @@ def gated_matmul(x, w, act="silu", save=False, stream=None):
         h = torch.empty(x.shape[:-1] + (F,), dtype=torch.bfloat16, device=x.device)
         gu = (torch.empty(x.shape[:-1] + (2 * F,), dtype=torch.bfloat16, device=x.device)
               if save else None)
-        _call("tgemm_run_gated", _flag(ta), _flag(tb), M, F, K, _ptr(x2), lda, _ptr(w), ldb,
-              _act(act), _ptr(h), F, _ptr(gu), 2 * F)
+        _call_ws("tgemm_run_gated", x.device, _flag(ta), _flag(tb), M, F, K, _ptr(x2), lda, _ptr(w),
+                 ldb, _act(act), _ptr(h), F, _ptr(gu), 2 * F)
     return (h, gu) if save else h
 
 
@@ -740,7 +765,7 @@ def gated_backward(dh, gu, x, w, act="silu", dw_dtype=torch.bfloat16, stream=Non
     and ``w`` its operands.  dw has w's layout (for ``W.t()``, dw.t() is the
     contiguous [2F, K] gradient of W) and ``dw_dtype`` (bf16 or fp32)."""
     F = _gate_width(w)
-    x2, _, _, tb, _ = _product(x, w, torch.bfloat16, "gated_backward")
+    x2, ta, lda, tb, ldb = _product(x, w, torch.bfloat16, "gated_backward")
     M, K = x2.shape
     if dh.shape != x.shape[:-1] + (F,) or gu.shape != x.shape[:-1] + (2 * F,):
         raise ValueError("dh must be [..., F] and gu [..., 2F] for x [..., K]")
@@ -749,14 +774,12 @@ def gated_backward(dh, gu, x, w, act="silu", dw_dtype=torch.bfloat16, stream=Non
     d2, ldd = _rows(dh, "dh", torch.bfloat16)
     g2, ldg = _rows(gu, "gu", torch.bfloat16)
     with _On(_same_device(dh, gu, x, w), stream):
-        dgu = torch.empty(M, 2 * F, dtype=torch.bfloat16, device=x.device)
-        _call("tgemm_gated_grad", M, F, _ptr(d2), ldd, _ptr(g2), ldg, _act(act), _ptr(dgu), 2 * F)
-        dx = matmul(dgu, w.t())
-        if tb == "T":
-            dw = matmul(dgu.t(), x2, out_dtype=dw_dtype).t()
-        else:
-            dw = matmul(x2.t(), dgu, out_dtype=dw_dtype)
-    return dx.view(x.shape), dw
+        dx = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        dw = torch.empty((2 * F, K) if tb == "T" else (K, 2 * F), dtype=dw_dtype, device=x.device)
+        _call_ws("tgemm_run_gated_backward", x.device, _flag(ta), _flag(tb), M, F, K, _ptr(x2),
+                 lda, _ptr(w), ldb, _ptr(d2), ldd, _ptr(g2), ldg, _act(act), _ptr(dx), K, _ptr(dw),
+                 dw.shape[1], EPI_STORE_BF16 if dw_dtype == torch.bfloat16 else EPI_STORE_F32)
+    return dx, dw.t() if tb == "T" else dw
 
 
 def outer_f32(a, b, stream=None):

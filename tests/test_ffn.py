@@ -130,6 +130,28 @@ def test_validate_gated_grad(kw, expect):
 
 
 @pytest.mark.parametrize("kw,expect", [
+    ({}, OK), (dict(epi=1), OK), (dict(tb="N"), OK), (dict(ta="T"), OK), (dict(epi=2), INV),
+    (dict(act=2), INV), (dict(M=0), INV), (dict(F=0), INV), (dict(K=0), INV), (dict(F=1 << 30), UNS),
+    (dict(A=None), INV), (dict(B=None), INV), (dict(dh=None), INV), (dict(gu=None), INV),
+    (dict(da=None), INV), (dict(db=None), INV), (dict(lda=10), INV), (dict(ldb=10), INV),
+    (dict(lddh=6), INV), (dict(ldgu=13), INV), (dict(ldda=10), INV), (dict(lddb=10), INV),
+    (dict(tb="N", lddb=13), INV), (dict(tb="N", lddb=14), OK), (dict(ldda=1 << 62), UNS),
+])
+def test_validate_gated_backward(kw, expect):
+    a = dict(ta="N", tb="T", M=3, F=7, K=11, A=P, lda=None, B=P, ldb=None, dh=P, lddh=None, gu=P,
+             ldgu=None, act=0, da=P, ldda=None, db=P, lddb=None, epi=0)
+    a.update(kw)
+    M, F, K = a["M"], a["F"], a["K"]
+    ldb = 2 * F if a["tb"] == "N" else K
+    st = tgemm.lib().tgemm_validate_gated_backward(
+        a["ta"].encode(), a["tb"].encode(), M, F, K, a["A"],
+        a["lda"] or (K if a["ta"] == "N" else M), a["B"], a["ldb"] or ldb, a["dh"], a["lddh"] or F,
+        a["gu"], a["ldgu"] or 2 * F, a["act"], a["da"], a["ldda"] or K, a["db"], a["lddb"] or ldb,
+        a["epi"])
+    assert st == expect
+
+
+@pytest.mark.parametrize("kw,expect", [
     ({}, OK), (dict(r=P, s=P), OK), (dict(eps=0.0), OK), (dict(r=P), INV), (dict(s=P), INV),
     (dict(eps=-1e-6), INV), (dict(eps=float("nan")), INV), (dict(eps=float("inf")), INV),
     (dict(x=None), INV), (dict(w=None), INV), (dict(q=None), INV), (dict(scale=None), INV),
@@ -147,6 +169,28 @@ def test_validate_rms_norm_i8(kw, expect):
     if not {"r", "s", "eps", "w"} & set(kw):
         assert tgemm.lib().tgemm_validate_quantize_i8(a["x"], a["ldx"], a["M"], a["K"], a["q"],
                                                       a["ldq"], a["scale"]) == expect
+
+
+def test_workspace_queries():
+    """Host-only: nothing for operands read in place, room for the copies of
+    others and for partial sums, a status for invalid arguments."""
+    L, N, T = tgemm.lib(), b"N", b"T"
+    assert L.tgemm_i8_workspace_bytes(N, T, 4, 4096, 4096, P, 4096, P, 4096) == 0
+    assert L.tgemm_i8_workspace_bytes(N, T, 4, 40, 33, P, 33, P, 33) >= (4 + 40) * 48
+    assert L.tgemm_i8_workspace_bytes(N, N, 4, 40, 64, P, 64, P, 40) >= 40 * 64
+    assert L.tgemm_i8_workspace_bytes(N, T, 4, 40, 64, P + 1, 64, P, 64) >= 4 * 64
+    assert L.tgemm_i8_workspace_bytes(N, T, 128, 128, 8192, P, 8192, P, 8192) == 4 * 4 * 128 * 128
+    assert L.tgemm_i8_workspace_bytes(N, T, 0, 40, 64, P, 64, P, 64) == INV
+    assert L.tgemm_i8_workspace_bytes(N, T, 4, 40, 1 << 20, P, 1 << 20, P, 1 << 20) == UNS
+    assert L.tgemm_gated_i8_workspace_bytes(N, T, 4, 64, 64, P, 64, P, 64) == 0
+    assert L.tgemm_gated_i8_workspace_bytes(N, T, 4, 64, 65, P, 65, P, 65) >= (4 + 128) * 80
+    assert L.tgemm_gated_workspace_bytes(N, T, 4, 64, 64, P, 64, P, 64) == 0
+    assert L.tgemm_gated_workspace_bytes(T, T, 4, 64, 64, P, 4, P, 64) == 4 * 128 * 4
+    assert L.tgemm_gated_workspace_bytes(N, T, 4, 64, 64, None, 64, P, 64) == INV
+    # dGU padded to whole tiles of rows, and 64 columns
+    assert L.tgemm_gated_backward_workspace_bytes(N, T, 4, 40, 64, P, 64, P, 64) >= 256 * 128 * 2
+    assert L.tgemm_gated_backward_workspace_bytes(N, N, 4, 40, 64, P, 64, P, 80) >= 4 * 80 * 2
+    assert L.tgemm_gated_backward_workspace_bytes(N, T, 4, 0, 64, P, 64, P, 64) == INV
 
 
 def test_binding_refuses():
