@@ -410,7 +410,8 @@ TGEMM_API int tgemm_validate_quantize_i8(const void* x, int64_t ldx, int64_t M, 
  *
  * A 'N' and B 'T' with 16-byte aligned bases and lda, ldb and K multiples of
  * 16 are read in place; other operands are first copied, K-contiguous, into
- * the workspace.  Up to 64 rows of op(A) run on a kernel that streams B once.
+ * the workspace.  Up to 64 rows of op(A) run on a kernel that streams B
+ * once.
  */
 TGEMM_API int tgemm_run_i8(char transA, char transB, int64_t M, int64_t N, int64_t K,
                            const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb,
@@ -436,9 +437,8 @@ TGEMM_API int tgemm_validate_i8(char transA, char transB, int64_t M, int64_t N, 
  * H is computed from the fp32 sums either way.
  *
  * A 'N' and B 'T' with 16-byte aligned bases and lda, ldb and K multiples of
- * 8 run on kernels of their own (up to 64 rows: one that streams B once);
- * others take the GEMM of tgemm_run into an fp32 [M, 2F] workspace and a
- * second pass.
+ * 8 are read in place; other operands are first copied, K-contiguous, into
+ * the workspace.  Few rows of op(A) run on a kernel that streams B once.
  */
 TGEMM_API int tgemm_run_gated(char transA, char transB, int64_t M, int64_t F, int64_t K,
                               const void* A, int64_t lda, const void* B, int64_t ldb,
@@ -497,9 +497,10 @@ TGEMM_API int tgemm_validate_gated_grad(int64_t M, int64_t F, const void* dH, in
  *                         (epilogue TGEMM_EPI_STORE_BF16) or fp32
  *                         (TGEMM_EPI_STORE_F32)
  * with fp32 sums.  A, B as in the forward call, dH bf16 [M, F], GU as the
- * forward call left it.  A 'N' and B 'T' with 16-byte aligned bases and lda,
- * ldb multiples of 8 run both products in one launch; other operands take
- * two.  Workspace: 4 * M * F bytes and, for few tiles, fp32 partial products.
+ * forward call left it.  Both products run in one launch.  Workspace: dGU
+ * (about 4 * M * F bytes), copies of operands other than A 'N' and B 'T' with
+ * 16-byte aligned bases and lda, ldb multiples of 8 (and of A for transB
+ * 'N'), and for few tiles fp32 partial products.  K and 2F up to about 2^23.
  */
 TGEMM_API int tgemm_run_gated_backward(char transA, char transB, int64_t M, int64_t F, int64_t K,
                                        const void* A, int64_t lda, const void* B, int64_t ldb,

@@ -217,6 +217,8 @@ hipError_t release_workspace(Workspace& w, hipStream_t s) {
   return e;
 }
 
+namespace {
+
 hipError_t launch_gemm(char ta, char tb, int cfg, int epi, const GemmParams& p, hipStream_t s) {
   const bool an = is_n(ta), bn = is_n(tb);
   if (an && bn) return launch_gemm_nn(cfg, epi, p, s);
@@ -225,6 +227,7 @@ hipError_t launch_gemm(char ta, char tb, int cfg, int epi, const GemmParams& p, 
   return launch_gemm_tt(cfg, epi, p, s);
 }
 
+}  // namespace
 }  // namespace tgemm
 
 using namespace tgemm;

@@ -66,11 +66,20 @@ hipError_t launch_rows_skinny(int type, int epi, const RowsParams& p, hipStream_
 // kRowsStoreBf16, kRowsStoreF32, kRowsGated) (rows_finish.hip).
 hipError_t launch_rows_finish(int type, int epi, const RowsParams& p, hipStream_t s);
 
-// Copy an int8 operand of any layout into K-contiguous rows [R][Kp], zero
-// past K: X [R][K] (k_contiguous) or [K][R], row stride ld bytes; Kp a
-// multiple of 16 (rows_finish.hip).
-hipError_t launch_pack_i8(const int8_t* X, int64_t ld, bool k_contiguous, int R, int K,
-                          int8_t* out, int Kp, hipStream_t s);
+// Copy an operand of any layout and alignment into K-contiguous rows with
+// 16-byte boundaries, out [Rz][ldo], zero past K and past R: X [R][K]
+// (k_contiguous) or [K][R], row stride ld (elements of 1 or 2 bytes); ldo
+// times the element size a multiple of 16 (rows_finish.hip).
+struct PackRows {
+  const void* X;
+  int64_t ld;
+  bool k_contiguous;
+  int R, K;
+  void* out;
+  int Rz;
+  int64_t ldo;
+};
+hipError_t launch_pack_rows(const PackRows& p, int elem, hipStream_t s);
 
 // dgu = [dh * u * act'(g) | dh * act(g)]; columns 2F .. cols - 1 and rows M
 // .. rows - 1 of dgu are set to zero (rows_finish.hip).
@@ -148,6 +157,9 @@ struct __attribute__((packed, aligned(2))) u16x4_any {
 };
 struct __attribute__((packed, aligned(4))) f32x4_any {
   float v[4];
+};
+struct __attribute__((packed, aligned(1))) b16_any {
+  uint32_t w[4];
 };
 struct __attribute__((packed, aligned(1))) u8x8_any {
   uint32_t w[2];

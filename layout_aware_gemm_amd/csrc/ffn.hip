@@ -162,13 +162,13 @@ int run_i8(char ta, char tb, const void* A, int64_t lda, const void* B, int64_t 
   hipError_t e = hipSuccess;
   if (packA) {
     int8_t* o = reinterpret_cast<int8_t*>(ws);
-    e = launch_pack_i8(static_cast<const int8_t*>(A), lda, is_n(ta), p.M, K, o, Kp, s);
+    e = launch_pack_rows({A, lda, is_n(ta), p.M, K, o, p.M, Kp}, 1, s);
     p.A = reinterpret_cast<const char*>(o);
     p.lda = Kp;
   }
   if (packB && e == hipSuccess) {
     int8_t* o = reinterpret_cast<int8_t*>(ws + bytesA);
-    e = launch_pack_i8(static_cast<const int8_t*>(B), ldb, !is_n(tb), p.N, K, o, Kp, s);
+    e = launch_pack_rows({B, ldb, !is_n(tb), p.N, K, o, p.N, Kp}, 1, s);
     p.B = reinterpret_cast<const char*>(o);
     p.ldb = Kp;
   }
@@ -180,35 +180,12 @@ int run_i8(char ta, char tb, const void* A, int64_t lda, const void* B, int64_t 
 
 inline int64_t round_up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 
-// A GEMM of the library's own (no K split), for what the kernels
-// here do not take.
-hipError_t run_plain(char ta, char tb, int M, int N, int K, const void* A, int64_t lda,
-                     const void* B, int64_t ldb, void* C, int64_t ldc, bool f32, hipStream_t s) {
-  GemmParams g = {};
-  const int64_t t256 = (int64_t)ceil_div(M, 256) * ceil_div(N, 256);
-  const int cfg = t256 >= 144 ? kTile256 : kTile128;
-  g.A = static_cast<const uint16_t*>(A);
-  g.B = static_cast<const uint16_t*>(B);
-  g.C = C;
-  g.lda = lda;
-  g.ldb = ldb;
-  g.ldc = ldc;
-  g.M = M;
-  g.N = N;
-  g.K = K;
-  g.tilesM = ceil_div(M, tile_rows(cfg));
-  g.tilesN = ceil_div(N, tile_cols(cfg));
-  g.splitk = 1;
-  g.kchunk = K;
-  if ((int64_t)g.tilesM * g.tilesN > kMaxWorkgroups) return hipErrorInvalidValue;
-  g.groupM = g.tilesM < 4 ? g.tilesM : (g.tilesM <= 8 ? g.tilesM : 4);
-  g.aligned = rows_aligned(A, 2 * lda, 0) && rows_aligned(B, 2 * ldb, 0);
-  return launch_gemm(ta, tb, cfg, f32 ? kEpiStoreF32 : kEpiStoreBf16, g, s);
-}
-
-// bf16 gated product.  K-contiguous operands with 16-byte rows run on the
-// gated kernels; any other layout or alignment as the library's GEMM into
-// an fp32 [M][2F] workspace and a pass that gates it.
+// bf16 gated product.  Operands that the kernels cannot read in place -- not
+// K-contiguous, or with rows off 16-byte boundaries -- are copied into the
+// workspace first.  (The copy costs a read and a write of the operand; the
+// alternative, the library's GEMM in the operand's own layout, has to write
+// and re-read the whole fp32 [M][2F] product instead, and runs rows off
+// 16-byte boundaries at a third of the rate.)
 int run_gated(char ta, char tb, int64_t M, int64_t F, int64_t K, const void* A, int64_t lda,
               const void* B, int64_t ldb, int act, void* H, int64_t ldh, void* GU, int64_t ldgu,
               const CallSpace& space, hipStream_t s) {
@@ -221,113 +198,122 @@ int run_gated(char ta, char tb, int64_t M, int64_t F, int64_t K, const void* A, 
   p.ldc = ldh;
   p.gu = static_cast<uint16_t*>(GU);
   p.ldgu = ldgu;
-  const int64_t ldx = is_n(ta) && M == 1 ? K : lda;
-  const bool direct = is_n(ta) && !is_n(tb) && rows_aligned(A, 2 * ldx, 2 * K) &&
-                      rows_aligned(B, 2 * ldb, 2 * K) && stride_fits(2 * ldx) &&
-                      stride_fits(2 * ldb) && K < (int64_t(1) << 30);
+  const int64_t Kp = round_up(K, 8);
+  if (Kp >= int64_t(1) << 30) return TGEMM_ERR_UNSUPPORTED;
+  if (is_n(ta) && M == 1) lda = Kp;  // (the stride of a single row is never used)
+  const bool packA = !is_n(ta) || !rows_aligned(A, 2 * lda, 2 * K) || !stride_fits(2 * lda);
+  const bool packB = is_n(tb) || !rows_aligned(B, 2 * ldb, 2 * K) || !stride_fits(2 * ldb);
+  if ((packA || packB) && !stride_fits(2 * Kp)) return TGEMM_ERR_UNSUPPORTED;
+  p.K = (int)(2 * Kp);
+  const RowsPlan r = plan_rows(&p, true);
+  if (!grid_fits(p, r, true)) return TGEMM_ERR_UNSUPPORTED;
+  const size_t bytesA = packA ? round256((size_t)p.M * Kp * 2) : 0;
+  const size_t bytesB = packB ? round256((size_t)p.N * Kp * 2) : 0;
+  const size_t bytesP = p.split > 1 ? (size_t)p.split * p.M * p.N * sizeof(float) : 0;
   Workspace w;
-  hipError_t e;
-  if (direct) {
-    p.A = static_cast<const char*>(A);
-    p.B = static_cast<const char*>(B);
-    p.lda = 2 * ldx;
-    p.ldb = 2 * ldb;
-    p.K = (int)(2 * K);
-    const RowsPlan r = plan_rows(&p, true);
-    if (!grid_fits(p, r, true)) return TGEMM_ERR_UNSUPPORTED;
-    const int st = take_workspace(
-        space, s, p.split > 1 ? (size_t)p.split * p.M * p.N * sizeof(float) : 0, &w);
-    if (st != TGEMM_OK) return st;
-    p.part = w.ptr;
-    say_rows("gated bf16", p, r);
-    e = launch_rows(kRowsBf16, p, r, kRowsGated, true, s);
-  } else {
-    const int st = take_workspace(space, s, (size_t)p.M * p.N * sizeof(float), &w);
-    if (st != TGEMM_OK) return st;
-    if (verbose())
-      fprintf(stderr, "tgemm: gated bf16 %c%c M=%d F=%d K=%lld through fp32 [M][2F]\n", ta, tb, p.M,
-              p.F, (long long)K);
-    e = run_plain(ta, tb, p.M, p.N, (int)K, A, lda, B, ldb, w.ptr, p.N, true, s);
-    p.part = w.ptr;
-    p.split = 1;
-    if (e == hipSuccess) e = launch_rows_finish(kRowsBf16, kRowsGated, p, s);
+  const int st = take_workspace(space, s, bytesA + bytesB + bytesP, &w);
+  if (st != TGEMM_OK) return st;
+  say_rows("gated bf16", p, r);
+  char* const ws = static_cast<char*>(w.ptr);
+  p.A = static_cast<const char*>(A);
+  p.B = static_cast<const char*>(B);
+  p.lda = 2 * lda;
+  p.ldb = 2 * ldb;
+  hipError_t e = hipSuccess;
+  if (packA) {
+    e = launch_pack_rows({A, lda, is_n(ta), p.M, (int)K, ws, p.M, Kp}, 2, s);
+    p.A = ws;
+    p.lda = 2 * Kp;
   }
+  if (packB && e == hipSuccess) {
+    e = launch_pack_rows({B, ldb, !is_n(tb), p.N, (int)K, ws + bytesA, p.N, Kp}, 2, s);
+    p.B = ws + bytesA;
+    p.ldb = 2 * Kp;
+  }
+  if (bytesP) p.part = ws + bytesA + bytesB;
+  if (e == hipSuccess) e = launch_rows(kRowsBf16, p, r, kRowsGated, true, s);
   const hipError_t f = release_workspace(w, s);
   return status_of(e != hipSuccess ? e : f);
 }
 
 // Gradient of the gated product: dGU into the workspace, then dA = dGU .
-// op(B)^T and dB.  A 'N' and B 'T' with 16-byte rows take the joint launch;
-// other operands two launches of the library's GEMM.
+// op(B)^T and dB in one launch, which reads A and B as [M][K] and [2F][K]
+// rows on 16-byte boundaries; others are copied first.  dB stored [K][2F] is
+// the product with the operands exchanged, A^T . dGU; its first operand is
+// then a zero-padded copy of A.
 int run_gated_backward(char ta, char tb, int64_t M, int64_t F, int64_t K, const void* A,
                        int64_t lda, const void* B, int64_t ldb, const void* dH, int64_t lddh,
                        const void* GU, int64_t ldgu, int act, void* dA, int64_t ldda, void* dB,
                        int64_t lddb, bool f32, const CallSpace& space, hipStream_t s) {
-  const int64_t N2 = 2 * F;
-  const int64_t ldx = M == 1 ? round_up(K, 8) : lda;  // (a single row's stride is never used)
-  const bool joint = is_n(ta) && !is_n(tb) && rows_aligned(A, 2 * ldx, 0) &&
-                     rows_aligned(B, 2 * ldb, 0) && ldx < (1 << 23) && ldb < (1 << 23) &&
-                     N2 + 64 < (1 << 23);
-  const int64_t ldg = joint ? round_up(N2, 64) : N2;
-  const int64_t rows = joint ? round_up(M, 64) : M;
-  // joint: tiles of 256 rows read on past the padding
-  const size_t bytesG = round256((size_t)((joint ? round_up(M, 256) * ldg + 256 : M * ldg) * 2));
+  const int64_t N2 = 2 * F, Kp = round_up(K, 8);
+  const int64_t ldg = round_up(N2, 64), rows = round_up(M, 64);
+  constexpr int64_t kLimit = int64_t(1) << 23;  // (32-bit copy offsets)
+  if (Kp >= kLimit || ldg >= kLimit) return TGEMM_ERR_UNSUPPORTED;
+  if (is_n(ta) && M == 1) lda = Kp;  // (the stride of a single row is never used)
+  const bool swap = is_n(tb);
+  const bool packA = !is_n(ta) || swap || !rows_aligned(A, 2 * lda, 0) || lda >= kLimit;
+  const bool packB = is_n(tb) || !rows_aligned(B, 2 * ldb, 0) || ldb >= kLimit;
+  // tiles of 256 rows (columns) read on past the padding of G (and of A)
+  const size_t bytesG = round256((size_t)(round_up(M, 256) * ldg + 256) * 2);
+  const size_t bytesA = packA ? round256((size_t)(rows * Kp + 256) * 2) : 0;
+  const size_t bytesB = packB ? round256((size_t)N2 * Kp * 2) : 0;
   GemmParams px = {}, pw = {};
-  size_t bytesX = 0, bytesW = 0;
-  if (joint) {
-    px.M = (int)M;
-    px.N = (int)K;
-    px.K = (int)ldg;
-    px.kvb = (int)N2;
-    px.B = static_cast<const uint16_t*>(B);
-    px.ldb = ldb;
-    px.lda = ldg;
-    px.C = dA;
-    px.ldc = ldda;
-    pw.M = (int)N2;
-    pw.N = (int)K;
-    pw.K = (int)rows;
-    pw.kvb = (int)M;
-    pw.B = static_cast<const uint16_t*>(A);
-    pw.ldb = ldx;
-    pw.lda = ldg;
-    pw.C = dB;
-    pw.ldc = lddb;
-    gated_bwd_plan(&px, &pw);
-    if (px.splitk > 1) bytesX = round256((size_t)px.splitk * px.M * px.N * sizeof(float));
-    if (pw.splitk > 1) bytesW = (size_t)pw.splitk * pw.M * pw.N * sizeof(float);
-  }
+  px.M = (int)M;
+  px.N = (int)K;
+  px.K = (int)ldg;
+  px.kvb = (int)N2;
+  px.lda = ldg;
+  px.C = dA;
+  px.ldc = ldda;
+  pw.M = (int)(swap ? K : N2);
+  pw.N = (int)(swap ? N2 : K);
+  pw.K = (int)rows;
+  pw.kvb = (int)M;
+  pw.C = dB;
+  pw.ldc = lddb;
+  gated_bwd_plan(&px, &pw);
+  const size_t bytesX =
+      px.splitk > 1 ? round256((size_t)px.splitk * px.M * px.N * sizeof(float)) : 0;
+  const size_t bytesW = pw.splitk > 1 ? (size_t)pw.splitk * pw.M * pw.N * sizeof(float) : 0;
   Workspace w;
-  const int st = take_workspace(space, s, bytesG + bytesX + bytesW, &w);
+  const int st = take_workspace(space, s, bytesG + bytesA + bytesB + bytesX + bytesW, &w);
   if (st != TGEMM_OK) return st;
   if (verbose())
-    fprintf(stderr, "tgemm: gated backward %c%c M=%lld F=%lld K=%lld joint=%d split=%d,%d\n", ta,
-            tb, (long long)M, (long long)F, (long long)K, joint, px.splitk, pw.splitk);
-  char* const ws = static_cast<char*>(w.ptr);
+    fprintf(stderr, "tgemm: gated backward %c%c M=%lld F=%lld K=%lld copies=%d,%d split=%d,%d\n",
+            ta, tb, (long long)M, (long long)F, (long long)K, packA, packB, px.splitk, pw.splitk);
+  char* ws = static_cast<char*>(w.ptr);
   uint16_t* const G = reinterpret_cast<uint16_t*>(ws);
+  ws += bytesG;
   hipError_t e = launch_gated_grad(static_cast<const uint16_t*>(dH), lddh,
                                    static_cast<const uint16_t*>(GU), ldgu, (int)M, F, act, G, ldg,
                                    (int)rows, ldg, s);
-  if (e == hipSuccess && joint) {
-    px.A = pw.A = G;
-    px.ws = reinterpret_cast<float*>(ws + bytesG);
-    pw.ws = reinterpret_cast<float*>(ws + bytesG + bytesX);
-    e = launch_gated_bwd(px, pw, false, f32, s);
-    if (e == hipSuccess && px.splitk > 1)
-      e = launch_splitk_sum(px.ws, px.splitk, px.M, px.N, dA, ldda, false, s);
-    if (e == hipSuccess && pw.splitk > 1)
-      e = launch_splitk_sum(pw.ws, pw.splitk, pw.M, pw.N, dB, lddb, f32, s);
-  } else if (e == hipSuccess) {
-    // dA = G . op(B)^T: B stored [2F][K] ('T') is read as it lies
-    e = run_plain('N', is_n(tb) ? 'T' : 'N', (int)M, (int)K, (int)N2, G, ldg, B, ldb, dA, ldda,
-                  false, s);
-    // dB in B's layout: [2F][K] = G^T . op(A), or [K][2F] = op(A)^T . G
-    if (e == hipSuccess && !is_n(tb))
-      e = run_plain('T', ta, (int)N2, (int)K, (int)M, G, ldg, A, lda, dB, lddb, f32, s);
-    else if (e == hipSuccess)
-      e = run_plain(is_n(ta) ? 'T' : 'N', 'N', (int)K, (int)N2, (int)M, A, lda, G, ldg, dB, lddb,
-                    f32, s);
+  const void *Ar = A, *Br = B;  // [M][K], [2F][K] rows
+  if (packA && e == hipSuccess) {
+    e = launch_pack_rows({A, lda, is_n(ta), (int)M, (int)K, ws, (int)rows, Kp}, 2, s);
+    Ar = ws;
+    lda = Kp;
   }
+  ws += bytesA;
+  if (packB && e == hipSuccess) {
+    e = launch_pack_rows({B, ldb, !is_n(tb), (int)N2, (int)K, ws, (int)N2, Kp}, 2, s);
+    Br = ws;
+    ldb = Kp;
+  }
+  ws += bytesB;
+  px.A = G;
+  px.B = static_cast<const uint16_t*>(Br);
+  px.ldb = ldb;
+  px.ws = reinterpret_cast<float*>(ws);
+  pw.A = swap ? static_cast<const uint16_t*>(Ar) : G;
+  pw.lda = swap ? lda : ldg;
+  pw.B = swap ? G : static_cast<const uint16_t*>(Ar);
+  pw.ldb = swap ? ldg : lda;
+  pw.ws = reinterpret_cast<float*>(ws + bytesX);
+  if (e == hipSuccess) e = launch_gated_bwd(px, pw, false, f32, s);
+  if (e == hipSuccess && px.splitk > 1)
+    e = launch_splitk_sum(px.ws, px.splitk, px.M, px.N, dA, ldda, false, s);
+  if (e == hipSuccess && pw.splitk > 1)
+    e = launch_splitk_sum(pw.ws, pw.splitk, pw.M, pw.N, dB, lddb, f32, s);
   const hipError_t f = release_workspace(w, s);
   return status_of(e != hipSuccess ? e : f);
 }

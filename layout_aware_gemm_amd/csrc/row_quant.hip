@@ -75,24 +75,24 @@ __device__ __forceinline__ uint32_t code_of(float t, const RowCode& c) {
 #endif
 }
 
-__device__ __forceinline__ uint64_t wave_sum_max(double& ss, uint32_t& mx) {
+__device__ __forceinline__ void wave_sum_max(double& ss, uint32_t& mx) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) {
     ss += __shfl_xor(ss, o, 64);
     const uint32_t m = __shfl_xor(mx, o, 64);
     mx = m > mx ? m : mx;
   }
-  return 0;
 }
 
-// Reduce over the workgroup, then thread-uniform row constants.
-template <int T, bool NORM>
+// Reduce over the workgroup (in wave order), then the row's constants.
+template <bool NORM>
 __device__ __forceinline__ RowCode row_code(const RowQuantParams& p, int row, double ss,
                                             uint32_t mx) {
   wave_sum_max(ss, mx);
-  if constexpr (T > 64) {
-    __shared__ double s_ss[T / 64];
-    __shared__ uint32_t s_mx[T / 64];
+  const int waves = (int)blockDim.x >> 6;
+  if (waves > 1) {
+    __shared__ double s_ss[16];
+    __shared__ uint32_t s_mx[16];
     if ((threadIdx.x & 63) == 0) {
       s_ss[threadIdx.x >> 6] = ss;
       s_mx[threadIdx.x >> 6] = mx;
@@ -100,8 +100,7 @@ __device__ __forceinline__ RowCode row_code(const RowQuantParams& p, int row, do
     __syncthreads();
     ss = s_ss[0];
     mx = s_mx[0];
-#pragma unroll
-    for (int w = 1; w < T / 64; ++w) {
+    for (int w = 1; w < waves; ++w) {
       ss += s_ss[w];
       mx = s_mx[w] > mx ? s_mx[w] : mx;
     }
@@ -181,12 +180,12 @@ __device__ __forceinline__ u16x8_any add8(const u16x8_any& x, const u16x8_any& r
   return h;
 }
 
-// V chunks of 8 elements per thread, T threads: rows of up to 8 T V.
+// V chunks of 8 elements per thread: rows of up to 8 V blockDim.x.
 // (x, residual and sum may be the same rows: a thread writes only what it
 // has read itself.)
-template <int T, int V, bool NORM, bool RES>
-__global__ void __launch_bounds__(T) row_quant_kernel(RowQuantParams p) {
-  const int row = blockIdx.x;
+template <int V, bool NORM, bool RES>
+__global__ void __launch_bounds__(1024) row_quant_kernel(RowQuantParams p) {
+  const int row = blockIdx.x, T = blockDim.x;
   const uint16_t* x = p.x + (int64_t)row * p.ldx;
   u16x8_any h[V], w[NORM ? V : 1];
   double ss = 0.0;
@@ -210,7 +209,7 @@ __global__ void __launch_bounds__(T) row_quant_kernel(RowQuantParams p) {
     }
     accumulate<NORM>(h[v], w[NORM ? v : 0], ss, mx);
   }
-  const RowCode rc = row_code<T, NORM>(p, row, ss, mx);
+  const RowCode rc = row_code<NORM>(p, row, ss, mx);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int64_t c = ((int64_t)v * T + threadIdx.x) * 8;
@@ -237,7 +236,7 @@ __global__ void __launch_bounds__(1024) row_quant_long(RowQuantParams p) {
     if constexpr (NORM) w = load8(p.weight, c, p.K);
     accumulate<NORM>(h, w, ss, mx);
   }
-  const RowCode rc = row_code<1024, NORM>(p, row, ss, mx);
+  const RowCode rc = row_code<NORM>(p, row, ss, mx);
   for (int64_t c = threadIdx.x * 8; c < p.K; c += 8192) {
     const u16x8_any h = load8(again, c, p.K);
     if constexpr (NORM) w = load8(p.weight, c, p.K);
@@ -245,33 +244,55 @@ __global__ void __launch_bounds__(1024) row_quant_long(RowQuantParams p) {
   }
 }
 
-template <int T, int V>
-hipError_t launch_tv(const RowQuantParams& p, hipStream_t s) {
+// The fewest whole waves that hold a row in V chunks per thread.
+int threads_of(const RowQuantParams& p, int V) {
+  const int64_t chunks = (p.K + 7) / 8;
+  return (int)((chunks + 64 * V - 1) / (64 * V)) * 64;
+}
+
+hipError_t launch_quant8(const RowQuantParams& p, hipStream_t s) {
+  hipLaunchKernelGGL((row_quant_kernel<8, false, false>), dim3(p.M), dim3(threads_of(p, 8)), 0, s,
+                     p);
+  return hipGetLastError();
+}
+
+template <int V>
+hipError_t launch_v(const RowQuantParams& p, hipStream_t s) {
+  const int T = threads_of(p, V);
   if (p.weight != nullptr && p.residual != nullptr)
-    hipLaunchKernelGGL((row_quant_kernel<T, V, true, true>), dim3(p.M), dim3(T), 0, s, p);
+    hipLaunchKernelGGL((row_quant_kernel<V, true, true>), dim3(p.M), dim3(T), 0, s, p);
   else if (p.weight != nullptr)
-    hipLaunchKernelGGL((row_quant_kernel<T, V, true, false>), dim3(p.M), dim3(T), 0, s, p);
+    hipLaunchKernelGGL((row_quant_kernel<V, true, false>), dim3(p.M), dim3(T), 0, s, p);
   else
-    hipLaunchKernelGGL((row_quant_kernel<T, V, false, false>), dim3(p.M), dim3(T), 0, s, p);
+    hipLaunchKernelGGL((row_quant_kernel<V, false, false>), dim3(p.M), dim3(T), 0, s, p);
   return hipGetLastError();
 }
 
 }  // namespace
 
+// Chunks per thread.  Few rows: as few as possible, the call is latency.
+// Many: workgroups of about four waves, which overlap best (us, MI355X:
+// norm with residual 8192 x 5120, 1 / 2 / 3 / 4 chunks per thread 65.4 / 54.8
+// / 53.2 / 58.5; codes alone 4096 x 13824, 2 / 4 / 8 chunks 44.9 / 38.0 /
+// 36.1; norm 8 x 5120, 1 / 2 / 4 chunks 4.3 / 4.7 / 5.4).  Eight chunks of a
+// norm's two inputs would not fit the registers of a full workgroup.
 hipError_t launch_row_quant(const RowQuantParams& p, hipStream_t s) {
   const int64_t chunks = (p.K + 7) / 8;
-  if (chunks <= 64) return launch_tv<64, 1>(p, s);
-  if (chunks <= 256) return launch_tv<256, 1>(p, s);
-  if (chunks <= 512) return launch_tv<256, 2>(p, s);
-  if (chunks <= 1024) return launch_tv<512, 2>(p, s);
-  if (chunks <= 2048) return launch_tv<1024, 2>(p, s);
-  if (chunks <= 4096) return launch_tv<1024, 4>(p, s);
-  if (p.weight != nullptr && p.residual != nullptr)
-    hipLaunchKernelGGL((row_quant_long<true, true>), dim3(p.M), dim3(1024), 0, s, p);
-  else if (p.weight != nullptr)
-    hipLaunchKernelGGL((row_quant_long<true, false>), dim3(p.M), dim3(1024), 0, s, p);
-  else
+  const int64_t v = p.M < 512 ? (chunks + 1023) / 1024 : (chunks + 255) / 256;
+  if (v <= 1) return launch_v<1>(p, s);
+  if (v <= 2) return launch_v<2>(p, s);
+  if (v <= 3) return launch_v<3>(p, s);
+  if (p.weight == nullptr) {
+    if (v > 4 && chunks <= 8192) return launch_quant8(p, s);
+    if (chunks <= 4096) return launch_v<4>(p, s);
     hipLaunchKernelGGL((row_quant_long<false, false>), dim3(p.M), dim3(1024), 0, s, p);
+    return hipGetLastError();
+  }
+  if (chunks <= 4096) return launch_v<4>(p, s);
+  if (p.residual != nullptr)
+    hipLaunchKernelGGL((row_quant_long<true, true>), dim3(p.M), dim3(1024), 0, s, p);
+  else
+    hipLaunchKernelGGL((row_quant_long<true, false>), dim3(p.M), dim3(1024), 0, s, p);
   return hipGetLastError();
 }
 

@@ -1,9 +1,11 @@
 // The row products' side passes: the sum of K chunks with its epilogue, the
-// copy of an int8 operand into the layout the products read, and the gated
+// copy of an operand into the layout the products read, and the gated
 // product's gradient.  All are bound by HBM bandwidth: each element is read
 // and written once, 8 or 4 per thread.
 #include "bf16_cvt.h"
 #include "ffn.h"
+
+#include <type_traits>
 
 namespace tgemm {
 namespace {
@@ -91,33 +93,60 @@ __global__ void __launch_bounds__(kThr) finish_kernel(RowsParams p) {
   }
 }
 
-// 64 x 64 bytes per workgroup.  K-contiguous operands are copied, others
-// transposed through LDS (65-byte rows: the column reads hit all banks).
-template <bool KC>
-__global__ void __launch_bounds__(kThr) pack_i8_kernel(const int8_t* __restrict__ X, int64_t ld,
-                                                       int R, int K, int8_t* __restrict__ out,
-                                                       int Kp, int kblocks) {
-  __shared__ int8_t t[64][65];
-  const int k0 = (int)(blockIdx.x % kblocks) * 64, r0 = (int)(blockIdx.x / kblocks) * 64;
-  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int y = ty + 4 * i;
-    if constexpr (KC) {
-      const int r = r0 + y, k = k0 + tx;
-      if (r < R && k < Kp) out[(int64_t)r * Kp + k] = k < K ? X[(int64_t)r * ld + k] : int8_t(0);
+// Copy a K-contiguous operand: 16 output bytes per thread, from any
+// alignment.  ES: bytes per element.
+template <int ES>
+__global__ void __launch_bounds__(kThr) pack_rows_kernel(PackRows p, int chunks) {
+  const int64_t t = (int64_t)blockIdx.x * kThr + threadIdx.x;
+  const int r = (int)(t / chunks), k = (int)(t - (int64_t)r * chunks) * (16 / ES);
+  if (r >= p.Rz) return;
+  b16_any v = {{0, 0, 0, 0}};
+  if (r < p.R && k < p.K) {
+    const char* src = static_cast<const char*>(p.X) + ((int64_t)r * p.ld + k) * ES;
+    if (k + 16 / ES <= p.K) {
+      v = *reinterpret_cast<const b16_any*>(src);
     } else {
-      const int k = k0 + y, r = r0 + tx;
-      t[y][tx] = k < K && r < R ? X[(int64_t)k * ld + r] : int8_t(0);
+      for (int i = 0; i < (p.K - k) * ES; ++i)
+        v.w[i >> 2] |= (uint32_t)(uint8_t)src[i] << ((i & 3) * 8);
     }
   }
-  if constexpr (!KC) {
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int r = r0 + ty + 4 * i, k = k0 + tx;
-      if (r < R && k < Kp) out[(int64_t)r * Kp + k] = t[tx][ty + 4 * i];
+  *reinterpret_cast<b16_any*>(static_cast<char*>(p.out) + ((int64_t)r * p.ldo + k) * ES) = v;
+}
+
+// Copy an operand stored [K][R] into rows of K: 64 x 64 elements per
+// workgroup, read 16 bytes along R, turned around in LDS (rows of 64 + 16 /
+// ES elements, a multiple of 16 bytes) and written 16 bytes along K.
+template <int ES>
+__global__ void __launch_bounds__(kThr) pack_cols_kernel(PackRows p, int kblocks) {
+  using E = std::conditional_t<ES == 1, uint8_t, uint16_t>;
+  constexpr int V = 16 / ES, LD = 64 + V, NV = 64 * 64 / V;  // elements per vector, vectors
+  __shared__ __attribute__((aligned(16))) E t[64 * LD];
+  const int k0 = (int)(blockIdx.x % kblocks) * 64, r0 = (int)(blockIdx.x / kblocks) * 64;
+  for (int i = threadIdx.x; i < NV; i += kThr) {
+    const int kl = i / (64 / V), rl = (i % (64 / V)) * V;
+    const int k = k0 + kl, r = r0 + rl;
+    b16_any v = {{0, 0, 0, 0}};
+    if (k < p.K && r < p.R) {
+      const char* src = static_cast<const char*>(p.X) + ((int64_t)k * p.ld + r) * ES;
+      if (r + V <= p.R) {
+        v = *reinterpret_cast<const b16_any*>(src);
+      } else {
+        for (int e = 0; e < (p.R - r) * ES; ++e)
+          v.w[e >> 2] |= (uint32_t)(uint8_t)src[e] << ((e & 3) * 8);
+      }
     }
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      t[(rl + e) * LD + kl] = (E)(v.w[e * ES >> 2] >> ((e * ES & 3) * 8));
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < NV; i += kThr) {
+    const int rl = i / (64 / V), kl = (i % (64 / V)) * V;
+    const int r = r0 + rl, k = k0 + kl;
+    // (ldo holds whole vectors)
+    if (r < p.Rz && k < p.ldo)
+      *reinterpret_cast<uint4*>(static_cast<char*>(p.out) + ((int64_t)r * p.ldo + k) * ES) =
+          *reinterpret_cast<const uint4*>(t + rl * LD + kl);
   }
 }
 
@@ -198,17 +227,24 @@ hipError_t launch_rows_finish(int type, int epi, const RowsParams& p, hipStream_
   return hipErrorInvalidValue;
 }
 
-hipError_t launch_pack_i8(const int8_t* X, int64_t ld, bool k_contiguous, int R, int K,
-                          int8_t* out, int Kp, hipStream_t s) {
-  const int kblocks = ceil_div(Kp, 64);
-  const int64_t blocks = (int64_t)kblocks * ceil_div(R, 64);
-  if (blocks > kMaxWorkgroups) return hipErrorInvalidValue;
-  if (k_contiguous)
-    hipLaunchKernelGGL(pack_i8_kernel<true>, dim3((unsigned)blocks), dim3(kThr), 0, s, X, ld, R, K,
-                       out, Kp, kblocks);
-  else
-    hipLaunchKernelGGL(pack_i8_kernel<false>, dim3((unsigned)blocks), dim3(kThr), 0, s, X, ld, R,
-                       K, out, Kp, kblocks);
+hipError_t launch_pack_rows(const PackRows& p, int elem, hipStream_t s) {
+  if (p.k_contiguous) {
+    const int chunks = (int)(p.ldo * elem / 16);
+    const int64_t blocks = ((int64_t)p.Rz * chunks + kThr - 1) / kThr;
+    if (blocks > kMaxWorkgroups) return hipErrorInvalidValue;
+    if (elem == 1)
+      hipLaunchKernelGGL(pack_rows_kernel<1>, dim3((unsigned)blocks), dim3(kThr), 0, s, p, chunks);
+    else
+      hipLaunchKernelGGL(pack_rows_kernel<2>, dim3((unsigned)blocks), dim3(kThr), 0, s, p, chunks);
+  } else {
+    const int kblocks = ceil_div(p.ldo, 64);
+    const int64_t blocks = (int64_t)kblocks * ceil_div(p.Rz, 64);
+    if (blocks > kMaxWorkgroups) return hipErrorInvalidValue;
+    if (elem == 1)
+      hipLaunchKernelGGL(pack_cols_kernel<1>, dim3((unsigned)blocks), dim3(kThr), 0, s, p, kblocks);
+    else
+      hipLaunchKernelGGL(pack_cols_kernel<2>, dim3((unsigned)blocks), dim3(kThr), 0, s, p, kblocks);
+  }
   return hipGetLastError();
 }
 

@@ -100,9 +100,6 @@ hipError_t launch_gemm_nt(int cfg, int epi, const GemmParams& p, hipStream_t s);
 hipError_t launch_gemm_tn(int cfg, int epi, const GemmParams& p, hipStream_t s);
 hipError_t launch_gemm_tt(int cfg, int epi, const GemmParams& p, hipStream_t s);
 
-// The one of them for the layout flags (dispatch.hip).
-hipError_t launch_gemm(char ta, char tb, int cfg, int epi, const GemmParams& p, hipStream_t s);
-
 // Split-K: C = sum over chunks q = 0, 1, ..., split-1 (in that order) of
 // the fp32 partial products ws[q][M][N] (defined in splitk.hip).
 hipError_t launch_splitk_sum(const float* ws, int split, int M, int N, void* C, int64_t ldc,

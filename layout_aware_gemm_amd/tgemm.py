@@ -552,24 +552,31 @@ def _act(act):
 
 def _same_device(*ts):
     """The one CUDA device every given tensor is on."""
-    ts = [t for t in ts if t is not None]
-    _check_dev(*ts)
     dev = ts[0].device
-    for t in ts[1:]:
-        if t.device != dev:
+    for t in ts:
+        if t is not None and (not t.is_cuda or t.device != dev):
+            _check_dev(t)
             raise ValueError(f"tensors on different devices: {dev} and {t.device}")
     return dev
 
 
-class _On:
-    """The operands' device and the given stream made current, so that the
-    outputs and temporaries of a helper are allocated for the stream its
-    kernels run on (a stream handle or torch stream; None: the current one)."""
+class _Here:
+    """No change of device or stream."""
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+class _There:
+    """The operands' device and the given stream (a handle or a torch
+    stream) made current, so that the outputs and temporaries of a helper
+    are allocated for the stream its kernels run on."""
 
     def __init__(self, dev, stream):
-        self._ctx = []
-        if dev.index is not None and torch.cuda.current_device() != dev.index:
-            self._ctx.append(torch.cuda.device(dev))
+        self._ctx = [torch.cuda.device(dev)]
         if stream is not None:
             if not isinstance(stream, torch.cuda.Stream):
                 stream = (torch.cuda.ExternalStream(int(stream), device=dev) if int(stream)
@@ -585,22 +592,37 @@ class _On:
             c.__exit__(*exc)
 
 
-def _call(name, *args):
-    st = getattr(lib(), name)(*args, torch.cuda.current_stream().cuda_stream)
+_HERE = _Here()
+
+
+def _on(dev, stream):
+    if stream is None and dev.index == torch.cuda.current_device():
+        return _HERE
+    return _There(dev, stream)
+
+
+def _raw_stream(dev):
+    """Handle of the device's current stream (torch's own shortcut: a Stream
+    object costs 3 us, as much as a small call's launch)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _call(name, dev, *args):
+    st = getattr(lib(), name)(*args, _raw_stream(dev))
     if st != TGEMM_OK:
         raise TgemmError(st, name)
 
 
-def _call_ws(name, device, *args):
+def _call_ws(name, dev, *args):
     """As ``_call`` for a call with workspace (its first nine arguments are
     the product's), which is a torch allocation: most calls need none, and
     one that does says so before it enqueues anything."""
-    fn, stream = getattr(lib(), name), torch.cuda.current_stream().cuda_stream
+    fn, stream = getattr(lib(), name), _raw_stream(dev)
     st = fn(*args, None, 0, stream)
     if st == TGEMM_ERR_WORKSPACE_LIMIT:
         need = getattr(lib(), name.replace("run_", "") + "_workspace_bytes")(*args[:9])
         if need > 0:
-            ws = torch.empty(need, dtype=torch.uint8, device=device)
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
             st = fn(*args, ws.data_ptr(), need, stream)
     if st != TGEMM_OK:
         raise TgemmError(st, name)
@@ -617,11 +639,14 @@ def _rows(x, what, dtype):
         if x.stride(-1) != 1 and x.shape[-1] != 1:
             raise ValueError(f"{what} needs a contiguous last dimension")
         x = x.view(-1, x.shape[-1])
-    if x.shape[1] != 1 and x.stride(1) != 1:
+    M, K = x.shape
+    ld, unit = x.stride()
+    if unit != 1 and K != 1:
         raise ValueError(f"{what} needs a contiguous last dimension")
-    ld = x.shape[1] if x.shape[0] == 1 else x.stride(0)
-    if ld < x.shape[1]:
-        raise ValueError(f"{what}: rows overlap (stride {ld} of {x.shape[1]} elements)")
+    if M == 1:
+        ld = K
+    if ld < K:
+        raise ValueError(f"{what}: rows overlap (stride {ld} of {K} elements)")
     return x, ld
 
 
@@ -651,7 +676,9 @@ def _product(a, b, dtype, what):
     a2 = a.view(1, -1) if a.dim() == 1 else _flatten_rows(a)
     if a2.shape[1] != b.shape[0]:
         raise ValueError(f"inner dimensions differ: {a2.shape[1]} vs {b.shape[0]}")
-    return (a2,) + layout_of(a2) + layout_of(b)
+    ta, lda = layout_of(a2)
+    tb, ldb = layout_of(b)
+    return a2, ta.encode(), lda, tb.encode(), ldb
 
 
 def rms_norm_i8(x, weight, eps=1e-6, residual=None, out_residual=None, stream=None):
@@ -668,23 +695,23 @@ def rms_norm_i8(x, weight, eps=1e-6, residual=None, out_residual=None, stream=No
     x2, ldx = _rows(x, "x", torch.bfloat16)
     M, K = x2.shape
     _vector(weight, K, "weight", torch.bfloat16)
-    ldr = lds = 0
+    r2, ldr, s2, lds = None, 0, None, 0
     if residual is not None:
         if residual.shape != x.shape:
             raise ValueError("x and residual differ in shape")
         r2, ldr = _rows(residual, "residual", torch.bfloat16)
-    with _On(_same_device(x, weight, residual, out_residual), stream):
-        q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
-        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        s2 = None
+    dev = _same_device(x, weight, residual, out_residual)
+    with _on(dev, stream):
+        q = torch.empty(x.shape, dtype=torch.int8, device=dev)
+        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
         if residual is not None:
             if out_residual is None:
-                out_residual = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+                out_residual = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
             if out_residual.shape != x.shape:
                 raise ValueError("x and out_residual differ in shape")
             s2, lds = _rows(out_residual, "out_residual", torch.bfloat16)
-        _call("tgemm_rms_norm_i8", _ptr(x2), ldx, _ptr(r2) if residual is not None else None, ldr,
-              _ptr(weight), float(eps), M, K, _ptr(s2), lds, _ptr(q), K, _ptr(scale))
+        _call("tgemm_rms_norm_i8", dev, _ptr(x2), ldx, _ptr(r2), ldr, _ptr(weight), float(eps), M,
+              K, _ptr(s2), lds, _ptr(q), K, _ptr(scale))
     return (q, scale) if residual is None else (q, scale, out_residual)
 
 
@@ -693,10 +720,11 @@ def quantize_i8(x, stream=None):
     ``q * scale[..., None]`` is x in 255 levels of its row's largest value."""
     x2, ldx = _rows(x, "x", torch.bfloat16)
     M, K = x2.shape
-    with _On(_same_device(x), stream):
-        q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
-        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        _call("tgemm_quantize_i8", _ptr(x2), ldx, M, K, _ptr(q), K, _ptr(scale))
+    dev = _same_device(x)
+    with _on(dev, stream):
+        q = torch.empty(x.shape, dtype=torch.int8, device=dev)
+        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+        _call("tgemm_quantize_i8", dev, _ptr(x2), ldx, M, K, _ptr(q), K, _ptr(scale))
     return q, scale
 
 
@@ -711,10 +739,11 @@ def matmul_i8(a, b, scale_a, scale_b, out_dtype=torch.bfloat16, stream=None):
     _vector(scale_b, N, "scale_b", torch.float32)
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("out_dtype must be bf16 or fp32")
-    with _On(_same_device(a, b, sa, scale_b), stream):
-        out = torch.empty(a.shape[:-1] + (N,), dtype=out_dtype, device=a.device)
-        _call_ws("tgemm_run_i8", a.device, _flag(ta), _flag(tb), M, N, K, _ptr(a2), lda, _ptr(b),
-                 ldb, _ptr(sa), _ptr(scale_b), _ptr(out), N,
+    dev = _same_device(a, b, sa, scale_b)
+    with _on(dev, stream):
+        out = torch.empty(a.shape[:-1] + (N,), dtype=out_dtype, device=dev)
+        _call_ws("tgemm_run_i8", dev, ta, tb, M, N, K, _ptr(a2), lda, _ptr(b), ldb, _ptr(sa),
+                 _ptr(scale_b), _ptr(out), N,
                  EPI_STORE_BF16 if out_dtype == torch.bfloat16 else EPI_STORE_F32)
     return out
 
@@ -734,9 +763,10 @@ def gated_matmul_i8(a, b, scale_a, scale_b, act="silu", stream=None):
     M, K = a2.shape
     sa = _row_scales(scale_a, a.shape[:-1], "scale_a")
     _vector(scale_b, 2 * F, "scale_b", torch.float32)
-    with _On(_same_device(a, b, sa, scale_b), stream):
-        h = torch.empty(a.shape[:-1] + (F,), dtype=torch.bfloat16, device=a.device)
-        _call_ws("tgemm_run_gated_i8", a.device, _flag(ta), _flag(tb), M, F, K, _ptr(a2), lda,
+    dev = _same_device(a, b, sa, scale_b)
+    with _on(dev, stream):
+        h = torch.empty(a.shape[:-1] + (F,), dtype=torch.bfloat16, device=dev)
+        _call_ws("tgemm_run_gated_i8", dev, ta, tb, M, F, K, _ptr(a2), lda,
                  _ptr(b), ldb, _ptr(sa), _ptr(scale_b), _act(act), _ptr(h), F)
     return h
 
@@ -750,11 +780,12 @@ def gated_matmul(x, w, act="silu", save=False, stream=None):
     F = _gate_width(w)
     x2, ta, lda, tb, ldb = _product(x, w, torch.bfloat16, "gated_matmul")
     M, K = x2.shape
-    with _On(_same_device(x, w), stream):
-        h = torch.empty(x.shape[:-1] + (F,), dtype=torch.bfloat16, device=x.device)
-        gu = (torch.empty(x.shape[:-1] + (2 * F,), dtype=torch.bfloat16, device=x.device)
+    dev = _same_device(x, w)
+    with _on(dev, stream):
+        h = torch.empty(x.shape[:-1] + (F,), dtype=torch.bfloat16, device=dev)
+        gu = (torch.empty(x.shape[:-1] + (2 * F,), dtype=torch.bfloat16, device=dev)
               if save else None)
-        _call_ws("tgemm_run_gated", x.device, _flag(ta), _flag(tb), M, F, K, _ptr(x2), lda, _ptr(w),
+        _call_ws("tgemm_run_gated", dev, ta, tb, M, F, K, _ptr(x2), lda, _ptr(w),
                  ldb, _act(act), _ptr(h), F, _ptr(gu), 2 * F)
     return (h, gu) if save else h
 
@@ -773,13 +804,14 @@ def gated_backward(dh, gu, x, w, act="silu", dw_dtype=torch.bfloat16, stream=Non
         raise TypeError("dw_dtype must be bf16 or fp32")
     d2, ldd = _rows(dh, "dh", torch.bfloat16)
     g2, ldg = _rows(gu, "gu", torch.bfloat16)
-    with _On(_same_device(dh, gu, x, w), stream):
-        dx = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
-        dw = torch.empty((2 * F, K) if tb == "T" else (K, 2 * F), dtype=dw_dtype, device=x.device)
-        _call_ws("tgemm_run_gated_backward", x.device, _flag(ta), _flag(tb), M, F, K, _ptr(x2),
+    dev = _same_device(dh, gu, x, w)
+    with _on(dev, stream):
+        dx = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
+        dw = torch.empty((2 * F, K) if tb == b"T" else (K, 2 * F), dtype=dw_dtype, device=dev)
+        _call_ws("tgemm_run_gated_backward", dev, ta, tb, M, F, K, _ptr(x2),
                  lda, _ptr(w), ldb, _ptr(d2), ldd, _ptr(g2), ldg, _act(act), _ptr(dx), K, _ptr(dw),
                  dw.shape[1], EPI_STORE_BF16 if dw_dtype == torch.bfloat16 else EPI_STORE_F32)
-    return dx, dw.t() if tb == "T" else dw
+    return dx, dw.t() if tb == b"T" else dw
 
 
 def outer_f32(a, b, stream=None):

@@ -185,7 +185,7 @@ def test_workspace_queries():
     assert L.tgemm_gated_i8_workspace_bytes(N, T, 4, 64, 64, P, 64, P, 64) == 0
     assert L.tgemm_gated_i8_workspace_bytes(N, T, 4, 64, 65, P, 65, P, 65) >= (4 + 128) * 80
     assert L.tgemm_gated_workspace_bytes(N, T, 4, 64, 64, P, 64, P, 64) == 0
-    assert L.tgemm_gated_workspace_bytes(T, T, 4, 64, 64, P, 4, P, 64) == 4 * 128 * 4
+    assert L.tgemm_gated_workspace_bytes(T, T, 4, 64, 64, P, 4, P, 64) == 4 * 64 * 2
     assert L.tgemm_gated_workspace_bytes(N, T, 4, 64, 64, None, 64, P, 64) == INV
     # dGU padded to whole tiles of rows, and 64 columns
     assert L.tgemm_gated_backward_workspace_bytes(N, T, 4, 40, 64, P, 64, P, 64) >= 256 * 128 * 2

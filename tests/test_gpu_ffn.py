@@ -72,7 +72,7 @@ def within(got, ref, bound):
 
 ROWS = [(1, 1), (3, 5), (2, 8), (1, 64), (7, 511), (2, 512), (3, 513), (5, 2048), (3, 2049),
         (2, 4096), (2, 5120), (1, 8191), (2, 8200), (2, 13824), (1, 16385), (2, 32768), (2, 32776),
-        (1, 70001)]
+        (1, 70001), (600, 264), (513, 2057), (520, 5000), (515, 8000), (515, 8201), (513, 33001)]
 
 
 def check_quant(q, scale, ref_q, ref_scale):
@@ -155,7 +155,7 @@ def test_quantize_leaves_the_rest_alone():
     buf = torch.full((5 * 90 + 8,), 99, dtype=I8, device=dev())
     scale = torch.empty(5, device=dev())
     q = torch.as_strided(buf, (5, 77), (90, 1), 1)
-    tgemm._call("tgemm_quantize_i8", x.data_ptr(), 77, 5, 77, q.data_ptr(), 90, scale.data_ptr())
+    tgemm._call("tgemm_quantize_i8", dev(), x.data_ptr(), 77, 5, 77, q.data_ptr(), 90, scale.data_ptr())
     ref, _ = oracle.ffn.quantize_rows(f64(x))
     assert np.array_equal(q.cpu().numpy(), ref)
     q.fill_(99)
@@ -222,7 +222,7 @@ def test_i8_nan_scale_and_bounds():
         sa, sb = scales(M, 1), scales(30, 2)
         sa[3] = float("nan")
         C = torch.full((M + 1, 41), 7.0, device=dev())
-        tgemm._call("tgemm_run_i8", tgemm._flag("N"), tgemm._flag("T"), M, 30, 64, a.data_ptr(), 64,
+        tgemm._call("tgemm_run_i8", dev(), tgemm._flag("N"), tgemm._flag("T"), M, 30, 64, a.data_ptr(), 64,
                     w.data_ptr(), 64, sa.data_ptr(), sb.data_ptr(), C.data_ptr(), 41,
                     tgemm.EPI_STORE_F32, None, -1)
         c = C[:M, :30]
@@ -357,7 +357,7 @@ def test_gradient_writes_nothing_else():
     dx, dw = tgemm.gated_backward(dh, gu, x, w.t())
     dA = torch.full((M + 1, K + 5), 3.0, dtype=BF, device=dev())
     dB = torch.full((2 * F + 1, K + 9), 4.0, dtype=BF, device=dev())
-    tgemm._call("tgemm_run_gated_backward", tgemm._flag("N"), tgemm._flag("T"), M, F, K,
+    tgemm._call("tgemm_run_gated_backward", dev(), tgemm._flag("N"), tgemm._flag("T"), M, F, K,
                 x.data_ptr(), K, w.data_ptr(), K, dh.data_ptr(), F, gu.data_ptr(), 2 * F, 0,
                 dA.data_ptr(), K + 5, dB.data_ptr(), K + 9, tgemm.EPI_STORE_BF16, None, -1)
     assert torch.equal(dA[:M, :K], dx) and torch.equal(dB[: 2 * F, :K], dw.t())
@@ -375,7 +375,7 @@ def test_gated_grad_values(kind):
     gu = torch.cat([g.repeat(3, 1), workloads.randn_bf16((3, F), 1.0, gen(1))], 1).to(dev())
     dh = workloads.randn_bf16((3, F), 1.0, gen(2)).to(dev())
     out = torch.full((3, 2 * F + 5), 7.0, dtype=BF, device=dev())
-    tgemm._call("tgemm_gated_grad", 3, F, dh.data_ptr(), F, gu.data_ptr(), 2 * F,
+    tgemm._call("tgemm_gated_grad", dev(), 3, F, dh.data_ptr(), F, gu.data_ptr(), 2 * F,
                 tgemm._act(kind), out.data_ptr(), 2 * F + 5)
     assert bool((out[:, 2 * F:] == 7).all())
     G, D = f64(gu), f64(dh)
@@ -407,7 +407,7 @@ def test_gated_writes_nothing_else():
         x, w = rows(M, K, 1), rows(2 * F, K, 2, 0.2)
         H = torch.full((M + 1, F + 7), 3.0, dtype=BF, device=dev())
         GU = torch.full((M + 1, 2 * F + 9), 4.0, dtype=BF, device=dev())
-        tgemm._call("tgemm_run_gated", tgemm._flag("N"), tgemm._flag("T"), M, F, K, x.data_ptr(), K,
+        tgemm._call("tgemm_run_gated", dev(), tgemm._flag("N"), tgemm._flag("T"), M, F, K, x.data_ptr(), K,
                     w.data_ptr(), K, 0, H.data_ptr(), F + 7, GU.data_ptr(), 2 * F + 9, None, -1)
         h, gu = tgemm.gated_matmul(x, w.t(), save=True)
         assert torch.equal(H[:M, :F], h) and torch.equal(GU[:M, : 2 * F], gu)
@@ -607,7 +607,7 @@ def test_backward_stays_inside(M, F, K, layout):
             w.data_ptr(), w.stride(0))
     need = tgemm.lib().tgemm_gated_backward_workspace_bytes(*prod)
     ws, dA, dB = Guarded(need), Guarded(2 * M * K), Guarded(8 * F * K)
-    tgemm._call("tgemm_run_gated_backward", *prod, dh.data_ptr(), F, gu.data_ptr(), 2 * F, 0,
+    tgemm._call("tgemm_run_gated_backward", dev(), *prod, dh.data_ptr(), F, gu.data_ptr(), 2 * F, 0,
                 dA.ptr(), K, dB.ptr(), w.shape[1], tgemm.EPI_STORE_F32, ws.ptr(), need)
     torch.cuda.synchronize()
     assert ws.intact() and dA.intact() and dB.intact()
@@ -629,10 +629,10 @@ def test_i8_stays_inside(M, N, K, layout, gated):
     need = (L.tgemm_gated_i8_workspace_bytes if gated else L.tgemm_i8_workspace_bytes)(*prod)
     ws, C = Guarded(need), Guarded(2 * M * N if gated else 4 * M * N)
     if gated:
-        tgemm._call("tgemm_run_gated_i8", *prod, sa.data_ptr(), sb.data_ptr(), 0, C.ptr(), N,
+        tgemm._call("tgemm_run_gated_i8", dev(), *prod, sa.data_ptr(), sb.data_ptr(), 0, C.ptr(), N,
                     ws.ptr(), need)
     else:
-        tgemm._call("tgemm_run_i8", *prod, sa.data_ptr(), sb.data_ptr(), C.ptr(), N,
+        tgemm._call("tgemm_run_i8", dev(), *prod, sa.data_ptr(), sb.data_ptr(), C.ptr(), N,
                     tgemm.EPI_STORE_F32, ws.ptr(), need)
     torch.cuda.synchronize()
     assert ws.intact() and C.intact()
@@ -649,7 +649,7 @@ def test_gated_stays_inside(M, F, K, layout):
             w.data_ptr(), w.stride(0))
     need = tgemm.lib().tgemm_gated_workspace_bytes(*prod)
     ws, H, GU = Guarded(need), Guarded(2 * M * F), Guarded(4 * M * F)
-    tgemm._call("tgemm_run_gated", *prod, 0, H.ptr(), F, GU.ptr(), 2 * F, ws.ptr(), need)
+    tgemm._call("tgemm_run_gated", dev(), *prod, 0, H.ptr(), F, GU.ptr(), 2 * F, ws.ptr(), need)
     torch.cuda.synchronize()
     assert ws.intact() and H.intact() and GU.intact()
 
@@ -659,10 +659,10 @@ def test_rows_stay_inside(M, K):
     print(f"rows guarded {M}x{K}", flush=True)
     x, r, w = rows(M, K, 1), rows(M, K, 2), rows(1, K, 3)
     q, s, h = Guarded(M * K), Guarded(4 * M), Guarded(2 * M * K)
-    tgemm._call("tgemm_quantize_i8", x.data_ptr(), K, M, K, q.ptr(), K, s.ptr())
+    tgemm._call("tgemm_quantize_i8", dev(), x.data_ptr(), K, M, K, q.ptr(), K, s.ptr())
     torch.cuda.synchronize()
     assert q.intact() and s.intact()
-    tgemm._call("tgemm_rms_norm_i8", x.data_ptr(), K, r.data_ptr(), K, w.data_ptr(), 1e-6, M, K,
+    tgemm._call("tgemm_rms_norm_i8", dev(), x.data_ptr(), K, r.data_ptr(), K, w.data_ptr(), 1e-6, M, K,
                 h.ptr(), K, q.ptr(), K, s.ptr())
     torch.cuda.synchronize()
     assert q.intact() and s.intact() and h.intact()
