@@ -547,6 +547,22 @@ def test_served_block_replays(M, D, F):
     replay(lambda: block(*args), lambda: args[0].mul_(-0.5))
 
 
+@pytest.mark.parametrize("M,F,K", [(96, 200, 264), (300, 130, 520)])
+def test_training_step_replays(M, F, K):
+    x, w, dh = rows(M, K, 1), rows(2 * F, K, 2, 0.05), rows(M, F, 3)
+
+    def step():
+        h, gu = tgemm.gated_matmul(x, w.t(), save=True)
+        dx, dw = tgemm.gated_backward(dh, gu, x, w.t())
+        return h, gu, dx, dw
+
+    def change():
+        x.mul_(-0.5)
+        dh.mul_(2.0)
+
+    replay(step, change)
+
+
 def test_workspace_contract():
     """The library's own workspace is refused under capture, a caller's that
     is too small always; nothing is written by a refused call, and the
