@@ -113,7 +113,9 @@ typedef enum {
   TGEMM_ERR_HIP = -3,         /* the HIP runtime reported an error while enqueueing   */
   TGEMM_ERR_NO_MEMORY = -4,   /* a CE or split-K workspace could not be allocated     */
   TGEMM_ERR_WORKSPACE_LIMIT = -5 /* tgemm_run_noalloc: the call needs more scratch than
-                                    its fixed buffer holds (tgemm_noalloc_scratch_bytes) */
+                                    its fixed buffer holds (tgemm_noalloc_scratch_bytes);
+                                    feed-forward calls: more than the caller's workspace
+                                    holds, or any under graph capture without one */
 } tgemm_status;
 
 typedef enum {
@@ -432,9 +434,8 @@ TGEMM_API int tgemm_validate_i8(char transA, char transB, int64_t M, int64_t N, 
  *   [g | u] = op(A) . op(B)   op(B) is [K, 2F]: columns 0 .. F-1 give g,
  *                             F .. 2F-1 give u (fp32 sums)
  *   H       = bf16(act(g) * u)                              [M, F]
- * g and u are not written unless GU is given: bf16 [M, 2F] (row stride ldgu
- * >= 2F), g in the first F columns and u in the last, for tgemm_gated_grad.
- * H is computed from the fp32 sums either way.
+ * g and u are not written unless GU is given: fp32 [M, 2F] (row stride ldgu
+ * >= 2F), g in the first F columns and u in the last, for the backward call.
  *
  * A 'N' and B 'T' with 16-byte aligned bases and lda, ldb and K multiples of
  * 8 are read in place; other operands are first copied, K-contiguous, into
@@ -442,7 +443,7 @@ TGEMM_API int tgemm_validate_i8(char transA, char transB, int64_t M, int64_t N, 
  */
 TGEMM_API int tgemm_run_gated(char transA, char transB, int64_t M, int64_t F, int64_t K,
                               const void* A, int64_t lda, const void* B, int64_t ldb,
-                              int activation, void* H, int64_t ldh, void* GU, int64_t ldgu,
+                              int activation, void* H, int64_t ldh, float* GU, int64_t ldgu,
                               void* workspace, int64_t workspace_bytes, void* stream);
 TGEMM_API int64_t tgemm_gated_workspace_bytes(char transA, char transB, int64_t M, int64_t F,
                                               int64_t K, const void* A, int64_t lda,
@@ -451,7 +452,7 @@ TGEMM_API int64_t tgemm_gated_workspace_bytes(char transA, char transB, int64_t 
 /* Host-only argument check of tgemm_run_gated (no GPU access). */
 TGEMM_API int tgemm_validate_gated(char transA, char transB, int64_t M, int64_t F, int64_t K,
                                    const void* A, int64_t lda, const void* B, int64_t ldb,
-                                   int activation, const void* H, int64_t ldh, const void* GU,
+                                   int activation, const void* H, int64_t ldh, const float* GU,
                                    int64_t ldgu);
 
 /*
@@ -476,16 +477,18 @@ TGEMM_API int tgemm_validate_gated_i8(char transA, char transB, int64_t M, int64
 /*
  * Gradient of H = act(g) * u with respect to g and u:
  *   dGU[:, :F] = bf16(dH * u * act'(g)),  dGU[:, F:] = bf16(dH * act(g))
- * dH bf16 [M, F], GU bf16 [M, 2F] as tgemm_run_gated left it, dGU bf16
- * [M, 2F].  No workspace.
+ * dH bf16 [M, F], dGU bf16 [M, 2F].  GU [M, 2F] as tgemm_run_gated left it
+ * (gu_type TGEMM_EPI_STORE_F32), or rounded to bf16 since
+ * (TGEMM_EPI_STORE_BF16: half the memory, and a rounding more in the
+ * gradients).  No workspace.
  */
 TGEMM_API int tgemm_gated_grad(int64_t M, int64_t F, const void* dH, int64_t lddh, const void* GU,
-                               int64_t ldgu, int activation, void* dGU, int64_t lddgu,
+                               int64_t ldgu, int gu_type, int activation, void* dGU, int64_t lddgu,
                                void* stream);
 
 /* Host-only argument check of tgemm_gated_grad (no GPU access). */
 TGEMM_API int tgemm_validate_gated_grad(int64_t M, int64_t F, const void* dH, int64_t lddh,
-                                        const void* GU, int64_t ldgu, int activation,
+                                        const void* GU, int64_t ldgu, int gu_type, int activation,
                                         const void* dGU, int64_t lddgu);
 
 /*
@@ -496,8 +499,8 @@ TGEMM_API int tgemm_validate_gated_grad(int64_t M, int64_t F, const void* dH, in
  *                         lddb >= K), [K, 2F] for 'N' (lddb >= 2F); bf16
  *                         (epilogue TGEMM_EPI_STORE_BF16) or fp32
  *                         (TGEMM_EPI_STORE_F32)
- * with fp32 sums.  A, B as in the forward call, dH bf16 [M, F], GU as the
- * forward call left it.  Both products run in one launch.  Workspace: dGU
+ * with fp32 sums.  A, B as in the forward call, dH bf16 [M, F], GU and gu_type
+ * as for tgemm_gated_grad.  Both products run in one launch.  Workspace: dGU
  * (about 4 * M * F bytes), copies of operands other than A 'N' and B 'T' with
  * 16-byte aligned bases and lda, ldb multiples of 8 (and of A for transB
  * 'N'), and for few tiles fp32 partial products.  K and 2F up to about 2^23.
@@ -505,7 +508,7 @@ TGEMM_API int tgemm_validate_gated_grad(int64_t M, int64_t F, const void* dH, in
 TGEMM_API int tgemm_run_gated_backward(char transA, char transB, int64_t M, int64_t F, int64_t K,
                                        const void* A, int64_t lda, const void* B, int64_t ldb,
                                        const void* dH, int64_t lddh, const void* GU, int64_t ldgu,
-                                       int activation, void* dA, int64_t ldda, void* dB,
+                                       int gu_type, int activation, void* dA, int64_t ldda, void* dB,
                                        int64_t lddb, int epilogue, void* workspace,
                                        int64_t workspace_bytes, void* stream);
 TGEMM_API int64_t tgemm_gated_backward_workspace_bytes(char transA, char transB, int64_t M,
@@ -516,8 +519,8 @@ TGEMM_API int64_t tgemm_gated_backward_workspace_bytes(char transA, char transB,
 TGEMM_API int tgemm_validate_gated_backward(char transA, char transB, int64_t M, int64_t F,
                                             int64_t K, const void* A, int64_t lda, const void* B,
                                             int64_t ldb, const void* dH, int64_t lddh,
-                                            const void* GU, int64_t ldgu, int activation,
-                                            const void* dA, int64_t ldda, const void* dB,
+                                            const void* GU, int64_t ldgu, int gu_type,
+                                            int activation, const void* dA, int64_t ldda, const void* dB,
                                             int64_t lddb, int epilogue);
 
 /* Human-readable name of a status code (static string, never NULL). */

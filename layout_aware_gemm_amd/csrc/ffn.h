@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "bf16_cvt.h"
 #include "tgemm_internal.h"
 
 namespace tgemm {
@@ -17,10 +18,18 @@ enum RowsType : int { kRowsI8 = 0, kRowsBf16 = 1 };
 //   kRowsStoreBf16 / F32  C[m][n] = sum * scale_a[m] * scale_b[n]   (int8)
 //   kRowsGated            C[m][f] = bf16(act(g) * u), g = column f of the
 //                         product, u = column F + f (int8: after the
-//                         scales; bf16: optionally g, u kept as bf16)
+//                         scales; bf16: optionally g, u kept)
 //   kRowsPart             the raw sums (int32 or fp32) of one K chunk, into
 //                         slice `chunk` of the partial buffer [split][M][N]
-enum RowsEpi : int { kRowsStoreBf16 = 0, kRowsStoreF32 = 1, kRowsGated = 2, kRowsPart = 3 };
+//   kRowsGatedKeep        kRowsGated of bf16 operands with g, u kept (chosen by
+//                         the tiled kernel's launcher when gu is set)
+enum RowsEpi : int {
+  kRowsStoreBf16 = 0,
+  kRowsStoreF32 = 1,
+  kRowsGated = 2,
+  kRowsPart = 3,
+  kRowsGatedKeep = 4
+};
 
 // A product of two row-major, K-contiguous operands: A [M][K], B [N][K]
 // (gated: N = 2F, rows 0..F-1 the gate, F..2F-1 the up projection).  Row
@@ -37,7 +46,7 @@ struct RowsParams {
   const float* scale_b;  // int8: [N]
   void* C;
   int64_t ldc;       // elements
-  uint16_t* gu;      // bf16 gated: optional [M][ldgu], g then u
+  float* gu;         // bf16 gated: optional [M][ldgu], g then u
   int64_t ldgu;
   void* part;        // kRowsPart: [split][M][N] int32 / fp32
   int tilesM, tilesN, groupM;
@@ -83,9 +92,9 @@ hipError_t launch_pack_rows(const PackRows& p, int elem, hipStream_t s);
 
 // dgu = [dh * u * act'(g) | dh * act(g)]; columns 2F .. cols - 1 and rows M
 // .. rows - 1 of dgu are set to zero (rows_finish.hip).
-hipError_t launch_gated_grad(const uint16_t* dh, int64_t lddh, const uint16_t* gu, int64_t ldgu,
-                             int M, int64_t F, int act, uint16_t* dgu, int64_t lddgu, int rows,
-                             int64_t cols, hipStream_t s);
+hipError_t launch_gated_grad(const uint16_t* dh, int64_t lddh, const void* gu, int64_t ldgu,
+                             bool gu_f32, int M, int64_t F, int act, uint16_t* dgu, int64_t lddgu,
+                             int rows, int64_t cols, hipStream_t s);
 
 // dX = G . W (px: A = G [M][K], B = W) and dW = G^T . X (pw: A = G stored
 // [K][M], B = X), both bf16, in one launch (gated_bwd.hip).  M, N, A, B, C,
@@ -155,8 +164,9 @@ struct __attribute__((packed, aligned(2))) u16x8_any {
 struct __attribute__((packed, aligned(2))) u16x4_any {
   uint32_t w[2];
 };
-struct __attribute__((packed, aligned(4))) f32x4_any {
-  float v[4];
+template <class T>
+struct __attribute__((packed, aligned(4))) x4_any {
+  T v[4];
 };
 struct __attribute__((packed, aligned(1))) b16_any {
   uint32_t w[4];
@@ -164,5 +174,23 @@ struct __attribute__((packed, aligned(1))) b16_any {
 struct __attribute__((packed, aligned(1))) u8x8_any {
   uint32_t w[2];
 };
+
+// n (1 to 4) consecutive values as bf16, fp32 or int32, at any element
+// alignment.
+__device__ __forceinline__ void put4(uint16_t* o, const float* v, int n) {
+  if (n >= 4) {
+    *reinterpret_cast<u16x4_any*>(o) = u16x4_any{{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}};
+  } else {
+    for (int i = 0; i < n; ++i) o[i] = to_bf16(v[i]);
+  }
+}
+template <class T>
+__device__ __forceinline__ void put4(T* o, const T* v, int n) {
+  if (n >= 4) {
+    *reinterpret_cast<x4_any<T>*>(o) = x4_any<T>{{v[0], v[1], v[2], v[3]}};
+  } else {
+    for (int i = 0; i < n; ++i) o[i] = v[i];
+  }
+}
 
 }  // namespace tgemm

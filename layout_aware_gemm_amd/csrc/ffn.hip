@@ -80,8 +80,9 @@ RowsPlan plan_rows(RowsParams* p, bool gate) {
 }
 
 bool grid_fits(const RowsParams& p, const RowsPlan& r, bool gate) {
-  const int64_t tiles = r.skinny ? ceil_div(gate ? p.F : p.N, 16) : (int64_t)p.tilesM * p.tilesN;
-  return tiles * p.split <= kMaxWorkgroups;
+  // (the few-row kernel: at most one workgroup of 512 threads per 16 outputs)
+  if (r.skinny) return ceil_div(gate ? p.F : p.N, 16) <= kMaxWorkgroups / 2;
+  return (int64_t)p.tilesM * p.tilesN * p.split <= kMaxWorkgroups;
 }
 
 hipError_t launch_rows(int type, const RowsParams& p, const RowsPlan& r, int epi, bool gate,
@@ -187,7 +188,7 @@ inline int64_t round_up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 // and re-read the whole fp32 [M][2F] product instead, and runs rows off
 // 16-byte boundaries at a third of the rate.)
 int run_gated(char ta, char tb, int64_t M, int64_t F, int64_t K, const void* A, int64_t lda,
-              const void* B, int64_t ldb, int act, void* H, int64_t ldh, void* GU, int64_t ldgu,
+              const void* B, int64_t ldb, int act, void* H, int64_t ldh, float* GU, int64_t ldgu,
               const CallSpace& space, hipStream_t s) {
   RowsParams p = {};
   p.M = (int)M;
@@ -196,7 +197,7 @@ int run_gated(char ta, char tb, int64_t M, int64_t F, int64_t K, const void* A, 
   p.act = act;
   p.C = H;
   p.ldc = ldh;
-  p.gu = static_cast<uint16_t*>(GU);
+  p.gu = GU;
   p.ldgu = ldgu;
   const int64_t Kp = round_up(K, 8);
   if (Kp >= int64_t(1) << 30) return TGEMM_ERR_UNSUPPORTED;
@@ -243,8 +244,8 @@ int run_gated(char ta, char tb, int64_t M, int64_t F, int64_t K, const void* A, 
 // then a zero-padded copy of A.
 int run_gated_backward(char ta, char tb, int64_t M, int64_t F, int64_t K, const void* A,
                        int64_t lda, const void* B, int64_t ldb, const void* dH, int64_t lddh,
-                       const void* GU, int64_t ldgu, int act, void* dA, int64_t ldda, void* dB,
-                       int64_t lddb, bool f32, const CallSpace& space, hipStream_t s) {
+                       const void* GU, int64_t ldgu, bool gu_f32, int act, void* dA, int64_t ldda,
+                       void* dB, int64_t lddb, bool f32, const CallSpace& space, hipStream_t s) {
   const int64_t N2 = 2 * F, Kp = round_up(K, 8);
   const int64_t ldg = round_up(N2, 64), rows = round_up(M, 64);
   constexpr int64_t kLimit = int64_t(1) << 23;  // (32-bit copy offsets)
@@ -284,9 +285,8 @@ int run_gated_backward(char ta, char tb, int64_t M, int64_t F, int64_t K, const 
   char* ws = static_cast<char*>(w.ptr);
   uint16_t* const G = reinterpret_cast<uint16_t*>(ws);
   ws += bytesG;
-  hipError_t e = launch_gated_grad(static_cast<const uint16_t*>(dH), lddh,
-                                   static_cast<const uint16_t*>(GU), ldgu, (int)M, F, act, G, ldg,
-                                   (int)rows, ldg, s);
+  hipError_t e = launch_gated_grad(static_cast<const uint16_t*>(dH), lddh, GU, ldgu, gu_f32, (int)M,
+                                   F, act, G, ldg, (int)rows, ldg, s);
   const void *Ar = A, *Br = B;  // [M][K], [2F][K] rows
   if (packA && e == hipSuccess) {
     e = launch_pack_rows({A, lda, is_n(ta), (int)M, (int)K, ws, (int)rows, Kp}, 2, s);
@@ -412,7 +412,7 @@ extern "C" int64_t tgemm_gated_i8_workspace_bytes(char transA, char transB, int6
 
 extern "C" int tgemm_run_gated(char transA, char transB, int64_t M, int64_t F, int64_t K,
                                const void* A, int64_t lda, const void* B, int64_t ldb,
-                               int activation, void* H, int64_t ldh, void* GU, int64_t ldgu,
+                               int activation, void* H, int64_t ldh, float* GU, int64_t ldgu,
                                void* workspace, int64_t workspace_bytes, void* stream) {
   const int st =
       tgemm_validate_gated(transA, transB, M, F, K, A, lda, B, ldb, activation, H, ldh, GU, ldgu);
@@ -438,14 +438,15 @@ extern "C" int64_t tgemm_gated_workspace_bytes(char transA, char transB, int64_t
 }
 
 extern "C" int tgemm_gated_grad(int64_t M, int64_t F, const void* dH, int64_t lddh, const void* GU,
-                                int64_t ldgu, int activation, void* dGU, int64_t lddgu,
-                                void* stream) {
-  const int st = tgemm_validate_gated_grad(M, F, dH, lddh, GU, ldgu, activation, dGU, lddgu);
+                                int64_t ldgu, int gu_type, int activation, void* dGU,
+                                int64_t lddgu, void* stream) {
+  const int st =
+      tgemm_validate_gated_grad(M, F, dH, lddh, GU, ldgu, gu_type, activation, dGU, lddgu);
   if (st != TGEMM_OK) return st;
   if (verbose())
     fprintf(stderr, "tgemm: gated grad M=%lld F=%lld\n", (long long)M, (long long)F);
-  return status_of(launch_gated_grad(static_cast<const uint16_t*>(dH), lddh,
-                                     static_cast<const uint16_t*>(GU), ldgu, (int)M, F, activation,
+  return status_of(launch_gated_grad(static_cast<const uint16_t*>(dH), lddh, GU, ldgu,
+                                     gu_type == TGEMM_EPI_STORE_F32, (int)M, F, activation,
                                      static_cast<uint16_t*>(dGU), lddgu, (int)M, 2 * F,
                                      reinterpret_cast<hipStream_t>(stream)));
 }
@@ -453,15 +454,16 @@ extern "C" int tgemm_gated_grad(int64_t M, int64_t F, const void* dH, int64_t ld
 extern "C" int tgemm_run_gated_backward(char transA, char transB, int64_t M, int64_t F, int64_t K,
                                         const void* A, int64_t lda, const void* B, int64_t ldb,
                                         const void* dH, int64_t lddh, const void* GU, int64_t ldgu,
-                                        int activation, void* dA, int64_t ldda, void* dB,
+                                        int gu_type, int activation, void* dA, int64_t ldda, void* dB,
                                         int64_t lddb, int epilogue, void* workspace,
                                         int64_t workspace_bytes, void* stream) {
   const int st = tgemm_validate_gated_backward(transA, transB, M, F, K, A, lda, B, ldb, dH, lddh,
-                                               GU, ldgu, activation, dA, ldda, dB, lddb, epilogue);
+                                               GU, ldgu, gu_type, activation, dA, ldda, dB, lddb,
+                                               epilogue);
   if (st != TGEMM_OK) return st;
   return no_throw([&] {
     return run_gated_backward(transA, transB, M, F, K, A, lda, B, ldb, dH, lddh, GU, ldgu,
-                              activation, dA, ldda, dB, lddb, epilogue == TGEMM_EPI_STORE_F32,
+                              gu_type == TGEMM_EPI_STORE_F32, activation, dA, ldda, dB, lddb, epilogue == TGEMM_EPI_STORE_F32,
                               {workspace, workspace_bytes, nullptr},
                               reinterpret_cast<hipStream_t>(stream));
   });
@@ -473,12 +475,13 @@ extern "C" int64_t tgemm_gated_backward_workspace_bytes(char transA, char transB
   const int64_t ldd = transB == 'N' || transB == 'n' ? 2 * F : K;
   const int st =
       tgemm_validate_gated_backward(transA, transB, M, F, K, A, lda, B, ldb, g_any, F, g_any, 2 * F,
-                                    TGEMM_ACT_SILU, g_any, K, g_any, ldd, TGEMM_EPI_STORE_BF16);
+                                    TGEMM_EPI_STORE_BF16, TGEMM_ACT_SILU, g_any, K, g_any, ldd, TGEMM_EPI_STORE_BF16);
   if (st != TGEMM_OK) return st;
   int64_t need = 0;
   return queried(no_throw([&] {
                    return run_gated_backward(transA, transB, M, F, K, A, lda, B, ldb, nullptr, F,
-                                             nullptr, 2 * F, 0, nullptr, K, nullptr, ldd, false,
+                                             nullptr, 2 * F, false, 0, nullptr, K, nullptr, ldd,
+                                             false,
                                              {nullptr, 0, &need}, nullptr);
                  }),
                  need);

@@ -39,8 +39,6 @@ __device__ __forceinline__ void store_block(const GemmParams& p, void* C, int64_
   const int h = lane >> 5, lc = lane & 31;
   const int c = col0 + 4 * lc;  // this lane's four columns on the way out
   const int n = p.N - c;        // of which so many exist
-  // (the base and the stride keep 4-element vectors aligned or not: the
-  // hardware takes either)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
 #pragma unroll
@@ -55,20 +53,10 @@ __device__ __forceinline__ void store_block(const GemmParams& p, void* C, int64_
       if (row >= p.M || n <= 0) continue;
       const float e[4] = {v.x, v.y, v.z, v.w};
       const int64_t off = (int64_t)row * ldc + c;
-      if (f32) {
-        float* const o = static_cast<float*>(C) + off;
-        if (n >= 4)
-          *reinterpret_cast<f32x4_any*>(o) = f32x4_any{{e[0], e[1], e[2], e[3]}};
-        else
-          for (int k = 0; k < n; ++k) o[k] = e[k];
-      } else {
-        uint16_t* const o = static_cast<uint16_t*>(C) + off;
-        if (n >= 4)
-          *reinterpret_cast<u16x4_any*>(o) =
-              u16x4_any{{pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3])}};
-        else
-          for (int k = 0; k < n; ++k) o[k] = to_bf16(e[k]);
-      }
+      if (f32)
+        put4(static_cast<float*>(C) + off, e, n);
+      else
+        put4(static_cast<uint16_t*>(C) + off, e, n);
     }
   }
 }

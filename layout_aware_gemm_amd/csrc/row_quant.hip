@@ -278,6 +278,9 @@ hipError_t launch_v(const RowQuantParams& p, hipStream_t s) {
 // norm's two inputs would not fit the registers of a full workgroup.
 hipError_t launch_row_quant(const RowQuantParams& p, hipStream_t s) {
   const int64_t chunks = (p.K + 7) / 8;
+  // (one workgroup per row, of at most 1024 threads: 2^32 - 1 in a launch)
+  const int64_t threads = chunks < 1024 ? (chunks + 63) / 64 * 64 : 1024;
+  if (p.M * threads >= (int64_t(1) << 32)) return hipErrorInvalidValue;
   const int64_t v = p.M < 512 ? (chunks + 1023) / 1024 : (chunks + 255) / 256;
   if (v <= 1) return launch_v<1>(p, s);
   if (v <= 2) return launch_v<2>(p, s);

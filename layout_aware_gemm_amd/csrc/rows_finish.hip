@@ -13,29 +13,6 @@ namespace {
 constexpr int kThr = 256;
 
 template <class T>
-struct __attribute__((packed, aligned(4))) x4_any {
-  T v[4];
-};
-
-// n (1 to 4) values as bf16 / fp32 at any element alignment.
-__device__ __forceinline__ void put4(uint16_t* o, const float* v, int n) {
-  if (n == 4) {
-    u16x4_any w;
-    w.w[0] = pack_bf16x2(v[0], v[1]);
-    w.w[1] = pack_bf16x2(v[2], v[3]);
-    *reinterpret_cast<u16x4_any*>(o) = w;
-  } else {
-    for (int i = 0; i < n; ++i) o[i] = to_bf16(v[i]);
-  }
-}
-__device__ __forceinline__ void put4(float* o, const float* v, int n) {
-  if (n == 4) {
-    *reinterpret_cast<x4_any<float>*>(o) = x4_any<float>{{v[0], v[1], v[2], v[3]}};
-  } else {
-    for (int i = 0; i < n; ++i) o[i] = v[i];
-  }
-}
-template <class T>
 __device__ __forceinline__ void add4(T* a, const T* p, int n) {
   if (n == 4) {
     const x4_any<T> t = *reinterpret_cast<const x4_any<T>*>(p);
@@ -86,7 +63,7 @@ __global__ void __launch_bounds__(kThr) finish_kernel(RowsParams p) {
     put4(static_cast<uint16_t*>(p.C) + o, h, n);
   if constexpr (GATE && !I8) {
     if (p.gu != nullptr) {
-      uint16_t* const w = p.gu + (int64_t)row * p.ldgu + c;
+      float* const w = p.gu + (int64_t)row * p.ldgu + c;
       put4(w, v, n);
       put4(w + p.F, u, n);
     }
@@ -150,30 +127,56 @@ __global__ void __launch_bounds__(kThr) pack_cols_kernel(PackRows p, int kblocks
   }
 }
 
-__device__ __forceinline__ void grad_pair(uint32_t dh, uint32_t g, uint32_t u, int act,
-                                          uint32_t& dg, uint32_t& du) {
-  float a[2], d[2], x[2], y[2];
-  act_value_grad(__uint_as_float(g << 16), act, a[0], d[0]);
-  act_value_grad(__uint_as_float(g & 0xffff0000u), act, a[1], d[1]);
-  const float h[2] = {__uint_as_float(dh << 16), __uint_as_float(dh & 0xffff0000u)};
-  const float v[2] = {__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)};
+// N consecutive values of a row of bf16 or fp32 (no alignment asked for).
+template <int N, class T>
+__device__ __forceinline__ void load_values(const T* p, float (&v)[N]) {
+  if constexpr (std::is_same<T, float>::value) {
+    if constexpr (N == 8) {
+      const x4_any<float> a = *reinterpret_cast<const x4_any<float>*>(p);
+      const x4_any<float> b = *reinterpret_cast<const x4_any<float>*>(p + 4);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    x[i] = h[i] * v[i] * d[i];
-    y[i] = h[i] * a[i];
+      for (int i = 0; i < 4; ++i) v[i] = a.v[i], v[4 + i] = b.v[i];
+    } else {
+      v[0] = p[0];
+    }
+  } else {
+    if constexpr (N == 8) {
+      const u16x8_any a = *reinterpret_cast<const u16x8_any*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(a.w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(a.w[i] & 0xffff0000u);
+      }
+    } else {
+      v[0] = from_bf16(p[0]);
+    }
   }
-  dg = pack_bf16x2(x[0], x[1]);
-  du = pack_bf16x2(y[0], y[1]);
 }
 
-// 8 outputs per thread; the arithmetic is fp32, dg and du are rounded once
-// to bf16, the type the gradient products read.  The padding (columns 2F ..
-// cols - 1, rows past M) is written by the threads whose chunk lies past F
-// and by the workgroups of rows past M.
+template <int N, class T>
+__device__ __forceinline__ void grad_values(const uint16_t* ph, const T* pg, int64_t F, int act,
+                                            float (&x)[N], float (&y)[N]) {
+  float h[N], g[N], u[N];
+  load_values<N>(ph, h);
+  load_values<N>(pg, g);
+  load_values<N>(pg + F, u);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float a, d;
+    act_value_grad(g[i], act, a, d);
+    x[i] = h[i] * u[i] * d;
+    y[i] = h[i] * a;
+  }
+}
+
+// 8 outputs per thread, T the type g and u were kept in; the arithmetic is
+// fp32, dg and du are rounded once to bf16, the type the gradient products
+// read.  The padding (columns 2F .. cols - 1, rows past M) is written by the
+// threads whose chunk lies past F and by the workgroups of rows past M.
+template <class T>
 __global__ void __launch_bounds__(kThr) gated_grad_kernel(
-    const uint16_t* __restrict__ dh, int64_t lddh, const uint16_t* __restrict__ gu, int64_t ldgu,
-    int M, int64_t F, int act, uint16_t* __restrict__ dgu, int64_t lddgu, int64_t cols,
-    int64_t per_row) {
+    const uint16_t* __restrict__ dh, int64_t lddh, const T* __restrict__ gu, int64_t ldgu, int M,
+    int64_t F, int act, uint16_t* __restrict__ dgu, int64_t lddgu, int64_t cols, int64_t per_row) {
   const int64_t row = blockIdx.x / per_row;
   const int64_t c = ((int64_t)(blockIdx.x % per_row) * kThr + threadIdx.x) * 8;
   uint16_t* const out = dgu + row * lddgu;
@@ -185,23 +188,25 @@ __global__ void __launch_bounds__(kThr) gated_grad_kernel(
   for (int64_t i = 2 * F + c; i < 2 * F + c + 8 && i < cols; ++i) out[i] = 0;
   if (c >= F) return;
   const uint16_t* ph = dh + row * lddh + c;
-  const uint16_t* pg = gu + row * ldgu + c;
+  const T* pg = gu + row * ldgu + c;
   uint16_t* po = out + c;
   if (c + 8 <= F) {
-    const u16x8_any h = *reinterpret_cast<const u16x8_any*>(ph);
-    const u16x8_any g = *reinterpret_cast<const u16x8_any*>(pg);
-    const u16x8_any u = *reinterpret_cast<const u16x8_any*>(pg + F);
-    u16x8_any x, y;
+    float x[8], y[8];
+    grad_values<8>(ph, pg, F, act, x, y);
+    u16x8_any ox, oy;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) grad_pair(h.w[i], g.w[i], u.w[i], act, x.w[i], y.w[i]);
-    *reinterpret_cast<u16x8_any*>(po) = x;
-    *reinterpret_cast<u16x8_any*>(po + F) = y;
+    for (int i = 0; i < 4; ++i) {
+      ox.w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+      oy.w[i] = pack_bf16x2(y[2 * i], y[2 * i + 1]);
+    }
+    *reinterpret_cast<u16x8_any*>(po) = ox;
+    *reinterpret_cast<u16x8_any*>(po + F) = oy;
   } else {
     for (int64_t i = 0; c + i < F; ++i) {
-      uint32_t x, y;
-      grad_pair(ph[i], pg[i], pg[F + i], act, x, y);
-      po[i] = (uint16_t)x;
-      po[F + i] = (uint16_t)y;
+      float x[1], y[1];
+      grad_values<1>(ph + i, pg + i, F, act, x, y);
+      po[i] = to_bf16(x[0]);
+      po[F + i] = to_bf16(y[0]);
     }
   }
 }
@@ -248,15 +253,21 @@ hipError_t launch_pack_rows(const PackRows& p, int elem, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_gated_grad(const uint16_t* dh, int64_t lddh, const uint16_t* gu, int64_t ldgu,
-                             int M, int64_t F, int act, uint16_t* dgu, int64_t lddgu, int rows,
-                             int64_t cols, hipStream_t s) {
+hipError_t launch_gated_grad(const uint16_t* dh, int64_t lddh, const void* gu, int64_t ldgu,
+                             bool gu_f32, int M, int64_t F, int act, uint16_t* dgu, int64_t lddgu,
+                             int rows, int64_t cols, hipStream_t s) {
   // (the padding of a row, cols - 2F < 64 elements, needs at most 8 threads)
   const int64_t chunks = (F + 7) / 8 > 8 ? (F + 7) / 8 : 8;
   const int64_t per_row = (chunks + kThr - 1) / kThr;
   if (rows * per_row > kMaxWorkgroups) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(gated_grad_kernel, dim3((unsigned)(rows * per_row)), dim3(kThr), 0, s, dh,
-                     lddh, gu, ldgu, M, F, act, dgu, lddgu, cols, per_row);
+  const dim3 grid((unsigned)(rows * per_row));
+  if (gu_f32)
+    hipLaunchKernelGGL(gated_grad_kernel<float>, grid, dim3(kThr), 0, s, dh, lddh,
+                       static_cast<const float*>(gu), ldgu, M, F, act, dgu, lddgu, cols, per_row);
+  else
+    hipLaunchKernelGGL(gated_grad_kernel<uint16_t>, grid, dim3(kThr), 0, s, dh, lddh,
+                       static_cast<const uint16_t*>(gu), ldgu, M, F, act, dgu, lddgu, cols,
+                       per_row);
   return hipGetLastError();
 }
 

@@ -206,9 +206,11 @@ __device__ __forceinline__ void ring_rows_substep(typename Op::acc (&acc)[FM][FN
 }
 
 // Lane l, register r of accumulator block (i, j) is row 8*(r/4) + 4*(l/32)
-// + r%4 and column l%32 of the block.  scl: the tile's scales in LDS (loaded
-// at the kernel's start, one per thread: fetched from memory between the
-// stores they cost 28 us per 256x256 tile, half of a K = 4096 main loop).
+// + r%4 and column l%32 of the block.  Stored from registers: through LDS, in
+// vectors of four, the 256x256 tile took 3 to 10% longer (8192^3 int8 449
+// against 428 us).  scl: the tile's scales in LDS (loaded at the kernel's
+// start, one per thread: fetched from memory between the stores they cost 28
+// us per 256x256 tile, half of a K = 4096 main loop).
 template <class Op, int BM, int BN, bool GATE, int EPI, bool FULL>
 __device__ __forceinline__ void rows_epilogue(const RowsParams& p,
                                               typename Op::acc (&acc)[BM / 64][BN / 64],
@@ -261,13 +263,6 @@ __device__ __forceinline__ void rows_epilogue(const RowsParams& p,
             }
             if (!FULL && c >= nout) continue;
             o[c] = to_bf16(act_value(g, p.act) * u);
-            if constexpr (!I8) {
-              if (p.gu != nullptr) {
-                uint16_t* const w = p.gu + (int64_t)row * p.ldgu;
-                w[c] = to_bf16(g);
-                w[p.F + c] = to_bf16(u);
-              }
-            }
           }
         } else {
 #pragma unroll
@@ -283,6 +278,55 @@ __device__ __forceinline__ void rows_epilogue(const RowsParams& p,
         }
       }
     }
+}
+
+// Words per row of a wave's 32-row buffer below: with 8 words of padding the
+// two halves of a wave, which write four rows apart, use different halves of
+// the banks.
+template <int BN>
+constexpr int keep_row() {
+  return BN / 2 + 8;
+}
+
+// The gated epilogue of bf16 operands that also keeps g and u, 32 rows at a
+// time through LDS words of the wave's own (st): each accumulator is used in
+// one place, where three outputs from registers ran the 256x256 tile out of
+// them, and the three rows leave in vectors of four.
+template <int BM, int BN>
+__device__ __forceinline__ void keep_epilogue(const RowsParams& p,
+                                              const f32x16_t (&acc)[BM / 64][BN / 64], float* st,
+                                              int row0, int n0, int wn, int lane) {
+  constexpr int FM = BM / 64, FN = BN / 64, LD = keep_row<BN>();
+  constexpr int NO = BN / 4;                   // outputs per row of the wave's block
+  constexpr int LPR = NO / 4, RPI = 64 / LPR;  // lanes per row, rows per pass
+  const int h = lane >> 5, lc = lane & 31;
+  const int o = (lane % LPR) * 4;              // this lane's four outputs on the way out
+  const int rc = (o >> 5) * 64 + (o & 31);     // their gates' columns; u is 32 behind
+  const int c = n0 + wn * NO + o;
+  const int n = p.F - c;                       // of which so many exist
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        st[(8 * (r >> 2) + 4 * h + (r & 3)) * LD + j * 32 + lc] = acc[i][j][r];
+#pragma unroll
+    for (int q = 0; q < 32 / RPI; ++q) {
+      const int rl = q * RPI + lane / LPR, row = row0 + i * 32 + rl;
+      const float4 a = *reinterpret_cast<const float4*>(st + rl * LD + rc);
+      const float4 b = *reinterpret_cast<const float4*>(st + rl * LD + rc + 32);
+      if (row >= p.M || n <= 0) continue;
+      const float g[4] = {a.x, a.y, a.z, a.w}, u[4] = {b.x, b.y, b.z, b.w};
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = act_value(g[e], p.act) * u[e];
+      put4(static_cast<uint16_t*>(p.C) + (int64_t)row * p.ldc + c, v, n);
+      float* const w = p.gu + (int64_t)row * p.ldgu + c;
+      put4(w, g, n);
+      put4(w + p.F, u, n);
+    }
+  }
 }
 
 template <class Op, int BM, int BN, bool GATE, int EPI>
@@ -444,18 +488,25 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(RowsParams p) {
   // the trailing re-reads must land before the LDS is reused or released
   wait_dma();
   __syncthreads();
-  float* const scl = reinterpret_cast<float*>(lds);  // BM row scales, BN column scales
-  if constexpr (SCALED) {
-    if ((int)threadIdx.x < BM) scl[threadIdx.x] = sa_t;
-    if ((int)threadIdx.x < BN) scl[BM + threadIdx.x] = sb_t;
-    __syncthreads();
+  if constexpr (EPI == kRowsGatedKeep) {
+    constexpr int kWave = 32 * keep_row<BN>();
+    static_assert(4 * kWave * 4 <= (int)sizeof(lds), "the waves' buffers fit");
+    keep_epilogue<BM, BN>(p, acc, reinterpret_cast<float*>(lds) + wave_u * kWave,
+                          m0 + wm * (BM / 2), n0, wn, lane);
+  } else {
+    float* const scl = reinterpret_cast<float*>(lds);  // BM row scales, BN column scales
+    if constexpr (SCALED) {
+      if ((int)threadIdx.x < BM) scl[threadIdx.x] = sa_t;
+      if ((int)threadIdx.x < BN) scl[BM + threadIdx.x] = sb_t;
+      __syncthreads();
+    }
+    // A wave whose whole block lies inside the output stores without tests.
+    const bool full = m0 + BM <= p.M && n0 + NT <= (GATE ? p.F : p.N);
+    if (full)
+      rows_epilogue<Op, BM, BN, GATE, EPI, true>(p, acc, scl, m0, n0, wm, wn, lane, ks);
+    else
+      rows_epilogue<Op, BM, BN, GATE, EPI, false>(p, acc, scl, m0, n0, wm, wn, lane, ks);
   }
-  // A wave whose whole block lies inside the output stores without tests.
-  const bool full = m0 + BM <= p.M && n0 + NT <= (GATE ? p.F : p.N);
-  if (full)
-    rows_epilogue<Op, BM, BN, GATE, EPI, true>(p, acc, scl, m0, n0, wm, wn, lane, ks);
-  else
-    rows_epilogue<Op, BM, BN, GATE, EPI, false>(p, acc, scl, m0, n0, wm, wn, lane, ks);
 }
 
 template <class Op, int BM, int BN, bool GATE, int EPI>
@@ -474,6 +525,8 @@ hipError_t launch_tile(int type, int epi, bool gate, const RowsParams& p, hipStr
     if (!gate && epi == kRowsStoreF32) return launch_one<OpI8, BM, BN, false, kRowsStoreF32>(p, s);
     if (!gate && epi == kRowsPart) return launch_one<OpI8, BM, BN, false, kRowsPart>(p, s);
   } else if (gate) {
+    if (epi == kRowsGated && p.gu != nullptr)
+      return launch_one<OpBf16, BM, BN, true, kRowsGatedKeep>(p, s);
     if (epi == kRowsGated) return launch_one<OpBf16, BM, BN, true, kRowsGated>(p, s);
     if (epi == kRowsPart) return launch_one<OpBf16, BM, BN, true, kRowsPart>(p, s);
   }

@@ -175,30 +175,32 @@ __global__ void __launch_bounds__(W * 64) skinny_kernel(RowsParams p) {
 #pragma unroll
       for (int w = 1; w < W; ++w) a2 += red[w * RED + (m * NB + NO + b) * 64 + l];
     }
+    const int n = min(4, nout - c0);
+    if (n <= 0) continue;
+    float v[4], g[4], u[4];
+    const float sa = I8 ? p.scale_a[row] : 1.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int c = c0 + e;
-      if (c >= nout) continue;
+      const int c = min(c0 + e, nout - 1);
+      v[e] = (float)a[e];
+      if constexpr (I8) v[e] = v[e] * sa * p.scale_b[c];
       if constexpr (GATE) {
-        float gv = (float)a[e], uv = (float)a2[e];
-        if constexpr (I8) {
-          const float sa = p.scale_a[row];
-          gv = gv * sa * p.scale_b[c];
-          uv = uv * sa * p.scale_b[p.F + c];
-        }
-        static_cast<uint16_t*>(p.C)[(int64_t)row * p.ldc + c] = to_bf16(act_value(gv, p.act) * uv);
-        if constexpr (!I8) {
-          if (p.gu != nullptr) {
-            p.gu[(int64_t)row * p.ldgu + c] = to_bf16(gv);
-            p.gu[(int64_t)row * p.ldgu + p.F + c] = to_bf16(uv);
-          }
-        }
-      } else {
-        const float v = (float)a[e] * p.scale_a[row] * p.scale_b[c];
-        if constexpr (EPI == kRowsStoreBf16)
-          static_cast<uint16_t*>(p.C)[(int64_t)row * p.ldc + c] = to_bf16(v);
-        else
-          static_cast<float*>(p.C)[(int64_t)row * p.ldc + c] = v;
+        g[e] = v[e];
+        u[e] = (float)a2[e];
+        if constexpr (I8) u[e] = u[e] * sa * p.scale_b[p.F + c];
+        v[e] = act_value(g[e], p.act) * u[e];
+      }
+    }
+    const int64_t o = (int64_t)row * p.ldc + c0;
+    if constexpr (EPI == kRowsStoreF32)
+      put4(static_cast<float*>(p.C) + o, v, n);
+    else
+      put4(static_cast<uint16_t*>(p.C) + o, v, n);
+    if constexpr (GATE && !I8) {
+      if (p.gu != nullptr) {
+        float* const w = p.gu + (int64_t)row * p.ldgu + c0;
+        put4(w, g, n);
+        put4(w + p.F, u, n);
       }
     }
   }
@@ -213,12 +215,12 @@ hipError_t launch_one(const RowsParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <class Op, int NB, int W, bool GATE, int EPI>
-hipError_t launch_nb(const RowsParams& p, hipStream_t s) {
-  if (p.M <= 8) return launch_one<Op, 1, NB, W, GATE, EPI>(p, s);
-  if (p.M <= 16) return launch_one<Op, 2, NB, W, GATE, EPI>(p, s);
-  if (p.M <= 32) return launch_one<Op, 4, NB, W, GATE, EPI>(p, s);
-  return launch_one<Op, 8, NB, W, GATE, EPI>(p, s);
+// up to 32 tokens
+template <class Op, int NB, bool GATE, int EPI>
+hipError_t launch_few(const RowsParams& p, hipStream_t s) {
+  if (p.M <= 8) return launch_one<Op, 1, NB, 8, GATE, EPI>(p, s);
+  if (p.M <= 16) return launch_one<Op, 2, NB, 8, GATE, EPI>(p, s);
+  return launch_one<Op, 4, NB, 8, GATE, EPI>(p, s);
 }
 
 // Blocks of weight rows per wave and waves per workgroup, by the number of
@@ -238,8 +240,10 @@ template <class Op, bool GATE, int EPI>
 hipError_t launch_blocks(const RowsParams& p, hipStream_t s) {
   constexpr int NB = GATE ? 4 : 2;
   const int nout = GATE ? p.F : p.N;
-  if (ceil_div(nout, 32) < 128) return launch_nb<Op, NB / 2, 8, GATE, EPI>(p, s);
-  if (p.M <= 32) return launch_nb<Op, NB, 8, GATE, EPI>(p, s);
+  const bool small = ceil_div(nout, 32) < 128;
+  if (p.M <= 32)
+    return small ? launch_few<Op, NB / 2, GATE, EPI>(p, s) : launch_few<Op, NB, GATE, EPI>(p, s);
+  if (small) return launch_one<Op, 8, NB / 2, 8, GATE, EPI>(p, s);
   if constexpr (!GATE) {
     if (ceil_div(nout, 64) >= 256) return launch_one<Op, 8, 4, 4, GATE, EPI>(p, s);
   }

@@ -91,11 +91,18 @@ namespace {
 // Products summed in int32: K codes of magnitude at most 128 each.
 constexpr int64_t kMaxK8 = 131071;
 
+// Rows of op(A) and columns of op(B) of the feed-forward products: their
+// tiles' last rows are still 32-bit numbers.
+constexpr int64_t kMaxRows = kMaxDim - 4096;
+
 // rows x cols elements with row stride ld, and offsets that fit 64 bits
 inline int check_rows(const void* p, int64_t rows, int64_t cols, int64_t ld) {
   if (p == nullptr || ld < cols) return TGEMM_ERR_INVALID_ARG;
   return ld > INT64_MAX / 4 / rows ? TGEMM_ERR_UNSUPPORTED : TGEMM_OK;
 }
+
+// the types of kept gate and up values
+inline bool type_ok(int t) { return t == TGEMM_EPI_STORE_BF16 || t == TGEMM_EPI_STORE_F32; }
 
 inline bool act_ok(int a) { return a == TGEMM_ACT_SILU || a == TGEMM_ACT_GELU_TANH; }
 
@@ -111,12 +118,12 @@ extern "C" int tgemm_validate_i8(char transA, char transB, int64_t M, int64_t N,
   const int st = tgemm_validate(transA, transB, M, N, K, A, lda, B, ldb, C, ldc, epilogue, nullptr,
                                 nullptr, nullptr);
   if (st != TGEMM_OK) return st;
-  return K > kMaxK8 ? TGEMM_ERR_UNSUPPORTED : TGEMM_OK;
+  return K > kMaxK8 || M > kMaxRows || N > kMaxRows ? TGEMM_ERR_UNSUPPORTED : TGEMM_OK;
 }
 
 extern "C" int tgemm_validate_gated(char transA, char transB, int64_t M, int64_t F, int64_t K,
                                     const void* A, int64_t lda, const void* B, int64_t ldb,
-                                    int activation, const void* H, int64_t ldh, const void* GU,
+                                    int activation, const void* H, int64_t ldh, const float* GU,
                                     int64_t ldgu) {
   if (!act_ok(activation)) return TGEMM_ERR_INVALID_ARG;
   if (F > kMaxDim / 2) return TGEMM_ERR_UNSUPPORTED;
@@ -125,7 +132,8 @@ extern "C" int tgemm_validate_gated(char transA, char transB, int64_t M, int64_t
   const int st = tgemm_validate(transA, transB, M, 2 * F, K, A, lda, B, ldb, H, 2 * F,
                                 TGEMM_EPI_STORE_BF16, nullptr, nullptr, nullptr);
   if (st != TGEMM_OK) return st;
-  if (check_rows(H, M, F, ldh) != TGEMM_OK) return TGEMM_ERR_UNSUPPORTED;
+  if (M > kMaxRows || 2 * F > kMaxRows || check_rows(H, M, F, ldh) != TGEMM_OK)
+    return TGEMM_ERR_UNSUPPORTED;
   return GU == nullptr ? TGEMM_OK : check_rows(GU, M, 2 * F, ldgu);
 }
 
@@ -141,10 +149,10 @@ extern "C" int tgemm_validate_gated_i8(char transA, char transB, int64_t M, int6
 }
 
 extern "C" int tgemm_validate_gated_grad(int64_t M, int64_t F, const void* dH, int64_t lddh,
-                                         const void* GU, int64_t ldgu, int activation,
+                                         const void* GU, int64_t ldgu, int gu_type, int activation,
                                          const void* dGU, int64_t lddgu) {
-  if (!act_ok(activation) || M < 1 || F < 1) return TGEMM_ERR_INVALID_ARG;
-  if (M > kMaxDim || F > kMaxDim / 2) return TGEMM_ERR_UNSUPPORTED;
+  if (!act_ok(activation) || !type_ok(gu_type) || M < 1 || F < 1) return TGEMM_ERR_INVALID_ARG;
+  if (M > kMaxRows || F > kMaxRows / 2) return TGEMM_ERR_UNSUPPORTED;
   int st = check_rows(dH, M, F, lddh);
   if (st == TGEMM_OK) st = check_rows(GU, M, 2 * F, ldgu);
   if (st == TGEMM_OK) st = check_rows(dGU, M, 2 * F, lddgu);
@@ -154,19 +162,18 @@ extern "C" int tgemm_validate_gated_grad(int64_t M, int64_t F, const void* dH, i
 extern "C" int tgemm_validate_gated_backward(char transA, char transB, int64_t M, int64_t F,
                                              int64_t K, const void* A, int64_t lda, const void* B,
                                              int64_t ldb, const void* dH, int64_t lddh,
-                                             const void* GU, int64_t ldgu, int activation,
-                                             const void* dA, int64_t ldda, const void* dB,
+                                             const void* GU, int64_t ldgu, int gu_type,
+                                             int activation, const void* dA, int64_t ldda, const void* dB,
                                              int64_t lddb, int epilogue) {
   if (epilogue != TGEMM_EPI_STORE_BF16 && epilogue != TGEMM_EPI_STORE_F32)
     return TGEMM_ERR_INVALID_ARG;
-  if (GU == nullptr) return TGEMM_ERR_INVALID_ARG;
-  int st = tgemm_validate_gated(transA, transB, M, F, K, A, lda, B, ldb, activation, dH, lddh, GU,
-                                ldgu);
+  if (!type_ok(gu_type)) return TGEMM_ERR_INVALID_ARG;
+  int st = tgemm_validate_gated(transA, transB, M, F, K, A, lda, B, ldb, activation, dH, lddh,
+                                nullptr, 0);
+  if (st == TGEMM_OK) st = check_rows(GU, M, 2 * F, ldgu);
   if (st == TGEMM_OK) st = check_rows(dA, M, K, ldda);
   if (st == TGEMM_OK)
     st = is_n(transB) ? check_rows(dB, K, 2 * F, lddb) : check_rows(dB, 2 * F, K, lddb);
-  // (the products' K dimensions, padded, are ints)
-  if (st == TGEMM_OK && (M > kMaxDim - 256 || 2 * F > kMaxDim - 256)) st = TGEMM_ERR_UNSUPPORTED;
   return st;
 }
 

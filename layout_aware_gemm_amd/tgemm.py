@@ -122,8 +122,8 @@ def lib():
                 ("run_i8", product + [vp, vp, vp, i64, ci], True),
                 ("run_gated", product + [ci, vp, i64, vp, i64], True),
                 ("run_gated_i8", product + [vp, vp, ci, vp, i64], True),
-                ("gated_grad", [i64, i64, vp, i64, vp, i64, ci, vp, i64], False),
-                ("run_gated_backward", product + [vp, i64, vp, i64, ci, vp, i64, vp, i64, ci],
+                ("gated_grad", [i64, i64, vp, i64, vp, i64, ci, ci, vp, i64], False),
+                ("run_gated_backward", product + [vp, i64, vp, i64, ci, ci, vp, i64, vp, i64, ci],
                  True)):
             bare = name.replace("run_", "")
             call = getattr(L, "tgemm_" + name)
@@ -776,14 +776,15 @@ def gated_matmul(x, w, act="silu", save=False, stream=None):
     [..., F], with [g | u] = x @ w for bf16 x [..., K] and w [K, 2F] (any
     row/column-major view, usually ``W.t()`` of a weight stored [2F, K] with
     the gate rows first).  ``act``: "silu" or "gelu_tanh".  ``save``: also
-    return gu, bf16 [..., 2F], which ``gated_backward`` reads."""
+    return gu = [g | u], fp32 [..., 2F], which ``gated_backward`` reads (as it
+    is, or cast to bf16 for half the memory)."""
     F = _gate_width(w)
     x2, ta, lda, tb, ldb = _product(x, w, torch.bfloat16, "gated_matmul")
     M, K = x2.shape
     dev = _same_device(x, w)
     with _on(dev, stream):
         h = torch.empty(x.shape[:-1] + (F,), dtype=torch.bfloat16, device=dev)
-        gu = (torch.empty(x.shape[:-1] + (2 * F,), dtype=torch.bfloat16, device=dev)
+        gu = (torch.empty(x.shape[:-1] + (2 * F,), dtype=torch.float32, device=dev)
               if save else None)
         _call_ws("tgemm_run_gated", dev, ta, tb, M, F, K, _ptr(x2), lda, _ptr(w),
                  ldb, _act(act), _ptr(h), F, _ptr(gu), 2 * F)
@@ -792,8 +793,9 @@ def gated_matmul(x, w, act="silu", save=False, stream=None):
 
 def gated_backward(dh, gu, x, w, act="silu", dw_dtype=torch.bfloat16, stream=None):
     """Gradients (dx [..., K] bf16, dw [K, 2F]) of ``gated_matmul`` for the
-    gradient ``dh`` bf16 [..., F] of h; ``gu`` as the forward saved it, ``x``
-    and ``w`` its operands.  dw has w's layout (for ``W.t()``, dw.t() is the
+    gradient ``dh`` bf16 [..., F] of h; ``gu`` as the forward saved it (or
+    cast to bf16: a rounding more in the gradients), ``x`` and ``w`` its
+    operands.  dw has w's layout (for ``W.t()``, dw.t() is the
     contiguous [2F, K] gradient of W) and ``dw_dtype`` (bf16 or fp32)."""
     F = _gate_width(w)
     x2, ta, lda, tb, ldb = _product(x, w, torch.bfloat16, "gated_backward")
@@ -803,14 +805,17 @@ def gated_backward(dh, gu, x, w, act="silu", dw_dtype=torch.bfloat16, stream=Non
     if dw_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("dw_dtype must be bf16 or fp32")
     d2, ldd = _rows(dh, "dh", torch.bfloat16)
-    g2, ldg = _rows(gu, "gu", torch.bfloat16)
+    if gu.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("gu must be fp32 or bf16")
+    g2, ldg = _rows(gu, "gu", gu.dtype)
     dev = _same_device(dh, gu, x, w)
     with _on(dev, stream):
         dx = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
         dw = torch.empty((2 * F, K) if tb == b"T" else (K, 2 * F), dtype=dw_dtype, device=dev)
         _call_ws("tgemm_run_gated_backward", dev, ta, tb, M, F, K, _ptr(x2),
-                 lda, _ptr(w), ldb, _ptr(d2), ldd, _ptr(g2), ldg, _act(act), _ptr(dx), K, _ptr(dw),
-                 dw.shape[1], EPI_STORE_BF16 if dw_dtype == torch.bfloat16 else EPI_STORE_F32)
+                 lda, _ptr(w), ldb, _ptr(d2), ldd, _ptr(g2), ldg,
+                 EPI_STORE_F32 if gu.dtype == torch.float32 else EPI_STORE_BF16, _act(act),
+                 _ptr(dx), K, _ptr(dw), dw.shape[1], EPI_STORE_BF16 if dw_dtype == torch.bfloat16 else EPI_STORE_F32)
     return dx, dw.t() if tb == b"T" else dw
 
 

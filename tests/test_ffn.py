@@ -80,6 +80,7 @@ def v_i8(ta="N", tb="T", M=4, N=5, K=32, A=P, lda=None, B=P, ldb=None, sa=P, sb=
 @pytest.mark.parametrize("kw,expect", [
     ({}, OK), (dict(epi=1), OK), (dict(ta="T", tb="N"), OK), (dict(K=131071), OK),
     (dict(K=131072), UNS), (dict(M=1 << 31), UNS), (dict(lda=1 << 62), UNS),
+    (dict(M=(1 << 31) - 100), UNS), (dict(N=(1 << 31) - 100), UNS),
     (dict(epi=2), INV), (dict(epi=-1), INV), (dict(ta="x"), INV),
     (dict(M=0), INV), (dict(N=0), INV), (dict(K=0), INV), (dict(lda=31), INV), (dict(ldb=31), INV),
     (dict(ldc=4), INV), (dict(A=None), INV), (dict(B=None), INV), (dict(C=None), INV),
@@ -103,6 +104,7 @@ def v_gated(ta="N", tb="T", M=4, F=5, K=32, A=P, lda=None, B=P, ldb=None, act=0,
 
 @pytest.mark.parametrize("kw,expect", [
     ({}, OK), (dict(act=1), OK), (dict(GU=None), OK), (dict(GU=None, ldgu=0), OK),
+    (dict(M=(1 << 31) - 100), UNS), (dict(F=(1 << 30) - 100), UNS),
     (dict(ta="T", tb="N"), OK), (dict(i8=True), OK), (dict(i8=True, K=131071), OK),
     (dict(i8=True, K=131072), UNS), (dict(K=131072), OK), (dict(F=1 << 30), UNS),
     (dict(act=2), INV), (dict(act=-1), INV), (dict(M=0), INV), (dict(F=0), INV), (dict(K=0), INV),
@@ -116,22 +118,24 @@ def test_validate_gated(kw, expect):
 
 @pytest.mark.parametrize("kw,expect", [
     ({}, OK), (dict(act=1), OK), (dict(M=0), INV), (dict(F=0), INV), (dict(act=3), INV),
+    (dict(gut=1), OK), (dict(gut=-1), INV),
     (dict(dh=None), INV), (dict(gu=None), INV), (dict(dgu=None), INV), (dict(lddh=6), INV),
     (dict(ldgu=13), INV), (dict(lddgu=13), INV), (dict(F=1 << 30), UNS), (dict(M=1 << 31), UNS),
 ])
 def test_validate_gated_grad(kw, expect):
-    a = dict(M=3, F=7, dh=P, lddh=None, gu=P, ldgu=None, act=0, dgu=P, lddgu=None)
+    a = dict(M=3, F=7, dh=P, lddh=None, gu=P, ldgu=None, gut=0, act=0, dgu=P, lddgu=None)
     a.update(kw)
     F = a["F"]
     st = tgemm.lib().tgemm_validate_gated_grad(
-        a["M"], F, a["dh"], a["lddh"] or F, a["gu"], a["ldgu"] or 2 * F, a["act"], a["dgu"],
+        a["M"], F, a["dh"], a["lddh"] or F, a["gu"], a["ldgu"] or 2 * F, a["gut"], a["act"],
+        a["dgu"],
         a["lddgu"] or 2 * F)
     assert st == expect
 
 
 @pytest.mark.parametrize("kw,expect", [
     ({}, OK), (dict(epi=1), OK), (dict(tb="N"), OK), (dict(ta="T"), OK), (dict(epi=2), INV),
-    (dict(act=2), INV), (dict(M=0), INV), (dict(F=0), INV), (dict(K=0), INV), (dict(F=1 << 30), UNS),
+    (dict(gut=1), OK), (dict(gut=3), INV), (dict(act=2), INV), (dict(M=0), INV), (dict(F=0), INV), (dict(K=0), INV), (dict(F=1 << 30), UNS),
     (dict(A=None), INV), (dict(B=None), INV), (dict(dh=None), INV), (dict(gu=None), INV),
     (dict(da=None), INV), (dict(db=None), INV), (dict(lda=10), INV), (dict(ldb=10), INV),
     (dict(lddh=6), INV), (dict(ldgu=13), INV), (dict(ldda=10), INV), (dict(lddb=10), INV),
@@ -139,14 +143,14 @@ def test_validate_gated_grad(kw, expect):
 ])
 def test_validate_gated_backward(kw, expect):
     a = dict(ta="N", tb="T", M=3, F=7, K=11, A=P, lda=None, B=P, ldb=None, dh=P, lddh=None, gu=P,
-             ldgu=None, act=0, da=P, ldda=None, db=P, lddb=None, epi=0)
+             ldgu=None, gut=0, act=0, da=P, ldda=None, db=P, lddb=None, epi=0)
     a.update(kw)
     M, F, K = a["M"], a["F"], a["K"]
     ldb = 2 * F if a["tb"] == "N" else K
     st = tgemm.lib().tgemm_validate_gated_backward(
         a["ta"].encode(), a["tb"].encode(), M, F, K, a["A"],
         a["lda"] or (K if a["ta"] == "N" else M), a["B"], a["ldb"] or ldb, a["dh"], a["lddh"] or F,
-        a["gu"], a["ldgu"] or 2 * F, a["act"], a["da"], a["ldda"] or K, a["db"], a["lddb"] or ldb,
+        a["gu"], a["ldgu"] or 2 * F, a["gut"], a["act"], a["da"], a["ldda"] or K, a["db"], a["lddb"] or ldb,
         a["epi"])
     assert st == expect
 
