@@ -49,7 +49,8 @@ struct RowsParams {
   float* gu;         // bf16 gated: optional [M][ldgu], g then u
   int64_t ldgu;
   void* part;        // kRowsPart: [split][M][N] int32 / fp32
-  int tilesM, tilesN, groupM;
+  int tilesM, tilesN, groupM;  // the tile grid,
+  int col0;          // from this output column on
   int split, kchunk; // K chunks and bytes per chunk (a multiple of 128)
 };
 

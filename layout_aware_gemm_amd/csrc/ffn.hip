@@ -26,16 +26,33 @@ constexpr size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 // The copy offsets of a tile (at most 256 rows) stay below 2^31 bytes.
 inline bool stride_fits(int64_t ld_bytes) { return ld_bytes < (int64_t(1) << 23); }
 
-// Kernel, tile and K chunks of a product whose operands are aligned.
+// Kernel and tiles of a product whose operands are aligned.
 struct RowsPlan {
   bool skinny;
   int tile;
+  int tail;        // -1, or the tile of the output columns from tail_col on
+  int tail_col;
 };
 
-void set_tile(RowsParams* p, bool gate, int tile) {
+inline int out_cols(int tile, bool gate) { return gate ? rows_tile_n(tile) / 2 : rows_tile_n(tile); }
+
+// The tile grid over output columns col0 .. end - 1.
+void set_tile(RowsParams* p, bool gate, int tile, int col0, int end) {
+  p->col0 = col0;
   p->tilesM = ceil_div(p->M, rows_tile_m(tile));
-  p->tilesN = gate ? ceil_div(p->F, rows_tile_n(tile) / 2) : ceil_div(p->N, rows_tile_n(tile));
+  p->tilesN = ceil_div(end - col0, out_cols(tile, gate));
   p->groupM = p->tilesM < 4 ? p->tilesM : (p->tilesM <= 8 ? p->tilesM : 4);
+}
+
+// Cost of a grid: rounds of 256 workgroups (one per compute unit) times the
+// tile's cost, relative, from int8 and bf16 products of 128 to 768 rows
+// (gated 13824 x 5120, us for 128x128 / 128x256 / 256x256 tiles: 256 rows 66.9
+// / 51.4 / 65.0 int8, 114 / 89 / 121 bf16; 512 rows 123 / 92 / 70 and 211 /
+// 158 / 125).
+double grid_cost(RowsParams* p, bool gate, int tile, int col0, int end) {
+  constexpr double cost[3] = {1.95, 1.33, 1.0};
+  set_tile(p, gate, tile, col0, end);
+  return (double)(((int64_t)p->tilesM * p->tilesN + 255) / 256) * cost[tile];
 }
 
 RowsPlan plan_rows(RowsParams* p, bool gate) {
@@ -45,25 +62,39 @@ RowsPlan plan_rows(RowsParams* p, bool gate) {
   // 30.6 / 29.4, 50.8 / 53.5; 24 rows 31.3 / 33.2, 52.0 / 56.6; 64 rows 37.0
   // / 38.9, 58.9 / 67.1), a plain one is not (32000 x 4096: 64 rows 35.9 /
   // 34.6), nor a small one (4096 x 1024 bf16: 64 rows 12.6 / 8.3).
-  RowsPlan r = {p->M <= 16 || (p->M <= kSkinnyRows && !(gate && p->F >= 192 * 64)), kRows256};
+  RowsPlan r = {p->M <= 16 || (p->M <= kSkinnyRows && !(gate && p->F >= 192 * 64)), kRows256, -1,
+                0};
   p->split = 1;
+  const int end = gate ? p->F : p->N;
   if (!r.skinny) {
-    // The tile whose rounds of 256 workgroups (one per compute unit) cost
-    // least.  Relative cost of a round, from int8 and bf16 products of 128 to
-    // 768 rows (gated 13824 x 5120, us for 128x128 / 128x256 / 256x256 tiles:
-    // 256 rows 66.9 / 51.4 / 65.0 int8, 114 / 89 / 121 bf16; 512 rows 123 /
-    // 92 / 70 and 211 / 158 / 125).
-    const double cost[3] = {1.95, 1.33, 1.0};
-    double best = 0.0;
-    for (int t = kRows256; t <= kRows128; ++t) {
-      set_tile(p, gate, t);
-      const double c = (double)(((int64_t)p->tilesM * p->tilesN + 255) / 256) * cost[t];
-      if (t == kRows256 || c < best) {
-        best = c;
-        r.tile = t;
+    double best = grid_cost(p, gate, kRows256, 0, end);
+    // 256x256 tiles whose last round is short: give its columns to smaller
+    // tiles, which need less than a whole round (a second launch: 0.1 of a
+    // round).  Gated products, us with and without: 513 x 13824 x 5120 102 /
+    // 115 int8, 178 / 208 bf16; 4096 x 2100 x 5120 96 / 122, 166 / 213; 2047 x
+    // 13824 x 5120, where the chip runs at its power limit, 278 / 279.
+    const int cols = (int)((int64_t)p->tilesM * p->tilesN / 256 * 256 / p->tilesM);
+    if (cols > 0 && cols < p->tilesN) {
+      const int col = cols * out_cols(kRows256, gate);
+      const double head = grid_cost(p, gate, kRows256, 0, col) + 0.1;
+      for (int t = kRows128x256; t <= kRows128; ++t) {
+        const double c = head + grid_cost(p, gate, t, col, end);
+        if (c < best) {
+          best = c;
+          r.tail = t;
+          r.tail_col = col;
+        }
       }
     }
-    set_tile(p, gate, r.tile);
+    for (int t = kRows128x256; t <= kRows128; ++t) {
+      const double c = grid_cost(p, gate, t, 0, end);
+      if (c < best) {
+        best = c;
+        r.tile = t;
+        r.tail = -1;
+      }
+    }
+    set_tile(p, gate, r.tile, 0, r.tail < 0 ? end : r.tail_col);
     // Few 128x128 tiles: split K to give every compute unit a workgroup, in
     // chunks of at least 2048 bytes (128 x 5120 x 13824 int8: 45.0 us whole,
     // 22.2 in 6 chunks with the second pass; 384 rows: 49.8 whole, 42.1 in 2).
@@ -87,16 +118,22 @@ bool grid_fits(const RowsParams& p, const RowsPlan& r, bool gate) {
 
 hipError_t launch_rows(int type, const RowsParams& p, const RowsPlan& r, int epi, bool gate,
                        hipStream_t s) {
+  if (r.skinny) return launch_rows_skinny(type, epi, p, s);
   const int e = p.split > 1 ? (int)kRowsPart : epi;
-  const hipError_t h = r.skinny ? launch_rows_skinny(type, e, p, s)
-                                : launch_rows_gemm(type, r.tile, e, gate, p, s);
+  hipError_t h = launch_rows_gemm(type, r.tile, e, gate, p, s);
+  if (h == hipSuccess && r.tail >= 0) {
+    RowsParams q = p;
+    set_tile(&q, gate, r.tail, r.tail_col, gate ? p.F : p.N);
+    h = launch_rows_gemm(type, r.tail, e, gate, q, s);
+  }
   return h != hipSuccess || p.split == 1 ? h : launch_rows_finish(type, epi, p, s);
 }
 
 void say_rows(const char* what, const RowsParams& p, const RowsPlan& r) {
   if (verbose())
-    fprintf(stderr, "tgemm: %s M=%d N=%d K=%d bytes tile=%dx%d split=%d\n", what, p.M, p.N, p.K,
-            r.skinny ? 0 : rows_tile_m(r.tile), r.skinny ? 0 : rows_tile_n(r.tile), p.split);
+    fprintf(stderr, "tgemm: %s M=%d N=%d K=%d bytes tile=%dx%d split=%d tail=%d\n", what, p.M, p.N,
+            p.K, r.skinny ? 0 : rows_tile_m(r.tile), r.skinny ? 0 : rows_tile_n(r.tile), p.split,
+            r.tail < 0 ? 0 : rows_tile_n(r.tail));
 }
 
 // ----------------------------------------------------------------------

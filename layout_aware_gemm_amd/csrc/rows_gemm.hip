@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(RowsParams p) {
   int tile, ks, tm, tn;
   xcd_remap(blockIdx.x, p.tilesM * p.tilesN * p.split, p.split, tile, ks);
   tile_coords(tile, p.tilesM, p.tilesN, p.groupM, tm, tn);
-  const int m0 = tm * BM, n0 = tn * NT;
+  const int m0 = tm * BM, n0 = p.col0 + tn * NT;
   const int kb = ks * p.kchunk, kend = min(p.K, kb + p.kchunk);
   const int nk = (kend - kb + kRowBytes - 1) / kRowBytes;
   const bool partial = ((kend - kb) & (kRowBytes - 1)) != 0;
