@@ -59,9 +59,9 @@ inline bool rows_aligned(const void* p, int64_t ld_bytes, int64_t k_bytes) {
 }
 
 // Output tile shapes of the large-product kernel.
-enum RowsTile : int { kRows256 = 0, kRows128x256 = 1, kRows128 = 2 };
-inline int rows_tile_m(int t) { return t == kRows256 ? 256 : 128; }
-inline int rows_tile_n(int t) { return t == kRows128 ? 128 : 256; }
+enum RowsTile : int { kRows256 = 0, kRows128x256 = 1, kRows128 = 2, kRows64 = 3 };
+inline int rows_tile_m(int t) { return t == kRows256 ? 256 : t == kRows64 ? 64 : 128; }
+inline int rows_tile_n(int t) { return t >= kRows128 ? 128 : 256; }
 
 // Large products (rows_gemm.hip).  `gate`: B's rows are interleaved in the
 // tile (kRowsGated, or kRowsPart of a gated product).

@@ -57,16 +57,20 @@ double grid_cost(RowsParams* p, bool gate, int tile, int col0, int end) {
 
 RowsPlan plan_rows(RowsParams* p, bool gate) {
   // Few rows of A: the kernel that streams B.  From 17 rows on a gated
-  // weight wide enough to fill the chip with 128x128 tiles is as fast or
-  // faster there (13824 x 5120, us tiles / streaming, int8 then bf16: 16 rows
-  // 30.6 / 29.4, 50.8 / 53.5; 24 rows 31.3 / 33.2, 52.0 / 56.6; 64 rows 37.0
-  // / 38.9, 58.9 / 67.1), a plain one is not (32000 x 4096: 64 rows 35.9 /
-  // 34.6), nor a small one (4096 x 1024 bf16: 64 rows 12.6 / 8.3).
-  RowsPlan r = {p->M <= 16 || (p->M <= kSkinnyRows && !(gate && p->F >= 192 * 64)), kRows256, -1,
-                0};
+  // weight wide enough to fill the chip with 64x128 tiles is faster there
+  // (13824 x 5120, us tiles / streaming, int8 then bf16: 16 rows 29.3 / 28.4,
+  // 49.6 / 52.5; 24 rows 30.2 / 31.6, 50.8 / 56.6; 64 rows 32.7 / 36.1, 56.0 /
+  // 65.9; 128x128 tiles 35.5 and 58.4), a plain one is not (32000 x 4096: 64
+  // rows 33.3 / 31.2), nor a smaller one (8192 x 4096 int8: 64 rows 14.8 /
+  // 14.5).
+  RowsPlan r = {p->M <= kSkinnyRows, kRows256, -1, 0};
   p->split = 1;
   const int end = gate ? p->F : p->N;
-  if (!r.skinny) {
+  if (r.skinny && p->M > 16 && gate && p->F >= 192 * 64) {
+    r.skinny = false;
+    r.tile = kRows64;
+    set_tile(p, gate, kRows64, 0, end);
+  } else if (!r.skinny) {
     double best = grid_cost(p, gate, kRows256, 0, end);
     // 256x256 tiles whose last round is short: give its columns to smaller
     // tiles, which need less than a whole round (a second launch: 0.1 of a

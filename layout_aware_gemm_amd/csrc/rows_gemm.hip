@@ -51,10 +51,10 @@ struct OpBf16 {
   }
 };
 
-// Stages of the ring of 128-row tiles (an A and a B panel each).
-template <int BN>
+// Stages of the ring of the smaller tiles (an A and a B panel each).
+template <int BM, int BN>
 constexpr int ring_rows() {
-  return BN == 128 ? 5 : 3;  // 160 KB, 144 KB
+  return BM == 64 ? 6 : BN == 128 ? 5 : 3;  // 144, 160, 144 KB
 }
 constexpr int kRowBytes = 128;  // bytes of K per k-step (one LDS row)
 
@@ -64,7 +64,8 @@ constexpr int kRowBytes = 128;  // bytes of K per k-step (one LDS row)
 template <int R, bool GATE>
 struct RowsPanel {
   static constexpr int PER_WAVE = R / 32;
-  static_assert(PER_WAVE == 4 || PER_WAVE == 8, "panels of 128 or 256 rows");
+  static_assert(PER_WAVE == 4 || PER_WAVE == 8 || (PER_WAVE == 2 && !GATE),
+                "panels of 128 or 256 rows, or 64 of A");
   uint32_t e[2];   // lane's byte offset in even / odd 8-row blocks
   uint32_t et[2];  // the same in a last, partial k-step: outside the range past K
   uint32_t row8;   // 8 rows in bytes
@@ -184,22 +185,26 @@ __device__ __forceinline__ void ring_rows_substep(typename Op::acc (&acc)[FM][FN
                                                   const PA& da, const PB& db, uint16_t* da_dst,
                                                   uint16_t* db_dst, int wave_u, uint32_t kofs,
                                                   bool tail) {
-  constexpr int SL = FM * FN, CN = (PA::PER_WAVE + PB::PER_WAVE) / 4;
+  constexpr int SL = FM * FN, CN = PA::PER_WAVE + PB::PER_WAVE, RD = FM + FN;
+  constexpr int C0 = (X * CN + 3) / 4, C1 = ((X + 1) * CN + 3) / 4;  // this quarter's copies
 #pragma unroll
   for (int q = 0; q < SL; ++q) {
     acc[q / FN][q % FN] = Op::mma(fa[q / FN], fb[q % FN], acc[q / FN][q % FN]);
-    if (q < FM)
-      na[q] = *reinterpret_cast<const typename Op::frag*>(pa + q * 32 * kBK);
-    else if (q < FM + FN)
-      nb[q - FM] = *reinterpret_cast<const typename Op::frag*>(pb + (q - FM) * 32 * kBK);
 #pragma unroll
-    for (int c = 0; c < CN; ++c) {
-      if ((c * SL) / CN != q) continue;
-      const int b = X * CN + c;
-      if (b < PA::PER_WAVE)
-        da.issue_one(da_dst, wave_u, b, kofs, tail);
+    for (int r = 0; r < RD; ++r) {
+      if ((RD > SL ? (r * SL) / RD : r) != q) continue;
+      if (r < FM)
+        na[r] = *reinterpret_cast<const typename Op::frag*>(pa + r * 32 * kBK);
       else
-        db.issue_one(db_dst, wave_u, b - PA::PER_WAVE, kofs, tail);
+        nb[r - FM] = *reinterpret_cast<const typename Op::frag*>(pb + (r - FM) * 32 * kBK);
+    }
+#pragma unroll
+    for (int c = C0; c < C1; ++c) {
+      if (((c - C0) * SL) / (C1 - C0) != q) continue;
+      if (c < PA::PER_WAVE)
+        da.issue_one(da_dst, wave_u, c, kofs, tail);
+      else
+        db.issue_one(db_dst, wave_u, c - PA::PER_WAVE, kofs, tail);
     }
     __builtin_amdgcn_sched_barrier(0);
   }
@@ -335,11 +340,11 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(RowsParams p) {
   constexpr int FM = BM / 64, FN = BN / 64;
   constexpr int NT = GATE ? BN / 2 : BN;       // output columns per tile
   constexpr int SA = BM * kBK, SB = BN * kBK;  // panel sizes in 16-bit units
-  static_assert(FM + FN <= FM * FN && FN % 2 == 0, "slots for the fragment reads, gate pairs");
-  static_assert((BM == 256 && BN == 256) || BM == 128, "one of the two schedules");
+  static_assert(FN % 2 == 0, "gate pairs");
+  static_assert((BM == 256 && BN == 256) || BM <= 128, "one of the two schedules");
   // two A and three B panels, or the ring
   __shared__ __attribute__((aligned(16)))
-  uint16_t lds[BM == 128 ? ring_rows<BN>() * (SA + SB) : 2 * SA + 3 * SB];
+  uint16_t lds[BM <= 128 ? ring_rows<BM, BN>() * (SA + SB) : 2 * SA + 3 * SB];
 
   const int lane = threadIdx.x & 63;
   const int wave_u = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -398,22 +403,24 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(RowsParams p) {
     for (int j = 0; j < FN; ++j)
       fb[0][j] = *reinterpret_cast<const typename Op::frag*>(b + b_base + xo[0] + j * 32 * kBK);
   };
-  if constexpr (BM == 128) {
+  if constexpr (BM <= 128) {
     // Ring of S stages: after the barrier of k-step kt its stage is free,
     // and the copies of k-step kt + S go there, a quarter in each of the next
     // four substeps.  A small tile's k-step is short (4 or 8 matrix
     // instructions per substep), so it takes several in flight to cover the
     // memory's latency.
-    constexpr int S = ring_rows<BN>(), CN = NA + NB;
+    constexpr int S = ring_rows<BM, BN>(), CN = NA + NB;
     auto stA = [&](int g) { return lds + g * (SA + SB); };
 #pragma unroll
     for (int g = 0; g < S - 1; ++g) {
       da.issue(stA(g), wave_u, kof(g), tail(g));
       db.issue(stA(g) + SA, wave_u, kof(g), tail(g));
     }
+    constexpr int C1 = (CN + 3) / 4;  // the first quarter of stage S - 1
+    static_assert(C1 <= NA, "copies of A");
 #pragma unroll
-    for (int c = 0; c < CN / 4; ++c) da.issue_one(stA(S - 1), wave_u, c, kof(S - 1), tail(S - 1));
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm((S - 2) * CN + CN / 4, 0));
+    for (int c = 0; c < C1; ++c) da.issue_one(stA(S - 1), wave_u, c, kof(S - 1), tail(S - 1));
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm((S - 2) * CN + C1, 0));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     read_first(lds, lds + SA);
@@ -539,6 +546,12 @@ hipError_t launch_rows_gemm(int type, int tile, int epi, bool gate, const RowsPa
                             hipStream_t s) {
   if (tile == kRows256) return launch_tile<256, 256>(type, epi, gate, p, s);
   if (tile == kRows128x256) return launch_tile<128, 256>(type, epi, gate, p, s);
+  if (tile == kRows64) {  // (gated products of few rows)
+    if (!gate || epi != kRowsGated) return hipErrorInvalidValue;
+    if (type == kRowsI8) return launch_one<OpI8, 64, 128, true, kRowsGated>(p, s);
+    if (p.gu != nullptr) return launch_one<OpBf16, 64, 128, true, kRowsGatedKeep>(p, s);
+    return launch_one<OpBf16, 64, 128, true, kRowsGated>(p, s);
+  }
   return launch_tile<128, 128>(type, epi, gate, p, s);
 }
 
