@@ -102,7 +102,7 @@ hipError_t launch_gated_grad(const uint16_t* dh, int64_t lddh, const void* gu, i
 // strides, K (a multiple of 64, G zero-padded to it) and kvb (the rows B
 // holds) are set by the caller; the plan sets tiles and K chunks.  Outputs
 // are bf16, or fp32 where asked; the fp32 partials of a product with more
-// than one chunk go to its ws instead.
+// than one chunk go to its ws, and a second launch adds them.
 void gated_bwd_plan(GemmParams* px, GemmParams* pw);
 hipError_t launch_gated_bwd(const GemmParams& px, const GemmParams& pw, bool f32x, bool f32w,
                             hipStream_t s);

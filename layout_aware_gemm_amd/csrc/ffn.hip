@@ -351,10 +351,6 @@ int run_gated_backward(char ta, char tb, int64_t M, int64_t F, int64_t K, const 
   pw.ldb = swap ? ldg : lda;
   pw.ws = reinterpret_cast<float*>(ws + bytesX);
   if (e == hipSuccess) e = launch_gated_bwd(px, pw, false, f32, s);
-  if (e == hipSuccess && px.splitk > 1)
-    e = launch_splitk_sum(px.ws, px.splitk, px.M, px.N, dA, ldda, false, s);
-  if (e == hipSuccess && pw.splitk > 1)
-    e = launch_splitk_sum(pw.ws, pw.splitk, pw.M, pw.N, dB, lddb, f32, s);
   const hipError_t f = release_workspace(w, s);
   return status_of(e != hipSuccess ? e : f);
 }

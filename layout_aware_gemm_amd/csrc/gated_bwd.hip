@@ -124,6 +124,49 @@ __global__ void __launch_bounds__(kThreads, 1) gated_bwd_kernel(GemmParams px, G
   }
 }
 
+// Sums of the K chunks' partials [split][M][N] of up to two products in one
+// launch, in ascending chunk order, four columns per thread.
+struct SumJob {
+  const float* ws;
+  int split, M, N;
+  void* C;
+  int64_t ldc;
+  int f32;
+  int per_row;  // workgroups per row
+};
+
+__global__ void __launch_bounds__(kThreads) bwd_sum_kernel(SumJob x, SumJob w, int xblocks) {
+  const bool second = (int)blockIdx.x >= xblocks;
+  const SumJob& j = second ? w : x;
+  const int b = second ? (int)blockIdx.x - xblocks : (int)blockIdx.x;
+  const int row = b / j.per_row;
+  const int c = ((b - row * j.per_row) * kThreads + (int)threadIdx.x) * 4;
+  const int n = min(4, j.N - c);
+  if (n <= 0) return;
+  const int64_t slice = (int64_t)j.M * j.N;
+  const float* p = j.ws + (int64_t)row * j.N + c;
+  float a[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int q = 0; q < j.split; ++q, p += slice) {
+    if (n == 4) {
+      const x4_any<float> t = *reinterpret_cast<const x4_any<float>*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] += t.v[i];
+    } else {
+      for (int i = 0; i < n; ++i) a[i] += p[i];
+    }
+  }
+  const int64_t o = (int64_t)row * j.ldc + c;
+  if (j.f32)
+    put4(static_cast<float*>(j.C) + o, a, n);
+  else
+    put4(static_cast<uint16_t*>(j.C) + o, a, n);
+}
+
+int64_t sum_job(const GemmParams& p, bool f32, SumJob* j) {
+  *j = {p.ws, p.splitk, p.M, p.N, p.C, p.ldc, f32 ? 1 : 0, ceil_div(p.N, 4 * kThreads)};
+  return p.splitk > 1 ? (int64_t)p.M * j->per_row : 0;
+}
+
 void set_split(GemmParams* p, int split) {
   const int steps = p->K / kBK;
   const int per = ceil_div(steps, split);
@@ -161,6 +204,13 @@ hipError_t launch_gated_bwd(const GemmParams& px, const GemmParams& pw, bool f32
   const dim3 grid((unsigned)(nfirst + (wfirst ? nx : nw))), block(kThreads);
   hipLaunchKernelGGL(gated_bwd_kernel, grid, block, 0, s, px, pw, nfirst, wfirst, f32x ? 1 : 0,
                      f32w ? 1 : 0);
+  // Only a product of at most 170 tiles is split (its K is 1.5 shares or
+  // more), so the sums' grid stays under 2^16 workgroups.
+  SumJob jx, jw;
+  const int64_t bx = sum_job(px, f32x, &jx), bw = sum_job(pw, f32w, &jw);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || bx + bw == 0) return e;
+  hipLaunchKernelGGL(bwd_sum_kernel, dim3((unsigned)(bx + bw)), block, 0, s, jx, jw, (int)bx);
   return hipGetLastError();
 }
 
