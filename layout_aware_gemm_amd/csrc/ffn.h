@@ -100,12 +100,13 @@ hipError_t launch_gated_grad(const uint16_t* dh, int64_t lddh, const void* gu, i
 // dX = G . W (px: A = G [M][K], B = W) and dW = G^T . X (pw: A = G stored
 // [K][M], B = X), both bf16, in one launch (gated_bwd.hip).  M, N, A, B, C,
 // strides, K (a multiple of 64, G zero-padded to it) and kvb (the rows B
-// holds) are set by the caller; the plan sets tiles and K chunks.  Outputs
-// are bf16, or fp32 where asked; the fp32 partials of a product with more
-// than one chunk go to its ws, and a second launch adds them.
-void gated_bwd_plan(GemmParams* px, GemmParams* pw);
-hipError_t launch_gated_bwd(const GemmParams& px, const GemmParams& pw, bool f32x, bool f32w,
-                            hipStream_t s);
+// holds) are set by the caller; the plan sets tiles and K chunks, and
+// returns the tiles' size.  Outputs are bf16, or fp32 where asked; the fp32
+// partials of a product with more than one chunk go to its ws, and a second
+// launch adds them.
+int gated_bwd_plan(GemmParams* px, GemmParams* pw);
+hipError_t launch_gated_bwd(int tile, const GemmParams& px, const GemmParams& pw, bool f32x,
+                            bool f32w, hipStream_t s);
 
 // Rows to 8-bit codes with one scale each (row_quant.hip).  weight null:
 // codes of x itself; else of the RMS norm of x (+ residual, whose bf16 sum

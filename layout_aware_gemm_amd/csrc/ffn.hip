@@ -313,7 +313,7 @@ int run_gated_backward(char ta, char tb, int64_t M, int64_t F, int64_t K, const 
   pw.kvb = (int)M;
   pw.C = dB;
   pw.ldc = lddb;
-  gated_bwd_plan(&px, &pw);
+  const int tile = gated_bwd_plan(&px, &pw);
   const size_t bytesX =
       px.splitk > 1 ? round256((size_t)px.splitk * px.M * px.N * sizeof(float)) : 0;
   const size_t bytesW = pw.splitk > 1 ? (size_t)pw.splitk * pw.M * pw.N * sizeof(float) : 0;
@@ -321,8 +321,9 @@ int run_gated_backward(char ta, char tb, int64_t M, int64_t F, int64_t K, const 
   const int st = take_workspace(space, s, bytesG + bytesA + bytesB + bytesX + bytesW, &w);
   if (st != TGEMM_OK) return st;
   if (verbose())
-    fprintf(stderr, "tgemm: gated backward %c%c M=%lld F=%lld K=%lld copies=%d,%d split=%d,%d\n",
-            ta, tb, (long long)M, (long long)F, (long long)K, packA, packB, px.splitk, pw.splitk);
+    fprintf(stderr,
+            "tgemm: gated backward %c%c M=%lld F=%lld K=%lld copies=%d,%d tile=%d split=%d,%d\n", ta,
+            tb, (long long)M, (long long)F, (long long)K, packA, packB, tile, px.splitk, pw.splitk);
   char* ws = static_cast<char*>(w.ptr);
   uint16_t* const G = reinterpret_cast<uint16_t*>(ws);
   ws += bytesG;
@@ -350,7 +351,7 @@ int run_gated_backward(char ta, char tb, int64_t M, int64_t F, int64_t K, const 
   pw.B = swap ? G : static_cast<const uint16_t*>(Ar);
   pw.ldb = swap ? ldg : lda;
   pw.ws = reinterpret_cast<float*>(ws + bytesX);
-  if (e == hipSuccess) e = launch_gated_bwd(px, pw, false, f32, s);
+  if (e == hipSuccess) e = launch_gated_bwd(tile, px, pw, false, f32, s);
   const hipError_t f = release_workspace(w, s);
   return status_of(e != hipSuccess ? e : f);
 }

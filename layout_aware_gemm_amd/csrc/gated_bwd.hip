@@ -1,7 +1,7 @@
 // The gated product's two gradient products in one launch:
 //   dX = G . W       [M][K],  G = dGU [M][2F], W [2F][K]     (NN)
 //   dW = G^T . X     [2F][K], X [M][K]                       (TN)
-// with 256x256 tiles on the library's NN and TN loops.
+// with 256x256 or 128x128 tiles on the library's NN and TN loops.
 //
 // Why one launch: dX has few, long tiles (K dimension 2F) and dW many short
 // ones (K dimension M).  Alone, dX's last round leaves most compute units
@@ -22,34 +22,38 @@
 namespace tgemm {
 namespace {
 
-constexpr int kT = 256;
-
-// Store a wave's 128x128 block of a tile (accumulator layout as in the
-// GEMM's epilogues) through LDS words of its own, 32 rows at a time: rows
-// leave as 256 or 512 contiguous bytes, and each accumulator is used in one
-// place only.  (Stored from registers under the tests for the edge and the
+// Store a wave's block of a T x T tile, a quarter of it (accumulator layout
+// as in the GEMM's epilogues) through LDS words of its own, 32 rows at a
+// time: rows leave as 128 to 512 contiguous bytes, and each accumulator is
+// used in one place only.  (Stored from registers under the tests for the edge and the
 // type, they were copied out of the matrix cores' registers all at once, and
-// some of them through scratch.)  Rows of 136 words: the two halves of a
-// wave, four rows apart, write to different halves of the banks.
-constexpr int kOutRow = 136;
+// some of them through scratch.)  With 8 words of padding per row the two
+// halves of a wave, four rows apart, write to different halves of the banks.
+template <int T>
+constexpr int out_row() {
+  return T / 2 + 8;
+}
 
+template <int T>
 __device__ __forceinline__ void store_block(const GemmParams& p, void* C, int64_t ldc, bool f32,
-                                            const f32x16_t (&acc)[4][4], float* st, int row0,
-                                            int col0, int lane) {
+                                            const f32x16_t (&acc)[T / 64][T / 64], float* st,
+                                            int row0, int col0, int lane) {
+  constexpr int F = T / 64, LD = out_row<T>();
+  constexpr int LPR = T / 8, RPI = 64 / LPR;  // lanes per row, rows per pass on the way out
   const int h = lane >> 5, lc = lane & 31;
-  const int c = col0 + 4 * lc;  // this lane's four columns on the way out
-  const int n = p.N - c;        // of which so many exist
+  const int cl = 4 * (lane % LPR), c = col0 + cl;  // this lane's four columns
+  const int n = p.N - c;                           // of which so many exist
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < F; ++i) {
 #pragma unroll
     for (int r = 0; r < 16; ++r)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        st[(8 * (r >> 2) + 4 * h + (r & 3)) * kOutRow + j * 32 + lc] = acc[i][j][r];
+      for (int j = 0; j < F; ++j)
+        st[(8 * (r >> 2) + 4 * h + (r & 3)) * LD + j * 32 + lc] = acc[i][j][r];
 #pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      const int rl = 2 * q + h, row = row0 + i * 32 + rl;
-      const float4 v = *reinterpret_cast<const float4*>(st + rl * kOutRow + 4 * lc);
+    for (int q = 0; q < 32 / RPI; ++q) {
+      const int rl = q * RPI + lane / LPR, row = row0 + i * 32 + rl;
+      const float4 v = *reinterpret_cast<const float4*>(st + rl * LD + cl);
       if (row >= p.M || n <= 0) continue;
       const float e[4] = {v.x, v.y, v.z, v.w};
       const int64_t off = (int64_t)row * ldc + c;
@@ -62,7 +66,7 @@ __device__ __forceinline__ void store_block(const GemmParams& p, void* C, int64_
 }
 
 // One tile of one product: dX (NN) or dW (TN).
-template <bool DW>
+template <int kT, bool DW>
 __device__ __forceinline__ void grad_tile(const GemmParams& p, int bid, bool f32, uint16_t* lds) {
   constexpr int FM = kT / 64, FN = kT / 64, SA = kT * kBK;
   const int tid = threadIdx.x;
@@ -102,14 +106,15 @@ __device__ __forceinline__ void grad_tile(const GemmParams& p, int bid, bool f32
     f32 = true;
   }
   __syncthreads();  // the stages become the rows' buffer
-  store_block(p, C, ldc, f32, acc, reinterpret_cast<float*>(lds) + wave * 32 * kOutRow,
-              m0 + wm * (kT / 2), n0 + wn * (kT / 2), lane);
+  store_block<kT>(p, C, ldc, f32, acc, reinterpret_cast<float*>(lds) + wave * 32 * out_row<kT>(),
+                  m0 + wm * (kT / 2), n0 + wn * (kT / 2), lane);
 }
 
 // Workgroups 0 .. nfirst - 1 (a multiple of 8, so that a product's tiles
 // keep their XCDs) take the product with the longer tiles, dW if wfirst.
 // f32x, f32w: the output types (K chunks are fp32).
-__global__ void __launch_bounds__(kThreads, 1) gated_bwd_kernel(GemmParams px, GemmParams pw,
+template <int kT>
+__global__ void __launch_bounds__(kThreads, kT == 128 ? 2 : 1) gated_bwd_kernel(GemmParams px, GemmParams pw,
                                                                 int nfirst, int wfirst, int f32x,
                                                                 int f32w) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[5 * kT * kBK];
@@ -118,9 +123,9 @@ __global__ void __launch_bounds__(kThreads, 1) gated_bwd_kernel(GemmParams px, G
   const int l = b < nfirst ? b : b - nfirst;
   // (workgroups past a product's last tile are the padding to a multiple of 8)
   if (w) {
-    if (l < pw.tilesM * pw.tilesN * pw.splitk) grad_tile<true>(pw, l, f32w != 0, lds);
+    if (l < pw.tilesM * pw.tilesN * pw.splitk) grad_tile<kT, true>(pw, l, f32w != 0, lds);
   } else {
-    if (l < px.tilesM * px.tilesN * px.splitk) grad_tile<false>(px, l, f32x != 0, lds);
+    if (l < px.tilesM * px.tilesN * px.splitk) grad_tile<kT, false>(px, l, f32x != 0, lds);
   }
 }
 
@@ -176,35 +181,55 @@ void set_split(GemmParams* p, int split) {
 
 }  // namespace
 
-void gated_bwd_plan(GemmParams* px, GemmParams* pw) {
-  for (GemmParams* p : {px, pw}) {
-    p->tilesM = ceil_div(p->M, kT);
-    p->tilesN = ceil_div(p->N, kT);
-    p->groupM = p->tilesM < 4 ? p->tilesM : (p->tilesM <= 8 ? p->tilesM : 4);
-  }
+int gated_bwd_plan(GemmParams* px, GemmParams* pw) {
+  auto tiles = [&](int t) {
+    double work = 0;  // k-steps of all tiles
+    for (GemmParams* p : {px, pw}) {
+      p->tilesM = ceil_div(p->M, t);
+      p->tilesN = ceil_div(p->N, t);
+      p->groupM = p->tilesM < 4 ? p->tilesM : (p->tilesM <= 8 ? p->tilesM : 4);
+      work += (double)p->tilesM * p->tilesN * (p->K / kBK);
+    }
+    return work;
+  };
+  // Under 60 k-steps of 256x256 tiles per compute unit the smaller tiles win
+  // (whole training steps, us, 256 against 128): 333 x 1000 x 520 (1.3) 45.3,
+  // 31.0; 1000 x 2048 x 1024 (8) 72, 58; 768 x 4096 x 4096 (48) 232, 214; 128
+  // x 13824 x 5120 (51) 345, 296.  Then they tie (1024 x 4096 x 4096, 64: 267,
+  // 269; 256 x 13824 x 5120, 68: 412, 416) and lose (2048 x 8192 x 2048, 128:
+  // 492, 540).
+  double total = tiles(256);
+  const int t = total < 60 * 256 ? 128 : 256;
+  if (t == 128) total = tiles(128);
   // Split the K dimension of a product whose tiles are longer than an even
-  // share of all the work, in chunks of at least kMinSteps k-steps.
-  constexpr int kMinSteps = 4;
-  const double total = (double)px->tilesM * px->tilesN * (px->K / kBK) +
-                       (double)pw->tilesM * pw->tilesN * (pw->K / kBK);
-  const double share = total / 256 > kMinSteps ? total / 256 : kMinSteps;
+  // share of all the work (two small tiles run per compute unit), in chunks
+  // of at least kMinSteps k-steps (333 x 1000 x 520: with 4, 6, 8 and 12 the
+  // step takes 37, 31, 31 and 33 us; 64 x 512 x 256: 17.6, 18.6, 18.9, 23).
+  constexpr int kMinSteps = 6;
+  const double even = total / (t == 128 ? 512 : 256);
+  const double share = even > kMinSteps ? even : kMinSteps;
   for (GemmParams* p : {px, pw}) {
     const double n = (p->K / kBK) / share;
     set_split(p, n < 1.5 ? 1 : n > 64 ? 64 : (int)(n + 0.5));
   }
+  return t;
 }
 
-hipError_t launch_gated_bwd(const GemmParams& px, const GemmParams& pw, bool f32x, bool f32w,
-                            hipStream_t s) {
+hipError_t launch_gated_bwd(int tile, const GemmParams& px, const GemmParams& pw, bool f32x,
+                            bool f32w, hipStream_t s) {
   const int64_t nx = (int64_t)px.tilesM * px.tilesN * px.splitk;
   const int64_t nw = (int64_t)pw.tilesM * pw.tilesN * pw.splitk;
   if (nx + nw + 8 > kMaxWorkgroups) return hipErrorInvalidValue;
   const int wfirst = pw.kchunk > px.kchunk;
   const int nfirst = (int)(((wfirst ? nw : nx) + 7) / 8 * 8);
   const dim3 grid((unsigned)(nfirst + (wfirst ? nx : nw))), block(kThreads);
-  hipLaunchKernelGGL(gated_bwd_kernel, grid, block, 0, s, px, pw, nfirst, wfirst, f32x ? 1 : 0,
-                     f32w ? 1 : 0);
-  // Only a product of at most 170 tiles is split (its K is 1.5 shares or
+  if (tile == 128)
+    hipLaunchKernelGGL(gated_bwd_kernel<128>, grid, block, 0, s, px, pw, nfirst, wfirst,
+                       f32x ? 1 : 0, f32w ? 1 : 0);
+  else
+    hipLaunchKernelGGL(gated_bwd_kernel<256>, grid, block, 0, s, px, pw, nfirst, wfirst,
+                       f32x ? 1 : 0, f32w ? 1 : 0);
+  // Only a product of at most 341 tiles is split (its K is 1.5 shares or
   // more), so the sums' grid stays under 2^16 workgroups.
   SumJob jx, jw;
   const int64_t bx = sum_job(px, f32x, &jx), bw = sum_job(pw, f32w, &jw);

@@ -1435,7 +1435,7 @@ __device__ __forceinline__ void mix_substep(f32x16_t (&acc)[FM][FN], const bf16x
                                             bool ld = false) {
   constexpr int SL = FM * FN;
   constexpr int NCP = DmaPanel<R>::PER_WAVE;
-  static_assert(SL % NCP == 0 && SL % LG::U == 0 && SL % LG::L == 0,
+  static_assert(SL % NCP == 0 && (SL % LG::U == 0 || LG::U % SL == 0) && SL % LG::L == 0,
                 "side work must divide the slots evenly");
 #pragma unroll
   for (int q = 0; q < SL; ++q) {
@@ -1444,7 +1444,11 @@ __device__ __forceinline__ void mix_substep(f32x16_t (&acc)[FM][FN], const bf16x
     if (q < FM) na[q] = *reinterpret_cast<const bf16x8_t*>(pa + q * 32 * kBK);
     else if (q < FM + FN) nb[q - FM] = *reinterpret_cast<const bf16x8_t*>(pb + (q - FM) * 32 * kBK);
     if (cp && q % (SL / NCP) == 0) d.issue_one(o, ddst, wave_u, q / (SL / NCP), zero);
-    if (st && q % (SL / LG::U) == 0) g.store_unit(gdst, tid, q / (SL / LG::U));
+    if (st) {
+#pragma unroll
+      for (int u = 0; u < LG::U; ++u)
+        if ((u * SL) / LG::U == q) g.store_unit(gdst, tid, u);
+    }
     if (ld && q % (SL / LG::L) == 0) g.load_unit(q / (SL / LG::L));
     __builtin_amdgcn_sched_barrier(0);
   }

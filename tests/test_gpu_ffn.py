@@ -320,7 +320,8 @@ def test_gated_and_gradient(M, F, K, layout, pad, kind, keep):
 
 @pytest.mark.parametrize("M,F,K", [(300, 1000, 520), (2000, 33, 72), (70, 5000, 136),
                                    (513, 260, 264), (1, 300, 40), (4099, 31, 8), (255, 129, 1000),
-                                   (100, 90, 67), (257, 33, 257), (64, 32, 1)])
+                                   (100, 90, 67), (257, 33, 257), (64, 32, 1),
+                                   (700, 5000, 4100), (4099, 5000, 700), (65, 20100, 4100)])
 def test_gradient_shapes(M, F, K):
     """The joint launch of both gradient products: K dimensions (2F and M)
     off the 64-element step, split or not, tiles cut in every direction.
@@ -616,7 +617,7 @@ class Guarded:
 
 
 @pytest.mark.parametrize("M,F,K", [(4, 40, 4096), (1, 1, 8), (70, 33, 72), (300, 130, 520),
-                                   (3, 500, 40), (257, 129, 65)])
+                                   (3, 500, 40), (257, 129, 65), (700, 5000, 4100)])
 @pytest.mark.parametrize("layout", ["NT", "NN", "TN"])
 def test_backward_stays_inside(M, F, K, layout):
     """Outputs and workspace of exactly the asked-for size, guarded on both
