@@ -44,15 +44,21 @@ void set_tile(RowsParams* p, bool gate, int tile, int col0, int end) {
   p->groupM = p->tilesM < 4 ? p->tilesM : (p->tilesM <= 8 ? p->tilesM : 4);
 }
 
-// Cost of a grid: rounds of 256 workgroups (one per compute unit) times the
-// tile's cost, relative, from int8 and bf16 products of 128 to 768 rows
-// (gated 13824 x 5120, us for 128x128 / 128x256 / 256x256 tiles: 256 rows 66.9
-// / 51.4 / 65.0 int8, 114 / 89 / 121 bf16; 512 rows 123 / 92 / 70 and 211 /
-// 158 / 125).
-double grid_cost(RowsParams* p, bool gate, int tile, int col0, int end) {
-  constexpr double cost[3] = {1.95, 1.33, 1.0};
+// Time of a grid in us: rounds of 256 workgroups (one per compute unit), each
+// a fixed part (the pipeline's fill, the epilogue) and the k-steps, plus the
+// second pass over the partial sums of a split K.  A round of 128x128 tiles
+// takes 6 us and 2.9 us per KB of K (gated 2048 wide, 128 rows: 1 KB 8.9, 2
+// KB 11.5, 4 KB 18.2, 8 KB 29.4; plain 5120 x 13.5 KB 45), the other tiles
+// 0.8 (64x128), 1.33 (128x256) and 1.95 (256x256) of it (gated 13824 x 5120,
+// us for 64x128 / 128x128 / 128x256 / 256x256 tiles: 256 rows 101 / 66.9 /
+// 51.4 / 65.0 int8, 170 / 114 / 89 / 121 bf16; 512 rows 163 / 123 / 92 / 70
+// and 272 / 211 / 158 / 125).
+double grid_cost(RowsParams* p, bool gate, int tile, int split, int col0, int end) {
+  constexpr double cost[4] = {1.95, 1.33, 1.0, 0.8};
   set_tile(p, gate, tile, col0, end);
-  return (double)(((int64_t)p->tilesM * p->tilesN + 255) / 256) * cost[tile];
+  const double round = cost[tile] * (6 + 2.9e-3 * p->K / split);
+  const double sums = split > 1 ? 4 + 1.7e-6 * split * p->M * p->N : 0;
+  return (double)(((int64_t)p->tilesM * p->tilesN * split + 255) / 256) * round + sums;
 }
 
 RowsPlan plan_rows(RowsParams* p, bool gate) {
@@ -71,18 +77,18 @@ RowsPlan plan_rows(RowsParams* p, bool gate) {
     r.tile = kRows64;
     set_tile(p, gate, kRows64, 0, end);
   } else if (!r.skinny) {
-    double best = grid_cost(p, gate, kRows256, 0, end);
+    double best = grid_cost(p, gate, kRows256, 1, 0, end);
     // 256x256 tiles whose last round is short: give its columns to smaller
-    // tiles, which need less than a whole round (a second launch: 0.1 of a
-    // round).  Gated products, us with and without: 513 x 13824 x 5120 102 /
-    // 115 int8, 178 / 208 bf16; 4096 x 2100 x 5120 96 / 122, 166 / 213; 2047 x
-    // 13824 x 5120, where the chip runs at its power limit, 278 / 279.
+    // tiles, which need less than a whole round (a second launch: 4 us).
+    // Gated products, us with and without: 513 x 13824 x 5120 102 / 115 int8,
+    // 178 / 208 bf16; 4096 x 2100 x 5120 96 / 122, 166 / 213; 2047 x 13824 x
+    // 5120, where the chip runs at its power limit, 278 / 279.
     const int cols = (int)((int64_t)p->tilesM * p->tilesN / 256 * 256 / p->tilesM);
     if (cols > 0 && cols < p->tilesN) {
       const int col = cols * out_cols(kRows256, gate);
-      const double head = grid_cost(p, gate, kRows256, 0, col) + 0.1;
-      for (int t = kRows128x256; t <= kRows128; ++t) {
-        const double c = head + grid_cost(p, gate, t, col, end);
+      const double head = grid_cost(p, gate, kRows256, 1, 0, col) + 4;
+      for (int t = kRows128x256; t <= kRows64; ++t) {
+        const double c = head + grid_cost(p, gate, t, 1, col, end);
         if (c < best) {
           best = c;
           r.tail = t;
@@ -90,24 +96,30 @@ RowsPlan plan_rows(RowsParams* p, bool gate) {
         }
       }
     }
-    for (int t = kRows128x256; t <= kRows128; ++t) {
-      const double c = grid_cost(p, gate, t, 0, end);
+    for (int t = kRows128x256; t <= kRows64; ++t) {
+      const double c = grid_cost(p, gate, t, 1, 0, end);
       if (c < best) {
         best = c;
         r.tile = t;
         r.tail = -1;
+        p->split = 1;
+      }
+      // Few small tiles: split K to give every compute unit a workgroup, in
+      // chunks of at least 2048 bytes (128 x 5120 x 13824 int8: 128x128 tiles
+      // 45 us whole, 26 in 6 chunks with the second pass; 64x128 tiles 23.5
+      // in 3).
+      const int64_t fill = 256 / ((int64_t)p->tilesM * p->tilesN), by_k = p->K / 2048;
+      const int split = (int)(fill < by_k ? fill : by_k);
+      if (t < kRows128 || split < 2) continue;
+      const double cs = grid_cost(p, gate, t, split, 0, end);
+      if (cs < best) {
+        best = cs;
+        r.tile = t;
+        r.tail = -1;
+        p->split = split;
       }
     }
     set_tile(p, gate, r.tile, 0, r.tail < 0 ? end : r.tail_col);
-    // Few 128x128 tiles: split K to give every compute unit a workgroup, in
-    // chunks of at least 2048 bytes (128 x 5120 x 13824 int8: 45.0 us whole,
-    // 22.2 in 6 chunks with the second pass; 384 rows: 49.8 whole, 42.1 in 2).
-    if (r.tile == kRows128) {
-      const int64_t t = (int64_t)p->tilesM * p->tilesN;
-      const int64_t fill = 256 / t, by_k = p->K / 2048;
-      const int64_t n = fill < by_k ? fill : by_k;
-      p->split = n < 1 ? 1 : (int)n;
-    }
   }
   p->kchunk = ceil_div(ceil_div(p->K, p->split), 128) * 128;
   p->split = ceil_div(p->K, p->kchunk);  // no empty chunks

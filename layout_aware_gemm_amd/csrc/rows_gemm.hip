@@ -523,19 +523,23 @@ hipError_t launch_one(const RowsParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
+// (the K dimension is split for the 128-column tiles only)
 template <int BM, int BN>
 hipError_t launch_tile(int type, int epi, bool gate, const RowsParams& p, hipStream_t s) {
-  if (type == kRowsI8) {
+  if (epi == kRowsPart) {
+    if constexpr (BN == 128) {
+      if (type == kRowsI8)
+        return gate ? launch_one<OpI8, BM, BN, true, kRowsPart>(p, s)
+                    : launch_one<OpI8, BM, BN, false, kRowsPart>(p, s);
+      if (gate) return launch_one<OpBf16, BM, BN, true, kRowsPart>(p, s);
+    }
+  } else if (type == kRowsI8) {
     if (gate && epi == kRowsGated) return launch_one<OpI8, BM, BN, true, kRowsGated>(p, s);
-    if (gate && epi == kRowsPart) return launch_one<OpI8, BM, BN, true, kRowsPart>(p, s);
     if (!gate && epi == kRowsStoreBf16) return launch_one<OpI8, BM, BN, false, kRowsStoreBf16>(p, s);
     if (!gate && epi == kRowsStoreF32) return launch_one<OpI8, BM, BN, false, kRowsStoreF32>(p, s);
-    if (!gate && epi == kRowsPart) return launch_one<OpI8, BM, BN, false, kRowsPart>(p, s);
-  } else if (gate) {
-    if (epi == kRowsGated && p.gu != nullptr)
-      return launch_one<OpBf16, BM, BN, true, kRowsGatedKeep>(p, s);
-    if (epi == kRowsGated) return launch_one<OpBf16, BM, BN, true, kRowsGated>(p, s);
-    if (epi == kRowsPart) return launch_one<OpBf16, BM, BN, true, kRowsPart>(p, s);
+  } else if (gate && epi == kRowsGated) {
+    return p.gu != nullptr ? launch_one<OpBf16, BM, BN, true, kRowsGatedKeep>(p, s)
+                           : launch_one<OpBf16, BM, BN, true, kRowsGated>(p, s);
   }
   return hipErrorInvalidValue;
 }
@@ -546,12 +550,7 @@ hipError_t launch_rows_gemm(int type, int tile, int epi, bool gate, const RowsPa
                             hipStream_t s) {
   if (tile == kRows256) return launch_tile<256, 256>(type, epi, gate, p, s);
   if (tile == kRows128x256) return launch_tile<128, 256>(type, epi, gate, p, s);
-  if (tile == kRows64) {  // (gated products of few rows)
-    if (!gate || epi != kRowsGated) return hipErrorInvalidValue;
-    if (type == kRowsI8) return launch_one<OpI8, 64, 128, true, kRowsGated>(p, s);
-    if (p.gu != nullptr) return launch_one<OpBf16, 64, 128, true, kRowsGatedKeep>(p, s);
-    return launch_one<OpBf16, 64, 128, true, kRowsGated>(p, s);
-  }
+  if (tile == kRows64) return launch_tile<64, 128>(type, epi, gate, p, s);
   return launch_tile<128, 128>(type, epi, gate, p, s);
 }
 
