@@ -63,16 +63,16 @@ double grid_cost(RowsParams* p, bool gate, int tile, int split, int col0, int en
 
 RowsPlan plan_rows(RowsParams* p, bool gate) {
   // Few rows of A: the kernel that streams B.  From 17 rows on a gated
-  // weight wide enough to fill the chip with 64x128 tiles is faster there
-  // (13824 x 5120, us tiles / streaming, int8 then bf16: 16 rows 29.3 / 28.4,
-  // 49.6 / 52.5; 24 rows 30.2 / 31.6, 50.8 / 56.6; 64 rows 32.7 / 36.1, 56.0 /
-  // 65.9; 128x128 tiles 35.5 and 58.4), a plain one is not (32000 x 4096: 64
-  // rows 33.3 / 31.2), nor a smaller one (8192 x 4096 int8: 64 rows 14.8 /
-  // 14.5).
+  // weight wide enough for 64x128 tiles on most of the chip is faster there
+  // (us tiles / streaming, int8 then bf16: 13824 x 5120, 16 rows 29.3 / 28.4,
+  // 49.6 / 52.5; 64 rows 32.7 / 36.1, 56.0 / 65.9; 11008 x 4096, 17 rows 18.1 /
+  // 20.8, 38.2 / 43.2; 64 rows 19.9 / 24.4, 43.2 / 50.1), a smaller one is not
+  // (8192 x 4096, 32 rows 15.3 / 13.1, 38.9 / 31.7), nor a plain one (32000 x
+  // 4096 int8, 48 rows 33.6 / 32.5).
   RowsPlan r = {p->M <= kSkinnyRows, kRows256, -1, 0};
   p->split = 1;
   const int end = gate ? p->F : p->N;
-  if (r.skinny && p->M > 16 && gate && p->F >= 192 * 64) {
+  if (r.skinny && p->M > 16 && gate && p->F >= 160 * 64) {
     r.skinny = false;
     r.tile = kRows64;
     set_tile(p, gate, kRows64, 0, end);

@@ -613,17 +613,16 @@ def _call(name, dev, *args):
         raise TgemmError(st, name)
 
 
-def _call_ws(name, dev, *args):
+def _call_ws(name, dev, *args, sure=False):
     """As ``_call`` for a call with workspace (its first nine arguments are
     the product's), which is a torch allocation: most calls need none, and
-    one that does says so before it enqueues anything."""
+    one that does says so before it enqueues anything.  sure: this one does."""
     fn, stream = getattr(lib(), name), _raw_stream(dev)
-    st = fn(*args, None, 0, stream)
+    st = TGEMM_ERR_WORKSPACE_LIMIT if sure else fn(*args, None, 0, stream)
     if st == TGEMM_ERR_WORKSPACE_LIMIT:
         need = getattr(lib(), name.replace("run_", "") + "_workspace_bytes")(*args[:9])
-        if need > 0:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-            st = fn(*args, ws.data_ptr(), need, stream)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
+        st = fn(*args, _ptr(ws), max(need, 0), stream)
     if st != TGEMM_OK:
         raise TgemmError(st, name)
 
@@ -815,7 +814,8 @@ def gated_backward(dh, gu, x, w, act="silu", dw_dtype=torch.bfloat16, stream=Non
         _call_ws("tgemm_run_gated_backward", dev, ta, tb, M, F, K, _ptr(x2),
                  lda, _ptr(w), ldb, _ptr(d2), ldd, _ptr(g2), ldg,
                  EPI_STORE_F32 if gu.dtype == torch.float32 else EPI_STORE_BF16, _act(act),
-                 _ptr(dx), K, _ptr(dw), dw.shape[1], EPI_STORE_BF16 if dw_dtype == torch.bfloat16 else EPI_STORE_F32)
+                 _ptr(dx), K, _ptr(dw), dw.shape[1],
+                 EPI_STORE_BF16 if dw_dtype == torch.bfloat16 else EPI_STORE_F32, sure=True)
     return dx, dw.t() if tb == b"T" else dw
 
 
