@@ -105,12 +105,12 @@ RowsPlan plan_rows(RowsParams* p, bool gate) {
         p->split = 1;
       }
       // Few small tiles: split K to give every compute unit a workgroup, in
-      // chunks of at least 2048 bytes (128 x 5120 x 13824 int8: 128x128 tiles
-      // 45 us whole, 26 in 6 chunks with the second pass; 64x128 tiles 23.5
-      // in 3).
+      // chunks of at least 2048 bytes (5120 x 13824 int8: 128 rows, 128x128
+      // tiles 45 us whole, 26 in 6 chunks with the second pass, 64x128 tiles
+      // 23.5 in 3; 512 rows, 128x128 tiles 51.4 whole, 128x256 tiles 46.6 in 3).
       const int64_t fill = 256 / ((int64_t)p->tilesM * p->tilesN), by_k = p->K / 2048;
       const int split = (int)(fill < by_k ? fill : by_k);
-      if (t < kRows128 || split < 2) continue;
+      if (split < 2) continue;
       const double cs = grid_cost(p, gate, t, split, 0, end);
       if (cs < best) {
         best = cs;

@@ -523,11 +523,11 @@ hipError_t launch_one(const RowsParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-// (the K dimension is split for the 128-column tiles only)
+// (the K dimension is split for the smaller tiles only)
 template <int BM, int BN>
 hipError_t launch_tile(int type, int epi, bool gate, const RowsParams& p, hipStream_t s) {
   if (epi == kRowsPart) {
-    if constexpr (BN == 128) {
+    if constexpr (BM <= 128) {
       if (type == kRowsI8)
         return gate ? launch_one<OpI8, BM, BN, true, kRowsPart>(p, s)
                     : launch_one<OpI8, BM, BN, false, kRowsPart>(p, s);
