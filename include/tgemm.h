@@ -480,7 +480,8 @@ TGEMM_API int tgemm_validate_gated_i8(char transA, char transB, int64_t M, int64
  * dH bf16 [M, F], dGU bf16 [M, 2F].  GU [M, 2F] as tgemm_run_gated left it
  * (gu_type TGEMM_EPI_STORE_F32), or rounded to bf16 since
  * (TGEMM_EPI_STORE_BF16: half the memory, and a rounding more in the
- * gradients).  No workspace.
+ * gradients).  No workspace.  M times F / 2048, rounded up, below 2^24, else
+ * TGEMM_ERR_UNSUPPORTED.
  */
 TGEMM_API int tgemm_gated_grad(int64_t M, int64_t F, const void* dH, int64_t lddh, const void* GU,
                                int64_t ldgu, int gu_type, int activation, void* dGU, int64_t lddgu,
@@ -503,7 +504,9 @@ TGEMM_API int tgemm_validate_gated_grad(int64_t M, int64_t F, const void* dH, in
  * as for tgemm_gated_grad.  Both products run in one launch.  Workspace: dGU
  * (about 4 * M * F bytes), copies of operands other than A 'N' and B 'T' with
  * 16-byte aligned bases and lda, ldb multiples of 8 (and of A for transB
- * 'N'), and for few tiles fp32 partial products.  K and 2F up to about 2^23.
+ * 'N'), and for few tiles fp32 partial products.  K and 2F up to about 2^23,
+ * M about 2^24 (past 2048 columns of F less: a workgroup per row and 2048
+ * columns), else TGEMM_ERR_UNSUPPORTED.
  */
 TGEMM_API int tgemm_run_gated_backward(char transA, char transB, int64_t M, int64_t F, int64_t K,
                                        const void* A, int64_t lda, const void* B, int64_t ldb,

@@ -89,10 +89,12 @@ struct PackRows {
   int Rz;
   int64_t ldo;
 };
+bool pack_rows_fits(const PackRows& p, int elem);  // the copy's grid is launchable
 hipError_t launch_pack_rows(const PackRows& p, int elem, hipStream_t s);
 
 // dgu = [dh * u * act'(g) | dh * act(g)]; columns 2F .. cols - 1 and rows M
 // .. rows - 1 of dgu are set to zero (rows_finish.hip).
+bool gated_grad_fits(int64_t rows, int64_t F);
 hipError_t launch_gated_grad(const uint16_t* dh, int64_t lddh, const void* gu, int64_t ldgu,
                              bool gu_f32, int M, int64_t F, int act, uint16_t* dgu, int64_t lddgu,
                              int rows, int64_t cols, hipStream_t s);
@@ -105,6 +107,7 @@ hipError_t launch_gated_grad(const uint16_t* dh, int64_t lddh, const void* gu, i
 // partials of a product with more than one chunk go to its ws, and a second
 // launch adds them.
 int gated_bwd_plan(GemmParams* px, GemmParams* pw);
+bool gated_bwd_fits(const GemmParams& px, const GemmParams& pw);
 hipError_t launch_gated_bwd(int tile, const GemmParams& px, const GemmParams& pw, bool f32x,
                             bool f32w, hipStream_t s);
 

@@ -200,7 +200,11 @@ int run_i8(char ta, char tb, const void* A, int64_t lda, const void* B, int64_t 
   const bool packB = is_n(tb) || !rows_aligned(B, ldb, K) || !stride_fits(ldb);
   p.K = packA || packB ? Kp : K;
   const RowsPlan r = plan_rows(&p, gate);
-  if (!grid_fits(p, r, gate)) return TGEMM_ERR_UNSUPPORTED;
+  PackRows ca = {A, lda, is_n(ta), p.M, K, nullptr, p.M, Kp};
+  PackRows cb = {B, ldb, !is_n(tb), p.N, K, nullptr, p.N, Kp};
+  if (!grid_fits(p, r, gate) || (packA && !pack_rows_fits(ca, 1)) ||
+      (packB && !pack_rows_fits(cb, 1)))
+    return TGEMM_ERR_UNSUPPORTED;
   const size_t bytesA = packA ? round256((size_t)p.M * Kp) : 0;
   const size_t bytesB = packB ? round256((size_t)p.N * Kp) : 0;
   const size_t bytesP = p.split > 1 ? (size_t)p.split * p.M * p.N * sizeof(int) : 0;
@@ -215,15 +219,15 @@ int run_i8(char ta, char tb, const void* A, int64_t lda, const void* B, int64_t 
   p.ldb = ldb;
   hipError_t e = hipSuccess;
   if (packA) {
-    int8_t* o = reinterpret_cast<int8_t*>(ws);
-    e = launch_pack_rows({A, lda, is_n(ta), p.M, K, o, p.M, Kp}, 1, s);
-    p.A = reinterpret_cast<const char*>(o);
+    ca.out = ws;
+    e = launch_pack_rows(ca, 1, s);
+    p.A = ws;
     p.lda = Kp;
   }
   if (packB && e == hipSuccess) {
-    int8_t* o = reinterpret_cast<int8_t*>(ws + bytesA);
-    e = launch_pack_rows({B, ldb, !is_n(tb), p.N, K, o, p.N, Kp}, 1, s);
-    p.B = reinterpret_cast<const char*>(o);
+    cb.out = ws + bytesA;
+    e = launch_pack_rows(cb, 1, s);
+    p.B = ws + bytesA;
     p.ldb = Kp;
   }
   if (bytesP) p.part = ws + bytesA + bytesB;
@@ -260,7 +264,11 @@ int run_gated(char ta, char tb, int64_t M, int64_t F, int64_t K, const void* A, 
   if ((packA || packB) && !stride_fits(2 * Kp)) return TGEMM_ERR_UNSUPPORTED;
   p.K = (int)(2 * Kp);
   const RowsPlan r = plan_rows(&p, true);
-  if (!grid_fits(p, r, true)) return TGEMM_ERR_UNSUPPORTED;
+  PackRows ca = {A, lda, is_n(ta), p.M, (int)K, nullptr, p.M, Kp};
+  PackRows cb = {B, ldb, !is_n(tb), p.N, (int)K, nullptr, p.N, Kp};
+  if (!grid_fits(p, r, true) || (packA && !pack_rows_fits(ca, 2)) ||
+      (packB && !pack_rows_fits(cb, 2)))
+    return TGEMM_ERR_UNSUPPORTED;
   const size_t bytesA = packA ? round256((size_t)p.M * Kp * 2) : 0;
   const size_t bytesB = packB ? round256((size_t)p.N * Kp * 2) : 0;
   const size_t bytesP = p.split > 1 ? (size_t)p.split * p.M * p.N * sizeof(float) : 0;
@@ -275,12 +283,14 @@ int run_gated(char ta, char tb, int64_t M, int64_t F, int64_t K, const void* A, 
   p.ldb = 2 * ldb;
   hipError_t e = hipSuccess;
   if (packA) {
-    e = launch_pack_rows({A, lda, is_n(ta), p.M, (int)K, ws, p.M, Kp}, 2, s);
+    ca.out = ws;
+    e = launch_pack_rows(ca, 2, s);
     p.A = ws;
     p.lda = 2 * Kp;
   }
   if (packB && e == hipSuccess) {
-    e = launch_pack_rows({B, ldb, !is_n(tb), p.N, (int)K, ws + bytesA, p.N, Kp}, 2, s);
+    cb.out = ws + bytesA;
+    e = launch_pack_rows(cb, 2, s);
     p.B = ws + bytesA;
     p.ldb = 2 * Kp;
   }
@@ -326,6 +336,11 @@ int run_gated_backward(char ta, char tb, int64_t M, int64_t F, int64_t K, const 
   pw.C = dB;
   pw.ldc = lddb;
   const int tile = gated_bwd_plan(&px, &pw);
+  PackRows ca = {A, lda, is_n(ta), (int)M, (int)K, nullptr, (int)rows, Kp};
+  PackRows cb = {B, ldb, !is_n(tb), (int)N2, (int)K, nullptr, (int)N2, Kp};
+  if (!gated_bwd_fits(px, pw) || !gated_grad_fits(rows, F) || (packA && !pack_rows_fits(ca, 2)) ||
+      (packB && !pack_rows_fits(cb, 2)))
+    return TGEMM_ERR_UNSUPPORTED;
   const size_t bytesX =
       px.splitk > 1 ? round256((size_t)px.splitk * px.M * px.N * sizeof(float)) : 0;
   const size_t bytesW = pw.splitk > 1 ? (size_t)pw.splitk * pw.M * pw.N * sizeof(float) : 0;
@@ -343,13 +358,15 @@ int run_gated_backward(char ta, char tb, int64_t M, int64_t F, int64_t K, const 
                                    F, act, G, ldg, (int)rows, ldg, s);
   const void *Ar = A, *Br = B;  // [M][K], [2F][K] rows
   if (packA && e == hipSuccess) {
-    e = launch_pack_rows({A, lda, is_n(ta), (int)M, (int)K, ws, (int)rows, Kp}, 2, s);
+    ca.out = ws;
+    e = launch_pack_rows(ca, 2, s);
     Ar = ws;
     lda = Kp;
   }
   ws += bytesA;
   if (packB && e == hipSuccess) {
-    e = launch_pack_rows({B, ldb, !is_n(tb), (int)N2, (int)K, ws, (int)N2, Kp}, 2, s);
+    cb.out = ws;
+    e = launch_pack_rows(cb, 2, s);
     Br = ws;
     ldb = Kp;
   }

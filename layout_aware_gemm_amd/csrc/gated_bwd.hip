@@ -215,11 +215,18 @@ int gated_bwd_plan(GemmParams* px, GemmParams* pw) {
   return t;
 }
 
+namespace {
+int64_t grid_of(const GemmParams& p) { return (int64_t)p.tilesM * p.tilesN * p.splitk; }
+}  // namespace
+
+bool gated_bwd_fits(const GemmParams& px, const GemmParams& pw) {
+  return grid_of(px) + grid_of(pw) + 8 <= kMaxWorkgroups;
+}
+
 hipError_t launch_gated_bwd(int tile, const GemmParams& px, const GemmParams& pw, bool f32x,
                             bool f32w, hipStream_t s) {
-  const int64_t nx = (int64_t)px.tilesM * px.tilesN * px.splitk;
-  const int64_t nw = (int64_t)pw.tilesM * pw.tilesN * pw.splitk;
-  if (nx + nw + 8 > kMaxWorkgroups) return hipErrorInvalidValue;
+  if (!gated_bwd_fits(px, pw)) return hipErrorInvalidValue;
+  const int64_t nx = grid_of(px), nw = grid_of(pw);
   const int wfirst = pw.kchunk > px.kchunk;
   const int nfirst = (int)(((wfirst ? nw : nx) + 7) / 8 * 8);
   const dim3 grid((unsigned)(nfirst + (wfirst ? nx : nw))), block(kThreads);

@@ -232,23 +232,42 @@ hipError_t launch_rows_finish(int type, int epi, const RowsParams& p, hipStream_
   return hipErrorInvalidValue;
 }
 
+namespace {
+// workgroups of a copy, of the gradient pass
+int64_t pack_blocks(const PackRows& p, int elem) {
+  if (p.k_contiguous) return ((int64_t)p.Rz * (p.ldo * elem / 16) + kThr - 1) / kThr;
+  return (int64_t)ceil_div(p.ldo, 64) * ceil_div(p.Rz, 64);
+}
+// (the padding of a row, less than 64 elements, needs at most 8 threads)
+int64_t grad_blocks_per_row(int64_t F) {
+  const int64_t chunks = (F + 7) / 8 > 8 ? (F + 7) / 8 : 8;
+  return (chunks + kThr - 1) / kThr;
+}
+}  // namespace
+
+bool pack_rows_fits(const PackRows& p, int elem) {
+  return pack_blocks(p, elem) <= kMaxWorkgroups;
+}
+
+bool gated_grad_fits(int64_t rows, int64_t F) {
+  return rows * grad_blocks_per_row(F) <= kMaxWorkgroups;
+}
+
 hipError_t launch_pack_rows(const PackRows& p, int elem, hipStream_t s) {
+  if (!pack_rows_fits(p, elem)) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)pack_blocks(p, elem));
   if (p.k_contiguous) {
     const int chunks = (int)(p.ldo * elem / 16);
-    const int64_t blocks = ((int64_t)p.Rz * chunks + kThr - 1) / kThr;
-    if (blocks > kMaxWorkgroups) return hipErrorInvalidValue;
     if (elem == 1)
-      hipLaunchKernelGGL(pack_rows_kernel<1>, dim3((unsigned)blocks), dim3(kThr), 0, s, p, chunks);
+      hipLaunchKernelGGL(pack_rows_kernel<1>, grid, dim3(kThr), 0, s, p, chunks);
     else
-      hipLaunchKernelGGL(pack_rows_kernel<2>, dim3((unsigned)blocks), dim3(kThr), 0, s, p, chunks);
+      hipLaunchKernelGGL(pack_rows_kernel<2>, grid, dim3(kThr), 0, s, p, chunks);
   } else {
     const int kblocks = ceil_div(p.ldo, 64);
-    const int64_t blocks = (int64_t)kblocks * ceil_div(p.Rz, 64);
-    if (blocks > kMaxWorkgroups) return hipErrorInvalidValue;
     if (elem == 1)
-      hipLaunchKernelGGL(pack_cols_kernel<1>, dim3((unsigned)blocks), dim3(kThr), 0, s, p, kblocks);
+      hipLaunchKernelGGL(pack_cols_kernel<1>, grid, dim3(kThr), 0, s, p, kblocks);
     else
-      hipLaunchKernelGGL(pack_cols_kernel<2>, dim3((unsigned)blocks), dim3(kThr), 0, s, p, kblocks);
+      hipLaunchKernelGGL(pack_cols_kernel<2>, grid, dim3(kThr), 0, s, p, kblocks);
   }
   return hipGetLastError();
 }
@@ -256,10 +275,8 @@ hipError_t launch_pack_rows(const PackRows& p, int elem, hipStream_t s) {
 hipError_t launch_gated_grad(const uint16_t* dh, int64_t lddh, const void* gu, int64_t ldgu,
                              bool gu_f32, int M, int64_t F, int act, uint16_t* dgu, int64_t lddgu,
                              int rows, int64_t cols, hipStream_t s) {
-  // (the padding of a row, cols - 2F < 64 elements, needs at most 8 threads)
-  const int64_t chunks = (F + 7) / 8 > 8 ? (F + 7) / 8 : 8;
-  const int64_t per_row = (chunks + kThr - 1) / kThr;
-  if (rows * per_row > kMaxWorkgroups) return hipErrorInvalidValue;
+  if (!gated_grad_fits(rows, F)) return hipErrorInvalidValue;
+  const int64_t per_row = grad_blocks_per_row(F);
   const dim3 grid((unsigned)(rows * per_row));
   if (gu_f32)
     hipLaunchKernelGGL(gated_grad_kernel<float>, grid, dim3(kThr), 0, s, dh, lddh,

@@ -229,3 +229,16 @@ def test_binding_refuses():
             bad()
     with pytest.raises(ValueError):
         tgemm._act("relu")
+
+
+def test_grids_past_the_limit_are_refused():
+    """Copies and gradient passes too large for one launch: the calls say so
+    before anything is enqueued (the queries run the same checks)."""
+    L = tgemm.lib()
+    N, T, P = tgemm._flag("N"), tgemm._flag("T"), 1 << 20
+    big = 1 << 25
+    assert L.tgemm_i8_workspace_bytes(N, N, 4, big, 131071, P, 131071, P, big) == UNS
+    assert L.tgemm_i8_workspace_bytes(N, T, 4, 1 << 17, 131071, P, 131071, P, 131071) > 0
+    assert L.tgemm_gated_workspace_bytes(N, N, 4, big, 131072, P, 131072, P, 2 * big) == UNS
+    assert L.tgemm_gated_backward_workspace_bytes(N, T, (1 << 24) + 64, 8, 8, P, 8, P, 8) == UNS
+    assert L.tgemm_gated_backward_workspace_bytes(N, T, 1 << 23, 8, 8, P, 8, P, 8) > 0
