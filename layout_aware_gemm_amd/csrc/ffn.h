@@ -58,6 +58,21 @@ inline bool rows_aligned(const void* p, int64_t ld_bytes, int64_t k_bytes) {
   return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)ld_bytes | (uintptr_t)k_bytes) & 15) == 0;
 }
 
+// Products of up to 64 rows read the weight once, and load it non-temporally
+// (auxiliary bit 1 of a buffer load) where it cannot stay in the 256 MB
+// last-level cache beside its neighbours until the next call, from
+// kCacheShare bytes on.  Cold weights (us, without and with; int8 unless
+// bf16): 8 x 32000 x 4096 28.4 / 26.1, gated 13824 x 5120 16 rows 30.7 / 27.7,
+// 32 rows 34.2 / 32.9, one row bf16 52.4 / 47.9.  A smaller weight gains less
+// cold (1 x 5120 x 13824 16.2 / 15.4) than it loses where it would have stayed
+// in the cache (12.5 / 15.3); 96 and 128 rows gain 2 to 4% at most (gated 128
+// rows 43.6 / 42.6) and lose up to 8% (96 x 8192 x 13824 34.2 / 37.1).
+constexpr int kNonTemporal = 2;
+constexpr int64_t kCacheShare = int64_t(96) << 20;
+inline bool streams_past_cache(const RowsParams& p) {
+  return (int64_t)p.N * p.K >= kCacheShare;
+}
+
 // Output tile shapes of the large-product kernel.
 enum RowsTile : int { kRows256 = 0, kRows128x256 = 1, kRows128 = 2, kRows64 = 3 };
 inline int rows_tile_m(int t) { return t == kRows256 ? 256 : t == kRows64 ? 64 : 128; }

@@ -61,7 +61,8 @@ constexpr int kRowBytes = 128;  // bytes of K per k-step (one LDS row)
 // This wave's share of one panel's copies: R tile rows, 1 KB (8 rows) per
 // copy.  Tile row r is row r of the operand, or with GATE row
 // (r >> 6) * 32 + (r & 31) of its gate (r & 32 == 0) or up half.
-template <int R, bool GATE>
+// AUX: the loads' cache policy.
+template <int R, bool GATE, int AUX = 0>
 struct RowsPanel {
   static constexpr int PER_WAVE = R / 32;
   static_assert(PER_WAVE == 4 || PER_WAVE == 8 || (PER_WAVE == 2 && !GATE),
@@ -133,7 +134,7 @@ struct RowsPanel {
 #if defined(__HIP_DEVICE_COMPILE__)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         rs[GATE && PER_WAVE == 8 ? (j >> 2) : 0],
-        (__attribute__((address_space(3))) void*)(panel + blk * 512), 16, (int)off, 0, 0, 0);
+        (__attribute__((address_space(3))) void*)(panel + blk * 512), 16, (int)off, 0, 0, AUX);
 #else
     (void)panel, (void)blk, (void)off;
 #endif
@@ -334,7 +335,8 @@ __device__ __forceinline__ void keep_epilogue(const RowsParams& p,
   }
 }
 
-template <class Op, int BM, int BN, bool GATE, int EPI>
+// ONCE: B is loaded non-temporally (one row of tiles only).
+template <class Op, int BM, int BN, bool GATE, int EPI, bool ONCE>
 __global__ void __launch_bounds__(kThreads, 1) rows_kernel(RowsParams p) {
   constexpr bool SCALED = std::is_same<Op, OpI8>::value && EPI != kRowsPart;
   constexpr int FM = BM / 64, FN = BN / 64;
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(RowsParams p) {
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
 
   RowsPanel<BM, false> da;
-  RowsPanel<BN, GATE> db;
+  RowsPanel<BN, GATE, ONCE ? kNonTemporal : 0> db;
   da.init(p.A, p.lda, p.M, m0, kb, kend, wave_u, lane);
   db.init(p.B, p.ldb, GATE ? p.F : p.N, n0, kb, kend, wave_u, lane);
 
@@ -519,7 +521,13 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(RowsParams p) {
 template <class Op, int BM, int BN, bool GATE, int EPI>
 hipError_t launch_one(const RowsParams& p, hipStream_t s) {
   const dim3 grid(p.tilesM * p.tilesN * p.split), block(kThreads);
-  hipLaunchKernelGGL((rows_kernel<Op, BM, BN, GATE, EPI>), grid, block, 0, s, p);
+  if constexpr (BM == 64) {
+    if (p.tilesM == 1 && streams_past_cache(p)) {
+      hipLaunchKernelGGL((rows_kernel<Op, BM, BN, GATE, EPI, true>), grid, block, 0, s, p);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((rows_kernel<Op, BM, BN, GATE, EPI, false>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 

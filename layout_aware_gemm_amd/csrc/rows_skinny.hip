@@ -53,8 +53,8 @@ constexpr int kStep = 128;  // bytes of K per row and step
 
 // TB groups of 8 tokens, NB blocks of 16 weight rows per wave (GATE: the
 // first half gate rows, the second half the up rows of the same outputs),
-// W waves.
-template <class Op, int TB, int NB, int W, bool GATE, int EPI>
+// W waves.  ONCE: non-temporal weight loads.
+template <class Op, int TB, int NB, int W, bool GATE, int EPI, bool ONCE>
 __global__ void __launch_bounds__(W * 64) skinny_kernel(RowsParams p) {
   constexpr bool I8 = std::is_same<Op, SkI8>::value;
   constexpr int NO = GATE ? NB / 2 : NB;  // blocks of 16 outputs
@@ -106,7 +106,8 @@ __global__ void __launch_bounds__(W * 64) skinny_kernel(RowsParams p) {
     for (int b = 0; b < 2 * NB; ++b)
       wv[b] = __builtin_bit_cast(
           i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rw[GATE ? b / (2 * NO) : 0],
-                                                         (int)(woff[b % (2 * NO)] + ko), 0, 0));
+                                                         (int)(woff[b % (2 * NO)] + ko), 0,
+                                                         ONCE ? kNonTemporal : 0));
 #pragma unroll
     for (int t = 0; t < TB; ++t)
       av[t] = __builtin_bit_cast(
@@ -210,8 +211,11 @@ template <class Op, int TB, int NB, int W, bool GATE, int EPI>
 hipError_t launch_one(const RowsParams& p, hipStream_t s) {
   constexpr int NO = GATE ? NB / 2 : NB;
   const int nblk = ceil_div(GATE ? p.F : p.N, 16 * NO);
-  hipLaunchKernelGGL((skinny_kernel<Op, TB, NB, W, GATE, EPI>), dim3(nblk), dim3(W * 64), 0, s,
-                     p);
+  const dim3 grid(nblk), block(W * 64);
+  if (streams_past_cache(p))
+    hipLaunchKernelGGL((skinny_kernel<Op, TB, NB, W, GATE, EPI, true>), grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL((skinny_kernel<Op, TB, NB, W, GATE, EPI, false>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 

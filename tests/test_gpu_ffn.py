@@ -172,6 +172,7 @@ I8_SHAPES = [(1, 1, 16), (1, 16, 48), (1, 1000, 4096), (1, 300, 13824), (5, 17, 
              (2050, 4200, 400), (520, 32000, 144),  # (256x256 tiles; a tail of smaller ones)
              (100, 20001, 144), (100, 5503, 10256),  # (128x128 tiles, whole and in K chunks)
              (130, 5003, 20496),  # (128x256 tiles in K chunks)
+             (5, 6151, 16400),  # (a weight loaded past the cache)
              (2300, 7268, 1040), (2300, 8418, 1040), (2300, 9698, 1040)]  # (each size of tail)
 
 
@@ -257,7 +258,8 @@ def act_bounds(gu, eg, eu, kind):
                                    (1030, 2100, 96), (3, 20, 33), (90, 70, 65), (24, 12300, 48),
                                    (64, 12289, 144), (2100, 2060, 160), (4096, 2100, 48),
                                    (100, 10001, 144), (100, 2751, 10256), (2300, 3634, 1040),
-                                   (2300, 4849, 1040), (130, 2501, 20496)])
+                                   (2300, 4849, 1040), (130, 2501, 20496),
+                                   (3, 3079, 16400), (20, 10250, 4912)])
 @pytest.mark.parametrize("kind", ["silu", "gelu_tanh"])
 def test_gated_i8(M, F, K, kind):
     print(f"gated i8 {M}x{F}x{K} {kind}", flush=True)
@@ -279,7 +281,7 @@ GATED = [(1, 1, 8, "NT", 0), (1, 1000, 2048, "NT", 0), (1, 500, 8192, "NT", 0),
          (100, 64, 136, "TT", 0), (2, 3, 1, "NT", 0), (30, 12300, 40, "NT", 0),
          (2100, 2060, 72, "NT", 0), (4096, 2100, 24, "NT", 0), (100, 10001, 72, "NT", 0),
          (100, 2751, 5128, "NT", 0), (2300, 3634, 520, "NT", 0), (2300, 4849, 520, "NT", 0),
-         (130, 2501, 10248, "NT", 0)]
+         (130, 2501, 10248, "NT", 0), (3, 3079, 8200, "NT", 0), (20, 10250, 2456, "NT", 0)]
 
 
 @pytest.mark.parametrize("M,F,K,layout,pad", GATED)
