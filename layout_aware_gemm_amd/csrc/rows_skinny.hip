@@ -16,8 +16,9 @@
 // never split over workgroups: the second pass costs more than the idle
 // compute units of a small weight (2048 x 8192: 6 us in all).
 //
-// Measured (MI355X, HBM-resident weights): 5.2 to 5.7 TB/s of weight for up
-// to 16 tokens, where a large copy reaches 4.7.
+// Measured (MI355X) for up to 16 tokens: cold weights of 67 to 283 MB 4.4 to
+// 5.9 TB/s, where a large copy reaches 4.7; a 71 MB weight that stayed in the
+// last-level cache 5.7.
 #include "ffn.h"
 #include "gemm_kernel.h"
 
@@ -228,8 +229,9 @@ hipError_t launch_few(const RowsParams& p, hipStream_t s) {
 }
 
 // Blocks of weight rows per wave and waves per workgroup, by the number of
-// tokens and of blocks (us on MI355X; int8, N x K = 5120 x 13824 / 32000 x
-// 4096, then gated 13824 x 5120 int8 / bf16):
+// tokens and of blocks (us on MI355X; int8, N x K = 5120 x 13824, its 71 MB
+// partly in the last-level cache / 32000 x 4096, then gated 13824 x 5120 int8
+// / bf16):
 //   one token    two blocks (gated four), 8 waves   12.4  27.9  28.6  52.3
 //                half the blocks                    12.9  26.9  29.6  54.5
 //                half the waves                     14.4  31.0  28.9  52.2
@@ -238,16 +240,23 @@ hipError_t launch_few(const RowsParams& p, hipStream_t s) {
 //   64 tokens    two (four), 8 waves                19.7  44.9  42.1  73.1
 //                the same, 4 waves                  20.1  43.0  40.5  71.5
 //                four, 4 waves                      27.4  36.9
-// Fewer than 128 such blocks leave compute units idle, and half the blocks
-// win (2048 x 4096: 4.6 against 4.9; 1024 x 16384: 8.6 against 9.6).
+// Up to 128 blocks leave half the compute units idle, and half the blocks win
+// (cold weights, 1 / 16 / 32 tokens, whole then half: int8 4096 x 4096 6.4 /
+// 7.1 / 8.2, 6.1 / 6.4 / 7.0; gated bf16 4096 x 4096 17.0 / 17.7 / 20.2, 15.7 /
+// 15.8 / 16.6).  About one block per compute unit gives it, halved, two that
+// overlap, which pays where every unit has two and the step is a gated one's
+// (gated bf16 8192 x 2048 18.0 / 17.6 / 18.2, 16.2 / 16.1 / 17.3; 7168 x 4096
+// 24.9 / 25.6 / 25.9, 22.2 / 24.0 / 26.8; but 5504 x 4096 20.6 / 21.5 / 23.4,
+// 21.4 / 23.2 / 24.9, and int8 8192 x 4096 9.3 / 9.6 / 10.2, 9.1 / 9.9 / 11.3).
 template <class Op, bool GATE, int EPI>
 hipError_t launch_blocks(const RowsParams& p, hipStream_t s) {
   constexpr int NB = GATE ? 4 : 2;
   const int nout = GATE ? p.F : p.N;
-  const bool small = ceil_div(nout, 32) < 128;
+  const int blocks = ceil_div(nout, 32);
+  const bool half = blocks <= 128 || (GATE && blocks > 208 && blocks <= 256);
   if (p.M <= 32)
-    return small ? launch_few<Op, NB / 2, GATE, EPI>(p, s) : launch_few<Op, NB, GATE, EPI>(p, s);
-  if (small) return launch_one<Op, 8, NB / 2, 8, GATE, EPI>(p, s);
+    return half ? launch_few<Op, NB / 2, GATE, EPI>(p, s) : launch_few<Op, NB, GATE, EPI>(p, s);
+  if (blocks < 128) return launch_one<Op, 8, NB / 2, 8, GATE, EPI>(p, s);
   if constexpr (!GATE) {
     if (ceil_div(nout, 64) >= 256) return launch_one<Op, 8, 4, 4, GATE, EPI>(p, s);
   }

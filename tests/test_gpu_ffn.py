@@ -173,6 +173,8 @@ I8_SHAPES = [(1, 1, 16), (1, 16, 48), (1, 1000, 4096), (1, 300, 13824), (5, 17, 
              (100, 20001, 144), (100, 5503, 10256),  # (128x128 tiles, whole and in K chunks)
              (130, 5003, 20496),  # (128x256 tiles in K chunks)
              (5, 6151, 16400),  # (a weight loaded past the cache)
+             # few rows: whole and half blocks of weight rows, and wide ones
+             (1, 4200, 80), (16, 4200, 80), (30, 5001, 48), (64, 4200, 80), (50, 17001, 48),
              (2300, 7268, 1040), (2300, 8418, 1040), (2300, 9698, 1040)]  # (each size of tail)
 
 
@@ -259,7 +261,9 @@ def act_bounds(gu, eg, eu, kind):
                                    (64, 12289, 144), (2100, 2060, 160), (4096, 2100, 48),
                                    (100, 10001, 144), (100, 2751, 10256), (2300, 3634, 1040),
                                    (2300, 4849, 1040), (130, 2501, 20496),
-                                   (3, 3079, 16400), (20, 10250, 4912)])
+                                   (3, 3079, 16400), (20, 10250, 4912), (2, 4200, 12000),
+                                   (1, 4201, 80), (9, 8300, 80), (30, 4200, 80), (50, 4200, 144),
+                                   (7, 7001, 272)])
 @pytest.mark.parametrize("kind", ["silu", "gelu_tanh"])
 def test_gated_i8(M, F, K, kind):
     print(f"gated i8 {M}x{F}x{K} {kind}", flush=True)
@@ -281,7 +285,9 @@ GATED = [(1, 1, 8, "NT", 0), (1, 1000, 2048, "NT", 0), (1, 500, 8192, "NT", 0),
          (100, 64, 136, "TT", 0), (2, 3, 1, "NT", 0), (30, 12300, 40, "NT", 0),
          (2100, 2060, 72, "NT", 0), (4096, 2100, 24, "NT", 0), (100, 10001, 72, "NT", 0),
          (100, 2751, 5128, "NT", 0), (2300, 3634, 520, "NT", 0), (2300, 4849, 520, "NT", 0),
-         (130, 2501, 10248, "NT", 0), (3, 3079, 8200, "NT", 0), (20, 10250, 2456, "NT", 0)]
+         (130, 2501, 10248, "NT", 0), (3, 3079, 8200, "NT", 0), (20, 10250, 2456, "NT", 0),
+         (1, 4201, 40, "NT", 0), (9, 8300, 40, "NT", 0), (30, 4200, 40, "NT", 0),
+         (50, 4200, 72, "NT", 0), (7, 7001, 136, "NT", 0)]
 
 
 @pytest.mark.parametrize("M,F,K,layout,pad", GATED)
