@@ -521,7 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(RowsParams p) {
 template <class Op, int BM, int BN, bool GATE, int EPI>
 hipError_t launch_one(const RowsParams& p, hipStream_t s) {
   const dim3 grid(p.tilesM * p.tilesN * p.split), block(kThreads);
-  if constexpr (BM == 64) {
+  // (one row of 64-row tiles: only gated products, whole in K, come here)
+  if constexpr (BM == 64 && GATE && EPI != kRowsPart) {
     if (p.tilesM == 1 && streams_past_cache(p)) {
       hipLaunchKernelGGL((rows_kernel<Op, BM, BN, GATE, EPI, true>), grid, block, 0, s, p);
       return hipGetLastError();
