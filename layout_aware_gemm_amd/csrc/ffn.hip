@@ -530,7 +530,8 @@ extern "C" int tgemm_run_gated_backward(char transA, char transB, int64_t M, int
   if (st != TGEMM_OK) return st;
   return no_throw([&] {
     return run_gated_backward(transA, transB, M, F, K, A, lda, B, ldb, dH, lddh, GU, ldgu,
-                              gu_type == TGEMM_EPI_STORE_F32, activation, dA, ldda, dB, lddb, epilogue == TGEMM_EPI_STORE_F32,
+                              gu_type == TGEMM_EPI_STORE_F32, activation, dA, ldda, dB, lddb,
+                              epilogue == TGEMM_EPI_STORE_F32,
                               {workspace, workspace_bytes, nullptr},
                               reinterpret_cast<hipStream_t>(stream));
   });
@@ -542,7 +543,8 @@ extern "C" int64_t tgemm_gated_backward_workspace_bytes(char transA, char transB
   const int64_t ldd = transB == 'N' || transB == 'n' ? 2 * F : K;
   const int st =
       tgemm_validate_gated_backward(transA, transB, M, F, K, A, lda, B, ldb, g_any, F, g_any, 2 * F,
-                                    TGEMM_EPI_STORE_BF16, TGEMM_ACT_SILU, g_any, K, g_any, ldd, TGEMM_EPI_STORE_BF16);
+                                    TGEMM_EPI_STORE_BF16, TGEMM_ACT_SILU, g_any, K, g_any, ldd,
+                                    TGEMM_EPI_STORE_BF16);
   if (st != TGEMM_OK) return st;
   int64_t need = 0;
   return queried(no_throw([&] {

@@ -25,10 +25,11 @@ namespace {
 // Store a wave's block of a T x T tile, a quarter of it (accumulator layout
 // as in the GEMM's epilogues) through LDS words of its own, 32 rows at a
 // time: rows leave as 128 to 512 contiguous bytes, and each accumulator is
-// used in one place only.  (Stored from registers under the tests for the edge and the
-// type, they were copied out of the matrix cores' registers all at once, and
-// some of them through scratch.)  With 8 words of padding per row the two
-// halves of a wave, four rows apart, write to different halves of the banks.
+// used in one place only.  (Stored from registers under the tests for the
+// edge and the type, they were copied out of the matrix cores' registers all
+// at once, and some of them through scratch.)  With 8 words of padding per
+// row the two halves of a wave, four rows apart, write to different halves of
+// the banks.
 template <int T>
 constexpr int out_row() {
   return T / 2 + 8;
