@@ -1,0 +1,59 @@
+"""The feed-forward operators where their other tests do not reach: the
+gradient's large tiles in every layout.
+
+Bounds as in test_gpu_ffn (u32 = 2^-24, ub = 2^-8).
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import workloads
+from layout_aware_gemm_amd import tgemm
+from parity_util import dev
+from test_gpu_ffn import BF, U32, UB, f64, gen, within
+
+pytestmark = pytest.mark.gpu
+
+
+def framed(n, k, seed, std):
+    """bf16 [n, k] on the GPU between NaNs: what lies behind each row."""
+    buf = torch.full((n, (k + 15) // 8 * 8), float("nan"), dtype=BF)
+    buf[:, :k] = workloads.randn_bf16((n, k), std, gen(seed))
+    return buf.to(dev())[:, :k]
+
+
+def operands(M, F, K, layout):
+    x = framed(M, K, 1, 1.0) if layout[0] == "N" else framed(K, M, 1, 1.0).t()
+    w = framed(K, 2 * F, 2, K ** -0.5) if layout[1] == "N" else framed(2 * F, K, 2, K ** -0.5).t()
+    return x, w, framed(M, F, 3, 1.0)
+
+
+def product(got, p, ep, q, n, out_u):
+    """got against p @ q for |p error| <= ep and an fp32 sum of n terms."""
+    r, m = p @ q, (ep * 1.01 + n * 1.01 * U32 * np.abs(p)) @ np.abs(q)
+    within(got, r, m * 1.01 + out_u * (np.abs(r) + m))
+
+
+# 256x256 tiles from 60 k-steps of them per compute unit on: 15360 in all.
+# These have 15487 (3 x 17 tiles of 157 and 40 x 17 of 11), 15807 and 16065.
+@pytest.mark.parametrize("M,F,K", [(707, 5003, 4101), (4099, 5000, 700), (65, 20100, 4100)])
+@pytest.mark.parametrize("layout", ["NT", "NN", "TN", "TT"])
+def test_gradient_large_tiles(M, F, K, layout):
+    """Both gradient products by value on the large tiles: dB stored [K][2F]
+    is the product with its operands exchanged."""
+    print(f"gradient {layout} {M}x{F}x{K}", flush=True)
+    x, w, dh = operands(M, F, K, layout)
+    gu = tgemm.gated_matmul(x, w, save=True)[1]
+    dx, dw = tgemm.gated_backward(dh, gu, x, w, dw_dtype=torch.float32)
+    G, D, X, W = f64(gu), f64(dh), f64(x), f64(w)
+    dgu = oracle.ffn.gated_grad(D, G, "silu")
+    # dgu: ub of itself, and fp32 terms below 2^-18 of |dh| (|u| + |act|):
+    # |s| < 30 here, so (3 |s| + 12) 2 u32 (1 + |g|) < 2^-18 (1 + |g|)
+    big = np.abs(D) * (1 + np.abs(G[:, :F])) * (np.abs(G[:, F:]) + np.abs(G[:, :F]))
+    eg = UB * np.abs(dgu) + 2.0 ** -18 * np.concatenate([big, big], 1)
+    product(dx, dgu, eg, W.T, 2 * F, UB)
+    product(dw.t(), dgu.T, eg.T, X, M, U32)
+    dx2, dw2 = tgemm.gated_backward(dh, gu, x, w)
+    assert torch.equal(dx, dx2) and torch.equal(dw.to(BF), dw2)
