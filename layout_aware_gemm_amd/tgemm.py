@@ -794,7 +794,8 @@ def gated_backward(dh, gu, x, w, act="silu", dw_dtype=torch.bfloat16, stream=Non
     """Gradients (dx [..., K] bf16, dw [K, 2F]) of ``gated_matmul`` for the
     gradient ``dh`` bf16 [..., F] of h; ``gu`` as the forward saved it (or
     cast to bf16: a rounding more in the gradients), ``x`` and ``w`` its
-    operands.  dw has w's layout (for ``W.t()``, dw.t() is the
+    operands.  The gradient of gu is rounded to bf16, the type both products
+    read it in; their sums are fp32.  dw has w's layout (for ``W.t()``, dw.t() is the
     contiguous [2F, K] gradient of W) and ``dw_dtype`` (bf16 or fp32)."""
     F = _gate_width(w)
     x2, ta, lda, tb, ldb = _product(x, w, torch.bfloat16, "gated_backward")

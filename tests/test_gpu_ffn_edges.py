@@ -1,5 +1,5 @@
 """The feed-forward operators where their other tests do not reach: the
-gradient's large tiles in every layout.
+gradient's large tiles in every layout, and what its error is made of.
 
 Bounds as in test_gpu_ffn (u32 = 2^-24, ub = 2^-8).
 """
@@ -30,6 +30,15 @@ def operands(M, F, K, layout):
     return x, w, framed(M, F, 3, 1.0)
 
 
+def rounded_dgu(dh, gu, kind):
+    """dGU in bf16 as the elementwise gradient leaves it."""
+    M, F = dh.shape
+    out = torch.empty(M, 2 * F, dtype=BF, device=dev())
+    tgemm._call("tgemm_gated_grad", dev(), M, F, dh.data_ptr(), dh.stride(0), gu.data_ptr(), 2 * F,
+                tgemm.EPI_STORE_F32, tgemm._act(kind), out.data_ptr(), 2 * F)
+    return out
+
+
 def product(got, p, ep, q, n, out_u):
     """got against p @ q for |p error| <= ep and an fp32 sum of n terms."""
     r, m = p @ q, (ep * 1.01 + n * 1.01 * U32 * np.abs(p)) @ np.abs(q)
@@ -57,3 +66,18 @@ def test_gradient_large_tiles(M, F, K, layout):
     product(dw.t(), dgu.T, eg.T, X, M, U32)
     dx2, dw2 = tgemm.gated_backward(dh, gu, x, w)
     assert torch.equal(dx, dx2) and torch.equal(dw.to(BF), dw2)
+
+
+@pytest.mark.parametrize("M,F,K,layout", [(333, 1000, 520, "NT"), (130, 70, 72, "TN"),
+                                          (707, 5003, 4101, "NT")])
+@pytest.mark.parametrize("kind", ["silu", "gelu_tanh"])
+def test_gradient_is_the_product_of_the_rounded_dgu(M, F, K, layout, kind):
+    """dX and dW against exact products of the bf16 dGU: beside that one
+    rounding there are the fp32 sums and the outputs' own rounding, no more."""
+    print(f"rounded dgu {layout} {M}x{F}x{K} {kind}", flush=True)
+    x, w, dh = operands(M, F, K, layout)
+    gu = tgemm.gated_matmul(x, w, act=kind, save=True)[1]
+    dx, dw = tgemm.gated_backward(dh, gu, x, w, act=kind, dw_dtype=torch.float32)
+    dgu = f64(rounded_dgu(dh, gu, kind))
+    product(dx, dgu, 0 * dgu, f64(w).T, 2 * F, UB)
+    product(dw.t(), dgu.T, 0 * dgu.T, f64(x), M, U32)
