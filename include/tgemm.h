@@ -73,8 +73,9 @@
  *   The library keeps one workspace buffer per (device, stream): calls on
  *   a stream run in order and reuse it; it grows with hipFreeAsync /
  *   hipMallocAsync on that stream, so calls on different streams never
- *   share memory.  While `stream` is being captured into a graph the call
- *   allocates and frees its own buffer in stream order instead.
+ *   share memory.  While `stream` is being captured into a graph, its calls
+ *   take a buffer of that capture instead (device memory allocated beside
+ *   the capture; a replay allocates nothing).  Graphs never share one.
  *
  * Threads
  *   tgemm_run may be called from several host threads, on the same stream
@@ -89,7 +90,10 @@
  *   tgemm_release_workspace(stream) frees it; a program that creates many
  *   short-lived streams should release each one's buffer before destroying
  *   the stream.  A stream must not be destroyed while a tgemm call on it is
- *   still executing.
+ *   still executing.  A capture's buffer is held until the process ends,
+ *   for a graph may be replayed at any time: one per capture with a call
+ *   that needs workspace (a program that captures anew without end takes
+ *   tgemm_run_noalloc).
  */
 #ifndef TGEMM_H
 #define TGEMM_H
@@ -344,7 +348,7 @@ TGEMM_API int tgemm_validate_rope_region(const void* q, int64_t ldq, int64_t P, 
  * then ignored) takes the library's buffer of the stream, as tgemm_run does,
  * except while the stream is being captured into a graph: then a call that
  * needs workspace fails with TGEMM_ERR_WORKSPACE_LIMIT, and the caller has to
- * bring its own, so that a replayed graph never allocates.  The
+ * bring its own, which lives and dies with the caller's graph.  The
  * ..._workspace_bytes functions return a negative tgemm_status for invalid
  * arguments; they look at the operands' addresses, strides and layouts, not
  * at their contents, and enqueue nothing.

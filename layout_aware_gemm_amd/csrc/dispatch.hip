@@ -109,10 +109,17 @@ int status_of(hipError_t e) { return e == hipSuccess ? TGEMM_OK : TGEMM_ERR_HIP;
 // the lookup until its last kernel is enqueued, so two host threads that
 // share a stream cannot grow (and free) a buffer the other has handed to
 // kernels it has not yet enqueued.  Calls on different streams never share
-// a buffer.  While the stream is being captured into a graph, a call gets a
-// buffer of its own that is freed in stream order at its end (the graph
-// owns it).  Cached buffers live until the process ends or until
+// a buffer.  Cached buffers live until the process ends or until
 // tgemm_release_workspace.
+//
+// While the stream is being captured into a graph, the buffer belongs to
+// (device, stream, capture): the calls captured on one stream run in order
+// in the graph and share it, two graphs never do, and the eager calls' buffer
+// is left alone.  It is ordinary device memory, allocated beside the capture
+// (so the graph holds kernels only and a replay allocates nothing) and held
+// until the process ends, since a graph may be replayed at any time.  A
+// captured call that needs more than the capture's buffer holds gets a
+// larger one; the calls before it keep theirs.
 //
 // tgemm_run_noalloc: the fixed device array `scratch` below, one per
 // device, found once per device with hipGetSymbolAddress; no allocation.
@@ -120,13 +127,26 @@ int status_of(hipError_t e) { return e == hipSuccess ? TGEMM_OK : TGEMM_ERR_HIP;
 struct WsEntry {
   int dev;
   hipStream_t stream;
+  unsigned long long capture;  // 0: the eager calls' buffer
   void* ptr;
   size_t bytes;
   std::mutex mu;
 };
 
-std::mutex g_ws_mu;                               // guards the list itself
-std::vector<std::unique_ptr<WsEntry>> g_ws;       // entries never move or go away
+std::mutex g_ws_mu;  // guards the lists themselves
+// entries never move or go away; the captures' have a list of their own, so
+// that eager calls do not search it
+std::vector<std::unique_ptr<WsEntry>> g_ws, g_capture_ws;
+
+// Ordinary device memory while a stream of this thread is being captured.
+hipError_t malloc_beside_capture(void** p, size_t bytes) {
+  hipStreamCaptureMode mode = hipStreamCaptureModeRelaxed;
+  hipError_t e = hipThreadExchangeStreamCaptureMode(&mode);
+  if (e != hipSuccess) return e;
+  e = hipMalloc(p, bytes);
+  const hipError_t back = hipThreadExchangeStreamCaptureMode(&mode);
+  return e != hipSuccess ? e : back;
+}
 
 // (the array `scratch` is defined at file scope, below the anonymous
 // namespace)
@@ -161,32 +181,30 @@ int scratch_address(void** out) {
 // failed), TGEMM_ERR_WORKSPACE_LIMIT (scratch too small) or TGEMM_ERR_HIP.
 int get_workspace(WsMode mode, hipStream_t s, size_t bytes, Workspace* w) {
   w->ptr = nullptr;
-  w->owned = false;
   if (mode == kWsScratch) {
     if (bytes > kScratchBytes) return TGEMM_ERR_WORKSPACE_LIMIT;
     return scratch_address(&w->ptr);
   }
   hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
-  if (s != nullptr && hipStreamIsCapturing(s, &cs) == hipSuccess &&
-      cs != hipStreamCaptureStatusNone) {
-    if (hipMallocAsync(&w->ptr, bytes, s) != hipSuccess || w->ptr == nullptr) {
-      (void)hipGetLastError();
-      return TGEMM_ERR_NO_MEMORY;
-    }
-    w->owned = true;
-    return TGEMM_OK;
+  unsigned long long capture = 0;
+  const bool capturing = s != nullptr &&
+                         hipStreamGetCaptureInfo(s, &cs, &capture) == hipSuccess &&
+                         cs != hipStreamCaptureStatusNone;
+  if (!capturing) {
+    (void)hipGetLastError();
+    capture = 0;
   }
-  (void)hipGetLastError();
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess) return TGEMM_ERR_HIP;
   WsEntry* e = nullptr;
   {
     std::lock_guard<std::mutex> lock(g_ws_mu);
-    for (auto& x : g_ws)
-      if (x->dev == dev && x->stream == s) e = x.get();
+    auto& list = capturing ? g_capture_ws : g_ws;
+    for (auto& x : list)
+      if (x->dev == dev && x->stream == s && x->capture == capture) e = x.get();
     if (e == nullptr) {
-      g_ws.push_back(std::unique_ptr<WsEntry>(new WsEntry{dev, s, nullptr, 0, {}}));
-      e = g_ws.back().get();
+      list.push_back(std::unique_ptr<WsEntry>(new WsEntry{dev, s, capture, nullptr, 0, {}}));
+      e = list.back().get();
     }
   }
   w->hold = std::unique_lock<std::mutex>(e->mu);
@@ -199,22 +217,22 @@ int get_workspace(WsMode mode, hipStream_t s, size_t bytes, Workspace* w) {
   size_t want = bytes;
   if (e->ptr != nullptr && want < e->bytes + e->bytes / 4) want = e->bytes + e->bytes / 4;
   void* p = nullptr;
-  if (hipMallocAsync(&p, want, s) != hipSuccess || p == nullptr) {
+  const hipError_t got = capturing ? malloc_beside_capture(&p, want) : hipMallocAsync(&p, want, s);
+  if (got != hipSuccess || p == nullptr) {
     (void)hipGetLastError();
     w->hold.unlock();
     return TGEMM_ERR_NO_MEMORY;
   }
-  if (e->ptr != nullptr) (void)hipFreeAsync(e->ptr, s);
+  // (a captured call's nodes keep the smaller buffer: it is not freed)
+  if (e->ptr != nullptr && !capturing) (void)hipFreeAsync(e->ptr, s);
   e->ptr = p;
   e->bytes = want;
   w->ptr = p;
   return TGEMM_OK;
 }
 
-hipError_t release_workspace(Workspace& w, hipStream_t s) {
-  const hipError_t e = w.owned ? hipFreeAsync(w.ptr, s) : hipSuccess;
+void release_workspace(Workspace& w) {
   if (w.hold.owns_lock()) w.hold.unlock();
-  return e;
 }
 
 namespace {
@@ -364,8 +382,7 @@ int run_impl(WsMode mode, char transA, char transB, int64_t M, int64_t N, int64_
     hipError_t e = launch_gemv(shape, X, ldx, sx, v, sv, L, K, (int)nkc,
                                static_cast<float*>(w.ptr), C, sc,
                                epilogue == TGEMM_EPI_STORE_F32, s);
-    const hipError_t ef = release_workspace(w, s);
-    if (e == hipSuccess) e = ef;
+    release_workspace(w);
     return status_of(e);
   }
 
@@ -408,8 +425,7 @@ int run_impl(WsMode mode, char transA, char transB, int64_t M, int64_t N, int64_
     hipError_t e = launch_gemm(transA, transB, cfg, kEpiStoreF32, p, s);
     if (e == hipSuccess)
       e = launch_splitk_sum(p.ws, split, m, n, C, ldc, epilogue == TGEMM_EPI_STORE_F32, s);
-    const hipError_t ef = release_workspace(w, s);
-    if (e == hipSuccess) e = ef;
+    release_workspace(w);
     return status_of(e);
   }
 
@@ -445,8 +461,7 @@ int run_impl(WsMode mode, char transA, char transB, int64_t M, int64_t N, int64_
     e = launch_ce_scale(p.part_m, lse, m, n, blk, out_scale, s);
   else if (e == hipSuccess && out_grad != nullptr)
     e = launch_ce_grad_fixup(p.grad, ldc, p.part_m, lse, labels, m, n, blk, s);
-  const hipError_t ef = release_workspace(w, s);
-  if (e == hipSuccess) e = ef;
+  release_workspace(w);
   return status_of(e);
 }
 
@@ -659,6 +674,6 @@ extern "C" int tgemm_run_fp8(char transA, char transB, int64_t M, int64_t N, int
     p.groupM = p.tilesM < 4 ? p.tilesM : (p.tilesM <= 8 ? p.tilesM : 4);
     e = launch_gemm_f8(f8t, bf16_out ? kEpiOsBf16 : kEpiOsF32, p, s);
   }
-  const hipError_t r = release_workspace(w, s);
-  return status_of(e != hipSuccess ? e : r);
+  release_workspace(w);
+  return status_of(e);
 }

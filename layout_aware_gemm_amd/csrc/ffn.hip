@@ -156,7 +156,7 @@ void say_rows(const char* what, const RowsParams& p, const RowsPlan& r) {
 // Workspace of one call.  bytes >= 0: the caller's buffer of that size (a
 // call that needs more fails before anything is enqueued); bytes < 0: the
 // library's own per-stream buffer, which a stream under capture does not
-// get: its graph would have to allocate and free memory as it replays.
+// get: a graph's memory is the caller's here.
 // query set: report the need and launch nothing.
 // ----------------------------------------------------------------------
 struct CallSpace {
@@ -232,8 +232,8 @@ int run_i8(char ta, char tb, const void* A, int64_t lda, const void* B, int64_t 
   }
   if (bytesP) p.part = ws + bytesA + bytesB;
   if (e == hipSuccess) e = launch_rows(kRowsI8, p, r, epi, gate, s);
-  const hipError_t f = release_workspace(w, s);
-  return status_of(e != hipSuccess ? e : f);
+  release_workspace(w);
+  return status_of(e);
 }
 
 inline int64_t round_up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
@@ -296,8 +296,8 @@ int run_gated(char ta, char tb, int64_t M, int64_t F, int64_t K, const void* A, 
   }
   if (bytesP) p.part = ws + bytesA + bytesB;
   if (e == hipSuccess) e = launch_rows(kRowsBf16, p, r, kRowsGated, true, s);
-  const hipError_t f = release_workspace(w, s);
-  return status_of(e != hipSuccess ? e : f);
+  release_workspace(w);
+  return status_of(e);
 }
 
 // Gradient of the gated product: dGU into the workspace, then dA = dGU .
@@ -381,8 +381,8 @@ int run_gated_backward(char ta, char tb, int64_t M, int64_t F, int64_t K, const 
   pw.ldb = swap ? ldg : lda;
   pw.ws = reinterpret_cast<float*>(ws + bytesX);
   if (e == hipSuccess) e = launch_gated_bwd(tile, px, pw, false, f32, s);
-  const hipError_t f = release_workspace(w, s);
-  return status_of(e != hipSuccess ? e : f);
+  release_workspace(w);
+  return status_of(e);
 }
 
 // The workspace list allocates host memory; no exception leaves the library.

@@ -11,20 +11,20 @@
 namespace tgemm {
 
 // ----------------------------------------------------------------------
-// Per-call workspace (dispatch.hip): the cached buffer of (device, stream)
-// or, for the no-allocation calls, the library's fixed device array.
+// Per-call workspace (dispatch.hip): the buffer of (device, stream), or of
+// the stream's capture, or, for the no-allocation calls, the library's fixed
+// device array.
 // get_workspace returns TGEMM_OK with ptr set, TGEMM_ERR_NO_MEMORY,
 // TGEMM_ERR_WORKSPACE_LIMIT or TGEMM_ERR_HIP; a call takes at most one
 // workspace and releases it after its last launch.
 // ----------------------------------------------------------------------
 struct Workspace {
   void* ptr = nullptr;
-  bool owned = false;                 // free in stream order at the end of this call
-  std::unique_lock<std::mutex> hold;  // the cache entry, until the last launch is enqueued
+  std::unique_lock<std::mutex> hold;  // the buffer's entry, until the last launch is enqueued
 };
 enum WsMode : int { kWsCached = 0, kWsScratch = 1 };
 int get_workspace(WsMode mode, hipStream_t s, size_t bytes, Workspace* w);
-hipError_t release_workspace(Workspace& w, hipStream_t s);
+void release_workspace(Workspace& w);
 
 // TGEMM_VERBOSE is set: each call prints the path it takes.
 bool verbose();
