@@ -381,6 +381,8 @@ typedef enum {
  *   q                 int8 [M, K], row stride ldq >= K.
  *   scale             fp32 [M].
  * Rows may start at any element: no alignment is asked for.  No workspace.
+ * M times ceil(K / 512) * 64 (at most 1024) below 2^32, else
+ * TGEMM_ERR_UNSUPPORTED.
  */
 TGEMM_API int tgemm_rms_norm_i8(const void* x, int64_t ldx, const void* residual, int64_t ldr,
                                 const void* weight, float eps, int64_t M, int64_t K, void* sum,

@@ -11,6 +11,17 @@
 
 namespace tgemm {
 
+// Enqueue a kernel; the status is this launch's own.  (hipGetLastError would
+// also report, and clear, an error that an earlier HIP call of the thread
+// left behind.)  Grids are checked by the entries, before the first launch.
+template <class... P, class... A>
+hipError_t enqueue(void (*kernel)(P...), dim3 grid, dim3 block, hipStream_t s, const A&... args) {
+  return [&](P... p) {
+    void* v[] = {static_cast<void*>(&p)...};
+    return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, v, 0, s);
+  }(args...);
+}
+
 // Operand element types of the row products.
 enum RowsType : int { kRowsI8 = 0, kRowsBf16 = 1 };
 
@@ -89,6 +100,7 @@ hipError_t launch_rows_skinny(int type, int epi, const RowsParams& p, hipStream_
 
 // Sum the partial products over the K chunks and apply `epi` (one of
 // kRowsStoreBf16, kRowsStoreF32, kRowsGated) (rows_finish.hip).
+bool rows_finish_fits(const RowsParams& p, bool gate);  // its grid is launchable
 hipError_t launch_rows_finish(int type, int epi, const RowsParams& p, hipStream_t s);
 
 // Copy an operand of any layout and alignment into K-contiguous rows with
@@ -144,6 +156,7 @@ struct RowQuantParams {
   int M;
   int64_t K;
 };
+bool row_quant_fits(const RowQuantParams& p);
 hipError_t launch_row_quant(const RowQuantParams& p, hipStream_t s);
 
 // ----------------------------------------------------------------------

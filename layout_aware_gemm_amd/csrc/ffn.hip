@@ -14,12 +14,7 @@ namespace {
 
 inline bool is_n(char t) { return t == 'N' || t == 'n'; }
 
-// hipErrorInvalidValue is what the launchers here return for a grid past
-// the dispatch limit.
-int status_of(hipError_t e) {
-  return e == hipSuccess ? TGEMM_OK : e == hipErrorInvalidValue ? TGEMM_ERR_UNSUPPORTED
-                                                                : TGEMM_ERR_HIP;
-}
+int status_of(hipError_t e) { return e == hipSuccess ? TGEMM_OK : TGEMM_ERR_HIP; }
 
 constexpr size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -129,6 +124,12 @@ RowsPlan plan_rows(RowsParams* p, bool gate) {
 bool grid_fits(const RowsParams& p, const RowsPlan& r, bool gate) {
   // (the few-row kernel: at most one workgroup of 512 threads per 16 outputs)
   if (r.skinny) return ceil_div(gate ? p.F : p.N, 16) <= kMaxWorkgroups / 2;
+  if (r.tail >= 0) {
+    RowsParams q = p;
+    set_tile(&q, gate, r.tail, r.tail_col, gate ? p.F : p.N);
+    if ((int64_t)q.tilesM * q.tilesN > kMaxWorkgroups) return false;
+  }
+  if (p.split > 1 && !rows_finish_fits(p, gate)) return false;
   return (int64_t)p.tilesM * p.tilesN * p.split <= kMaxWorkgroups;
 }
 
@@ -510,6 +511,7 @@ extern "C" int tgemm_gated_grad(int64_t M, int64_t F, const void* dH, int64_t ld
   const int st =
       tgemm_validate_gated_grad(M, F, dH, lddh, GU, ldgu, gu_type, activation, dGU, lddgu);
   if (st != TGEMM_OK) return st;
+  if (!gated_grad_fits(M, F)) return TGEMM_ERR_UNSUPPORTED;
   if (verbose())
     fprintf(stderr, "tgemm: gated grad M=%lld F=%lld\n", (long long)M, (long long)F);
   return status_of(launch_gated_grad(static_cast<const uint16_t*>(dH), lddh, GU, ldgu,
@@ -562,13 +564,14 @@ extern "C" int tgemm_rms_norm_i8(const void* x, int64_t ldx, const void* residua
   const int st = tgemm_validate_rms_norm_i8(x, ldx, residual, ldr, weight, eps, M, K, sum, lds, q,
                                             ldq, scale);
   if (st != TGEMM_OK) return st;
-  if (verbose())
-    fprintf(stderr, "tgemm: rms norm i8 M=%lld K=%lld residual=%d\n", (long long)M, (long long)K,
-            residual != nullptr);
   const RowQuantParams p = {static_cast<const uint16_t*>(x), ldx,
                             static_cast<const uint16_t*>(residual), ldr,
                             static_cast<const uint16_t*>(weight), eps,
                             static_cast<uint16_t*>(sum), lds, q, ldq, scale, (int)M, K};
+  if (!row_quant_fits(p)) return TGEMM_ERR_UNSUPPORTED;
+  if (verbose())
+    fprintf(stderr, "tgemm: rms norm i8 M=%lld K=%lld residual=%d\n", (long long)M, (long long)K,
+            residual != nullptr);
   return status_of(launch_row_quant(p, reinterpret_cast<hipStream_t>(stream)));
 }
 
@@ -576,9 +579,10 @@ extern "C" int tgemm_quantize_i8(const void* x, int64_t ldx, int64_t M, int64_t 
                                  int64_t ldq, float* scale, void* stream) {
   const int st = tgemm_validate_quantize_i8(x, ldx, M, K, q, ldq, scale);
   if (st != TGEMM_OK) return st;
-  if (verbose())
-    fprintf(stderr, "tgemm: quantize i8 M=%lld K=%lld\n", (long long)M, (long long)K);
   const RowQuantParams p = {static_cast<const uint16_t*>(x), ldx, nullptr, 0, nullptr, 0.f,
                             nullptr, 0, q, ldq, scale, (int)M, K};
+  if (!row_quant_fits(p)) return TGEMM_ERR_UNSUPPORTED;
+  if (verbose())
+    fprintf(stderr, "tgemm: quantize i8 M=%lld K=%lld\n", (long long)M, (long long)K);
   return status_of(launch_row_quant(p, reinterpret_cast<hipStream_t>(stream)));
 }

@@ -226,25 +226,18 @@ bool gated_bwd_fits(const GemmParams& px, const GemmParams& pw) {
 
 hipError_t launch_gated_bwd(int tile, const GemmParams& px, const GemmParams& pw, bool f32x,
                             bool f32w, hipStream_t s) {
-  if (!gated_bwd_fits(px, pw)) return hipErrorInvalidValue;
   const int64_t nx = grid_of(px), nw = grid_of(pw);
   const int wfirst = pw.kchunk > px.kchunk;
   const int nfirst = (int)(((wfirst ? nw : nx) + 7) / 8 * 8);
   const dim3 grid((unsigned)(nfirst + (wfirst ? nx : nw))), block(kThreads);
-  if (tile == 128)
-    hipLaunchKernelGGL(gated_bwd_kernel<128>, grid, block, 0, s, px, pw, nfirst, wfirst,
-                       f32x ? 1 : 0, f32w ? 1 : 0);
-  else
-    hipLaunchKernelGGL(gated_bwd_kernel<256>, grid, block, 0, s, px, pw, nfirst, wfirst,
-                       f32x ? 1 : 0, f32w ? 1 : 0);
+  const hipError_t e = enqueue(tile == 128 ? gated_bwd_kernel<128> : gated_bwd_kernel<256>, grid,
+                               block, s, px, pw, nfirst, wfirst, f32x ? 1 : 0, f32w ? 1 : 0);
   // Only a product of at most 341 tiles is split (its K is 1.5 shares or
   // more), so the sums' grid stays under 2^16 workgroups.
   SumJob jx, jw;
   const int64_t bx = sum_job(px, f32x, &jx), bw = sum_job(pw, f32w, &jw);
-  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || bx + bw == 0) return e;
-  hipLaunchKernelGGL(bwd_sum_kernel, dim3((unsigned)(bx + bw)), block, 0, s, jx, jw, (int)bx);
-  return hipGetLastError();
+  return enqueue(bwd_sum_kernel, dim3((unsigned)(bx + bw)), block, s, jx, jw, (int)bx);
 }
 
 }  // namespace tgemm

@@ -251,24 +251,25 @@ int threads_of(const RowQuantParams& p, int V) {
 }
 
 hipError_t launch_quant8(const RowQuantParams& p, hipStream_t s) {
-  hipLaunchKernelGGL((row_quant_kernel<8, false, false>), dim3(p.M), dim3(threads_of(p, 8)), 0, s,
-                     p);
-  return hipGetLastError();
+  return enqueue(row_quant_kernel<8, false, false>, dim3(p.M), dim3(threads_of(p, 8)), s, p);
 }
 
 template <int V>
 hipError_t launch_v(const RowQuantParams& p, hipStream_t s) {
-  const int T = threads_of(p, V);
+  const dim3 grid(p.M), block(threads_of(p, V));
   if (p.weight != nullptr && p.residual != nullptr)
-    hipLaunchKernelGGL((row_quant_kernel<V, true, true>), dim3(p.M), dim3(T), 0, s, p);
-  else if (p.weight != nullptr)
-    hipLaunchKernelGGL((row_quant_kernel<V, true, false>), dim3(p.M), dim3(T), 0, s, p);
-  else
-    hipLaunchKernelGGL((row_quant_kernel<V, false, false>), dim3(p.M), dim3(T), 0, s, p);
-  return hipGetLastError();
+    return enqueue(row_quant_kernel<V, true, true>, grid, block, s, p);
+  if (p.weight != nullptr) return enqueue(row_quant_kernel<V, true, false>, grid, block, s, p);
+  return enqueue(row_quant_kernel<V, false, false>, grid, block, s, p);
 }
 
 }  // namespace
+
+// One workgroup per row, of at most 1024 threads: 2^32 - 1 in a launch.
+bool row_quant_fits(const RowQuantParams& p) {
+  const int64_t chunks = (p.K + 7) / 8;
+  return p.M * (chunks < 1024 ? (chunks + 63) / 64 * 64 : 1024) < (int64_t(1) << 32);
+}
 
 // Chunks per thread.  Few rows: as few as possible, the call is latency.
 // Many: workgroups of about four waves, which overlap best (us, MI355X:
@@ -278,9 +279,6 @@ hipError_t launch_v(const RowQuantParams& p, hipStream_t s) {
 // norm's two inputs would not fit the registers of a full workgroup.
 hipError_t launch_row_quant(const RowQuantParams& p, hipStream_t s) {
   const int64_t chunks = (p.K + 7) / 8;
-  // (one workgroup per row, of at most 1024 threads: 2^32 - 1 in a launch)
-  const int64_t threads = chunks < 1024 ? (chunks + 63) / 64 * 64 : 1024;
-  if (p.M * threads >= (int64_t(1) << 32)) return hipErrorInvalidValue;
   const int64_t v = p.M < 512 ? (chunks + 1023) / 1024 : (chunks + 255) / 256;
   if (v <= 1) return launch_v<1>(p, s);
   if (v <= 2) return launch_v<2>(p, s);
@@ -288,15 +286,12 @@ hipError_t launch_row_quant(const RowQuantParams& p, hipStream_t s) {
   if (p.weight == nullptr) {
     if (v > 4 && chunks <= 8192) return launch_quant8(p, s);
     if (chunks <= 4096) return launch_v<4>(p, s);
-    hipLaunchKernelGGL((row_quant_long<false, false>), dim3(p.M), dim3(1024), 0, s, p);
-    return hipGetLastError();
+    return enqueue(row_quant_long<false, false>, dim3(p.M), dim3(1024), s, p);
   }
   if (chunks <= 4096) return launch_v<4>(p, s);
   if (p.residual != nullptr)
-    hipLaunchKernelGGL((row_quant_long<true, true>), dim3(p.M), dim3(1024), 0, s, p);
-  else
-    hipLaunchKernelGGL((row_quant_long<true, false>), dim3(p.M), dim3(1024), 0, s, p);
-  return hipGetLastError();
+    return enqueue(row_quant_long<true, true>, dim3(p.M), dim3(1024), s, p);
+  return enqueue(row_quant_long<true, false>, dim3(p.M), dim3(1024), s, p);
 }
 
 }  // namespace tgemm

@@ -211,15 +211,21 @@ __global__ void __launch_bounds__(kThr) gated_grad_kernel(
   }
 }
 
+int64_t finish_blocks(const RowsParams& p, bool gate) {
+  return (int64_t)p.M * ceil_div(gate ? p.F : p.N, 4 * kThr);
+}
+
 template <class T, int EPI>
 hipError_t finish_one(const RowsParams& p, hipStream_t s) {
-  const int64_t blocks = (int64_t)p.M * ceil_div(EPI == kRowsGated ? p.F : p.N, 4 * kThr);
-  if (blocks > kMaxWorkgroups) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((finish_kernel<T, EPI>), dim3((unsigned)blocks), dim3(kThr), 0, s, p);
-  return hipGetLastError();
+  return enqueue(finish_kernel<T, EPI>, dim3((unsigned)finish_blocks(p, EPI == kRowsGated)),
+                 dim3(kThr), s, p);
 }
 
 }  // namespace
+
+bool rows_finish_fits(const RowsParams& p, bool gate) {
+  return finish_blocks(p, gate) <= kMaxWorkgroups;
+}
 
 hipError_t launch_rows_finish(int type, int epi, const RowsParams& p, hipStream_t s) {
   if (type == kRowsI8) {
@@ -254,38 +260,24 @@ bool gated_grad_fits(int64_t rows, int64_t F) {
 }
 
 hipError_t launch_pack_rows(const PackRows& p, int elem, hipStream_t s) {
-  if (!pack_rows_fits(p, elem)) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)pack_blocks(p, elem));
-  if (p.k_contiguous) {
-    const int chunks = (int)(p.ldo * elem / 16);
-    if (elem == 1)
-      hipLaunchKernelGGL(pack_rows_kernel<1>, grid, dim3(kThr), 0, s, p, chunks);
-    else
-      hipLaunchKernelGGL(pack_rows_kernel<2>, grid, dim3(kThr), 0, s, p, chunks);
-  } else {
-    const int kblocks = ceil_div(p.ldo, 64);
-    if (elem == 1)
-      hipLaunchKernelGGL(pack_cols_kernel<1>, grid, dim3(kThr), 0, s, p, kblocks);
-    else
-      hipLaunchKernelGGL(pack_cols_kernel<2>, grid, dim3(kThr), 0, s, p, kblocks);
-  }
-  return hipGetLastError();
+  const dim3 grid((unsigned)pack_blocks(p, elem)), block(kThr);
+  if (p.k_contiguous)
+    return enqueue(elem == 1 ? pack_rows_kernel<1> : pack_rows_kernel<2>, grid, block, s, p,
+                   (int)(p.ldo * elem / 16));
+  return enqueue(elem == 1 ? pack_cols_kernel<1> : pack_cols_kernel<2>, grid, block, s, p,
+                 ceil_div(p.ldo, 64));
 }
 
 hipError_t launch_gated_grad(const uint16_t* dh, int64_t lddh, const void* gu, int64_t ldgu,
                              bool gu_f32, int M, int64_t F, int act, uint16_t* dgu, int64_t lddgu,
                              int rows, int64_t cols, hipStream_t s) {
-  if (!gated_grad_fits(rows, F)) return hipErrorInvalidValue;
   const int64_t per_row = grad_blocks_per_row(F);
-  const dim3 grid((unsigned)(rows * per_row));
+  const dim3 grid((unsigned)(rows * per_row)), block(kThr);
   if (gu_f32)
-    hipLaunchKernelGGL(gated_grad_kernel<float>, grid, dim3(kThr), 0, s, dh, lddh,
-                       static_cast<const float*>(gu), ldgu, M, F, act, dgu, lddgu, cols, per_row);
-  else
-    hipLaunchKernelGGL(gated_grad_kernel<uint16_t>, grid, dim3(kThr), 0, s, dh, lddh,
-                       static_cast<const uint16_t*>(gu), ldgu, M, F, act, dgu, lddgu, cols,
-                       per_row);
-  return hipGetLastError();
+    return enqueue(gated_grad_kernel<float>, grid, block, s, dh, lddh,
+                   static_cast<const float*>(gu), ldgu, M, F, act, dgu, lddgu, cols, per_row);
+  return enqueue(gated_grad_kernel<uint16_t>, grid, block, s, dh, lddh,
+                 static_cast<const uint16_t*>(gu), ldgu, M, F, act, dgu, lddgu, cols, per_row);
 }
 
 }  // namespace tgemm

@@ -523,13 +523,10 @@ hipError_t launch_one(const RowsParams& p, hipStream_t s) {
   const dim3 grid(p.tilesM * p.tilesN * p.split), block(kThreads);
   // (one row of 64-row tiles: only gated products, whole in K, come here)
   if constexpr (BM == 64 && GATE && EPI != kRowsPart) {
-    if (p.tilesM == 1 && streams_past_cache(p)) {
-      hipLaunchKernelGGL((rows_kernel<Op, BM, BN, GATE, EPI, true>), grid, block, 0, s, p);
-      return hipGetLastError();
-    }
+    if (p.tilesM == 1 && streams_past_cache(p))
+      return enqueue(rows_kernel<Op, BM, BN, GATE, EPI, true>, grid, block, s, p);
   }
-  hipLaunchKernelGGL((rows_kernel<Op, BM, BN, GATE, EPI, false>), grid, block, 0, s, p);
-  return hipGetLastError();
+  return enqueue(rows_kernel<Op, BM, BN, GATE, EPI, false>, grid, block, s, p);
 }
 
 // (the K dimension is split for the smaller tiles only)

@@ -214,10 +214,8 @@ hipError_t launch_one(const RowsParams& p, hipStream_t s) {
   const int nblk = ceil_div(GATE ? p.F : p.N, 16 * NO);
   const dim3 grid(nblk), block(W * 64);
   if (streams_past_cache(p))
-    hipLaunchKernelGGL((skinny_kernel<Op, TB, NB, W, GATE, EPI, true>), grid, block, 0, s, p);
-  else
-    hipLaunchKernelGGL((skinny_kernel<Op, TB, NB, W, GATE, EPI, false>), grid, block, 0, s, p);
-  return hipGetLastError();
+    return enqueue(skinny_kernel<Op, TB, NB, W, GATE, EPI, true>, grid, block, s, p);
+  return enqueue(skinny_kernel<Op, TB, NB, W, GATE, EPI, false>, grid, block, s, p);
 }
 
 // up to 32 tokens

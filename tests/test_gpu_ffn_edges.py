@@ -1,8 +1,11 @@
 """The feed-forward operators where their other tests do not reach: the
-gradient's large tiles in every layout, and what its error is made of.
+gradient's large tiles in every layout, what its error is made of, and the
+statuses of the calls.
 
 Bounds as in test_gpu_ffn (u32 = 2^-24, ub = 2^-8).
 """
+
+import ctypes
 
 import numpy as np
 import pytest
@@ -81,3 +84,48 @@ def test_gradient_is_the_product_of_the_rounded_dgu(M, F, K, layout, kind):
     dgu = f64(rounded_dgu(dh, gu, kind))
     product(dx, dgu, 0 * dgu, f64(w).T, 2 * F, UB)
     product(dw.t(), dgu.T, 0 * dgu.T, f64(x), M, U32)
+
+
+# ---- statuses ----------------------------------------------------------------
+
+
+def test_errors_of_other_calls_are_left_alone():
+    """A HIP error that the caller's thread left behind is neither reported
+    by the feed-forward calls nor taken from the caller."""
+    M, F, K = 70, 40, 72
+    x, w, dh = framed(M, K, 1, 1.0), framed(2 * F, K, 2, 0.2), framed(M, F, 3, 1.0)
+    (q, s), (qw, sw) = tgemm.quantize_i8(x), tgemm.quantize_i8(w)
+    h, gu = tgemm.gated_matmul(x, w.t(), save=True)
+    dx, dw = tgemm.gated_backward(dh, gu, x, w.t())
+    c = tgemm.matmul_i8(q, qw.t(), s, sw)
+    h8 = tgemm.gated_matmul_i8(q, qw.t(), s, sw)
+    out = [torch.zeros_like(t) for t in (q, s, h, gu, dx, dw.t(), c, h8)]
+    Q, S, H, GU, DX, DW, C, H8 = (t.data_ptr() for t in out)
+    n, t = tgemm._flag("N"), tgemm._flag("T")
+    prod = (n, t, M, F, K, x.data_ptr(), x.stride(0), w.data_ptr(), w.stride(0))
+    i8 = (K, q.data_ptr(), K, qw.data_ptr(), K, s.data_ptr(), sw.data_ptr())
+    L = tgemm.lib()
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device=dev())
+    assert ws.numel() >= max(L.tgemm_gated_backward_workspace_bytes(*prod),
+                             L.tgemm_i8_workspace_bytes(n, t, M, 2 * F, *i8[:-2]))
+    work = (ws.data_ptr(), ws.numel())
+    calls = [
+        ("tgemm_quantize_i8", (x.data_ptr(), x.stride(0), M, K, Q, K, S)),
+        ("tgemm_run_gated", prod + (0, H, F, GU, 2 * F) + work),
+        ("tgemm_run_gated_backward",
+         prod + (dh.data_ptr(), dh.stride(0), gu.data_ptr(), 2 * F, tgemm.EPI_STORE_F32, 0, DX, K,
+                 DW, K, tgemm.EPI_STORE_BF16) + work),
+        ("tgemm_run_i8", (n, t, M, 2 * F) + i8 + (C, 2 * F, tgemm.EPI_STORE_BF16) + work),
+        ("tgemm_run_gated_i8", (n, t, M, F) + i8 + (0, H8, F) + work),
+    ]
+    stream = torch.cuda.current_stream().cuda_stream
+    torch.cuda.synchronize()
+    L.hipMalloc.argtypes = [ctypes.c_void_p, ctypes.c_size_t]
+    got = []
+    for name, args in calls:
+        assert L.hipMalloc(None, 16) == 1      # hipErrorInvalidValue, left pending
+        got.append((name, getattr(L, name)(*args, stream), L.hipGetLastError()))
+    torch.cuda.synchronize()
+    assert got == [(name, tgemm.TGEMM_OK, 1) for name, _ in calls]
+    for i, (o, r) in enumerate(zip(out, (q, s, h, gu, dx, dw.t(), c, h8))):
+        assert torch.equal(o, r), i
