@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kThr) finish_kernel(RowsParams p) {
       v[i] = v[i] * sa * p.scale_b[ci];
       if constexpr (GATE) u[i] = u[i] * sa * p.scale_b[p.F + ci];
     }
-    h[i] = GATE ? act_value(v[i], p.act) * u[i] : v[i];
+    h[i] = GATE ? act_times(v[i], u[i], p.act) : v[i];
   }
   const int64_t o = (int64_t)row * p.ldc + c;
   if constexpr (EPI == kRowsStoreF32)
@@ -161,12 +161,7 @@ __device__ __forceinline__ void grad_values(const uint16_t* ph, const T* pg, int
   load_values<N>(pg, g);
   load_values<N>(pg + F, u);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float a, d;
-    act_value_grad(g[i], act, a, d);
-    x[i] = h[i] * u[i] * d;
-    y[i] = h[i] * a;
-  }
+  for (int i = 0; i < N; ++i) act_gradients(g[i], u[i], h[i], act, x[i], y[i]);
 }
 
 // 8 outputs per thread, T the type g and u were kept in; the arithmetic is

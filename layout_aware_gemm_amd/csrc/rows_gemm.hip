@@ -268,7 +268,7 @@ __device__ __forceinline__ void rows_epilogue(const RowsParams& p,
               u = u * s * sb[2 * j + 1];
             }
             if (!FULL && c >= nout) continue;
-            o[c] = to_bf16(act_value(g, p.act) * u);
+            o[c] = to_bf16(act_times(g, u, p.act));
           }
         } else {
 #pragma unroll
@@ -326,7 +326,7 @@ __device__ __forceinline__ void keep_epilogue(const RowsParams& p,
       const float g[4] = {a.x, a.y, a.z, a.w}, u[4] = {b.x, b.y, b.z, b.w};
       float v[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = act_value(g[e], p.act) * u[e];
+      for (int e = 0; e < 4; ++e) v[e] = act_times(g[e], u[e], p.act);
       put4(static_cast<uint16_t*>(p.C) + (int64_t)row * p.ldc + c, v, n);
       float* const w = p.gu + (int64_t)row * p.ldgu + c;
       put4(w, g, n);

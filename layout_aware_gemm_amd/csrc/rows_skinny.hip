@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(W * 64) skinny_kernel(RowsParams p) {
         g[e] = v[e];
         u[e] = (float)a2[e];
         if constexpr (I8) u[e] = u[e] * sa * p.scale_b[p.F + c];
-        v[e] = act_value(g[e], p.act) * u[e];
+        v[e] = act_times(g[e], u[e], p.act);
       }
     }
     const int64_t o = (int64_t)row * p.ldc + c0;

@@ -1,6 +1,6 @@
 """The feed-forward operators where their other tests do not reach: the
-gradient's large tiles in every layout, what its error is made of, and the
-statuses of the calls.
+gradient's large tiles in every layout, what its error is made of, the
+statuses of the calls, and gates far below zero.
 
 Bounds as in test_gpu_ffn (u32 = 2^-24, ub = 2^-8).
 """
@@ -129,3 +129,127 @@ def test_errors_of_other_calls_are_left_alone():
     assert got == [(name, tgemm.TGEMM_OK, 1) for name, _ in calls]
     for i, (o, r) in enumerate(zip(out, (q, s, h, gu, dx, dw.t(), c, h8))):
         assert torch.equal(o, r), i
+
+
+# ---- gates far below zero ----------------------------------------------------
+
+
+def far_gates(kind, n):
+    """Gates whose sigmoid runs from e^-55 to e^-150, past where 1 / (1 + e^-s)
+    leaves fp32; the argument s of the last is -150."""
+    lo = 150.0 if kind == "silu" else 12.23  # s(-12.23) = -150
+    return -np.linspace(0.37 * lo if kind == "silu" else 0.67 * lo, lo, n)
+
+
+def relative(s):
+    """Of act(g) v in fp32: the exponent's argument (3 roundings of s, one of
+    the constant, one of the product: each |s| u32, doubled), exp2 and the
+    products; then the store's ub."""
+    return ((10 * np.abs(s) + 24) * U32 + UB) * 1.05
+
+
+def check_far(got, ref, rel):
+    assert np.min(np.abs(ref)) > 2.0 ** -120
+    within(got, ref, rel * np.abs(ref))
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu_tanh"])
+def test_far_gates_gradient(kind):
+    """dgu where dh brings the gate's tail back into range (by 2^127 at most)."""
+    F = 333
+    g = np.float32(far_gates(kind, F))
+    a, d, s = oracle.ffn.act(g.astype(np.float64), kind)
+    assert s.min() > -153 and s.max() < -50
+    up = np.exp2(np.minimum(127, np.round(-np.log2(np.abs(a)))))
+    sign = np.array([[1.0], [-1.0], [1.0]])
+    u = 1 + np.arange(3 * F).reshape(3, F) % 7 / 8
+    dh = torch.tensor(sign * up, dtype=torch.float32).to(BF).to(dev())
+    gu = torch.tensor(np.concatenate([np.tile(g, (3, 1)), u], 1), dtype=torch.float32).to(dev())
+    got = f64(rounded_dgu(dh, gu, kind))
+    check_far(got[:, :F], sign * up * u * d, relative(s))
+    check_far(got[:, F:], sign * up * a, relative(s))
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("M,K", [(9, 64), (100, 64), (70, 4096)])
+@pytest.mark.parametrize("op", ["i8", "bf16", "bf16 keep"])
+def test_far_gates_products(kind, M, K, op):
+    """h for gates in the tail and large u, on the few-row kernel, the tiles
+    and the sum of K chunks.  Row m holds one value, so g and u are products
+    of two numbers, exact in fp32."""
+    print(f"far gates {kind} {op} {M} {K}", flush=True)
+    F = 50
+    big = 2.0 ** 100
+    if op == "i8":
+        # g = code * step: the code's column scale carries the step
+        code = np.round(np.linspace(45, 127, F) if kind == "silu" else np.linspace(83, 127, F))
+        step = np.float32(150 / 127 if kind == "silu" else 12.23 / 127)
+        a, b = torch.zeros(M, K, dtype=torch.int8), torch.zeros(2 * F, K, dtype=torch.int8)
+        a[:, 3] = 1
+        b[:F, 3] = torch.tensor(-code).to(torch.int8)
+        b[F:, 3] = torch.arange(1, F + 1)
+        sb = torch.cat([torch.full((F,), float(step)), torch.full((F,), big)]).to(dev())
+        h = tgemm.gated_matmul_i8(a.to(dev()), b.to(dev()).t(), torch.ones(M, device=dev()), sb,
+                                  act=kind)
+        g, u = (-code * step).astype(np.float32), np.arange(1, F + 1) * big
+    else:
+        g = f64(torch.tensor(far_gates(kind, F)).to(BF))
+        u = f64(torch.tensor(np.linspace(1, 3, F) * big).to(BF))
+        x, w = torch.zeros(M, K, dtype=BF), torch.zeros(2 * F, K, dtype=BF)
+        x[:, 3] = 1
+        w[:, 3] = torch.tensor(np.concatenate([g, u])).to(BF)
+        keep = op == "bf16 keep"
+        h = tgemm.gated_matmul(x.to(dev()), w.to(dev()).t(), act=kind, save=keep)
+        h = h[0] if keep else h
+    act, _, s = oracle.ffn.act(np.asarray(g, np.float64), kind)
+    check_far(h, np.tile(act * u, (M, 1)), relative(s))
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu_tanh"])
+def test_far_gates_leave_others_alone(kind):
+    """One far gate per 8 columns: the others' bits do not change."""
+    M, F = 5, 333
+    gu = torch.randn(M, 2 * F, generator=gen(1)) * 3
+    dh = workloads.randn_bf16((M, F), 1.0, gen(2)).to(dev())
+    far = gu.clone()
+    far[:, 5:F:8] = -100.0
+    near = torch.ones(2 * F, dtype=torch.bool)
+    near[5:F:8] = near[F + 5::8] = False
+    a, b = rounded_dgu(dh, gu.to(dev()), kind), rounded_dgu(dh, far.to(dev()), kind)
+    assert torch.equal(a[:, near.to(dev())], b[:, near.to(dev())])
+    x, w = framed(M, 64, 1, 1.0), framed(2 * F, 64, 2, 0.1)
+    w2 = w.clone()
+    w2[5:F:8] = 0
+    w2[5:F:8, 0] = -200.0
+    x[:, 0] = 1
+    keep = near[:F].to(dev())
+    for rows in (x, x.repeat(40, 1)):
+        h, h2 = tgemm.gated_matmul(rows, w.t(), act=kind), tgemm.gated_matmul(rows, w2.t(), act=kind)
+        assert torch.equal(h[:, keep], h2[:, keep])
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu_tanh"])
+def test_gates_without_a_finite_value(kind):
+    """NaN gates make dg, du and h NaN, infinite ones give the limits, and
+    their neighbours keep their values."""
+    M, F = 3, 40
+    gu = torch.randn(M, 2 * F, generator=gen(1))
+    dh = workloads.randn_bf16((M, F), 1.0, gen(2)).to(dev())
+    want = rounded_dgu(dh, gu.to(dev()), kind)
+    gu[1, 7], gu[2, 9] = float("nan"), float("inf")
+    got = rounded_dgu(dh, gu.to(dev()), kind)
+    bad = torch.zeros(M, 2 * F, dtype=torch.bool, device=dev())
+    bad[1, 7] = bad[1, F + 7] = bad[2, 9] = bad[2, F + 9] = True
+    assert torch.equal(got[~bad], want[~bad])
+    assert torch.isnan(got[1, [7, F + 7]]).all()
+    assert got[2, F + 9].item() == float("inf") * np.sign(dh[2, 9].item())
+    assert got[2, 9] == (dh[2, 9].float() * gu[2, F + 9].item()).to(BF)
+    # forward: one token's NaN in x reaches its own row only
+    x, w = framed(70, 64, 1, 1.0), framed(2 * F, 64, 2, 0.1)
+    h = tgemm.gated_matmul(x, w.t(), act=kind)
+    x[13, 3] = float("nan")
+    for m in (70, 20):
+        h2 = tgemm.gated_matmul(x[:m], w.t(), act=kind)
+        assert torch.isnan(h2[13]).all() and torch.isfinite(h2[:13]).all()
+        assert torch.isfinite(h2[14:]).all()
+    assert torch.equal(tgemm.gated_matmul(x, w.t(), act=kind)[14:], h[14:])
