@@ -212,6 +212,19 @@ __device__ __forceinline__ void act_gradients(float g, float u, float h, int act
   y = hw * g * a.w;
 }
 
+// Orders a wave's LDS accesses before this point and after it, for lanes of
+// one wave that exchange words of their own buffer without a workgroup
+// barrier.  The hardware keeps a wave's LDS accesses in order, so this costs
+// no instruction: it keeps the compiler from moving one lane's read past
+// another lane's write.
+__device__ __forceinline__ void wave_lds_order() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+#endif
+}
+
 // Vectors at any element alignment: the hardware takes
 // unaligned vector accesses to global memory, so rows of odd length cost no
 // variant of their own.

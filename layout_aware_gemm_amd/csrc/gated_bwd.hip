@@ -51,6 +51,7 @@ __device__ __forceinline__ void store_block(const GemmParams& p, void* C, int64_
 #pragma unroll
       for (int j = 0; j < F; ++j)
         st[(8 * (r >> 2) + 4 * h + (r & 3)) * LD + j * 32 + lc] = acc[i][j][r];
+    wave_lds_order();
 #pragma unroll
     for (int q = 0; q < 32 / RPI; ++q) {
       const int rl = q * RPI + lane / LPR, row = row0 + i * 32 + rl;
@@ -63,6 +64,7 @@ __device__ __forceinline__ void store_block(const GemmParams& p, void* C, int64_
       else
         put4(static_cast<uint16_t*>(C) + off, e, n);
     }
+    wave_lds_order();
   }
 }
 

@@ -317,6 +317,7 @@ __device__ __forceinline__ void keep_epilogue(const RowsParams& p,
 #pragma unroll
       for (int j = 0; j < FN; ++j)
         st[(8 * (r >> 2) + 4 * h + (r & 3)) * LD + j * 32 + lc] = acc[i][j][r];
+    wave_lds_order();
 #pragma unroll
     for (int q = 0; q < 32 / RPI; ++q) {
       const int rl = q * RPI + lane / LPR, row = row0 + i * 32 + rl;
@@ -332,6 +333,7 @@ __device__ __forceinline__ void keep_epilogue(const RowsParams& p,
       put4(w, g, n);
       put4(w + p.F, u, n);
     }
+    wave_lds_order();
   }
 }
 

@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(W * 64) skinny_kernel(RowsParams p) {
     for (int b = 0; b < 2 * NB; ++b) st[b * 64 + wr[b & 1]] = wv[b];
 #pragma unroll
     for (int t = 0; t < TB; ++t) st[NB * 128 + t * 64 + wr[t & 1]] = av[t];
+    wave_lds_order();
     if (s + W < steps) load(s + W);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
@@ -148,6 +149,7 @@ __global__ void __launch_bounds__(W * 64) skinny_kernel(RowsParams p) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) acc[m][b] = Op::mma(wf[b], af[m], acc[m][b]);
     }
+    wave_lds_order();
   }
 #else
   (void)steps, (void)n0;
