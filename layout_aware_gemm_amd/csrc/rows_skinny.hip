@@ -16,9 +16,9 @@
 // never split over workgroups: the second pass costs more than the idle
 // compute units of a small weight (2048 x 8192: 6 us in all).
 //
-// Measured (MI355X) for up to 16 tokens: cold weights of 67 to 283 MB 4.4 to
-// 5.9 TB/s, where a large copy reaches 4.7; a 71 MB weight that stayed in the
-// last-level cache 5.7.
+// Measured (MI355X) for one token: cold weights of 71 to 283 MB 4.8 to 5.9
+// TB/s, where a large copy reaches 4.7; a 71 MB weight that stayed in part in
+// the last-level cache 5.7.
 #include "ffn.h"
 #include "gemm_kernel.h"
 
@@ -229,25 +229,38 @@ hipError_t launch_few(const RowsParams& p, hipStream_t s) {
 }
 
 // Blocks of weight rows per wave and waves per workgroup, by the number of
-// tokens and of blocks (us on MI355X; int8, N x K = 5120 x 13824, its 71 MB
-// partly in the last-level cache / 32000 x 4096, then gated 13824 x 5120 int8
-// / bf16):
-//   one token    two blocks (gated four), 8 waves   12.4  27.9  28.6  52.3
-//                half the blocks                    12.9  26.9  29.6  54.5
-//                half the waves                     14.4  31.0  28.9  52.2
-//   32 tokens    two (four), 8 waves                14.3  32.9  37.0  63.1
-//                half the blocks                    19.5  38.6  38.6  67.6
-//   64 tokens    two (four), 8 waves                19.7  44.9  42.1  73.1
-//                the same, 4 waves                  20.1  43.0  40.5  71.5
-//                four, 4 waves                      27.4  36.9
-// Up to 128 blocks leave half the compute units idle, and half the blocks win
-// (cold weights, 1 / 16 / 32 tokens, whole then half: int8 4096 x 4096 6.4 /
-// 7.1 / 8.2, 6.1 / 6.4 / 7.0; gated bf16 4096 x 4096 17.0 / 17.7 / 20.2, 15.7 /
-// 15.8 / 16.6).  About one block per compute unit gives it, halved, two that
-// overlap, which pays where every unit has two and the step is a gated one's
-// (gated bf16 8192 x 2048 18.0 / 17.6 / 18.2, 16.2 / 16.1 / 17.3; 7168 x 4096
-// 24.9 / 25.6 / 25.9, 22.2 / 24.0 / 26.8; but 5504 x 4096 20.6 / 21.5 / 23.4,
-// 21.4 / 23.2 / 24.9, and int8 8192 x 4096 9.3 / 9.6 / 10.2, 9.1 / 9.9 / 11.3).
+// tokens and of workgroups.  Figures in us on MI355X, N x K (gated: F x K) with
+// cold weights (copies of 1.2 GB in turn):
+//                       two blocks (gated four),  half the  4 waves  twice the blocks,
+//                                       8 waves    blocks                     4 waves
+//    1 token   int8 5120 x 13824           14.8      15.0     21.5
+//              int8 32000 x 4096           24.9      25.5     27.3
+//              gated int8 13824 x 5120     25.1      26.7     26.0
+//              gated bf16 13824 x 5120     48.3      49.8     48.3
+//   16 tokens  gated bf16 13824 x 5120     51.8      54.2     52.0
+//   32 tokens  int8 5120 x 13824           21.0      28.2     23.3
+//              int8 32000 x 4096           28.7      33.3     27.4
+//   64 tokens  int8 5120 x 13824           27.7      38.1     28.3        37.1
+//              int8 32000 x 4096           39.7      46.8     36.8        29.3
+//              gated int8 8192 x 5120      21.9      27.2     22.1
+//              gated bf16 8192 x 5120      37.5      48.3     37.9
+// Up to 128 workgroups leave half the compute units idle, and half the blocks
+// win (1 / 16 / 32 tokens, whole then half: int8 4096 x 4096 6.4 / 7.1 / 8.2,
+// 6.1 / 6.4 / 7.0; gated bf16 4096 x 4096 17.0 / 17.7 / 20.2, 15.7 / 15.8 / 16.6;
+// 33 / 64 tokens, four waves whole then eight half: int8 4096 x 4096 10.1 /
+// 10.5, 8.0 / 8.9; gated bf16 4096 x 2048 14.9 / 15.0, 11.0 / 12.1, 4096 x 8192
+// 42.8 / 46.2, 30.9 / 33.7).  About one workgroup per compute unit gives it,
+// halved, two that overlap.  That pays for most gated weights (1 / 8 / 16 / 32
+// tokens, whole then half: bf16 6688 x 4096 25.3 / 24.7 / 24.8 / 25.9, 21.6 /
+// 21.7 / 23.5 / 25.8; 7680 x 4096 27.3 / 27.3 / 27.5 / 28.6, 23.8 / 23.7 / 24.2
+// / 27.3; 8192 x 2048 17.7 / 17.4 / 17.5 / 17.8, 15.9 / 15.9 / 15.8 / 16.4; int8
+// 7680 x 4096 15.7 / 15.3 / 15.4 / 15.9, 14.5 / 14.5 / 14.6 / 15.7), is even for
+// short K (int8 8192 x 2048 8.2 / 8.0 / 8.2 / 9.2, 8.3 / 8.2 / 8.3 / 9.3) and
+// loses at the band's upper end for long K (bf16 8192 x 5120 29.4 / 29.3 / 30.3
+// / 32.8, 29.0 / 30.2 / 31.4 / 35.9).  Below the band whole blocks win (bf16
+// 5504 x 4096 20.6 / 21.5 / 23.4 at 1 / 16 / 32 tokens, half 21.4 / 23.2 / 24.9),
+// as they do for plain products (int8 8192 x 4096 9.3 / 9.6 / 10.2, 9.1 / 9.9 /
+// 11.3).
 template <class Op, bool GATE, int EPI>
 hipError_t launch_blocks(const RowsParams& p, hipStream_t s) {
   constexpr int NB = GATE ? 4 : 2;
@@ -256,7 +269,7 @@ hipError_t launch_blocks(const RowsParams& p, hipStream_t s) {
   const bool half = blocks <= 128 || (GATE && blocks > 208 && blocks <= 256);
   if (p.M <= 32)
     return half ? launch_few<Op, NB / 2, GATE, EPI>(p, s) : launch_few<Op, NB, GATE, EPI>(p, s);
-  if (blocks < 128) return launch_one<Op, 8, NB / 2, 8, GATE, EPI>(p, s);
+  if (blocks <= 128) return launch_one<Op, 8, NB / 2, 8, GATE, EPI>(p, s);
   if constexpr (!GATE) {
     if (ceil_div(nout, 64) >= 256) return launch_one<Op, 8, 4, 4, GATE, EPI>(p, s);
   }

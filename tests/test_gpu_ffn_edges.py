@@ -1,6 +1,6 @@
 """The feed-forward operators where their other tests do not reach: the
 gradient's large tiles in every layout, what its error is made of, the
-statuses of the calls, and gates far below zero.
+statuses of the calls, gates far below zero, and block sizes of few rows.
 
 Bounds as in test_gpu_ffn (u32 = 2^-24, ub = 2^-8).
 """
@@ -15,7 +15,7 @@ import oracle
 import workloads
 from layout_aware_gemm_amd import tgemm
 from parity_util import dev
-from test_gpu_ffn import BF, U32, UB, f64, gen, within
+from test_gpu_ffn import BF, U32, UB, act_bounds, codes, f64, gen, scales, within
 
 pytestmark = pytest.mark.gpu
 
@@ -253,3 +253,25 @@ def test_gates_without_a_finite_value(kind):
         assert torch.isnan(h2[13]).all() and torch.isfinite(h2[:13]).all()
         assert torch.isfinite(h2[14:]).all()
     assert torch.equal(tgemm.gated_matmul(x, w.t(), act=kind)[14:], h[14:])
+
+
+# ---- few rows ----------------------------------------------------------------
+
+
+@pytest.mark.parametrize("M", [33, 64])
+@pytest.mark.parametrize("N", [4065, 4096, 4097])
+def test_few_rows_around_half_the_compute_units(M, N):
+    """127.03, 128 and 128.03 blocks of 32 outputs: both block sizes for 33
+    to 64 rows."""
+    K = 208
+    a, w = codes(M, K, 1, full=True), codes(N, K, 2, full=True)
+    sa, sb = scales(M, 1), scales(N, 2)
+    ref = oracle.ffn.matmul_i8(a.cpu().numpy(), w.t().cpu().numpy(), f64(sa), f64(sb))
+    within(tgemm.matmul_i8(a, w.t(), sa, sb, out_dtype=torch.float32), ref,
+           np.abs(ref) * 3.01 * U32)
+    x, v = framed(M, K, 1, 1.0), framed(2 * N, K, 2, 0.1)
+    h, gu = tgemm.gated_matmul(x, v.t(), save=True)
+    X, V = f64(x), f64(v).T
+    e = K * U32 * 1.01 * (np.abs(X) @ np.abs(V))
+    within(gu, X @ V, e)
+    within(h, *act_bounds(X @ V, e[:, :N], e[:, N:], "silu"))
