@@ -1,6 +1,7 @@
 """The feed-forward operators where their other tests do not reach: the
 gradient's large tiles in every layout, what its error is made of, the
-statuses of the calls, gates far below zero, and block sizes of few rows.
+statuses of the calls, gates far below zero, block sizes of few rows, and rows
+of the smallest values.
 
 Bounds as in test_gpu_ffn (u32 = 2^-24, ub = 2^-8).
 """
@@ -15,7 +16,8 @@ import oracle
 import workloads
 from layout_aware_gemm_amd import tgemm
 from parity_util import dev
-from test_gpu_ffn import BF, U32, UB, act_bounds, codes, f64, gen, scales, within
+from test_gpu_ffn import (BF, U32, UB, act_bounds, check_quant, codes, f64, gen, scales,
+                          within)
 
 pytestmark = pytest.mark.gpu
 
@@ -275,3 +277,26 @@ def test_few_rows_around_half_the_compute_units(M, N):
     e = K * U32 * 1.01 * (np.abs(X) @ np.abs(V))
     within(gu, X @ V, e)
     within(h, *act_bounds(X @ V, e[:, :N], e[:, N:], "silu"))
+
+
+# ---- rows of the smallest values ---------------------------------------------
+
+
+@pytest.mark.parametrize("K", [5, 513, 9000, 40001])
+def test_rows_below_the_normal_range(K):
+    """Rows of bf16 subnormals (multiples of 2^-133), alone and beside a
+    normal value: exact codes, scales to their own rounding."""
+    n = torch.randint(-127, 128, (4, K), generator=gen(K)).double()
+    n[0, 0], n[1, 0] = 127, 1
+    n[1, 1:] = 0
+    n[2, 0], n[2, 2] = 64.0, -3
+    x = (n * 2.0 ** -133).to(BF)
+    x[3, 1] = 2.0 ** -126
+    assert torch.equal(x.double()[:3], n[:3] * 2.0 ** -133)
+    q, scale = tgemm.quantize_i8(x.to(dev()))
+    check_quant(q, scale, *oracle.ffn.quantize_rows(f64(x)))
+    # the norm's scale is of order 1 whatever the row's size
+    w = torch.ones(K, dtype=BF, device=dev())
+    q2, s2 = tgemm.rms_norm_i8(x.to(dev()), w, eps=0.0)
+    h = f64(x)
+    check_quant(q2, s2, *oracle.ffn.quantize_rows(h, 1 / np.sqrt(np.mean(h * h, 1))))
