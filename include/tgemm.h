@@ -354,7 +354,8 @@ TGEMM_API int tgemm_validate_rope_region(const void* q, int64_t ldq, int64_t P, 
  * at their contents, and enqueue nothing.
  */
 
-/* Activations of the gated products (fp32 arithmetic). */
+/* Activations of the gated products (fp32 arithmetic; 0 for g below about
+ * -174.7 and -12.9). */
 typedef enum {
   TGEMM_ACT_SILU = 0,     /* g / (1 + exp(-g))                                         */
   TGEMM_ACT_GELU_TANH = 1 /* g/2 * (1 + tanh(sqrt(2/pi) * (g + 0.044715 * g^3)))       */

@@ -127,7 +127,7 @@ int status_of(hipError_t e) { return e == hipSuccess ? TGEMM_OK : TGEMM_ERR_HIP;
 struct WsEntry {
   int dev;
   hipStream_t stream;
-  unsigned long long capture;  // 0: the eager calls' buffer
+  unsigned long long capture;  // its id, unique in the process; 0: the eager calls' buffer
   void* ptr;
   size_t bytes;
   std::mutex mu;
