@@ -358,7 +358,9 @@ TGEMM_API int tgemm_validate_rope_region(const void* q, int64_t ldq, int64_t P, 
  * -174.7 and -12.9). */
 typedef enum {
   TGEMM_ACT_SILU = 0,     /* g / (1 + exp(-g))                                         */
-  TGEMM_ACT_GELU_TANH = 1 /* g/2 * (1 + tanh(sqrt(2/pi) * (g + 0.044715 * g^3)))       */
+  TGEMM_ACT_GELU_TANH = 1, /* g/2 * (1 + tanh(sqrt(2/pi) * (g + 0.044715 * g^3)))      */
+  TGEMM_ACT_NONE = 2,     /* z: linear products only                                   */
+  TGEMM_ACT_RELU = 3      /* max(z, 0), NaN stays: linear products only                */
 } tgemm_activation;
 
 /*
@@ -532,6 +534,75 @@ TGEMM_API int tgemm_validate_gated_backward(char transA, char transB, int64_t M,
                                             const void* GU, int64_t ldgu, int gu_type,
                                             int activation, const void* dA, int64_t ldda, const void* dB,
                                             int64_t lddb, int epilogue);
+
+/*
+ * ---- Linear layers: product, bias, activation, residual -------------------
+ *
+ *   z = op(A) . op(B) + bias          bf16 operands, fp32 sums
+ *   Y = residual + act(z)             rounded once, to Y's type
+ *
+ *   A, B        bf16, in any layout.
+ *   bias        bf16 [N], or NULL.
+ *   activation  a tgemm_activation.
+ *   Y           [M, N], ldy >= N: bf16 (epilogue TGEMM_EPI_STORE_BF16) or fp32
+ *               (TGEMM_EPI_STORE_F32).
+ *   residual    [M, N] of Y's type, ldr >= N, or NULL.  It may be Y itself
+ *               (same address and stride).
+ *   Z           [M, N], ldz >= N, or NULL: receives z for the backward call,
+ *               fp32 or bf16 (z_type, an epilogue's name as for Y; ignored
+ *               without Z).
+ *
+ * Operands, workspace and errors as for tgemm_run_gated.
+ */
+TGEMM_API int tgemm_run_linear(char transA, char transB, int64_t M, int64_t N, int64_t K,
+                               const void* A, int64_t lda, const void* B, int64_t ldb,
+                               const void* bias, int activation, const void* residual, int64_t ldr,
+                               void* Y, int64_t ldy, int epilogue, void* Z, int64_t ldz,
+                               int z_type, void* workspace, int64_t workspace_bytes, void* stream);
+TGEMM_API int64_t tgemm_linear_workspace_bytes(char transA, char transB, int64_t M, int64_t N,
+                                               int64_t K, const void* A, int64_t lda,
+                                               const void* B, int64_t ldb);
+
+/* Host-only argument check of tgemm_run_linear (no GPU access). */
+TGEMM_API int tgemm_validate_linear(char transA, char transB, int64_t M, int64_t N, int64_t K,
+                                    const void* A, int64_t lda, const void* B, int64_t ldb,
+                                    const void* bias, int activation, const void* residual,
+                                    int64_t ldr, const void* Y, int64_t ldy, int epilogue,
+                                    const void* Z, int64_t ldz, int z_type);
+
+/*
+ * The gradient of tgemm_run_linear for the gradient dY (bf16 [M, N]) of Y:
+ *   dz    = dY * act'(z)
+ *   dA    = dz . op(B)^T      bf16 [M, K] (op(A)'s shape, row stride ldda >= K)
+ *   dB    = op(A)^T . dz      in B's layout, bf16 or fp32 (epilogue), as in
+ *                             tgemm_run_gated_backward
+ *   dbias = sum_m dz[m, :]    fp32 [N], or NULL
+ * (the residual's gradient is dY).  dz is rounded to bf16 once for the
+ * products; dbias is the sum before that rounding, in fp32.  A, B as in the
+ * forward call; Z and z_type as it left Z (or rounded to bf16 since), not read
+ * for TGEMM_ACT_NONE.  relu's derivative is 0 at z = 0.  Workspace: dz (2 * M
+ * * N bytes, padded), 4 * ceil(M / 64) * N bytes, and copies and partial
+ * products as in tgemm_run_gated_backward, whose size limits hold with N for
+ * 2F.
+ */
+TGEMM_API int tgemm_run_linear_backward(char transA, char transB, int64_t M, int64_t N, int64_t K,
+                                        const void* A, int64_t lda, const void* B, int64_t ldb,
+                                        const void* dY, int64_t lddy, const void* Z, int64_t ldz,
+                                        int z_type, int activation, void* dA, int64_t ldda,
+                                        void* dB, int64_t lddb, int epilogue, float* dbias,
+                                        void* workspace, int64_t workspace_bytes, void* stream);
+TGEMM_API int64_t tgemm_linear_backward_workspace_bytes(char transA, char transB, int64_t M,
+                                                        int64_t N, int64_t K, const void* A,
+                                                        int64_t lda, const void* B, int64_t ldb);
+
+/* Host-only argument check of tgemm_run_linear_backward (no GPU access). */
+TGEMM_API int tgemm_validate_linear_backward(char transA, char transB, int64_t M, int64_t N,
+                                             int64_t K, const void* A, int64_t lda, const void* B,
+                                             int64_t ldb, const void* dY, int64_t lddy,
+                                             const void* Z, int64_t ldz, int z_type,
+                                             int activation, const void* dA, int64_t ldda,
+                                             const void* dB, int64_t lddb, int epilogue,
+                                             const float* dbias);
 
 /* Human-readable name of a status code (static string, never NULL). */
 TGEMM_API const char* tgemm_status_string(int status);

@@ -14,6 +14,8 @@ from .tgemm import (  # noqa: F401
     gated_matmul,
     gated_matmul_i8,
     layout_of,
+    linear,
+    linear_backward,
     matmul,
     matmul_i8,
     outer_f32,

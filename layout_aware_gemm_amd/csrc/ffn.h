@@ -34,12 +34,15 @@ enum RowsType : int { kRowsI8 = 0, kRowsBf16 = 1 };
 //                         slice `chunk` of the partial buffer [split][M][N]
 //   kRowsGatedKeep        kRowsGated of bf16 operands with g, u kept (chosen by
 //                         the tiled kernel's launcher when gu is set)
+//   kRowsLinear           C[m][n] = residual + act(sum + bias), bf16 operands,
+//                         sum + bias optionally kept
 enum RowsEpi : int {
   kRowsStoreBf16 = 0,
   kRowsStoreF32 = 1,
   kRowsGated = 2,
   kRowsPart = 3,
-  kRowsGatedKeep = 4
+  kRowsGatedKeep = 4,
+  kRowsLinear = 5
 };
 
 // A product of two row-major, K-contiguous operands: A [M][K], B [N][K]
@@ -59,6 +62,13 @@ struct RowsParams {
   int64_t ldc;       // elements
   float* gu;         // bf16 gated: optional [M][ldgu], g then u
   int64_t ldgu;
+  // linear: all optional but C; the residual has C's type
+  const uint16_t* bias;  // bf16 [N]
+  const void* res;
+  int64_t ldr;
+  void* z;           // [M][ldz]: sum + bias
+  int64_t ldz;
+  int z_f32, c_f32;  // types of z, and of C and res (else bf16)
   void* part;        // kRowsPart: [split][M][N] int32 / fp32
   int tilesM, tilesN, groupM;  // the tile grid,
   int col0;          // from this output column on
@@ -125,6 +135,15 @@ bool gated_grad_fits(int64_t rows, int64_t F);
 hipError_t launch_gated_grad(const uint16_t* dh, int64_t lddh, const void* gu, int64_t ldgu,
                              bool gu_f32, int M, int64_t F, int act, uint16_t* dgu, int64_t lddgu,
                              int rows, int64_t cols, hipStream_t s);
+
+// dz = dy act'(z), zero past column N and row M to cols (a multiple of 64) and
+// rows; z is not read for kActNone.  With part (fp32 [strips][N]) also db =
+// the column sums of dz (rows_finish.hip).
+int linear_grad_strips(int64_t rows);
+bool linear_grad_fits(int64_t rows, int64_t cols);
+hipError_t launch_linear_grad(const uint16_t* dy, int64_t lddy, const void* z, int64_t ldz,
+                              bool z_f32, int M, int64_t N, int act, uint16_t* dz, int64_t lddz,
+                              int rows, int64_t cols, float* part, float* db, hipStream_t s);
 
 // dX = G . W (px: A = G [M][K], B = W) and dW = G^T . X (pw: A = G stored
 // [K][M], B = X), both bf16, in one launch (gated_bwd.hip).  M, N, A, B, C,
@@ -212,6 +231,24 @@ __device__ __forceinline__ void act_gradients(float g, float u, float h, int act
   y = hw * g * a.w;
 }
 
+// The linear product's activations: the two above, none and relu.
+constexpr int kActNone = 2, kActRelu = 3;
+
+__device__ __forceinline__ float linear_act(float z, int act) {
+  if (act == kActNone) return z;
+  if (act == kActRelu) return z <= 0.f ? 0.f : z;  // (NaN stays)
+  return act_times(z, 1.f, act);
+}
+
+// d act'(z)
+__device__ __forceinline__ float linear_act_grad(float z, float d, int act) {
+  if (act == kActNone) return d;
+  if (act == kActRelu) return z <= 0.f ? 0.f : d;
+  float x, y;
+  act_gradients(z, 1.f, d, act, x, y);
+  return x;
+}
+
 // Orders a wave's LDS accesses before this point and after it, for lanes of
 // one wave that exchange words of their own buffer without a workgroup
 // barrier.  The hardware keeps a wave's LDS accesses in order, so this costs
@@ -261,6 +298,73 @@ __device__ __forceinline__ void put4(T* o, const T* v, int n) {
   } else {
     for (int i = 0; i < n; ++i) o[i] = v[i];
   }
+}
+
+// 4 (or the first n) consecutive values of a bf16 or fp32 row.
+__device__ __forceinline__ void get4(const uint16_t* p, float* v, int n) {
+  if (n >= 4) {
+    const u16x4_any a = *reinterpret_cast<const u16x4_any*>(p);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      v[2 * i] = __uint_as_float(a.w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(a.w[i] & 0xffff0000u);
+    }
+  } else {
+    for (int i = 0; i < n; ++i) v[i] = from_bf16(p[i]);
+  }
+}
+__device__ __forceinline__ void get4(const float* p, float* v, int n) {
+  if (n >= 4) {
+    const x4_any<float> a = *reinterpret_cast<const x4_any<float>*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = a.v[i];
+  } else {
+    for (int i = 0; i < n; ++i) v[i] = p[i];
+  }
+}
+
+// The linear product's epilogue for up to 4 consecutive outputs, in three
+// steps, so that a caller can load early.  A residual may be C itself: a
+// thread loads its values before it stores over them.
+__device__ __forceinline__ void linear_bias4(const RowsParams& p, int c, int n, float (&b)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[i] = 0.f;
+  if (p.bias != nullptr && n > 0) get4(p.bias + c, b, n);
+}
+__device__ __forceinline__ void linear_res4(const RowsParams& p, int row, int c, int n,
+                                            float (&r)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = 0.f;
+  if (p.res == nullptr || row >= p.M || n <= 0) return;
+  const int64_t o = (int64_t)row * p.ldr + c;
+  if (p.c_f32)
+    get4(static_cast<const float*>(p.res) + o, r, n);
+  else
+    get4(static_cast<const uint16_t*>(p.res) + o, r, n);
+}
+__device__ __forceinline__ void linear_put4(const RowsParams& p, int row, int c, int n,
+                                            const float* sum, const float (&b)[4],
+                                            const float (&r)[4]) {
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = sum[i] + b[i];
+  if (p.z != nullptr) {
+    const int64_t o = (int64_t)row * p.ldz + c;
+    if (p.z_f32)
+      put4(static_cast<float*>(p.z) + o, v, n);
+    else
+      put4(static_cast<uint16_t*>(p.z) + o, v, n);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = linear_act(v[i], p.act);
+    if (p.res != nullptr) v[i] += r[i];
+  }
+  const int64_t o = (int64_t)row * p.ldc + c;
+  if (p.c_f32)
+    put4(static_cast<float*>(p.C) + o, v, n);
+  else
+    put4(static_cast<uint16_t*>(p.C) + o, v, n);
 }
 
 }  // namespace tgemm

@@ -1,5 +1,5 @@
-// Host entries of the feed-forward operators: 8-bit products, gated
-// products and their gradient, the row quantiser.  Validation (validate.cpp),
+// Host entries of the feed-forward operators: 8-bit products, gated and linear
+// products and their gradients, the row quantiser.  Validation (validate.cpp),
 // choice of kernel, workspace, launches.
 #include "ffn.h"
 
@@ -239,35 +239,28 @@ int run_i8(char ta, char tb, const void* A, int64_t lda, const void* B, int64_t 
 
 inline int64_t round_up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 
-// bf16 gated product.  Operands that the kernels cannot read in place -- not
+// bf16 product, gated or linear: p holds everything but the operands and K.
+// Operands that the kernels cannot read in place -- not
 // K-contiguous, or with rows off 16-byte boundaries -- are copied into the
 // workspace first.  (The copy costs a read and a write of the operand; the
 // alternative, the library's GEMM in the operand's own layout, has to write
 // and re-read the whole fp32 [M][2F] product instead, and runs rows off
 // 16-byte boundaries at a third of the rate.)
-int run_gated(char ta, char tb, int64_t M, int64_t F, int64_t K, const void* A, int64_t lda,
-              const void* B, int64_t ldb, int act, void* H, int64_t ldh, float* GU, int64_t ldgu,
-              const CallSpace& space, hipStream_t s) {
-  RowsParams p = {};
-  p.M = (int)M;
-  p.N = (int)(2 * F);
-  p.F = (int)F;
-  p.act = act;
-  p.C = H;
-  p.ldc = ldh;
-  p.gu = GU;
-  p.ldgu = ldgu;
+int run_bf16(char ta, char tb, int64_t K, const void* A, int64_t lda, const void* B, int64_t ldb,
+             RowsParams p, int epi, bool gate, const CallSpace& space, hipStream_t s) {
   const int64_t Kp = round_up(K, 8);
   if (Kp >= int64_t(1) << 30) return TGEMM_ERR_UNSUPPORTED;
-  if (is_n(ta) && M == 1) lda = Kp;  // (the stride of a single row is never used)
+  // (the stride of a single row is never used)
+  if (is_n(ta) && p.M == 1) lda = Kp;
+  if (!is_n(tb) && p.N == 1) ldb = Kp;
   const bool packA = !is_n(ta) || !rows_aligned(A, 2 * lda, 2 * K) || !stride_fits(2 * lda);
   const bool packB = is_n(tb) || !rows_aligned(B, 2 * ldb, 2 * K) || !stride_fits(2 * ldb);
   if ((packA || packB) && !stride_fits(2 * Kp)) return TGEMM_ERR_UNSUPPORTED;
   p.K = (int)(2 * Kp);
-  const RowsPlan r = plan_rows(&p, true);
+  const RowsPlan r = plan_rows(&p, gate);
   PackRows ca = {A, lda, is_n(ta), p.M, (int)K, nullptr, p.M, Kp};
   PackRows cb = {B, ldb, !is_n(tb), p.N, (int)K, nullptr, p.N, Kp};
-  if (!grid_fits(p, r, true) || (packA && !pack_rows_fits(ca, 2)) ||
+  if (!grid_fits(p, r, gate) || (packA && !pack_rows_fits(ca, 2)) ||
       (packB && !pack_rows_fits(cb, 2)))
     return TGEMM_ERR_UNSUPPORTED;
   const size_t bytesA = packA ? round256((size_t)p.M * Kp * 2) : 0;
@@ -276,7 +269,7 @@ int run_gated(char ta, char tb, int64_t M, int64_t F, int64_t K, const void* A, 
   Workspace w;
   const int st = take_workspace(space, s, bytesA + bytesB + bytesP, &w);
   if (st != TGEMM_OK) return st;
-  say_rows("gated bf16", p, r);
+  say_rows(gate ? "gated bf16" : "linear", p, r);
   char* const ws = static_cast<char*>(w.ptr);
   p.A = static_cast<const char*>(A);
   p.B = static_cast<const char*>(B);
@@ -296,25 +289,51 @@ int run_gated(char ta, char tb, int64_t M, int64_t F, int64_t K, const void* A, 
     p.ldb = 2 * Kp;
   }
   if (bytesP) p.part = ws + bytesA + bytesB;
-  if (e == hipSuccess) e = launch_rows(kRowsBf16, p, r, kRowsGated, true, s);
+  if (e == hipSuccess) e = launch_rows(kRowsBf16, p, r, epi, gate, s);
   release_workspace(w);
   return status_of(e);
 }
 
-// Gradient of the gated product: dGU into the workspace, then dA = dGU .
-// op(B)^T and dB in one launch, which reads A and B as [M][K] and [2F][K]
-// rows on 16-byte boundaries; others are copied first.  dB stored [K][2F] is
-// the product with the operands exchanged, A^T . dGU; its first operand is
-// then a zero-padded copy of A.
-int run_gated_backward(char ta, char tb, int64_t M, int64_t F, int64_t K, const void* A,
-                       int64_t lda, const void* B, int64_t ldb, const void* dH, int64_t lddh,
-                       const void* GU, int64_t ldgu, bool gu_f32, int act, void* dA, int64_t ldda,
-                       void* dB, int64_t lddb, bool f32, const CallSpace& space, hipStream_t s) {
-  const int64_t N2 = 2 * F, Kp = round_up(K, 8);
+int run_gated(char ta, char tb, int64_t M, int64_t F, int64_t K, const void* A, int64_t lda,
+              const void* B, int64_t ldb, int act, void* H, int64_t ldh, float* GU, int64_t ldgu,
+              const CallSpace& space, hipStream_t s) {
+  RowsParams p = {};
+  p.M = (int)M;
+  p.N = (int)(2 * F);
+  p.F = (int)F;
+  p.act = act;
+  p.C = H;
+  p.ldc = ldh;
+  p.gu = GU;
+  p.ldgu = ldgu;
+  return run_bf16(ta, tb, K, A, lda, B, ldb, p, kRowsGated, true, space, s);
+}
+
+// The two gradient products of a bf16 product with N2 columns, given the
+// gradient G [M][N2] of its sums: dA = G . op(B)^T and dB in one launch, which
+// reads A and B as [M][K] and [N2][K] rows on 16-byte boundaries; others are
+// copied first.  dB stored [K][N2] is the product with the operands exchanged,
+// A^T . G; its first operand is then a zero-padded copy of A.
+// grad(G, ldg, rows, extra) enqueues the kernels that write G into the
+// workspace, zero-padded, with extra_bytes of their own there; grad_fits:
+// their grids are launchable.
+struct GradSource {
+  size_t extra_bytes;
+  bool fits;
+};
+
+template <class Grad>
+int run_backward(const char* what, char ta, char tb, int64_t M, int64_t N2, int64_t K,
+                 const void* A, int64_t lda, const void* B, int64_t ldb, void* dA, int64_t ldda,
+                 void* dB, int64_t lddb, bool f32, const GradSource& src, Grad&& grad,
+                 const CallSpace& space, hipStream_t s) {
+  const int64_t Kp = round_up(K, 8);
   const int64_t ldg = round_up(N2, 64), rows = round_up(M, 64);
   constexpr int64_t kLimit = int64_t(1) << 23;  // (32-bit copy offsets)
   if (Kp >= kLimit || ldg >= kLimit) return TGEMM_ERR_UNSUPPORTED;
-  if (is_n(ta) && M == 1) lda = Kp;  // (the stride of a single row is never used)
+  // (the stride of a single row is never used)
+  if (is_n(ta) && M == 1) lda = Kp;
+  if (!is_n(tb) && N2 == 1) ldb = Kp;
   const bool swap = is_n(tb);
   const bool packA = !is_n(ta) || swap || !rows_aligned(A, 2 * lda, 0) || lda >= kLimit;
   const bool packB = is_n(tb) || !rows_aligned(B, 2 * ldb, 0) || ldb >= kLimit;
@@ -339,24 +358,26 @@ int run_gated_backward(char ta, char tb, int64_t M, int64_t F, int64_t K, const 
   const int tile = gated_bwd_plan(&px, &pw);
   PackRows ca = {A, lda, is_n(ta), (int)M, (int)K, nullptr, (int)rows, Kp};
   PackRows cb = {B, ldb, !is_n(tb), (int)N2, (int)K, nullptr, (int)N2, Kp};
-  if (!gated_bwd_fits(px, pw) || !gated_grad_fits(rows, F) || (packA && !pack_rows_fits(ca, 2)) ||
+  if (!gated_bwd_fits(px, pw) || !src.fits || (packA && !pack_rows_fits(ca, 2)) ||
       (packB && !pack_rows_fits(cb, 2)))
     return TGEMM_ERR_UNSUPPORTED;
   const size_t bytesX =
       px.splitk > 1 ? round256((size_t)px.splitk * px.M * px.N * sizeof(float)) : 0;
-  const size_t bytesW = pw.splitk > 1 ? (size_t)pw.splitk * pw.M * pw.N * sizeof(float) : 0;
+  const size_t bytesW =
+      pw.splitk > 1 ? round256((size_t)pw.splitk * pw.M * pw.N * sizeof(float)) : 0;
   Workspace w;
-  const int st = take_workspace(space, s, bytesG + bytesA + bytesB + bytesX + bytesW, &w);
+  const int st =
+      take_workspace(space, s, bytesG + bytesA + bytesB + bytesX + bytesW + src.extra_bytes, &w);
   if (st != TGEMM_OK) return st;
   if (verbose())
     fprintf(stderr,
-            "tgemm: gated backward %c%c M=%lld F=%lld K=%lld copies=%d,%d tile=%d split=%d,%d\n", ta,
-            tb, (long long)M, (long long)F, (long long)K, packA, packB, tile, px.splitk, pw.splitk);
+            "tgemm: %s backward %c%c M=%lld N=%lld K=%lld copies=%d,%d tile=%d split=%d,%d\n", what,
+            ta, tb, (long long)M, (long long)N2, (long long)K, packA, packB, tile, px.splitk,
+            pw.splitk);
   char* ws = static_cast<char*>(w.ptr);
   uint16_t* const G = reinterpret_cast<uint16_t*>(ws);
   ws += bytesG;
-  hipError_t e = launch_gated_grad(static_cast<const uint16_t*>(dH), lddh, GU, ldgu, gu_f32, (int)M,
-                                   F, act, G, ldg, (int)rows, ldg, s);
+  hipError_t e = grad(G, ldg, (int)rows, ws + bytesA + bytesB + bytesX + bytesW);
   const void *Ar = A, *Br = B;  // [M][K], [2F][K] rows
   if (packA && e == hipSuccess) {
     ca.out = ws;
@@ -384,6 +405,40 @@ int run_gated_backward(char ta, char tb, int64_t M, int64_t F, int64_t K, const 
   if (e == hipSuccess) e = launch_gated_bwd(tile, px, pw, false, f32, s);
   release_workspace(w);
   return status_of(e);
+}
+
+// Gradient of the gated product, by way of dGU.
+int run_gated_backward(char ta, char tb, int64_t M, int64_t F, int64_t K, const void* A,
+                       int64_t lda, const void* B, int64_t ldb, const void* dH, int64_t lddh,
+                       const void* GU, int64_t ldgu, bool gu_f32, int act, void* dA, int64_t ldda,
+                       void* dB, int64_t lddb, bool f32, const CallSpace& space, hipStream_t s) {
+  return run_backward(
+      "gated", ta, tb, M, 2 * F, K, A, lda, B, ldb, dA, ldda, dB, lddb, f32,
+      {0, gated_grad_fits(round_up(M, 64), F)},
+      [&](uint16_t* G, int64_t ldg, int rows, char*) {
+        return launch_gated_grad(static_cast<const uint16_t*>(dH), lddh, GU, ldgu, gu_f32, (int)M,
+                                 F, act, G, ldg, rows, ldg, s);
+      },
+      space, s);
+}
+
+// Gradient of the linear product, by way of dZ; db: its column sums.
+int run_linear_backward(char ta, char tb, int64_t M, int64_t N, int64_t K, const void* A,
+                        int64_t lda, const void* B, int64_t ldb, const void* dY, int64_t lddy,
+                        const void* Z, int64_t ldz, bool z_f32, int act, void* dA, int64_t ldda,
+                        void* dB, int64_t lddb, bool f32, float* db, const CallSpace& space,
+                        hipStream_t s) {
+  const int64_t rows = round_up(M, 64), cols = round_up(N, 64);
+  const size_t sums = db != nullptr ? (size_t)linear_grad_strips(rows) * N * sizeof(float) : 0;
+  return run_backward(
+      "linear", ta, tb, M, N, K, A, lda, B, ldb, dA, ldda, dB, lddb, f32,
+      {sums, linear_grad_fits(rows, cols)},
+      [&](uint16_t* G, int64_t ldg, int r, char* extra) {
+        return launch_linear_grad(static_cast<const uint16_t*>(dY), lddy, Z, ldz, z_f32, (int)M, N,
+                                  act, G, ldg, r, ldg,
+                                  db != nullptr ? reinterpret_cast<float*>(extra) : nullptr, db, s);
+      },
+      space, s);
 }
 
 // The workspace list allocates host memory; no exception leaves the library.
@@ -554,6 +609,89 @@ extern "C" int64_t tgemm_gated_backward_workspace_bytes(char transA, char transB
                                              nullptr, 2 * F, false, 0, nullptr, K, nullptr, ldd,
                                              false,
                                              {nullptr, 0, &need}, nullptr);
+                 }),
+                 need);
+}
+
+extern "C" int tgemm_run_linear(char transA, char transB, int64_t M, int64_t N, int64_t K,
+                                const void* A, int64_t lda, const void* B, int64_t ldb,
+                                const void* bias, int activation, const void* residual, int64_t ldr,
+                                void* Y, int64_t ldy, int epilogue, void* Z, int64_t ldz,
+                                int z_type, void* workspace, int64_t workspace_bytes,
+                                void* stream) {
+  const int st = tgemm_validate_linear(transA, transB, M, N, K, A, lda, B, ldb, bias, activation,
+                                       residual, ldr, Y, ldy, epilogue, Z, ldz, z_type);
+  if (st != TGEMM_OK) return st;
+  RowsParams p = {};
+  p.M = (int)M;
+  p.N = (int)N;
+  p.act = activation;
+  p.C = Y;
+  p.ldc = ldy;
+  p.c_f32 = epilogue == TGEMM_EPI_STORE_F32;
+  p.bias = static_cast<const uint16_t*>(bias);
+  p.res = residual;
+  p.ldr = ldr;
+  p.z = Z;
+  p.ldz = ldz;
+  p.z_f32 = z_type == TGEMM_EPI_STORE_F32;
+  return no_throw([&] {
+    return run_bf16(transA, transB, K, A, lda, B, ldb, p, kRowsLinear, false,
+                    {workspace, workspace_bytes, nullptr}, reinterpret_cast<hipStream_t>(stream));
+  });
+}
+
+extern "C" int64_t tgemm_linear_workspace_bytes(char transA, char transB, int64_t M, int64_t N,
+                                                int64_t K, const void* A, int64_t lda,
+                                                const void* B, int64_t ldb) {
+  const int st =
+      tgemm_validate_linear(transA, transB, M, N, K, A, lda, B, ldb, nullptr, TGEMM_ACT_NONE,
+                            nullptr, 0, g_any, N, TGEMM_EPI_STORE_BF16, nullptr, 0,
+                            TGEMM_EPI_STORE_BF16);
+  if (st != TGEMM_OK) return st;
+  RowsParams p = {};
+  p.M = (int)M;
+  p.N = (int)N;
+  int64_t need = 0;
+  return queried(no_throw([&] {
+                   return run_bf16(transA, transB, K, A, lda, B, ldb, p, kRowsLinear, false,
+                                   {nullptr, 0, &need}, nullptr);
+                 }),
+                 need);
+}
+
+extern "C" int tgemm_run_linear_backward(char transA, char transB, int64_t M, int64_t N, int64_t K,
+                                         const void* A, int64_t lda, const void* B, int64_t ldb,
+                                         const void* dY, int64_t lddy, const void* Z, int64_t ldz,
+                                         int z_type, int activation, void* dA, int64_t ldda,
+                                         void* dB, int64_t lddb, int epilogue, float* dbias,
+                                         void* workspace, int64_t workspace_bytes, void* stream) {
+  const int st = tgemm_validate_linear_backward(transA, transB, M, N, K, A, lda, B, ldb, dY, lddy,
+                                                Z, ldz, z_type, activation, dA, ldda, dB, lddb,
+                                                epilogue, dbias);
+  if (st != TGEMM_OK) return st;
+  return no_throw([&] {
+    return run_linear_backward(transA, transB, M, N, K, A, lda, B, ldb, dY, lddy, Z, ldz,
+                               z_type == TGEMM_EPI_STORE_F32, activation, dA, ldda, dB, lddb,
+                               epilogue == TGEMM_EPI_STORE_F32, dbias,
+                               {workspace, workspace_bytes, nullptr},
+                               reinterpret_cast<hipStream_t>(stream));
+  });
+}
+
+extern "C" int64_t tgemm_linear_backward_workspace_bytes(char transA, char transB, int64_t M,
+                                                         int64_t N, int64_t K, const void* A,
+                                                         int64_t lda, const void* B, int64_t ldb) {
+  const int64_t ldd = transB == 'N' || transB == 'n' ? N : K;
+  const int st = tgemm_validate_linear_backward(
+      transA, transB, M, N, K, A, lda, B, ldb, g_any, N, nullptr, 0, TGEMM_EPI_STORE_BF16,
+      TGEMM_ACT_NONE, g_any, K, g_any, ldd, TGEMM_EPI_STORE_BF16, nullptr);
+  if (st != TGEMM_OK) return st;
+  int64_t need = 0;
+  return queried(no_throw([&] {
+                   return run_linear_backward(transA, transB, M, N, K, A, lda, B, ldb, nullptr, N,
+                                              nullptr, 0, false, kActNone, nullptr, K, nullptr, ldd,
+                                              false, g_any, {nullptr, 0, &need}, nullptr);
                  }),
                  need);
 }

@@ -43,6 +43,13 @@ __global__ void __launch_bounds__(kThr) finish_kernel(RowsParams p) {
     add4(a, part + q * slice, n);
     if constexpr (GATE) add4(a2, part + q * slice + p.F, n);
   }
+  if constexpr (EPI == kRowsLinear) {
+    float bias[4], res[4];
+    linear_bias4(p, c, n, bias);
+    linear_res4(p, row, c, n, res);
+    linear_put4(p, row, c, n, a, bias, res);
+    return;
+  }
   float v[4], u[4], h[4];
   const float sa = I8 ? p.scale_a[row] : 1.f;
 #pragma unroll
@@ -206,6 +213,85 @@ __global__ void __launch_bounds__(kThr) gated_grad_kernel(
   }
 }
 
+// The linear product's dz = dy act'(z), rounded once to bf16, the type the
+// gradient products read, and the column sums of dz before that rounding.  A
+// workgroup takes 256 columns (8 per thread) of a strip of kStrip rows, eight
+// rows at a time; its sums over the strip meet in LDS, in row order, and a
+// second kernel adds the strips in order: nothing depends on timing.  Rows
+// M .. rows - 1 and columns N .. cols - 1 of dz are set to zero.
+constexpr int kStrip = 64;
+
+template <class T>  // the type of z
+__global__ void __launch_bounds__(kThr) linear_grad_kernel(
+    const uint16_t* __restrict__ dy, int64_t lddy, const T* __restrict__ z, int64_t ldz, int M,
+    int64_t N, int act, uint16_t* __restrict__ dz, int64_t lddz, int rows, int64_t cols,
+    float* __restrict__ part, int cblocks) {
+  __shared__ float sums[8][256 + 8];
+  const int strip = (int)(blockIdx.x / cblocks);
+  const int64_t c0 = (int64_t)(blockIdx.x % cblocks) * 256;
+  const int cl = ((int)threadIdx.x & 31) * 8, rl = (int)threadIdx.x >> 5;
+  const int64_t c = c0 + cl;
+  const int n = (int)min((int64_t)8, N - c);  // values this thread computes
+  float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+  for (int i = 0; i < kStrip; i += 8) {
+    const int row = strip * kStrip + i + rl;
+    if (row >= rows || c >= cols) continue;
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (row < M) {
+      const uint16_t* const pd = dy + row * lddy + c;
+      if (n == 8) {
+        float d[8], v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        load_values<8>(pd, d);
+        if (act != kActNone) load_values<8>(z + row * ldz + c, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = linear_act_grad(v[e], d[e], act);
+      } else {
+        for (int e = 0; e < n; ++e) {
+          float d[1], v[1] = {0.f};
+          load_values<1>(pd + e, d);
+          if (act != kActNone) load_values<1>(z + row * ldz + c + e, v);
+          x[e] = linear_act_grad(v[0], d[0], act);
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] += x[e];
+    // (cols is a multiple of 64, lddz of 8)
+    uint4 o;
+    o.x = pack_bf16x2(x[0], x[1]);
+    o.y = pack_bf16x2(x[2], x[3]);
+    o.z = pack_bf16x2(x[4], x[5]);
+    o.w = pack_bf16x2(x[6], x[7]);
+    *reinterpret_cast<uint4*>(dz + row * lddz + c) = o;
+  }
+  if (part == nullptr) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sums[rl][cl + e] = t[e];
+  __syncthreads();
+  float s = 0.f;
+#pragma unroll
+  for (int r = 0; r < 8; ++r) s += sums[r][threadIdx.x];
+  if (c0 + (int)threadIdx.x < N) part[strip * N + c0 + (int)threadIdx.x] = s;
+}
+
+// Columns of part [strips][N] added up: 64 columns by 4 groups of strips per
+// workgroup, the groups in order.
+__global__ void __launch_bounds__(kThr) column_sum_kernel(const float* __restrict__ part,
+                                                          int strips, int64_t N,
+                                                          float* __restrict__ out) {
+  __shared__ float s[4][64];
+  const int l = (int)threadIdx.x & 63, g = (int)threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + l;
+  const int per = (strips + 3) / 4, end = min(strips, (g + 1) * per);
+  float a = 0.f;
+  if (c < N)
+    for (int i = g * per; i < end; ++i) a += part[i * N + c];
+  s[g][l] = a;
+  __syncthreads();
+  if (g == 0 && c < N) out[c] = s[0][l] + s[1][l] + s[2][l] + s[3][l];
+}
+
 int64_t finish_blocks(const RowsParams& p, bool gate) {
   return (int64_t)p.M * ceil_div(gate ? p.F : p.N, 4 * kThr);
 }
@@ -229,6 +315,8 @@ hipError_t launch_rows_finish(int type, int epi, const RowsParams& p, hipStream_
     if (epi == kRowsGated) return finish_one<int, kRowsGated>(p, s);
   } else if (epi == kRowsGated) {
     return finish_one<float, kRowsGated>(p, s);
+  } else if (epi == kRowsLinear) {
+    return finish_one<float, kRowsLinear>(p, s);
   }
   return hipErrorInvalidValue;
 }
@@ -273,6 +361,30 @@ hipError_t launch_gated_grad(const uint16_t* dh, int64_t lddh, const void* gu, i
                    static_cast<const float*>(gu), ldgu, M, F, act, dgu, lddgu, cols, per_row);
   return enqueue(gated_grad_kernel<uint16_t>, grid, block, s, dh, lddh,
                  static_cast<const uint16_t*>(gu), ldgu, M, F, act, dgu, lddgu, cols, per_row);
+}
+
+int linear_grad_strips(int64_t rows) { return ceil_div(rows, kStrip); }
+
+bool linear_grad_fits(int64_t rows, int64_t cols) {
+  return (int64_t)linear_grad_strips(rows) * ceil_div(cols, 256) <= kMaxWorkgroups;
+}
+
+hipError_t launch_linear_grad(const uint16_t* dy, int64_t lddy, const void* z, int64_t ldz,
+                              bool z_f32, int M, int64_t N, int act, uint16_t* dz, int64_t lddz,
+                              int rows, int64_t cols, float* part, float* db, hipStream_t s) {
+  const int strips = linear_grad_strips(rows), cblocks = ceil_div(cols, 256);
+  const dim3 grid((unsigned)((int64_t)strips * cblocks)), block(kThr);
+  hipError_t e;
+  if (z_f32)
+    e = enqueue(linear_grad_kernel<float>, grid, block, s, dy, lddy, static_cast<const float*>(z),
+                ldz, M, N, act, dz, lddz, rows, cols, part, cblocks);
+  else
+    e = enqueue(linear_grad_kernel<uint16_t>, grid, block, s, dy, lddy,
+                static_cast<const uint16_t*>(z), ldz, M, N, act, dz, lddz, rows, cols, part,
+                cblocks);
+  if (e != hipSuccess || part == nullptr) return e;
+  return enqueue(column_sum_kernel, dim3(ceil_div(N, 64)), block, s,
+                 static_cast<const float*>(part), strips, N, db);
 }
 
 }  // namespace tgemm

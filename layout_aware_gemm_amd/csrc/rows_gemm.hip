@@ -1,6 +1,6 @@
 // Large products of two K-contiguous operands on the matrix cores, int8
-// (scaled, or gated) and bf16 (gated): out = epilogue(A . B^T), A [M][K],
-// B [N][K].
+// (scaled, or gated) and bf16 (gated, or with bias, activation and residual):
+// out = epilogue(A . B^T), A [M][K], B [N][K].
 //
 // The LDS image, copy schedule and tile shapes are those of the bf16 NT
 // kernel: a k-step is 128 bytes of every row (128 int8 or 64 bf16), copied
@@ -337,6 +337,48 @@ __device__ __forceinline__ void keep_epilogue(const RowsParams& p,
   }
 }
 
+// The linear epilogue, 32 rows at a time through LDS words of the wave's own,
+// as above: rows enter and leave in vectors of four (a residual read from the
+// accumulators' layout takes a request for every 32 values).
+template <int BM, int BN>
+__device__ __forceinline__ void linear_epilogue(const RowsParams& p,
+                                                const f32x16_t (&acc)[BM / 64][BN / 64], float* st,
+                                                int row0, int col0, int lane) {
+  constexpr int FM = BM / 64, FN = BN / 64, LD = keep_row<BN>();
+  constexpr int LPR = BN / 8, RPI = 64 / LPR, NQ = 32 / RPI;  // lanes per row, rows per pass
+  constexpr int U = 4;                                        // passes whose loads go ahead
+  const int h = lane >> 5, lc = lane & 31;
+  const int cl = 4 * (lane % LPR), c = col0 + cl;  // this lane's four columns
+  const int n = p.N - c;                           // of which so many exist
+  float b[4];
+  linear_bias4(p, c, n, b);
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        st[(8 * (r >> 2) + 4 * h + (r & 3)) * LD + j * 32 + lc] = acc[i][j][r];
+    wave_lds_order();
+#pragma unroll
+    for (int q0 = 0; q0 < NQ; q0 += U) {
+      float r[U][4];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        linear_res4(p, row0 + i * 32 + (q0 + u) * RPI + lane / LPR, c, n, r[u]);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int rl = (q0 + u) * RPI + lane / LPR, row = row0 + i * 32 + rl;
+        const float4 v = *reinterpret_cast<const float4*>(st + rl * LD + cl);
+        if (row >= p.M || n <= 0) continue;
+        const float e[4] = {v.x, v.y, v.z, v.w};
+        linear_put4(p, row, c, n, e, b, r[u]);
+      }
+    }
+    wave_lds_order();
+  }
+}
+
 // ONCE: B is loaded non-temporally (one row of tiles only).
 template <class Op, int BM, int BN, bool GATE, int EPI, bool ONCE>
 __global__ void __launch_bounds__(kThreads, 1) rows_kernel(RowsParams p) {
@@ -504,6 +546,11 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(RowsParams p) {
     static_assert(4 * kWave * 4 <= (int)sizeof(lds), "the waves' buffers fit");
     keep_epilogue<BM, BN>(p, acc, reinterpret_cast<float*>(lds) + wave_u * kWave,
                           m0 + wm * (BM / 2), n0, wn, lane);
+  } else if constexpr (EPI == kRowsLinear) {
+    constexpr int kWave = 32 * keep_row<BN>();
+    static_assert(4 * kWave * 4 <= (int)sizeof(lds), "the waves' buffers fit");
+    linear_epilogue<BM, BN>(p, acc, reinterpret_cast<float*>(lds) + wave_u * kWave,
+                            m0 + wm * (BM / 2), n0 + wn * (BN / 2), lane);
   } else {
     float* const scl = reinterpret_cast<float*>(lds);  // BM row scales, BN column scales
     if constexpr (SCALED) {
@@ -539,7 +586,8 @@ hipError_t launch_tile(int type, int epi, bool gate, const RowsParams& p, hipStr
       if (type == kRowsI8)
         return gate ? launch_one<OpI8, BM, BN, true, kRowsPart>(p, s)
                     : launch_one<OpI8, BM, BN, false, kRowsPart>(p, s);
-      if (gate) return launch_one<OpBf16, BM, BN, true, kRowsPart>(p, s);
+      return gate ? launch_one<OpBf16, BM, BN, true, kRowsPart>(p, s)
+                  : launch_one<OpBf16, BM, BN, false, kRowsPart>(p, s);
     }
   } else if (type == kRowsI8) {
     if (gate && epi == kRowsGated) return launch_one<OpI8, BM, BN, true, kRowsGated>(p, s);
@@ -548,6 +596,8 @@ hipError_t launch_tile(int type, int epi, bool gate, const RowsParams& p, hipStr
   } else if (gate && epi == kRowsGated) {
     return p.gu != nullptr ? launch_one<OpBf16, BM, BN, true, kRowsGatedKeep>(p, s)
                            : launch_one<OpBf16, BM, BN, true, kRowsGated>(p, s);
+  } else if (!gate && epi == kRowsLinear) {
+    return launch_one<OpBf16, BM, BN, false, kRowsLinear>(p, s);
   }
   return hipErrorInvalidValue;
 }

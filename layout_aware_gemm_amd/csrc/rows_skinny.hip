@@ -181,6 +181,14 @@ __global__ void __launch_bounds__(W * 64) skinny_kernel(RowsParams p) {
     }
     const int n = min(4, nout - c0);
     if (n <= 0) continue;
+    if constexpr (EPI == kRowsLinear) {
+      const float e[4] = {(float)a[0], (float)a[1], (float)a[2], (float)a[3]};
+      float bias[4], res[4];
+      linear_bias4(p, c0, n, bias);
+      linear_res4(p, row, c0, n, res);
+      linear_put4(p, row, c0, n, e, bias, res);
+      continue;
+    }
     float v[4], g[4], u[4];
     const float sa = I8 ? p.scale_a[row] : 1.f;
 #pragma unroll
@@ -280,8 +288,10 @@ hipError_t launch_blocks(const RowsParams& p, hipStream_t s) {
 
 hipError_t launch_rows_skinny(int type, int epi, const RowsParams& p, hipStream_t s) {
   if (p.M > kSkinnyRows) return hipErrorInvalidValue;
-  if (type == kRowsBf16)
+  if (type == kRowsBf16) {
+    if (epi == kRowsLinear) return launch_blocks<SkBf16, false, kRowsLinear>(p, s);
     return epi == kRowsGated ? launch_blocks<SkBf16, true, kRowsGated>(p, s) : hipErrorInvalidValue;
+  }
   if (epi == kRowsGated) return launch_blocks<SkI8, true, kRowsGated>(p, s);
   if (epi == kRowsStoreBf16) return launch_blocks<SkI8, false, kRowsStoreBf16>(p, s);
   if (epi == kRowsStoreF32) return launch_blocks<SkI8, false, kRowsStoreF32>(p, s);

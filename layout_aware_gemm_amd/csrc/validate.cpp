@@ -106,6 +106,10 @@ inline bool type_ok(int t) { return t == TGEMM_EPI_STORE_BF16 || t == TGEMM_EPI_
 
 inline bool act_ok(int a) { return a == TGEMM_ACT_SILU || a == TGEMM_ACT_GELU_TANH; }
 
+inline bool linear_act_ok(int a) {
+  return act_ok(a) || a == TGEMM_ACT_NONE || a == TGEMM_ACT_RELU;
+}
+
 }  // namespace
 
 extern "C" int tgemm_validate_i8(char transA, char transB, int64_t M, int64_t N, int64_t K,
@@ -174,6 +178,46 @@ extern "C" int tgemm_validate_gated_backward(char transA, char transB, int64_t M
   if (st == TGEMM_OK) st = check_rows(dA, M, K, ldda);
   if (st == TGEMM_OK)
     st = is_n(transB) ? check_rows(dB, K, 2 * F, lddb) : check_rows(dB, 2 * F, K, lddb);
+  return st;
+}
+
+extern "C" int tgemm_validate_linear(char transA, char transB, int64_t M, int64_t N, int64_t K,
+                                     const void* A, int64_t lda, const void* B, int64_t ldb,
+                                     const void* bias, int activation, const void* residual,
+                                     int64_t ldr, const void* Y, int64_t ldy, int epilogue,
+                                     const void* Z, int64_t ldz, int z_type) {
+  (void)bias;
+  if (!type_ok(epilogue) || !linear_act_ok(activation)) return TGEMM_ERR_INVALID_ARG;
+  int st = tgemm_validate(transA, transB, M, N, K, A, lda, B, ldb, Y, ldy, epilogue, nullptr,
+                          nullptr, nullptr);
+  if (st != TGEMM_OK) return st;
+  if (M > kMaxRows || N > kMaxRows) return TGEMM_ERR_UNSUPPORTED;
+  st = check_rows(Y, M, N, ldy);
+  if (st == TGEMM_OK && residual != nullptr) st = check_rows(residual, M, N, ldr);
+  if (st == TGEMM_OK && Z != nullptr)
+    st = type_ok(z_type) ? check_rows(Z, M, N, ldz) : TGEMM_ERR_INVALID_ARG;
+  return st;
+}
+
+extern "C" int tgemm_validate_linear_backward(char transA, char transB, int64_t M, int64_t N,
+                                              int64_t K, const void* A, int64_t lda, const void* B,
+                                              int64_t ldb, const void* dY, int64_t lddy,
+                                              const void* Z, int64_t ldz, int z_type,
+                                              int activation, const void* dA, int64_t ldda,
+                                              const void* dB, int64_t lddb, int epilogue,
+                                              const float* dbias) {
+  (void)dbias;
+  if (!type_ok(epilogue) || !linear_act_ok(activation)) return TGEMM_ERR_INVALID_ARG;
+  int st = tgemm_validate(transA, transB, M, N, K, A, lda, B, ldb, dY, lddy, TGEMM_EPI_STORE_BF16,
+                          nullptr, nullptr, nullptr);
+  if (st != TGEMM_OK) return st;
+  if (M > kMaxRows || N > kMaxRows) return TGEMM_ERR_UNSUPPORTED;
+  st = check_rows(dY, M, N, lddy);
+  if (st == TGEMM_OK && activation != TGEMM_ACT_NONE)
+    st = type_ok(z_type) ? check_rows(Z, M, N, ldz) : TGEMM_ERR_INVALID_ARG;
+  if (st == TGEMM_OK) st = check_rows(dA, M, K, ldda);
+  if (st == TGEMM_OK)
+    st = is_n(transB) ? check_rows(dB, K, N, lddb) : check_rows(dB, N, K, lddb);
   return st;
 }
 

@@ -42,11 +42,16 @@ EXPORTS = ("tgemm_run", "tgemm_run_fp8", "tgemm_validate", "tgemm_validate_fp8",
            "tgemm_validate_gated_grad", "tgemm_run_gated_backward",
            "tgemm_validate_gated_backward", "tgemm_i8_workspace_bytes",
            "tgemm_gated_workspace_bytes", "tgemm_gated_i8_workspace_bytes",
-           "tgemm_gated_backward_workspace_bytes")
+           "tgemm_gated_backward_workspace_bytes", "tgemm_run_linear", "tgemm_validate_linear",
+           "tgemm_linear_workspace_bytes", "tgemm_run_linear_backward",
+           "tgemm_validate_linear_backward", "tgemm_linear_backward_workspace_bytes")
 
 ACT_SILU = 0
 ACT_GELU_TANH = 1
+ACT_NONE = 2
+ACT_RELU = 3
 _ACTS = {"silu": ACT_SILU, "gelu_tanh": ACT_GELU_TANH}
+_LINEAR_ACTS = {"none": ACT_NONE, "relu": ACT_RELU, **_ACTS}
 
 
 class TgemmError(RuntimeError):
@@ -124,7 +129,10 @@ def lib():
                 ("run_gated_i8", product + [vp, vp, ci, vp, i64], True),
                 ("gated_grad", [i64, i64, vp, i64, vp, i64, ci, ci, vp, i64], False),
                 ("run_gated_backward", product + [vp, i64, vp, i64, ci, ci, vp, i64, vp, i64, ci],
-                 True)):
+                 True),
+                ("run_linear", product + [vp, ci, vp, i64, vp, i64, ci, vp, i64, ci], True),
+                ("run_linear_backward",
+                 product + [vp, i64, vp, i64, ci, ci, vp, i64, vp, i64, ci, vp], True)):
             bare = name.replace("run_", "")
             call = getattr(L, "tgemm_" + name)
             call.argtypes, call.restype = args + ([vp, i64, vp] if ws else [vp]), ci
@@ -542,12 +550,21 @@ def rope_region(q, pos, inv_freq, heads, stream=None):
 # ---- the feed-forward block --------------------------------------------------
 
 
-def _act(act):
+def _act(act, known=_ACTS):
     if isinstance(act, str):
-        if act not in _ACTS:
-            raise ValueError(f"unknown activation {act!r}: one of {sorted(_ACTS)}")
-        return _ACTS[act]
+        if act not in known:
+            raise ValueError(f"unknown activation {act!r}: one of {sorted(known)}")
+        return known[act]
     return int(act)
+
+
+def _store(dtype, what):
+    """The epilogue that stores ``dtype``."""
+    if dtype == torch.bfloat16:
+        return EPI_STORE_BF16
+    if dtype == torch.float32:
+        return EPI_STORE_F32
+    raise TypeError(f"{what} must be bf16 or fp32")
 
 
 def _same_device(*ts):
@@ -818,6 +835,78 @@ def gated_backward(dh, gu, x, w, act="silu", dw_dtype=torch.bfloat16, stream=Non
                  _ptr(dx), K, _ptr(dw), dw.shape[1],
                  EPI_STORE_BF16 if dw_dtype == torch.bfloat16 else EPI_STORE_F32, sure=True)
     return dx, dw.t() if tb == b"T" else dw
+
+
+# ---- linear layers -----------------------------------------------------------
+
+
+def linear(x, w, bias=None, act="none", residual=None, out_dtype=torch.bfloat16, save=False,
+           stream=None):
+    """residual + act(x @ w + bias), [..., N], for bf16 x [..., K] and w [K, N]
+    (any row/column-major view, usually ``W.t()`` of a weight stored [N, K]).
+
+    ``bias`` bf16 [N]; ``act`` "none", "relu", "silu" or "gelu_tanh";
+    ``residual`` [..., N] of the output's type, ``out_dtype`` (bf16 or fp32).
+    ``save``: also return z = x @ w + bias, [..., N], which
+    ``linear_backward`` reads: True (fp32), or its type, fp32 or bf16 (half
+    the memory, and a rounding more in the gradients).
+    """
+    x2, ta, lda, tb, ldb = _product(x, w, torch.bfloat16, "linear")
+    (M, K), N = x2.shape, w.shape[1]
+    epi = _store(out_dtype, "out_dtype")
+    shape = x.shape[:-1] + (N,)
+    if bias is not None:
+        _vector(bias, N, "bias", torch.bfloat16)
+    r2, ldr, z, zt = None, 0, None, EPI_STORE_F32
+    if residual is not None:
+        if residual.shape != shape:
+            raise ValueError("residual must be [..., N] for x [..., K] and w [K, N]")
+        r2, ldr = _rows(residual, "residual", out_dtype)
+    if save is not False:
+        save = torch.float32 if save is True else save
+        zt = _store(save, "save")
+    a = _act(act, _LINEAR_ACTS)
+    dev = _same_device(x, w, bias, residual)
+    with _on(dev, stream):
+        y = torch.empty(shape, dtype=out_dtype, device=dev)
+        if save is not False:
+            z = torch.empty(shape, dtype=save, device=dev)
+        _call_ws("tgemm_run_linear", dev, ta, tb, M, N, K, _ptr(x2), lda, _ptr(w), ldb, _ptr(bias),
+                 a, _ptr(r2), ldr, _ptr(y), N, epi, _ptr(z), N, zt)
+    return y if z is None else (y, z)
+
+
+def linear_backward(dy, x, w, z=None, act="none", bias=False, dw_dtype=torch.bfloat16,
+                    stream=None):
+    """Gradients (dx [..., K] bf16, dw [K, N], db fp32 [N] or None) of
+    ``linear`` for the gradient ``dy`` bf16 [..., N] of its output; ``x`` and
+    ``w`` its operands, ``z`` as the forward saved it (or cast to bf16; not
+    needed for "none"), ``bias``: whether it had one.  The residual's gradient
+    is ``dy``.  dw has w's layout (for ``W.t()``, dw.t() is the contiguous [N, K]
+    gradient of W) and ``dw_dtype`` (bf16 or fp32)."""
+    x2, ta, lda, tb, ldb = _product(x, w, torch.bfloat16, "linear_backward")
+    (M, K), N = x2.shape, w.shape[1]
+    shape = x.shape[:-1] + (N,)
+    if dy.shape != shape:
+        raise ValueError("dy must be [..., N] for x [..., K] and w [K, N]")
+    epi = _store(dw_dtype, "dw_dtype")
+    a = _act(act, _LINEAR_ACTS)
+    d2, ldd = _rows(dy, "dy", torch.bfloat16)
+    z2, ldz, zt = None, 0, EPI_STORE_F32
+    if a != ACT_NONE:
+        if z is None or z.shape != shape:
+            raise ValueError("linear_backward needs the z that linear saved, [..., N]")
+        zt = _store(z.dtype, "z")
+        z2, ldz = _rows(z, "z", z.dtype)
+    dev = _same_device(dy, x, w, z2)
+    with _on(dev, stream):
+        dx = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
+        dw = torch.empty((N, K) if tb == b"T" else (K, N), dtype=dw_dtype, device=dev)
+        db = torch.empty(N, dtype=torch.float32, device=dev) if bias else None
+        _call_ws("tgemm_run_linear_backward", dev, ta, tb, M, N, K, _ptr(x2), lda, _ptr(w), ldb,
+                 _ptr(d2), ldd, _ptr(z2), ldz, zt, a, _ptr(dx), K, _ptr(dw), dw.shape[1], epi,
+                 _ptr(db), sure=True)
+    return dx, dw.t() if tb == b"T" else dw, db
 
 
 def outer_f32(a, b, stream=None):

@@ -34,6 +34,9 @@ Everything is computed from the plain definitions in fp64 with NumPy:
 * ``ffn``         -- the feed-forward block around the down projection: row
                      quantiser with and without RMS norm, 8-bit products,
                      gated projections and their gradient.
+* ``block``       -- what stands around a block's products: linear layers with
+                     bias, activation and residual, the norms before and after
+                     a block, mixture-of-experts layers, and their gradients.
 
 Parity pins: every function is pinned in ``tests/test_oracle.py`` against
 brute force, closed forms, identities or library routines.  The exact bf16
@@ -46,7 +49,7 @@ from .gemm import op_matrix, gemm
 from .xent import cross_entropy, logsumexp_rows, tile_partials, merge_partials, merge_pair
 from .rope import k1_outer, rope_angles, rope_tables, rope_region
 from .fp8 import E4M3_MAX, e4m3_round, quantize, gemm_fp8
-from . import ffn
+from . import block, ffn
 
 __all__ = [
     "bf16_bits_to_f64",
@@ -66,5 +69,6 @@ __all__ = [
     "e4m3_round",
     "quantize",
     "gemm_fp8",
+    "block",
     "ffn",
 ]
