@@ -604,6 +604,84 @@ TGEMM_API int tgemm_validate_linear_backward(char transA, char transB, int64_t M
                                              const void* dB, int64_t lddb, int epilogue,
                                              const float* dbias);
 
+/*
+ * ---- The norms before and after a block -----------------------------------
+ *
+ * Between two blocks of a residual stream: the output y of one, normed, gated
+ * and scaled, is added to the stream, whose norm is the input of the next.
+ * Per row of K elements:
+ *   p = y * ry * post_weight,  ry = 1 / sqrt(mean(y^2) + eps)    (p = y
+ *                              without a post_weight)
+ *   s = residual + scale * gate * p                              (gate 1
+ *                              without one)
+ *   n = s * rs * weight,       rs = 1 / sqrt(mean(s^2) + eps)
+ * in fp32 (the means in 64 bits); s is rounded for its store only.
+ *
+ *   y, n             bf16 [M, K], row strides ldy, ldn >= K.
+ *   residual, sum    [M, K] of stream_type (TGEMM_EPI_STORE_BF16 or
+ *                    TGEMM_EPI_STORE_F32); sum receives s and may be residual
+ *                    itself (same address and stride), where no backward call
+ *                    follows.
+ *   weight           bf16 [K]; post_weight bf16 [K] or NULL.
+ *   gate             bf16 [gates, K], row stride ldgate >= K, or NULL.  gates
+ *                    divides M; each row of it serves M / gates consecutive
+ *                    rows: 1 for a learned gate per channel, the number of
+ *                    sequences for one per sequence, M for one per token.
+ *   scale, eps       finite; eps >= 0.
+ *   rstd             fp32 [M] of rs, then with a post_weight [M] of ry, for the
+ *                    backward call; or NULL.
+ * K up to 16384, M times the threads of a row below 2^32, else
+ * TGEMM_ERR_UNSUPPORTED.  Rows may start at any element.  No workspace.
+ */
+TGEMM_API int tgemm_block_norm(const void* y, int64_t ldy, const void* residual, int64_t ldr,
+                               int stream_type, const void* post_weight, const void* gate,
+                               int64_t ldgate, int64_t gates, float scale, const void* weight,
+                               float eps, int64_t M, int64_t K, void* sum, int64_t lds, void* n,
+                               int64_t ldn, float* rstd, void* stream);
+
+/* Host-only argument check of tgemm_block_norm (no GPU access). */
+TGEMM_API int tgemm_validate_block_norm(const void* y, int64_t ldy, const void* residual,
+                                        int64_t ldr, int stream_type, const void* post_weight,
+                                        const void* gate, int64_t ldgate, int64_t gates,
+                                        float scale, const void* weight, float eps, int64_t M,
+                                        int64_t K, const void* sum, int64_t lds, const void* n,
+                                        int64_t ldn, const float* rstd);
+
+/*
+ * Its gradient, for the gradients dn (bf16 [M, K]) of n and ds (stream_type
+ * [M, K], or NULL) of s:
+ *   dresidual  stream_type [M, K]; may be ds itself (same address and stride)
+ *   dy         bf16 [M, K]; may be dn itself
+ *   dweight    fp32 [K]
+ *   dpost      fp32 [K], with a post_weight
+ *   dgate      fp32 [gates, K], contiguous, with a gate
+ * The other arguments as in the forward call; rstd as it left them.  s is
+ * computed again from y and residual, in fp32.  The sums over rows are fp32,
+ * in an order that depends on the sizes alone.  K up to 16384, else
+ * TGEMM_ERR_UNSUPPORTED.  Workspace (as for the feed-forward calls): partial
+ * sums of at most 512 groups of rows, at most 16 * 512 * K bytes.
+ */
+TGEMM_API int tgemm_block_norm_backward(const void* dn, int64_t lddn, const void* ds, int64_t ldds,
+                                        const void* y, int64_t ldy, const void* residual,
+                                        int64_t ldr, int stream_type, const void* post_weight,
+                                        const void* gate, int64_t ldgate, int64_t gates,
+                                        float scale, const void* weight, const float* rstd,
+                                        int64_t M, int64_t K, void* dresidual, int64_t lddr,
+                                        void* dy, int64_t lddy, float* dweight, float* dpost,
+                                        float* dgate, void* workspace, int64_t workspace_bytes,
+                                        void* stream);
+/* post: 1 with a post_weight, else 0; gates: 0 without a gate. */
+TGEMM_API int64_t tgemm_block_norm_backward_workspace_bytes(int64_t M, int64_t K, int post,
+                                                            int64_t gates);
+
+/* Host-only argument check of tgemm_block_norm_backward (no GPU access). */
+TGEMM_API int tgemm_validate_block_norm_backward(
+    const void* dn, int64_t lddn, const void* ds, int64_t ldds, const void* y, int64_t ldy,
+    const void* residual, int64_t ldr, int stream_type, const void* post_weight, const void* gate,
+    int64_t ldgate, int64_t gates, float scale, const void* weight, const float* rstd, int64_t M,
+    int64_t K, const void* dresidual, int64_t lddr, const void* dy, int64_t lddy,
+    const float* dweight, const float* dpost, const float* dgate);
+
 /* Human-readable name of a status code (static string, never NULL). */
 TGEMM_API const char* tgemm_status_string(int status);
 

@@ -9,6 +9,8 @@ does, and raises if it has not been built.
 from . import tgemm  # noqa: F401
 from .tgemm import (  # noqa: F401
     TgemmError,
+    block_norm,
+    block_norm_backward,
     cross_entropy,
     gated_backward,
     gated_matmul,

@@ -178,6 +178,65 @@ struct RowQuantParams {
 bool row_quant_fits(const RowQuantParams& p);
 hipError_t launch_row_quant(const RowQuantParams& p, hipStream_t s);
 
+// The norms around a residual sum (block_norm.hip): p = post-norm(y) or y, s =
+// h + scale gate p, n = norm(s).  post, gate and rstd may be null; h and s are
+// bf16 or (f32) fp32.  rstd: [M] of s, then [M] of y.
+struct BlockNormParams {
+  const uint16_t* y;
+  int64_t ldy;
+  const void* h;
+  int64_t ldh;
+  const uint16_t* post;
+  const uint16_t* gate;  // [M / rows_per_gate][ldgate]
+  int64_t ldgate;
+  int rows_per_gate;
+  float scale;
+  const uint16_t* weight;
+  float eps;
+  void* s;
+  int64_t lds;
+  uint16_t* n;
+  int64_t ldn;
+  float* rstd;
+  int M;
+  int64_t K;
+};
+bool block_norm_fits(int64_t M, int64_t K);
+hipError_t launch_block_norm(const BlockNormParams& p, bool f32, hipStream_t s);
+
+// Its gradient; ds may be null.  part: block_norm_bwd_bytes of partial sums.
+struct BlockNormGradParams {
+  const uint16_t* dn;
+  int64_t lddn;
+  const void* ds;
+  int64_t ldds;
+  const uint16_t* y;
+  int64_t ldy;
+  const void* h;
+  int64_t ldh;
+  const uint16_t* post;
+  const uint16_t* gate;
+  int64_t ldgate;
+  int rows_per_gate;
+  float scale;
+  const uint16_t* weight;
+  const float* rstd;
+  void* dh;
+  int64_t lddh;
+  uint16_t* dy;
+  int64_t lddy;
+  float* dweight;  // [K]
+  float* dpost;    // [K]
+  float* dgate;    // [M / rows_per_gate][K]
+  int M;
+  int64_t K;
+  float* part;
+  int per_group;   // set by the launcher
+};
+bool block_norm_bwd_fits(int64_t M, int64_t K, int64_t gates);
+size_t block_norm_bwd_bytes(int64_t M, int64_t K, bool post, bool gate);
+hipError_t launch_block_norm_bwd(BlockNormGradParams p, bool f32, hipStream_t s);
+
 // ----------------------------------------------------------------------
 // Activations.  Both are g * sigmoid(s(g)): silu with s = g; the tanh form
 // of gelu, g/2 (1 + tanh z) with z = sqrt(2/pi)(g + 0.044715 g^3), with

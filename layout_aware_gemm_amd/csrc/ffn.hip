@@ -724,3 +724,71 @@ extern "C" int tgemm_quantize_i8(const void* x, int64_t ldx, int64_t M, int64_t 
     fprintf(stderr, "tgemm: quantize i8 M=%lld K=%lld\n", (long long)M, (long long)K);
   return status_of(launch_row_quant(p, reinterpret_cast<hipStream_t>(stream)));
 }
+
+extern "C" int tgemm_block_norm(const void* y, int64_t ldy, const void* residual, int64_t ldr,
+                                int stream_type, const void* post_weight, const void* gate,
+                                int64_t ldgate, int64_t gates, float scale, const void* weight,
+                                float eps, int64_t M, int64_t K, void* sum, int64_t lds, void* n,
+                                int64_t ldn, float* rstd, void* stream) {
+  const int st = tgemm_validate_block_norm(y, ldy, residual, ldr, stream_type, post_weight, gate,
+                                           ldgate, gates, scale, weight, eps, M, K, sum, lds, n, ldn,
+                                           rstd);
+  if (st != TGEMM_OK) return st;
+  if (!block_norm_fits(M, K)) return TGEMM_ERR_UNSUPPORTED;
+  if (verbose())
+    fprintf(stderr, "tgemm: block norm M=%lld K=%lld post=%d gates=%lld\n", (long long)M,
+            (long long)K, post_weight != nullptr, (long long)(gate != nullptr ? gates : 0));
+  const BlockNormParams p = {static_cast<const uint16_t*>(y), ldy, residual, ldr,
+                             static_cast<const uint16_t*>(post_weight),
+                             static_cast<const uint16_t*>(gate), ldgate,
+                             gate != nullptr ? (int)(M / gates) : 1, scale,
+                             static_cast<const uint16_t*>(weight), eps, sum, lds,
+                             static_cast<uint16_t*>(n), ldn, rstd, (int)M, K};
+  return status_of(launch_block_norm(p, stream_type == TGEMM_EPI_STORE_F32,
+                                     reinterpret_cast<hipStream_t>(stream)));
+}
+
+extern "C" int64_t tgemm_block_norm_backward_workspace_bytes(int64_t M, int64_t K, int post,
+                                                             int64_t gates) {
+  if (M < 1 || K < 1 || gates < 0 || (gates > 0 && M % gates != 0)) return TGEMM_ERR_INVALID_ARG;
+  if (M >= int64_t(1) << 31 || !block_norm_bwd_fits(M, K, gates)) return TGEMM_ERR_UNSUPPORTED;
+  return (int64_t)block_norm_bwd_bytes(M, K, post != 0, gates > 0);
+}
+
+extern "C" int tgemm_block_norm_backward(const void* dn, int64_t lddn, const void* ds, int64_t ldds,
+                                         const void* y, int64_t ldy, const void* residual,
+                                         int64_t ldr, int stream_type, const void* post_weight,
+                                         const void* gate, int64_t ldgate, int64_t gates,
+                                         float scale, const void* weight, const float* rstd,
+                                         int64_t M, int64_t K, void* dresidual, int64_t lddr,
+                                         void* dy, int64_t lddy, float* dweight, float* dpost,
+                                         float* dgate, void* workspace, int64_t workspace_bytes,
+                                         void* stream) {
+  const int st = tgemm_validate_block_norm_backward(
+      dn, lddn, ds, ldds, y, ldy, residual, ldr, stream_type, post_weight, gate, ldgate, gates,
+      scale, weight, rstd, M, K, dresidual, lddr, dy, lddy, dweight, dpost, dgate);
+  if (st != TGEMM_OK) return st;
+  if (!block_norm_bwd_fits(M, K, gate != nullptr ? gates : 0)) return TGEMM_ERR_UNSUPPORTED;
+  return no_throw([&] {
+    const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    Workspace w;
+    const int sw = take_workspace({workspace, workspace_bytes, nullptr}, s,
+                                  block_norm_bwd_bytes(M, K, post_weight != nullptr, gate != nullptr),
+                                  &w);
+    if (sw != TGEMM_OK) return sw;
+    if (verbose())
+      fprintf(stderr, "tgemm: block norm backward M=%lld K=%lld post=%d gates=%lld\n", (long long)M,
+              (long long)K, post_weight != nullptr, (long long)(gate != nullptr ? gates : 0));
+    const BlockNormGradParams p = {static_cast<const uint16_t*>(dn), lddn, ds, ldds,
+                                   static_cast<const uint16_t*>(y), ldy, residual, ldr,
+                                   static_cast<const uint16_t*>(post_weight),
+                                   static_cast<const uint16_t*>(gate), ldgate,
+                                   gate != nullptr ? (int)(M / gates) : 1, scale,
+                                   static_cast<const uint16_t*>(weight), rstd, dresidual, lddr,
+                                   static_cast<uint16_t*>(dy), lddy, dweight, dpost, dgate, (int)M,
+                                   K, static_cast<float*>(w.ptr), 0};
+    const hipError_t e = launch_block_norm_bwd(p, stream_type == TGEMM_EPI_STORE_F32, s);
+    release_workspace(w);
+    return status_of(e);
+  });
+}

@@ -13,41 +13,11 @@
 // One workgroup per row; the row stays in registers between the reduction
 // and the codes, so each element moves once: 7 bytes per element with a
 // residual, 3 without.  Bound: HBM bandwidth.
-#include "bf16_cvt.h"
 #include "ffn.h"
+#include "row_vec.h"
 
 namespace tgemm {
 namespace {
-
-__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
-// 8 elements from column c of a row of n (zeros past the end).
-__device__ __forceinline__ u16x8_any load8(const uint16_t* p, int64_t c, int64_t n) {
-  u16x8_any v;
-  if (c + 8 <= n) {
-    v = *reinterpret_cast<const u16x8_any*>(p + c);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t w = 0;
-      if (c + 2 * i < n) w = p[c + 2 * i];
-      if (c + 2 * i + 1 < n) w |= (uint32_t)p[c + 2 * i + 1] << 16;
-      v.w[i] = w;
-    }
-  }
-  return v;
-}
-
-__device__ __forceinline__ void store8(uint16_t* p, int64_t c, int64_t n, const u16x8_any& v) {
-  if (c + 8 <= n) {
-    *reinterpret_cast<u16x8_any*>(p + c) = v;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < n) p[c + i] = (uint16_t)(v.w[i >> 1] >> ((i & 1) * 16));
-  }
-}
 
 // The row's constants for its codes.
 struct RowCode {

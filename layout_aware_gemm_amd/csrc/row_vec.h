@@ -1,0 +1,119 @@
+// Rows of bf16 or fp32 in vectors of 8, at any element alignment, and sums
+// over a workgroup: shared by the kernels that keep a row in registers.
+#pragma once
+
+#include "ffn.h"
+
+namespace tgemm {
+
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// 8 elements from column c of a row of n (zeros past the end).
+__device__ __forceinline__ u16x8_any load8(const uint16_t* p, int64_t c, int64_t n) {
+  u16x8_any v;
+  if (c + 8 <= n) {
+    v = *reinterpret_cast<const u16x8_any*>(p + c);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w = 0;
+      if (c + 2 * i < n) w = p[c + 2 * i];
+      if (c + 2 * i + 1 < n) w |= (uint32_t)p[c + 2 * i + 1] << 16;
+      v.w[i] = w;
+    }
+  }
+  return v;
+}
+
+__device__ __forceinline__ void store8(uint16_t* p, int64_t c, int64_t n, const u16x8_any& v) {
+  if (c + 8 <= n) {
+    *reinterpret_cast<u16x8_any*>(p + c) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < n) p[c + i] = (uint16_t)(v.w[i >> 1] >> ((i & 1) * 16));
+  }
+}
+
+struct f32x8_any {
+  x4_any<float> a, b;
+};
+
+__device__ __forceinline__ f32x8_any load8(const float* p, int64_t c, int64_t n) {
+  f32x8_any v;
+  if (c + 8 <= n) {
+    v.a = *reinterpret_cast<const x4_any<float>*>(p + c);
+    v.b = *reinterpret_cast<const x4_any<float>*>(p + c + 4);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v.a.v[i] = c + i < n ? p[c + i] : 0.f;
+      v.b.v[i] = c + 4 + i < n ? p[c + 4 + i] : 0.f;
+    }
+  }
+  return v;
+}
+
+// The value i (a constant after unrolling) of such a vector.
+__device__ __forceinline__ float value(const u16x8_any& v, int i) {
+  return (i & 1) ? hi_f(v.w[i >> 1]) : lo_f(v.w[i >> 1]);
+}
+__device__ __forceinline__ float value(const f32x8_any& v, int i) {
+  return i < 4 ? v.a.v[i & 3] : v.b.v[i & 3];
+}
+
+// 8 fp32 values to a row of either type.
+__device__ __forceinline__ void put8(uint16_t* p, int64_t c, int64_t n, const float (&f)[8]) {
+  u16x8_any v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v.w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+  store8(p, c, n, v);
+}
+__device__ __forceinline__ void put8(float* p, int64_t c, int64_t n, const float (&f)[8]) {
+  if (c + 8 <= n) {
+    *reinterpret_cast<x4_any<float>*>(p + c) = x4_any<float>{{f[0], f[1], f[2], f[3]}};
+    *reinterpret_cast<x4_any<float>*>(p + c + 4) = x4_any<float>{{f[4], f[5], f[6], f[7]}};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < n) p[c + i] = f[i];
+  }
+}
+
+// The type a row of T is held in.
+template <class T>
+struct Vec8;
+template <>
+struct Vec8<uint16_t> {
+  typedef u16x8_any type;
+};
+template <>
+struct Vec8<float> {
+  typedef f32x8_any type;
+};
+
+// Sums of N values each over the workgroup, in wave order (the same in every
+// thread).  `buf`: LDS for the waves' sums, not to be in use by another wave:
+// callers in a loop alternate between two.
+template <int N, class T>
+__device__ __forceinline__ void group_sum(T (&v)[N], T (*buf)[N]) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], o, 64);
+  const int waves = (int)blockDim.x >> 6;
+  if (waves == 1) return;
+  if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) buf[threadIdx.x >> 6][i] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = buf[0][i];
+  for (int w = 1; w < waves; ++w)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += buf[w][i];
+}
+
+}  // namespace tgemm

@@ -242,6 +242,57 @@ extern "C" int tgemm_validate_quantize_i8(const void* x, int64_t ldx, int64_t M,
   return st == TGEMM_OK ? check_rows(q, M, K, ldq) : st;
 }
 
+namespace {
+
+// what both directions of the block norm take
+int check_block_norm(const void* y, int64_t ldy, const void* residual, int64_t ldr, int stream_type,
+                     const void* gate, int64_t ldgate, int64_t gates, float scale,
+                     const void* weight, int64_t M, int64_t K) {
+  if (!type_ok(stream_type) || weight == nullptr || M < 1 || K < 1) return TGEMM_ERR_INVALID_ARG;
+  if (!(scale - scale == 0.f)) return TGEMM_ERR_INVALID_ARG;  // (infinite or NaN)
+  if (M > kMaxDim || K > kMaxDim) return TGEMM_ERR_UNSUPPORTED;
+  int st = check_rows(y, M, K, ldy);
+  if (st == TGEMM_OK) st = check_rows(residual, M, K, ldr);
+  if (st == TGEMM_OK && gate != nullptr)
+    st = gates < 1 || M % gates != 0 ? TGEMM_ERR_INVALID_ARG : check_rows(gate, gates, K, ldgate);
+  return st;
+}
+
+}  // namespace
+
+extern "C" int tgemm_validate_block_norm(const void* y, int64_t ldy, const void* residual,
+                                         int64_t ldr, int stream_type, const void* post_weight,
+                                         const void* gate, int64_t ldgate, int64_t gates,
+                                         float scale, const void* weight, float eps, int64_t M,
+                                         int64_t K, const void* sum, int64_t lds, const void* n,
+                                         int64_t ldn, const float* rstd) {
+  (void)post_weight, (void)rstd;
+  if (!(eps >= 0.f) || eps > 3.402823466e38f) return TGEMM_ERR_INVALID_ARG;
+  int st = check_block_norm(y, ldy, residual, ldr, stream_type, gate, ldgate, gates, scale, weight,
+                            M, K);
+  if (st == TGEMM_OK) st = check_rows(sum, M, K, lds);
+  if (st == TGEMM_OK) st = check_rows(n, M, K, ldn);
+  return st;
+}
+
+extern "C" int tgemm_validate_block_norm_backward(
+    const void* dn, int64_t lddn, const void* ds, int64_t ldds, const void* y, int64_t ldy,
+    const void* residual, int64_t ldr, int stream_type, const void* post_weight, const void* gate,
+    int64_t ldgate, int64_t gates, float scale, const void* weight, const float* rstd, int64_t M,
+    int64_t K, const void* dresidual, int64_t lddr, const void* dy, int64_t lddy,
+    const float* dweight, const float* dpost, const float* dgate) {
+  if (rstd == nullptr || dweight == nullptr) return TGEMM_ERR_INVALID_ARG;
+  if ((post_weight != nullptr && dpost == nullptr) || (gate != nullptr && dgate == nullptr))
+    return TGEMM_ERR_INVALID_ARG;
+  int st = check_block_norm(y, ldy, residual, ldr, stream_type, gate, ldgate, gates, scale, weight,
+                            M, K);
+  if (st == TGEMM_OK) st = check_rows(dn, M, K, lddn);
+  if (st == TGEMM_OK && ds != nullptr) st = check_rows(ds, M, K, ldds);
+  if (st == TGEMM_OK) st = check_rows(dresidual, M, K, lddr);
+  if (st == TGEMM_OK) st = check_rows(dy, M, K, lddy);
+  return st;
+}
+
 extern "C" const char* tgemm_status_string(int status) {
   switch (status) {
     case TGEMM_OK: return "TGEMM_OK";

@@ -44,7 +44,9 @@ EXPORTS = ("tgemm_run", "tgemm_run_fp8", "tgemm_validate", "tgemm_validate_fp8",
            "tgemm_gated_workspace_bytes", "tgemm_gated_i8_workspace_bytes",
            "tgemm_gated_backward_workspace_bytes", "tgemm_run_linear", "tgemm_validate_linear",
            "tgemm_linear_workspace_bytes", "tgemm_run_linear_backward",
-           "tgemm_validate_linear_backward", "tgemm_linear_backward_workspace_bytes")
+           "tgemm_validate_linear_backward", "tgemm_linear_backward_workspace_bytes",
+           "tgemm_block_norm", "tgemm_validate_block_norm", "tgemm_block_norm_backward",
+           "tgemm_validate_block_norm_backward", "tgemm_block_norm_backward_workspace_bytes")
 
 ACT_SILU = 0
 ACT_GELU_TANH = 1
@@ -121,6 +123,7 @@ def lib():
         # without workspace and stream
         ch, ci, cf = ctypes.c_char, ctypes.c_int, ctypes.c_float
         product = [ch, ch, i64, i64, i64, vp, i64, vp, i64]
+        norm = [ci, vp, vp, i64, i64, cf, vp]  # stream_type .. weight
         for name, args, ws in (
                 ("rms_norm_i8", [vp, i64, vp, i64, vp, cf, i64, i64, vp, i64, vp, i64, vp], False),
                 ("quantize_i8", [vp, i64, i64, i64, vp, i64, vp], False),
@@ -132,15 +135,20 @@ def lib():
                  True),
                 ("run_linear", product + [vp, ci, vp, i64, vp, i64, ci, vp, i64, ci], True),
                 ("run_linear_backward",
-                 product + [vp, i64, vp, i64, ci, ci, vp, i64, vp, i64, ci, vp], True)):
+                 product + [vp, i64, vp, i64, ci, ci, vp, i64, vp, i64, ci, vp], True),
+                ("block_norm", [vp, i64] * 2 + norm + [cf, i64, i64, vp, i64, vp, i64, vp], False),
+                ("block_norm_backward",
+                 [vp, i64] * 4 + norm + [vp, i64, i64, vp, i64, vp, i64, vp, vp, vp], True)):
             bare = name.replace("run_", "")
             call = getattr(L, "tgemm_" + name)
             call.argtypes, call.restype = args + ([vp, i64, vp] if ws else [vp]), ci
             check = getattr(L, "tgemm_validate_" + bare)
             check.argtypes, check.restype = args, ci
-            if ws:
+            if ws and args[:9] == product:
                 need = getattr(L, f"tgemm_{bare}_workspace_bytes")
                 need.argtypes, need.restype = product, i64
+        need = L.tgemm_block_norm_backward_workspace_bytes
+        need.argtypes, need.restype = [i64, i64, ci, i64], i64
         _lib = L
     return _lib
 
@@ -907,6 +915,97 @@ def linear_backward(dy, x, w, z=None, act="none", bias=False, dw_dtype=torch.bfl
                  _ptr(d2), ldd, _ptr(z2), ldz, zt, a, _ptr(dx), K, _ptr(dw), dw.shape[1], epi,
                  _ptr(db), sure=True)
     return dx, dw.t() if tb == b"T" else dw, db
+
+
+# ---- the norms before and after a block --------------------------------------
+
+
+def _gate(gate, M, K):
+    """(gate rows, row stride) of a gate [K] or [G, K], G a divisor of M."""
+    if gate is None:
+        return 0, 0
+    g2 = gate.view(1, -1) if gate.dim() == 1 else gate
+    if g2.dim() != 2 or g2.shape[1] != K or g2.shape[0] < 1 or M % g2.shape[0]:
+        raise ValueError("gate must be [K] or [G, K], G a divisor of the rows")
+    return g2.shape[0], _rows(g2, "gate", torch.bfloat16)[1]
+
+
+def _norm_operands(y, residual, weight, post_weight, gate):
+    y2, ldy = _rows(y, "y", torch.bfloat16)
+    M, K = y2.shape
+    st = _store(residual.dtype, "residual")
+    if residual.shape != y.shape:
+        raise ValueError("y and residual differ in shape")
+    r2, ldr = _rows(residual, "residual", residual.dtype)
+    _vector(weight, K, "weight", torch.bfloat16)
+    if post_weight is not None:
+        _vector(post_weight, K, "post_weight", torch.bfloat16)
+    G, ldg = _gate(gate, M, K)
+    return y2, ldy, r2, ldr, st, G, ldg, M, K
+
+
+def block_norm(y, residual, weight, post_weight=None, gate=None, scale=1.0, eps=1e-6, save=False,
+               out_residual=None, stream=None):
+    """The norms between two blocks: with p = RMS norm of ``y`` times
+    ``post_weight`` (y itself without one), returns (n, s):
+
+      s = residual + scale * gate * p      in residual's type
+      n = RMS norm of s times ``weight``   bf16
+
+    ``y`` bf16 [..., K], ``residual`` bf16 or fp32 [..., K], any row strides;
+    weights bf16 [K]; ``gate`` bf16 [K], or [G, K] with one row for each G-th of
+    the rows (a gate per sequence, or per token).  s is written to
+    ``out_residual`` if given (which may be ``residual``, where no backward call
+    follows).  ``save``: also return rstd, fp32 [1 or 2, rows], for
+    ``block_norm_backward``.
+    """
+    y2, ldy, r2, ldr, st, G, ldg, M, K = _norm_operands(y, residual, weight, post_weight, gate)
+    dev = _same_device(y, residual, weight, post_weight, gate, out_residual)
+    with _on(dev, stream):
+        if out_residual is None:
+            out_residual = torch.empty(y.shape, dtype=residual.dtype, device=dev)
+        if out_residual.shape != y.shape:
+            raise ValueError("y and out_residual differ in shape")
+        s2, lds = _rows(out_residual, "out_residual", residual.dtype)
+        n = torch.empty(y.shape, dtype=torch.bfloat16, device=dev)
+        rstd = (torch.empty(1 if post_weight is None else 2, M, dtype=torch.float32, device=dev)
+                if save else None)
+        _call("tgemm_block_norm", dev, _ptr(y2), ldy, _ptr(r2), ldr, st, _ptr(post_weight),
+              _ptr(gate), ldg, G, float(scale), _ptr(weight), float(eps), M, K, _ptr(s2), lds,
+              _ptr(n), K, _ptr(rstd))
+    return (n, out_residual, rstd) if save else (n, out_residual)
+
+
+def block_norm_backward(dn, y, residual, rstd, weight, post_weight=None, gate=None, scale=1.0,
+                        ds=None, stream=None):
+    """Gradients (dresidual, dy, dweight, dpost_weight, dgate) of ``block_norm``
+    for the gradients ``dn`` bf16 [..., K] of n and ``ds`` (of residual's type,
+    or None) of s; the other arguments as in the forward call, ``rstd`` as it
+    saved it.  dresidual has residual's type, dy is bf16, the others are fp32,
+    in their operands' shapes (None without them)."""
+    y2, ldy, r2, ldr, st, G, ldg, M, K = _norm_operands(y, residual, weight, post_weight, gate)
+    if dn.shape != y.shape or (ds is not None and ds.shape != y.shape):
+        raise ValueError("dn and ds must have y's shape")
+    d2, ldd = _rows(dn, "dn", torch.bfloat16)
+    s2, lds = (None, 0) if ds is None else _rows(ds, "ds", residual.dtype)
+    post = 0 if post_weight is None else 1
+    if rstd.dtype != torch.float32 or rstd.shape != (1 + post, M) or not rstd.is_contiguous():
+        raise ValueError("rstd must be the contiguous fp32 tensor that block_norm saved")
+    dev = _same_device(dn, y, residual, rstd, weight, post_weight, gate, ds)
+    with _on(dev, stream):
+        f32 = {"dtype": torch.float32, "device": dev}
+        dh = torch.empty(y.shape, dtype=residual.dtype, device=dev)
+        dy = torch.empty(y.shape, dtype=torch.bfloat16, device=dev)
+        dw = torch.empty(K, **f32)
+        dp = torch.empty(K, **f32) if post else None
+        dg = torch.empty(gate.shape, **f32) if G else None
+        need = lib().tgemm_block_norm_backward_workspace_bytes(M, K, post, G)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
+        _call("tgemm_block_norm_backward", dev, _ptr(d2), ldd, _ptr(s2), lds, _ptr(y2), ldy,
+              _ptr(r2), ldr, st, _ptr(post_weight), _ptr(gate), ldg, G, float(scale), _ptr(weight),
+              _ptr(rstd), M, K, _ptr(dh), K, _ptr(dy), K, _ptr(dw), _ptr(dp), _ptr(dg), _ptr(ws),
+              max(need, 0))
+    return dh, dy, dw, dp, dg
 
 
 def outer_f32(a, b, stream=None):
