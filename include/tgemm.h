@@ -682,6 +682,54 @@ TGEMM_API int tgemm_validate_block_norm_backward(
     int64_t K, const void* dresidual, int64_t lddr, const void* dy, int64_t lddy,
     const float* dweight, const float* dpost, const float* dgate);
 
+/*
+ * ---- Mixture-of-experts layers for few tokens -----------------------------
+ *
+ *   Y[m] = sum_j weights[m, j] * H[m, j] . W2[ids[m, j]]^T          bf16 [M, K]
+ *   H[m, j] = bf16(act(g) * u),  [g | u] = X[m] . W1[ids[m, j]]^T
+ * with fp32 sums: `top` of E gated experts for each token.  With a router the
+ * call chooses them: the top largest of the logits X[m] . router^T (sums in 64
+ * bits, so that the choice depends on no order of summation; the lowest index
+ * first among equals; NaN counts as largest), with the weights
+ *   weights[m, j] = scale * exp(l_j - l_0) / sum exp(l_i - l_0),
+ * the sum over the chosen (renormalize != 0) or over all experts; ids and
+ * weights are then outputs.  Without a router (NULL) they are inputs: an id
+ * outside 0 .. E-1 adds nothing (its expert lives elsewhere), one that a token
+ * lists twice counts twice, and top may pass E.
+ *
+ *   X, Y        bf16 [M, K], row strides ldx, ldy >= K.
+ *   router      [E, K] bf16 or fp32 (router_type, an epilogue's name as
+ *               elsewhere), row stride ldr >= K.
+ *   ids         int32 [M, top], weights fp32 [M, top], contiguous.
+ *   W1          bf16 [E, 2F, K]: per expert F gate rows, then F up rows, row
+ *               stride ldw1 >= K, experts sw1 elements apart.
+ *   W2          bf16 [E, K, F], row stride ldw2 >= F, experts sw2 apart.
+ *   activation  TGEMM_ACT_SILU or TGEMM_ACT_GELU_TANH.
+ * E up to 1024, top up to 16, rows of X, W1 and W2 less than 2^22 elements
+ * apart, else TGEMM_ERR_UNSUPPORTED.  The layer is made for few tokens: 64 rows
+ * run at a time, and each pass reads the experts it hits.  Weights on 16-byte
+ * boundaries (bases and strides; F a multiple of 8) are read at full rate,
+ * others in place too, more slowly.  Workspace as for the feed-forward calls;
+ * nearly every call needs some.
+ */
+TGEMM_API int tgemm_run_moe(int64_t M, int64_t K, int64_t F, int64_t E, int64_t top, const void* X,
+                            int64_t ldx, const void* router, int64_t ldr, int router_type,
+                            int renormalize, float scale, int32_t* ids, float* weights,
+                            const void* W1, int64_t ldw1, int64_t sw1, const void* W2,
+                            int64_t ldw2, int64_t sw2, int activation, void* Y, int64_t ldy,
+                            void* workspace, int64_t workspace_bytes, void* stream);
+/* routed: 1 with a router, else 0. */
+TGEMM_API int64_t tgemm_moe_workspace_bytes(int64_t M, int64_t K, int64_t F, int64_t E,
+                                            int64_t top, int routed);
+
+/* Host-only argument check of tgemm_run_moe (no GPU access). */
+TGEMM_API int tgemm_validate_moe(int64_t M, int64_t K, int64_t F, int64_t E, int64_t top,
+                                 const void* X, int64_t ldx, const void* router, int64_t ldr,
+                                 int router_type, int renormalize, float scale,
+                                 const int32_t* ids, const float* weights, const void* W1,
+                                 int64_t ldw1, int64_t sw1, const void* W2, int64_t ldw2,
+                                 int64_t sw2, int activation, const void* Y, int64_t ldy);
+
 /* Human-readable name of a status code (static string, never NULL). */
 TGEMM_API const char* tgemm_status_string(int status);
 

@@ -20,6 +20,8 @@ from .tgemm import (  # noqa: F401
     linear_backward,
     matmul,
     matmul_i8,
+    moe,
+    moe_experts,
     outer_f32,
     quantize_i8,
     rms_norm_i8,

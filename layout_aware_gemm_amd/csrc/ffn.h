@@ -237,6 +237,41 @@ bool block_norm_bwd_fits(int64_t M, int64_t K, int64_t gates);
 size_t block_norm_bwd_bytes(int64_t M, int64_t K, bool post, bool gate);
 hipError_t launch_block_norm_bwd(BlockNormGradParams p, bool f32, hipStream_t s);
 
+// A mixture-of-experts layer for up to kMoeTokens tokens (moe.hip).
+constexpr int kMoeTokens = 64, kMoeTop = 16, kMoeExperts = 1024;
+struct MoeParams {
+  int M;              // tokens
+  int64_t K;
+  int F, E, top;
+  const uint16_t* x;  // [M][ldx]
+  int64_t ldx;
+  const void* router; // [E][ldr], bf16 or fp32, or null: ids and weights are given
+  int64_t ldr;
+  int router_f32, renormalize;
+  float scale;
+  int32_t* ids;       // [M][top]; outside 0 .. E - 1: no expert
+  float* weights;     // [M][top]
+  const uint16_t* w1; // [E][2F][ldw1], experts sw1 apart
+  int64_t ldw1, sw1;
+  const uint16_t* w2; // [E][K][ldw2], experts sw2 apart
+  int64_t ldw2, sw2;
+  int act;
+  uint16_t* y;        // [M][ldy]
+  int64_t ldy;
+  // workspace: 64-bit logits [M][E], h [M * top][ldh] (ldh a multiple of 64),
+  // the shares' sums [shares][M][K]
+  double* logits;
+  uint16_t* h;
+  int64_t ldh;
+  float* part;
+  int run;            // set by the launcher
+};
+struct MoeSpace {
+  size_t logits, h, part;  // bytes
+};
+MoeSpace moe_space(const MoeParams& p);
+hipError_t launch_moe(const MoeParams& p, hipStream_t s);
+
 // ----------------------------------------------------------------------
 // Activations.  Both are g * sigmoid(s(g)): silu with s = g; the tanh form
 // of gelu, g/2 (1 + tanh z) with z = sqrt(2/pi)(g + 0.044715 g^3), with

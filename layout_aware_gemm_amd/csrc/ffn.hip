@@ -441,6 +441,36 @@ int run_linear_backward(char ta, char tb, int64_t M, int64_t N, int64_t K, const
       space, s);
 }
 
+// A mixture-of-experts layer, kMoeTokens rows of X at a time; p holds all but
+// the rows' part and the workspace.
+int run_moe(MoeParams p, int64_t M, const CallSpace& space, hipStream_t s) {
+  p.ldh = round_up(p.F, 64);
+  p.M = (int)(M < kMoeTokens ? M : kMoeTokens);
+  const MoeSpace need = moe_space(p);
+  const size_t bytesL = round256(need.logits), bytesH = round256(need.h);
+  Workspace w;
+  const int st = take_workspace(space, s, bytesL + bytesH + need.part, &w);
+  if (st != TGEMM_OK) return st;
+  if (verbose())
+    fprintf(stderr, "tgemm: moe M=%lld K=%lld F=%d E=%d top=%d\n", (long long)M, (long long)p.K, p.F,
+            p.E, p.top);
+  char* const ws = static_cast<char*>(w.ptr);
+  p.logits = reinterpret_cast<double*>(ws);
+  p.h = reinterpret_cast<uint16_t*>(ws + bytesL);
+  p.part = reinterpret_cast<float*>(ws + bytesL + bytesH);
+  hipError_t e = hipSuccess;
+  for (int64_t m = 0; m < M && e == hipSuccess; m += kMoeTokens) {
+    p.M = (int)(M - m < kMoeTokens ? M - m : kMoeTokens);
+    e = launch_moe(p, s);
+    p.x += kMoeTokens * p.ldx;
+    p.y += kMoeTokens * p.ldy;
+    p.ids += kMoeTokens * p.top;
+    p.weights += kMoeTokens * p.top;
+  }
+  release_workspace(w);
+  return status_of(e);
+}
+
 // The workspace list allocates host memory; no exception leaves the library.
 template <class Fn>
 int no_throw(Fn&& fn) {
@@ -791,4 +821,60 @@ extern "C" int tgemm_block_norm_backward(const void* dn, int64_t lddn, const voi
     release_workspace(w);
     return status_of(e);
   });
+}
+
+extern "C" int tgemm_run_moe(int64_t M, int64_t K, int64_t F, int64_t E, int64_t top, const void* X,
+                             int64_t ldx, const void* router, int64_t ldr, int router_type,
+                             int renormalize, float scale, int32_t* ids, float* weights,
+                             const void* W1, int64_t ldw1, int64_t sw1, const void* W2,
+                             int64_t ldw2, int64_t sw2, int activation, void* Y, int64_t ldy,
+                             void* workspace, int64_t workspace_bytes, void* stream) {
+  const int st = tgemm_validate_moe(M, K, F, E, top, X, ldx, router, ldr, router_type, renormalize,
+                                    scale, ids, weights, W1, ldw1, sw1, W2, ldw2, sw2, activation, Y,
+                                    ldy);
+  if (st != TGEMM_OK) return st;
+  MoeParams p = {};
+  p.K = K;
+  p.F = (int)F;
+  p.E = (int)E;
+  p.top = (int)top;
+  p.x = static_cast<const uint16_t*>(X);
+  p.ldx = M == 1 ? K : ldx;  // (the stride of a single row is never used)
+  p.router = router;
+  p.ldr = ldr;
+  p.router_f32 = router_type == TGEMM_EPI_STORE_F32;
+  p.renormalize = renormalize != 0;
+  p.scale = scale;
+  p.ids = ids;
+  p.weights = weights;
+  p.w1 = static_cast<const uint16_t*>(W1);
+  p.ldw1 = ldw1;
+  p.sw1 = E == 1 ? 0 : sw1;
+  p.w2 = static_cast<const uint16_t*>(W2);
+  p.ldw2 = K == 1 ? F : ldw2;
+  p.sw2 = E == 1 ? 0 : sw2;
+  p.act = activation;
+  p.y = static_cast<uint16_t*>(Y);
+  p.ldy = ldy;
+  return no_throw([&] {
+    return run_moe(p, M, {workspace, workspace_bytes, nullptr},
+                   reinterpret_cast<hipStream_t>(stream));
+  });
+}
+
+extern "C" int64_t tgemm_moe_workspace_bytes(int64_t M, int64_t K, int64_t F, int64_t E,
+                                             int64_t top, int routed) {
+  const int st = tgemm_validate_moe(M, K, F, E, top, g_any, K, routed ? g_any : nullptr, K,
+                                    TGEMM_EPI_STORE_BF16, 1, 1.f, reinterpret_cast<int32_t*>(g_any),
+                                    g_any, g_any, K, 2 * F * K, g_any, F, K * F, TGEMM_ACT_SILU,
+                                    g_any, K);
+  if (st != TGEMM_OK) return st;
+  MoeParams p = {};
+  p.K = K;
+  p.F = (int)F;
+  p.E = (int)E;
+  p.top = (int)top;
+  p.router = routed ? g_any : nullptr;
+  int64_t need = 0;
+  return queried(no_throw([&] { return run_moe(p, M, {nullptr, 0, &need}, nullptr); }), need);
 }

@@ -293,6 +293,45 @@ extern "C" int tgemm_validate_block_norm_backward(
   return st;
 }
 
+namespace {
+
+// [E] matrices of rows x cols, row stride ld, sx elements apart
+int check_experts(const void* p, int64_t E, int64_t rows, int64_t cols, int64_t ld, int64_t sx) {
+  const int st = check_rows(p, rows, cols, ld);
+  if (st != TGEMM_OK || E == 1) return st;
+  if (sx < (rows - 1) * ld + cols) return TGEMM_ERR_INVALID_ARG;
+  return sx > INT64_MAX / 4 / E ? TGEMM_ERR_UNSUPPORTED : TGEMM_OK;
+}
+
+}  // namespace
+
+extern "C" int tgemm_validate_moe(int64_t M, int64_t K, int64_t F, int64_t E, int64_t top,
+                                  const void* X, int64_t ldx, const void* router, int64_t ldr,
+                                  int router_type, int renormalize, float scale,
+                                  const int32_t* ids, const float* weights, const void* W1,
+                                  int64_t ldw1, int64_t sw1, const void* W2, int64_t ldw2,
+                                  int64_t sw2, int activation, const void* Y, int64_t ldy) {
+  (void)renormalize;
+  if (M < 1 || K < 1 || F < 1 || E < 1 || top < 1) return TGEMM_ERR_INVALID_ARG;
+  if (!act_ok(activation) || ids == nullptr || weights == nullptr) return TGEMM_ERR_INVALID_ARG;
+  if (router != nullptr && (top > E || !type_ok(router_type) || ldr < K || !(scale - scale == 0.f)))
+    return TGEMM_ERR_INVALID_ARG;
+  // rows of the weights and of X at most 2^23 - 1 bytes apart, so that the
+  // offsets of 64 rows fit 31 bits
+  constexpr int64_t kMaxStride = (int64_t(1) << 22) - 1;
+  if (M > kMaxRows || E > 1024 || top > 16 || K > kMaxStride || F > kMaxStride / 2)
+    return TGEMM_ERR_UNSUPPORTED;
+  if (router != nullptr && ldr > INT64_MAX / 4 / E) return TGEMM_ERR_UNSUPPORTED;
+  int st = check_rows(X, M, K, ldx);
+  if (st == TGEMM_OK) st = check_rows(Y, M, K, ldy);
+  if (st == TGEMM_OK) st = check_experts(W1, E, 2 * F, K, ldw1, sw1);
+  if (st == TGEMM_OK) st = check_experts(W2, E, K, F, ldw2, sw2);
+  if (st != TGEMM_OK) return st;
+  return ldw1 > kMaxStride || (ldw2 > kMaxStride && K > 1) || (ldx > kMaxStride && M > 1)
+             ? TGEMM_ERR_UNSUPPORTED
+             : TGEMM_OK;
+}
+
 extern "C" const char* tgemm_status_string(int status) {
   switch (status) {
     case TGEMM_OK: return "TGEMM_OK";

@@ -46,7 +46,8 @@ EXPORTS = ("tgemm_run", "tgemm_run_fp8", "tgemm_validate", "tgemm_validate_fp8",
            "tgemm_linear_workspace_bytes", "tgemm_run_linear_backward",
            "tgemm_validate_linear_backward", "tgemm_linear_backward_workspace_bytes",
            "tgemm_block_norm", "tgemm_validate_block_norm", "tgemm_block_norm_backward",
-           "tgemm_validate_block_norm_backward", "tgemm_block_norm_backward_workspace_bytes")
+           "tgemm_validate_block_norm_backward", "tgemm_block_norm_backward_workspace_bytes",
+           "tgemm_run_moe", "tgemm_validate_moe", "tgemm_moe_workspace_bytes")
 
 ACT_SILU = 0
 ACT_GELU_TANH = 1
@@ -138,7 +139,10 @@ def lib():
                  product + [vp, i64, vp, i64, ci, ci, vp, i64, vp, i64, ci, vp], True),
                 ("block_norm", [vp, i64] * 2 + norm + [cf, i64, i64, vp, i64, vp, i64, vp], False),
                 ("block_norm_backward",
-                 [vp, i64] * 4 + norm + [vp, i64, i64, vp, i64, vp, i64, vp, vp, vp], True)):
+                 [vp, i64] * 4 + norm + [vp, i64, i64, vp, i64, vp, i64, vp, vp, vp], True),
+                ("run_moe",
+                 [i64] * 5 + [vp, i64, vp, i64, ci, ci, cf, vp, vp] + [vp, i64, i64] * 2 +
+                 [ci, vp, i64], True)):
             bare = name.replace("run_", "")
             call = getattr(L, "tgemm_" + name)
             call.argtypes, call.restype = args + ([vp, i64, vp] if ws else [vp]), ci
@@ -149,6 +153,8 @@ def lib():
                 need.argtypes, need.restype = product, i64
         need = L.tgemm_block_norm_backward_workspace_bytes
         need.argtypes, need.restype = [i64, i64, ci, i64], i64
+        need = L.tgemm_moe_workspace_bytes
+        need.argtypes, need.restype = [i64] * 5 + [ci], i64
         _lib = L
     return _lib
 
@@ -1006,6 +1012,81 @@ def block_norm_backward(dn, y, residual, rstd, weight, post_weight=None, gate=No
               _ptr(rstd), M, K, _ptr(dh), K, _ptr(dy), K, _ptr(dw), _ptr(dp), _ptr(dg), _ptr(ws),
               max(need, 0))
     return dh, dy, dw, dp, dg
+
+
+# ---- mixture-of-experts layers for few tokens --------------------------------
+
+
+def _experts(w, what):
+    """(expert stride, row stride) of logical [E, K, N] stored [E, N, K]."""
+    if w.dtype != torch.bfloat16:
+        raise TypeError(f"{what} must be torch.bfloat16")
+    if w.dim() != 3 or 0 in w.shape:
+        raise ValueError(f"{what} must be a non-empty [E, K, N] tensor")
+    E, K, N = w.shape
+    sx, unit, ld = w.stride()
+    if N == 1:
+        ld = K
+    if (unit != 1 and K != 1) or ld < K:
+        raise ValueError(f"{what} must be stored [E, N, K] (pass w.transpose(1, 2))")
+    return sx, ld
+
+
+def _run_moe(x, router, ids, weights, w_gate_up, w_down, top, act, renormalize, scale, dev):
+    x2, ldx = _rows(x, "x", torch.bfloat16)
+    M, K = x2.shape
+    s1, ld1 = _experts(w_gate_up, "w_gate_up")
+    s2, ld2 = _experts(w_down, "w_down")
+    E, F = w_down.shape[0], w_down.shape[1]
+    if w_gate_up.shape != (E, K, 2 * F) or w_down.shape[2] != K:
+        raise ValueError("w_gate_up must be [E, K, 2F] and w_down [E, F, K] for x [..., K]")
+    r2, ldr, rt = None, 0, EPI_STORE_BF16
+    if router is not None:
+        if router.shape != (K, E):
+            raise ValueError("router must be [K, E]")
+        rt = _store(router.dtype, "router")
+        r2, ldr = _rows(router.t(), "router (stored [E, K])", router.dtype)
+    y = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
+    need = lib().tgemm_moe_workspace_bytes(M, K, F, E, top, 0 if router is None else 1)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
+    _call("tgemm_run_moe", dev, M, K, F, E, top, _ptr(x2), ldx, _ptr(r2), ldr, rt,
+          1 if renormalize else 0, float(scale), _ptr(ids), _ptr(weights), _ptr(w_gate_up), ld1, s1,
+          _ptr(w_down), ld2, s2, _act(act), _ptr(y), K, _ptr(ws), max(need, 0))
+    return y
+
+
+def moe(x, router, w_gate_up, w_down, top_k, act="silu", renormalize=True, scale=1.0,
+        routing=False, stream=None):
+    """A mixture-of-experts layer for few tokens: sum_j p_j * (act(g) * u) @
+    w_down[e_j], [g | u] = x @ w_gate_up[e_j], over the ``top_k`` experts e_j
+    with the largest logits x @ router (ties: the lowest index first).
+
+    ``x`` bf16 [..., K]; ``router`` bf16 or fp32 [K, E], usually ``R.t()`` of a
+    weight stored [E, K]; ``w_gate_up`` bf16 [E, K, 2F] (g first) and ``w_down``
+    bf16 [E, F, K], views ``w.transpose(1, 2)`` of weights stored [E, 2F, K] and
+    [E, K, F].  p is ``scale`` times the softmax of the logits, over the chosen
+    (``renormalize``) or over all experts.  ``routing``: also return (ids int32,
+    p fp32), [..., top_k].
+    """
+    dev = _same_device(x, router, w_gate_up, w_down)
+    with _on(dev, stream):
+        ids = torch.empty(x.shape[:-1] + (top_k,), dtype=torch.int32, device=dev)
+        p = torch.empty(ids.shape, dtype=torch.float32, device=dev)
+        y = _run_moe(x, router, ids, p, w_gate_up, w_down, top_k, act, renormalize, scale, dev)
+    return (y, ids, p) if routing else y
+
+
+def moe_experts(x, ids, weights, w_gate_up, w_down, act="silu", stream=None):
+    """The experts of ``moe`` for a routing of the caller's: ``ids`` int32 and
+    ``weights`` fp32, [..., top_k].  An id outside the experts adds nothing."""
+    if ids.dtype != torch.int32 or weights.dtype != torch.float32:
+        raise TypeError("ids must be int32 and weights fp32")
+    if ids.dim() != x.dim() or ids.shape[:-1] != x.shape[:-1] or weights.shape != ids.shape or \
+            not (ids.is_contiguous() and weights.is_contiguous()):
+        raise ValueError("ids and weights must be contiguous [..., top_k] for x [..., K]")
+    dev = _same_device(x, ids, weights, w_gate_up, w_down)
+    with _on(dev, stream):
+        return _run_moe(x, None, ids, weights, w_gate_up, w_down, ids.shape[-1], act, True, 1.0, dev)
 
 
 def outer_f32(a, b, stream=None):
