@@ -95,9 +95,14 @@ inline bool streams_past_cache(const RowsParams& p) {
 }
 
 // Output tile shapes of the large-product kernel.
-enum RowsTile : int { kRows256 = 0, kRows128x256 = 1, kRows128 = 2, kRows64 = 3 };
-inline int rows_tile_m(int t) { return t == kRows256 ? 256 : t == kRows64 ? 64 : 128; }
-inline int rows_tile_n(int t) { return t >= kRows128 ? 128 : 256; }
+// (256x192: linear products only)
+enum RowsTile : int { kRows256 = 0, kRows128x256 = 1, kRows128 = 2, kRows64 = 3, kRows256x192 = 4 };
+inline int rows_tile_m(int t) {
+  return t == kRows256 || t == kRows256x192 ? 256 : t == kRows64 ? 64 : 128;
+}
+inline int rows_tile_n(int t) {
+  return t == kRows256x192 ? 192 : t >= kRows128 ? 128 : 256;
+}
 
 // Large products (rows_gemm.hip).  `gate`: B's rows are interleaved in the
 // tile (kRowsGated, or kRowsPart of a gated product).
@@ -328,11 +333,7 @@ __device__ __forceinline__ void act_gradients(float g, float u, float h, int act
 // The linear product's activations: the two above, none and relu.
 constexpr int kActNone = 2, kActRelu = 3;
 
-__device__ __forceinline__ float linear_act(float z, int act) {
-  if (act == kActNone) return z;
-  if (act == kActRelu) return z <= 0.f ? 0.f : z;  // (NaN stays)
-  return act_times(z, 1.f, act);
-}
+__device__ __forceinline__ float relu(float z) { return z <= 0.f ? 0.f : z; }  // (NaN stays)
 
 // d act'(z)
 __device__ __forceinline__ float linear_act_grad(float z, float d, int act) {
@@ -417,28 +418,33 @@ __device__ __forceinline__ void get4(const float* p, float* v, int n) {
   }
 }
 
-// The linear product's epilogue for up to 4 consecutive outputs, in three
-// steps, so that a caller can load early.  A residual may be C itself: a
-// thread loads its values before it stores over them.
+// The linear product's epilogue for up to 4 consecutive outputs (FOUR: exactly
+// 4, of a row that exists), in three steps, so that a caller can load early.  A
+// residual may be C itself: a thread loads its values before it stores over
+// them.
 __device__ __forceinline__ void linear_bias4(const RowsParams& p, int c, int n, float (&b)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) b[i] = 0.f;
   if (p.bias != nullptr && n > 0) get4(p.bias + c, b, n);
 }
+template <bool FOUR>
 __device__ __forceinline__ void linear_res4(const RowsParams& p, int row, int c, int n,
                                             float (&r)[4]) {
+  if constexpr (FOUR) n = 4;
 #pragma unroll
   for (int i = 0; i < 4; ++i) r[i] = 0.f;
-  if (p.res == nullptr || row >= p.M || n <= 0) return;
+  if (p.res == nullptr) return;
   const int64_t o = (int64_t)row * p.ldr + c;
   if (p.c_f32)
     get4(static_cast<const float*>(p.res) + o, r, n);
   else
     get4(static_cast<const uint16_t*>(p.res) + o, r, n);
 }
+template <bool FOUR>
 __device__ __forceinline__ void linear_put4(const RowsParams& p, int row, int c, int n,
                                             const float* sum, const float (&b)[4],
                                             const float (&r)[4]) {
+  if constexpr (FOUR) n = 4;
   float v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = sum[i] + b[i];
@@ -449,10 +455,16 @@ __device__ __forceinline__ void linear_put4(const RowsParams& p, int row, int c,
     else
       put4(static_cast<uint16_t*>(p.z) + o, v, n);
   }
+  if (p.act == kActRelu) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[i] = linear_act(v[i], p.act);
-    if (p.res != nullptr) v[i] += r[i];
+    for (int i = 0; i < 4; ++i) v[i] = relu(v[i]);
+  } else if (p.act != kActNone) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = act_times(v[i], 1.f, p.act);
+  }
+  if (p.res != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += r[i];
   }
   const int64_t o = (int64_t)row * p.ldc + c;
   if (p.c_f32)

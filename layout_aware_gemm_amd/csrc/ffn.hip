@@ -47,16 +47,20 @@ void set_tile(RowsParams* p, bool gate, int tile, int col0, int end) {
 // 0.8 (64x128), 1.33 (128x256) and 1.95 (256x256) of it (gated 13824 x 5120,
 // us for 64x128 / 128x128 / 128x256 / 256x256 tiles: 256 rows 101 / 66.9 /
 // 51.4 / 65.0 int8, 170 / 114 / 89 / 121 bf16; 512 rows 163 / 123 / 92 / 70
-// and 272 / 211 / 158 / 125).
+// and 272 / 211 / 158 / 125).  256x192 tiles (linear products) take 0.77 of a
+// 256x256 round: 2047 x 5120 x 13824, one round of either, 278 us against 307
+// (216 workgroups instead of 160, cold operands; rows off 128-byte lines 360
+// against 431).
 double grid_cost(RowsParams* p, bool gate, int tile, int split, int col0, int end) {
-  constexpr double cost[4] = {1.95, 1.33, 1.0, 0.8};
+  constexpr double cost[5] = {1.95, 1.33, 1.0, 0.8, 1.5};
   set_tile(p, gate, tile, col0, end);
   const double round = cost[tile] * (6 + 2.9e-3 * p->K / split);
   const double sums = split > 1 ? 4 + 1.7e-6 * split * p->M * p->N : 0;
   return (double)(((int64_t)p->tilesM * p->tilesN * split + 255) / 256) * round + sums;
 }
 
-RowsPlan plan_rows(RowsParams* p, bool gate) {
+// linear: 256x192 tiles may be used.
+RowsPlan plan_rows(RowsParams* p, bool gate, bool linear) {
   // Few rows of A: the kernel that streams B.  From 17 rows on a gated
   // weight wide enough for 64x128 tiles on most of the chip is faster there
   // (us tiles / streaming, int8 then bf16: 13824 x 5120, 16 rows 29.3 / 28.4,
@@ -89,6 +93,14 @@ RowsPlan plan_rows(RowsParams* p, bool gate) {
           r.tail = t;
           r.tail_col = col;
         }
+      }
+    }
+    if (linear) {
+      const double c = grid_cost(p, gate, kRows256x192, 1, 0, end);
+      if (c < best) {
+        best = c;
+        r.tile = kRows256x192;
+        r.tail = -1;
       }
     }
     for (int t = kRows128x256; t <= kRows64; ++t) {
@@ -200,7 +212,7 @@ int run_i8(char ta, char tb, const void* A, int64_t lda, const void* B, int64_t 
   const bool packA = !is_n(ta) || !rows_aligned(A, lda, K) || !stride_fits(lda);
   const bool packB = is_n(tb) || !rows_aligned(B, ldb, K) || !stride_fits(ldb);
   p.K = packA || packB ? Kp : K;
-  const RowsPlan r = plan_rows(&p, gate);
+  const RowsPlan r = plan_rows(&p, gate, false);
   PackRows ca = {A, lda, is_n(ta), p.M, K, nullptr, p.M, Kp};
   PackRows cb = {B, ldb, !is_n(tb), p.N, K, nullptr, p.N, Kp};
   if (!grid_fits(p, r, gate) || (packA && !pack_rows_fits(ca, 1)) ||
@@ -257,7 +269,7 @@ int run_bf16(char ta, char tb, int64_t K, const void* A, int64_t lda, const void
   const bool packB = is_n(tb) || !rows_aligned(B, 2 * ldb, 2 * K) || !stride_fits(2 * ldb);
   if ((packA || packB) && !stride_fits(2 * Kp)) return TGEMM_ERR_UNSUPPORTED;
   p.K = (int)(2 * Kp);
-  const RowsPlan r = plan_rows(&p, gate);
+  const RowsPlan r = plan_rows(&p, gate, epi == kRowsLinear);
   PackRows ca = {A, lda, is_n(ta), p.M, (int)K, nullptr, p.M, Kp};
   PackRows cb = {B, ldb, !is_n(tb), p.N, (int)K, nullptr, p.N, Kp};
   if (!grid_fits(p, r, gate) || (packA && !pack_rows_fits(ca, 2)) ||

@@ -46,8 +46,8 @@ __global__ void __launch_bounds__(kThr) finish_kernel(RowsParams p) {
   if constexpr (EPI == kRowsLinear) {
     float bias[4], res[4];
     linear_bias4(p, c, n, bias);
-    linear_res4(p, row, c, n, res);
-    linear_put4(p, row, c, n, a, bias, res);
+    linear_res4<false>(p, row, c, n, res);
+    linear_put4<false>(p, row, c, n, a, bias, res);
     return;
   }
   float v[4], u[4], h[4];

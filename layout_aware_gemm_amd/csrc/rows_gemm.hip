@@ -65,8 +65,8 @@ constexpr int kRowBytes = 128;  // bytes of K per k-step (one LDS row)
 template <int R, bool GATE, int AUX = 0>
 struct RowsPanel {
   static constexpr int PER_WAVE = R / 32;
-  static_assert(PER_WAVE == 4 || PER_WAVE == 8 || (PER_WAVE == 2 && !GATE),
-                "panels of 128 or 256 rows, or 64 of A");
+  static_assert(PER_WAVE == 4 || PER_WAVE == 8 || (PER_WAVE % 2 == 0 && !GATE),
+                "panels of 128 or 256 rows; without gates 64 or 192 too");
   uint32_t e[2];   // lane's byte offset in even / odd 8-row blocks
   uint32_t et[2];  // the same in a last, partial k-step: outside the range past K
   uint32_t row8;   // 8 rows in bytes
@@ -339,40 +339,75 @@ __device__ __forceinline__ void keep_epilogue(const RowsParams& p,
 
 // The linear epilogue, 32 rows at a time through LDS words of the wave's own,
 // as above: rows enter and leave in vectors of four (a residual read from the
-// accumulators' layout takes a request for every 32 values).
+// accumulators' layout takes a request for every 32 values).  A wave whose
+// block lies inside the output takes U rows of lanes at a time, their loads
+// ahead of the first use; others test each value.
+//
+// The code is kept small: all of it is run once per tile, from a cold
+// instruction cache.  (Unrolled over the blocks of 32 rows it was 75 KB, and a
+// 4096 x 12288 x 5120 product took 437 us, not 403.)  So the blocks are a loop,
+// with the accumulators, which only constants can index, chosen by a switch.
 template <int BM, int BN>
 __device__ __forceinline__ void linear_epilogue(const RowsParams& p,
                                                 const f32x16_t (&acc)[BM / 64][BN / 64], float* st,
                                                 int row0, int col0, int lane) {
   constexpr int FM = BM / 64, FN = BN / 64, LD = keep_row<BN>();
   constexpr int LPR = BN / 8, RPI = 64 / LPR, NQ = 32 / RPI;  // lanes per row, rows per pass
-  constexpr int U = 4;                                        // passes whose loads go ahead
+  constexpr int U = 4;
+  static_assert(NQ % U == 0 && RPI * NQ == 32, "whole passes");
   const int h = lane >> 5, lc = lane & 31;
   const int cl = 4 * (lane % LPR), c = col0 + cl;  // this lane's four columns
   const int n = p.N - c;                           // of which so many exist
+  const int rl = lane / LPR;
+  const bool idle = rl >= RPI;  // (192 columns: 24 lanes a row, 16 left over)
+  const bool full = row0 + BM / 2 <= p.M && col0 + BN / 2 <= p.N;
   float b[4];
   linear_bias4(p, c, n, b);
-#pragma unroll
-  for (int i = 0; i < FM; ++i) {
+  auto stage = [&](const f32x16_t (&a)[FN]) __attribute__((always_inline)) {
 #pragma unroll
     for (int r = 0; r < 16; ++r)
 #pragma unroll
       for (int j = 0; j < FN; ++j)
-        st[(8 * (r >> 2) + 4 * h + (r & 3)) * LD + j * 32 + lc] = acc[i][j][r];
+        st[(8 * (r >> 2) + 4 * h + (r & 3)) * LD + j * 32 + lc] = a[j][r];
+  };
+#pragma unroll 1
+  for (int i = 0; i < FM; ++i) {
+    if (i == 0) stage(acc[0]);
+    if constexpr (FM > 1)
+      if (i == 1) stage(acc[1]);
+    if constexpr (FM > 2)
+      if (i == 2) stage(acc[2]);
+    if constexpr (FM > 3)
+      if (i == 3) stage(acc[3]);
     wave_lds_order();
+    const int row = row0 + i * 32 + rl;
+    const float* const src = st + rl * LD + cl;
+    if (idle) {
+    } else if (full) {
+#pragma unroll 1
+      for (int q = 0; q < NQ; q += U) {
+        float4 v[U];
+        float r[U][4];
 #pragma unroll
-    for (int q0 = 0; q0 < NQ; q0 += U) {
-      float r[U][4];
+        for (int u = 0; u < U; ++u) linear_res4<true>(p, row + (q + u) * RPI, c, 4, r[u]);
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        linear_res4(p, row0 + i * 32 + (q0 + u) * RPI + lane / LPR, c, n, r[u]);
+        for (int u = 0; u < U; ++u)
+          v[u] = *reinterpret_cast<const float4*>(src + (q + u) * RPI * LD);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int rl = (q0 + u) * RPI + lane / LPR, row = row0 + i * 32 + rl;
-        const float4 v = *reinterpret_cast<const float4*>(st + rl * LD + cl);
-        if (row >= p.M || n <= 0) continue;
+        for (int u = 0; u < U; ++u) {
+          const float e[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+          linear_put4<true>(p, row + (q + u) * RPI, c, 4, e, b, r[u]);
+        }
+      }
+    } else {
+#pragma unroll 1
+      for (int q = 0; q < NQ; ++q) {
+        const float4 v = *reinterpret_cast<const float4*>(src + q * RPI * LD);
+        if (row + q * RPI >= p.M || n <= 0) continue;
         const float e[4] = {v.x, v.y, v.z, v.w};
-        linear_put4(p, row, c, n, e, b, r[u]);
+        float r[4];
+        linear_res4<false>(p, row + q * RPI, c, n, r);
+        linear_put4<false>(p, row + q * RPI, c, n, e, b, r);
       }
     }
     wave_lds_order();
@@ -386,8 +421,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(RowsParams p) {
   constexpr int FM = BM / 64, FN = BN / 64;
   constexpr int NT = GATE ? BN / 2 : BN;       // output columns per tile
   constexpr int SA = BM * kBK, SB = BN * kBK;  // panel sizes in 16-bit units
-  static_assert(FN % 2 == 0, "gate pairs");
-  static_assert((BM == 256 && BN == 256) || BM <= 128, "one of the two schedules");
+  static_assert(!GATE || FN % 2 == 0, "gate pairs");
+  static_assert((BM == 256 && BN >= 192) || BM <= 128, "one of the two schedules");
   // two A and three B panels, or the ring
   __shared__ __attribute__((aligned(16)))
   uint16_t lds[BM <= 128 ? ring_rows<BM, BN>() * (SA + SB) : 2 * SA + 3 * SB];
@@ -607,6 +642,10 @@ hipError_t launch_tile(int type, int epi, bool gate, const RowsParams& p, hipStr
 hipError_t launch_rows_gemm(int type, int tile, int epi, bool gate, const RowsParams& p,
                             hipStream_t s) {
   if (tile == kRows256) return launch_tile<256, 256>(type, epi, gate, p, s);
+  if (tile == kRows256x192)
+    return type == kRowsBf16 && !gate && epi == kRowsLinear
+               ? launch_one<OpBf16, 256, 192, false, kRowsLinear>(p, s)
+               : hipErrorInvalidValue;
   if (tile == kRows128x256) return launch_tile<128, 256>(type, epi, gate, p, s);
   if (tile == kRows64) return launch_tile<64, 128>(type, epi, gate, p, s);
   return launch_tile<128, 128>(type, epi, gate, p, s);

@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(W * 64) skinny_kernel(RowsParams p) {
       const float e[4] = {(float)a[0], (float)a[1], (float)a[2], (float)a[3]};
       float bias[4], res[4];
       linear_bias4(p, c0, n, bias);
-      linear_res4(p, row, c0, n, res);
-      linear_put4(p, row, c0, n, e, bias, res);
+      linear_res4<false>(p, row, c0, n, res);
+      linear_put4<false>(p, row, c0, n, e, bias, res);
       continue;
     }
     float v[4], g[4], u[4];
