@@ -19,7 +19,8 @@
 //
 // Bound: HBM bandwidth.  A row stays in registers between its reduction and
 // its results, so each element moves once: 8 bytes forward (bf16), 12
-// backward.  The gradients of the weights are kept per column in registers
+// backward.  Measured: 8192 x 4096 51 us forward (5.3 TB/s, a large copy's
+// rate), 89 us backward (4.5 TB/s) and 7 us for the sums.  The gradients of the weights are kept per column in registers
 // while a workgroup works through its rows; the workgroups' sums are added
 // in order by a second kernel (no atomics: the same bits every time).
 #include "ffn.h"
@@ -129,17 +130,23 @@ struct ColumnSums {
       }
     }
   }
-  __device__ __forceinline__ void add(float4* m, int v, const float (&x)[8]) {
+  // a * b to the sum of the chunk's element i; those of a chunk in LDS wait in
+  // r[0] for done.
+  __device__ __forceinline__ void fma_to(int v, int i, float a, float b) {
+    if constexpr (LDS)
+      r[0][i] = a * b;
+    else
+      r[v][i] = fmaf(a, b, r[v][i]);
+  }
+  __device__ __forceinline__ void done(float4* m, int v) {
     if constexpr (LDS) {
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         float4& w = m[(2 * v + q) * THREADS + threadIdx.x];
         const float4 o = w;
-        w = make_float4(o.x + x[4 * q], o.y + x[4 * q + 1], o.z + x[4 * q + 2], o.w + x[4 * q + 3]);
+        w = make_float4(o.x + r[0][4 * q], o.y + r[0][4 * q + 1], o.z + r[0][4 * q + 2],
+                        o.w + r[0][4 * q + 3]);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r[v][i] += x[i];
     }
   }
   __device__ __forceinline__ void get(const float4* m, int v, float (&x)[8]) const {
@@ -155,17 +162,68 @@ struct ColumnSums {
   }
 };
 
-// Workgroup b takes rows b * p.per_group .. of its p.per_group.  At most 512
-// threads: with half the registers of a full workgroup the column sums and the
-// row would not fit.  Four chunks per thread (K past 8192) leave no room for the
-// sums of the two weights, which move to LDS, nor for the weights and dn over
-// the reduction: they are read again (from the cache).
-constexpr int kBwdThreads = 512;
+// The inputs of one row, as they are stored.
+template <int V, class T>
+struct GradRow {
+  u16x8_any y[V], dn[V];
+  typename Vec8<T>::type h[V], ds[V];
+};
 
-template <int V, class T, bool POST, bool GATE>
-__global__ void __launch_bounds__(kBwdThreads) block_norm_bwd_kernel(BlockNormGradParams p) {
-  typedef ColumnSums<V, V == 4, kBwdThreads> Wide;
-  __shared__ float sums[2][kBwdThreads / 64][3];
+// 8 elements of a row, in and out; WHOLE: its length is a multiple of 8.  (Bytes
+// in 32 bits: a row's address then stays in scalar registers, the lane's place
+// in one vector register for all rows.)
+template <bool WHOLE, class P>
+__device__ __forceinline__ auto row8(const P* p, uint32_t c, int64_t K) {
+  if constexpr (WHOLE) {
+    typename Vec8<P>::type v = {};
+    if (c < K)
+      v = *reinterpret_cast<const typename Vec8<P>::type*>(reinterpret_cast<const char*>(p) +
+                                                           (uint32_t)(c * sizeof(P)));
+    return v;
+  } else {
+    return load8(p, c, K);
+  }
+}
+template <bool WHOLE, class P>
+__device__ __forceinline__ void put_row8(P* p, uint32_t c, int64_t K, const float (&f)[8]) {
+  if constexpr (WHOLE)
+    p = reinterpret_cast<P*>(reinterpret_cast<char*>(p) + (uint32_t)(c * sizeof(P)));
+  if (c >= K) return;
+  if constexpr (WHOLE)
+    put8(p, 0, 8, f);
+  else
+    put8(p, c, K, f);
+}
+
+// Keeps a vector packed: the compiler would hold its eight unpacked values from
+// one use to the next, in twice the registers.
+__device__ __forceinline__ void stay_packed(u16x8_any& v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  uint32_t a = v.w[0], b = v.w[1], c = v.w[2], d = v.w[3];
+  asm volatile("" : "+v"(a), "+v"(b), "+v"(c), "+v"(d));
+  v = u16x8_any{{a, b, c, d}};
+#endif
+}
+
+// Workgroup b takes rows b * p.per_group .. of its p.per_group.  The next row's
+// loads are issued before the reduction of this one; the weights stay in
+// registers, the gate while its group lasts.  One chunk per thread: up to 1024
+// threads and 128 registers.  With a post-norm and a gate, and for four chunks
+// (K past 8192; 512 threads, 256 registers), the sums of the two weights move to
+// LDS; where the rest does not fit either (AHEAD false), the weights and dn are
+// read when they are used, and no row ahead.
+template <int V>
+constexpr int bwd_threads() {
+  return V == 4 ? 512 : 1024;
+}
+
+template <int V, class T, bool POST, bool GATE, bool WHOLE>
+__global__ void __launch_bounds__(bwd_threads<V>()) block_norm_bwd_kernel(BlockNormGradParams p) {
+  typedef ColumnSums<V, V == 4 || (POST && GATE), bwd_threads<V>()> Wide;
+  // registers for the weights and the next row
+  constexpr bool AHEAD =
+      V < 4 && (!POST || !GATE || (WHOLE && std::is_same<T, uint16_t>::value));
+  __shared__ float sums[2][bwd_threads<V>() / 64][3];
   __shared__ __attribute__((aligned(16))) float4 m_an[Wide::kWords];
   __shared__ __attribute__((aligned(16))) float4 m_ap[POST ? Wide::kWords : 1];
   const int W = blockDim.x;
@@ -175,62 +233,82 @@ __global__ void __launch_bounds__(kBwdThreads) block_norm_bwd_kernel(BlockNormGr
   constexpr PartRows R = {1, 1 + (POST ? 1 : 0), 2 + (POST ? 1 : 0),
                           1 + (POST ? 1 : 0) + (GATE ? 2 : 0)};
   float* const part = p.part + (int64_t)blockIdx.x * R.count * K;
-  typedef typename Vec8<T>::type tvec;
-  Wide an, ap;
-  ColumnSums<V, false, kBwdThreads> ag;
-  an.clear(m_an);
-  if constexpr (POST) ap.clear(m_ap);
-  if constexpr (GATE) ag.clear(nullptr);
-  for (int row = first; row < end; ++row) {
+  auto col = [&](int v) __attribute__((always_inline)) {
+    return (uint32_t)(v * W + (int)threadIdx.x) * 8;
+  };
+  auto load = [&](GradRow<V, T>& r, int row) __attribute__((always_inline)) {
     const uint16_t* const y = p.y + (int64_t)row * p.ldy;
     const uint16_t* const dn = p.dn + (int64_t)row * p.lddn;
     const T* const h = static_cast<const T*>(p.h) + (int64_t)row * p.ldh;
-    const T* const ds =
-        p.ds == nullptr ? nullptr : static_cast<const T*>(p.ds) + (int64_t)row * p.ldds;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const uint32_t c = col(v);
+      r.y[v] = row8<WHOLE>(y, c, K);
+      r.dn[v] = row8<WHOLE>(dn, c, K);
+      r.h[v] = row8<WHOLE>(h, c, K);
+      r.ds[v] = {};
+      if (p.ds != nullptr)
+        r.ds[v] = row8<WHOLE>(static_cast<const T*>(p.ds) + (int64_t)row * p.ldds, c, K);
+    }
+  };
+  Wide an, ap;
+  ColumnSums<V, false, bwd_threads<V>()> ag;
+  an.clear(m_an);
+  if constexpr (POST) ap.clear(m_ap);
+  if constexpr (GATE) ag.clear(nullptr);
+  u16x8_any wn[V], wp[POST ? V : 1], gv[GATE ? V : 1];
+  if constexpr (AHEAD) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      wn[v] = row8<WHOLE>(p.weight, col(v), K);
+      if constexpr (POST) wp[v] = row8<WHOLE>(p.post, col(v), K);
+    }
+  }
+  GradRow<V, T> next;
+  if constexpr (AHEAD) load(next, first);
+  int held = -1;  // the group whose gate is in gv
+  for (int row = first; row < end; ++row) {
     const int grp = GATE ? row / p.rows_per_gate : 0;
     const uint16_t* const gate = GATE ? p.gate + (int64_t)grp * p.ldgate : nullptr;
     const float rs = p.rstd[row], ry = POST ? p.rstd[p.M + row] : 1.f;
-    u16x8_any yv[V], dv[V], wn[V], wp[POST ? V : 1], gv[GATE ? V : 1];
+    if constexpr (GATE && AHEAD) {
+      if (grp != held) {
+        held = grp;
+#pragma unroll
+        for (int v = 0; v < V; ++v) gv[v] = row8<WHOLE>(gate, col(v), K);
+      }
+    }
+    GradRow<V, T> cur;
+    if constexpr (AHEAD) {
+      cur = next;
+      if (row + 1 < end) load(next, row + 1);
+    } else {
+      load(cur, row);
+    }
     float s[V][8], t[V][8];
     float q[3] = {0.f, 0.f, 0.f};  // sum e s, sum q (ds + rs e), sum q s
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int64_t c = ((int64_t)v * W + threadIdx.x) * 8;
-      yv[v] = load8(y, c, K);
-      dv[v] = load8(dn, c, K);
-      const tvec hv = load8(h, c, K);
-      tvec sv = {};
-      if (ds != nullptr) sv = load8(ds, c, K);
-      if constexpr (V < 4) {
-        wn[v] = load8(p.weight, c, K);
-        if constexpr (POST) wp[v] = load8(p.post, c, K);
-        if constexpr (GATE) gv[v] = load8(gate, c, K);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        s[v][i] = value(hv, i);
-        t[v][i] = value(sv, i);
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
       float a[8];
-      if constexpr (V == 4) {
-        const int64_t c = ((int64_t)v * W + threadIdx.x) * 8;
+      if constexpr (AHEAD) {
+        stay_packed(wn[v]);
+        if constexpr (POST) stay_packed(wp[v]);
+        if constexpr (GATE) stay_packed(gv[v]);
+      } else {
         __builtin_amdgcn_sched_barrier(0);
-        wn[v] = load8(p.weight, c, K);
-        if constexpr (POST) wp[v] = load8(p.post, c, K);
-        if constexpr (GATE) gv[v] = load8(gate, c, K);
+        wn[v] = row8<WHOLE>(p.weight, col(v), K);
+        if constexpr (POST) wp[v] = row8<WHOLE>(p.post, col(v), K);
+        if constexpr (GATE) gv[v] = row8<WHOLE>(gate, col(v), K);
       }
       gate8<GATE>(gv[GATE ? v : 0], p.scale, a);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float yi = value(yv[v], i);
+        const float yi = value(cur.y[v], i);
         float pi = yi;
         if constexpr (POST) pi = yi * ry * value(wp[v], i);
-        s[v][i] = fmaf(a[i], pi, s[v][i]);
-        const float e = value(dv[v], i) * value(wn[v], i);
-        t[v][i] = fmaf(rs, e, t[v][i]);
+        s[v][i] = fmaf(a[i], pi, value(cur.h[v], i));
+        const float e = value(cur.dn[v], i) * value(wn[v], i);
+        t[v][i] = fmaf(rs, e, value(cur.ds[v], i));
         q[0] = fmaf(e, s[v][i], q[0]);
         if constexpr (POST) {
           const float w = a[i] * value(wp[v], i) * yi;
@@ -244,38 +322,40 @@ __global__ void __launch_bounds__(kBwdThreads) block_norm_bwd_kernel(BlockNormGr
     const float ky = ry * (ry * fmaf(-k, q[2], q[1]) * rk) * ry;  // of y in dy
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int64_t c = ((int64_t)v * W + threadIdx.x) * 8;
-      float a[8], o[8], xn[8], xp[8], xg[8];
-      if constexpr (V == 4) {
+      const uint32_t c = col(v);
+      float a[8], o[8];
+      stay_packed(cur.y[v]);
+      if constexpr (AHEAD) {
+        stay_packed(cur.dn[v]);
+        if constexpr (POST) stay_packed(wp[v]);
+        if constexpr (GATE) stay_packed(gv[v]);
+      } else {
         __builtin_amdgcn_sched_barrier(0);
-        dv[v] = load8(dn, c, K);
-        if constexpr (POST) wp[v] = load8(p.post, c, K);
-        if constexpr (GATE) gv[v] = load8(gate, c, K);
+        cur.dn[v] = row8<WHOLE>(p.dn + (int64_t)row * p.lddn, c, K);
+        if constexpr (POST) wp[v] = row8<WHOLE>(p.post, c, K);
+        if constexpr (GATE) gv[v] = row8<WHOLE>(gate, c, K);
       }
       gate8<GATE>(gv[GATE ? v : 0], p.scale, a);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float yi = value(yv[v], i);
+        const float yi = value(cur.y[v], i);
         t[v][i] = fmaf(-k, s[v][i], t[v][i]);
-        xn[i] = value(dv[v], i) * (s[v][i] * rs);
+        an.fma_to(v, i, value(cur.dn[v], i), s[v][i] * rs);
         const float u = a[i] * t[v][i];
         if constexpr (POST) {
           const float w = value(wp[v], i);
-          xp[i] = u * (yi * ry);
-          xg[i] = p.scale * t[v][i] * (yi * ry * w);
+          ap.fma_to(v, i, u, yi * ry);
+          if constexpr (GATE) ag.fma_to(v, i, p.scale * t[v][i], yi * ry * w);
           o[i] = fmaf(-ky, yi, ry * (u * w));
         } else {
-          xg[i] = p.scale * t[v][i] * yi;
+          if constexpr (GATE) ag.fma_to(v, i, p.scale * t[v][i], yi);
           o[i] = u;
         }
       }
-      an.add(m_an, v, xn);
-      if constexpr (POST) ap.add(m_ap, v, xp);
-      if constexpr (GATE) ag.add(nullptr, v, xg);
-      if (c < K) {
-        put8(static_cast<T*>(p.dh) + (int64_t)row * p.lddh, c, K, t[v]);
-        put8(p.dy + (int64_t)row * p.lddy, c, K, o);
-      }
+      an.done(m_an, v);
+      if constexpr (POST) ap.done(m_ap, v);
+      put_row8<WHOLE>(static_cast<T*>(p.dh) + (int64_t)row * p.lddh, c, K, t[v]);
+      put_row8<WHOLE>(p.dy + (int64_t)row * p.lddy, c, K, o);
     }
     if constexpr (GATE) {
       // the group's last row here: a whole group's sums are final
@@ -286,10 +366,9 @@ __global__ void __launch_bounds__(kBwdThreads) block_norm_bwd_kernel(BlockNormGr
                                            : part + (before ? R.head : R.tail) * K;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const int64_t c = ((int64_t)v * W + threadIdx.x) * 8;
           float x[8];
           ag.get(nullptr, v, x);
-          if (c < K) put8(o, c, K, x);
+          put_row8<WHOLE>(o, col(v), K, x);
         }
         ag.clear(nullptr);
       }
@@ -297,14 +376,12 @@ __global__ void __launch_bounds__(kBwdThreads) block_norm_bwd_kernel(BlockNormGr
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int64_t c = ((int64_t)v * W + threadIdx.x) * 8;
-    if (c >= K) continue;
     float x[8];
     an.get(m_an, v, x);
-    put8(part, c, K, x);
+    put_row8<WHOLE>(part, col(v), K, x);
     if constexpr (POST) {
       ap.get(m_ap, v, x);
-      put8(part + R.post * K, c, K, x);
+      put_row8<WHOLE>(part + R.post * K, col(v), K, x);
     }
   }
 }
@@ -370,44 +447,54 @@ hipError_t launch_fwd(const BlockNormParams& p, hipStream_t s) {
                  grid, block, s, p);
 }
 
-template <int V, class T>
+template <int V, class T, bool WHOLE>
 hipError_t launch_bwd(const BlockNormGradParams& p, int groups, hipStream_t s) {
   const dim3 grid(groups), block(threads_of(p.K, V));
   if (p.post != nullptr)
-    return enqueue(p.gate != nullptr ? block_norm_bwd_kernel<V, T, true, true>
-                                     : block_norm_bwd_kernel<V, T, true, false>,
+    return enqueue(p.gate != nullptr ? block_norm_bwd_kernel<V, T, true, true, WHOLE>
+                                     : block_norm_bwd_kernel<V, T, true, false, WHOLE>,
                    grid, block, s, p);
-  return enqueue(p.gate != nullptr ? block_norm_bwd_kernel<V, T, false, true>
-                                   : block_norm_bwd_kernel<V, T, false, false>,
+  return enqueue(p.gate != nullptr ? block_norm_bwd_kernel<V, T, false, true, WHOLE>
+                                   : block_norm_bwd_kernel<V, T, false, false, WHOLE>,
                  grid, block, s, p);
 }
 
+// Chunks per thread of the forward kernel.  Few rows: as few as possible, the
+// call is latency.  Many: workgroups of about four waves (8192 x 5120, two /
+// three / four chunks per thread: 77.9 / 67.8 / 69.8 us, 5.0 TB/s at best).
 template <class T>
 hipError_t launch_fwd_v(const BlockNormParams& p, hipStream_t s) {
   const int64_t chunks = (p.K + 7) / 8;
   const int64_t v = p.M < 512 ? (chunks + 1023) / 1024 : (chunks + 255) / 256;
   if (v <= 1) return launch_fwd<1, T>(p, s);
   if (v <= 2) return launch_fwd<2, T>(p, s);
+  if (v <= 3) return launch_fwd<3, T>(p, s);
   return launch_fwd<4, T>(p, s);
 }
 
-// Chunks per thread of the backward kernel: as few as a workgroup holds the
-// row with.
-int bwd_chunks(int64_t K) { return K <= 8 * kBwdThreads ? 1 : K <= 16 * kBwdThreads ? 2 : 4; }
+// Chunks per thread of the backward kernel: one, while a workgroup holds the row
+// so.
+int bwd_chunks(int64_t K) { return K <= 8 * bwd_threads<1>() ? 1 : 4; }
 
 template <class T>
 hipError_t launch_bwd_v(const BlockNormGradParams& p, int groups, hipStream_t s) {
-  const int v = bwd_chunks(p.K);
-  if (v == 1) return launch_bwd<1, T>(p, groups, s);
-  if (v == 2) return launch_bwd<2, T>(p, groups, s);
-  return launch_bwd<4, T>(p, groups, s);
+  const bool one = bwd_chunks(p.K) == 1;
+  if (p.K % 8 == 0)
+    return one ? launch_bwd<1, T, true>(p, groups, s) : launch_bwd<4, T, true>(p, groups, s);
+  return one ? launch_bwd<1, T, false>(p, groups, s) : launch_bwd<4, T, false>(p, groups, s);
 }
 
-// Workgroups of the backward kernel: two per compute unit.  More hide more of
-// a row's latency, but each writes its sums, which are then read once more.
-int bwd_groups(int64_t M) { return (int)(M < 512 ? M : 512); }
-
-int64_t per_group(int64_t M) { return ceil_div(M, bwd_groups(M)); }
+// Rows per workgroup of the backward kernel: one workgroup for each that the
+// compute units hold at once, two each up to K = 4096 (8 waves) and one past it.
+// Fewer rows each hide no more of a row's latency, and every workgroup writes
+// its sums, which are then read once more (us, both kernels, with 256 / 512 /
+// 1024 workgroups, post-norm and gate: 8192 x 512 50 / 33 / 38, 4096 x 2048 39 /
+// 31 / 39, 8192 x 4096 112 / 96 / 120 (768), 2048 x 8192 54 / 65 / 91, 2048 x
+// 13824 114 / 133 / 169).
+int64_t per_group(int64_t M, int64_t K) {
+  const int64_t groups = K <= 4096 ? 512 : 256;
+  return ceil_div(M, M < groups ? M : groups);
+}
 
 }  // namespace
 
@@ -424,7 +511,7 @@ bool block_norm_bwd_fits(int64_t M, int64_t K, int64_t gates) {
 }
 
 size_t block_norm_bwd_bytes(int64_t M, int64_t K, bool post, bool gate) {
-  const int64_t groups = ceil_div(M, per_group(M));
+  const int64_t groups = ceil_div(M, per_group(M, K));
   return (size_t)(groups * part_rows(post, gate).count * K) * sizeof(float);
 }
 
@@ -433,7 +520,7 @@ hipError_t launch_block_norm(const BlockNormParams& p, bool f32, hipStream_t s) 
 }
 
 hipError_t launch_block_norm_bwd(BlockNormGradParams p, bool f32, hipStream_t s) {
-  p.per_group = (int)per_group(p.M);
+  p.per_group = (int)per_group(p.M, p.K);
   const int groups = ceil_div(p.M, p.per_group);
   const hipError_t e =
       f32 ? launch_bwd_v<float>(p, groups, s) : launch_bwd_v<uint16_t>(p, groups, s);

@@ -2,6 +2,8 @@
 // over a workgroup: shared by the kernels that keep a row in registers.
 #pragma once
 
+#include <type_traits>
+
 #include "ffn.h"
 
 namespace tgemm {
@@ -93,15 +95,39 @@ struct Vec8<float> {
   typedef f32x8_any type;
 };
 
+// The sum over a wave, in every lane, without the LDS that shuffles go
+// through: within rows of 16 lanes, then across them to the last lane.
+__device__ __forceinline__ float wave_sum(float v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  auto moved = [](float x, auto ctrl, auto rows) __attribute__((always_inline)) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), decltype(ctrl)::value,
+                                                      decltype(rows)::value, 0xf, false));
+  };
+  using std::integral_constant;
+  v += moved(v, integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});  // row_shr 1
+  v += moved(v, integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});  // 2
+  v += moved(v, integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});  // 4
+  v += moved(v, integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});  // 8
+  v += moved(v, integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});  // row_bcast 15
+  v += moved(v, integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});  // row_bcast 31
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+#else
+  return v;
+#endif
+}
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
 // Sums of N values each over the workgroup, in wave order (the same in every
 // thread).  `buf`: LDS for the waves' sums, not to be in use by another wave:
 // callers in a loop alternate between two.
 template <int N, class T>
 __device__ __forceinline__ void group_sum(T (&v)[N], T (*buf)[N]) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], o, 64);
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
   const int waves = (int)blockDim.x >> 6;
   if (waves == 1) return;
   if ((threadIdx.x & 63) == 0) {
