@@ -581,9 +581,9 @@ TGEMM_API int tgemm_validate_linear(char transA, char transB, int64_t M, int64_t
  * products; dbias is the sum before that rounding, in fp32.  A, B as in the
  * forward call; Z and z_type as it left Z (or rounded to bf16 since), not read
  * for TGEMM_ACT_NONE.  relu's derivative is 0 at z = 0.  Workspace: dz (2 * M
- * * N bytes, padded), 4 * ceil(M / 64) * N bytes, and copies and partial
- * products as in tgemm_run_gated_backward, whose size limits hold with N for
- * 2F.
+ * * N bytes, padded), the bias's partial sums (up to 4 bytes for every 8
+ * elements of it), and copies and partial products as in
+ * tgemm_run_gated_backward, whose size limits hold with N for 2F.
  */
 TGEMM_API int tgemm_run_linear_backward(char transA, char transB, int64_t M, int64_t N, int64_t K,
                                         const void* A, int64_t lda, const void* B, int64_t ldb,

@@ -142,13 +142,22 @@ hipError_t launch_gated_grad(const uint16_t* dh, int64_t lddh, const void* gu, i
                              int rows, int64_t cols, hipStream_t s);
 
 // dz = dy act'(z), zero past column N and row M to cols (a multiple of 64) and
-// rows; z is not read for kActNone.  With part (fp32 [strips][N]) also db =
-// the column sums of dz (rows_finish.hip).
-int linear_grad_strips(int64_t rows);
+// rows; z is not read for kActNone.  With part (fp32 [strips][N], strips of
+// linear_grad_strip rows) also the strips' column sums of dz (rows_finish.hip).
+int linear_grad_strip(int64_t rows, int64_t cols);
 bool linear_grad_fits(int64_t rows, int64_t cols);
 hipError_t launch_linear_grad(const uint16_t* dy, int64_t lddy, const void* z, int64_t ldz,
                               bool z_f32, int M, int64_t N, int act, uint16_t* dz, int64_t lddz,
-                              int rows, int64_t cols, float* part, float* db, hipStream_t s);
+                              int rows, int64_t cols, float* part, hipStream_t s);
+
+// out[c] = the sum of part[0 .. rows - 1][c], in order: added by the launch of
+// the gradient products, where given.
+struct ColumnSum {
+  const float* part;  // null: none
+  int rows;
+  int64_t cols;
+  float* out;
+};
 
 // dX = G . W (px: A = G [M][K], B = W) and dW = G^T . X (pw: A = G stored
 // [K][M], B = X), both bf16, in one launch (gated_bwd.hip).  M, N, A, B, C,
@@ -158,9 +167,9 @@ hipError_t launch_linear_grad(const uint16_t* dy, int64_t lddy, const void* z, i
 // partials of a product with more than one chunk go to its ws, and a second
 // launch adds them.
 int gated_bwd_plan(GemmParams* px, GemmParams* pw);
-bool gated_bwd_fits(const GemmParams& px, const GemmParams& pw);
+bool gated_bwd_fits(const GemmParams& px, const GemmParams& pw, int64_t sum_cols);
 hipError_t launch_gated_bwd(int tile, const GemmParams& px, const GemmParams& pw, bool f32x,
-                            bool f32w, hipStream_t s);
+                            bool f32w, const ColumnSum& sum, hipStream_t s);
 
 // Rows to 8-bit codes with one scale each (row_quant.hip).  weight null:
 // codes of x itself; else of the RMS norm of x (+ residual, whose bf16 sum

@@ -326,12 +326,13 @@ int run_gated(char ta, char tb, int64_t M, int64_t F, int64_t K, const void* A, 
 // reads A and B as [M][K] and [N2][K] rows on 16-byte boundaries; others are
 // copied first.  dB stored [K][N2] is the product with the operands exchanged,
 // A^T . G; its first operand is then a zero-padded copy of A.
-// grad(G, ldg, rows, extra) enqueues the kernels that write G into the
-// workspace, zero-padded, with extra_bytes of their own there; grad_fits:
-// their grids are launchable.
+// grad(G, ldg, rows, part) enqueues the kernel that writes G into the
+// workspace, zero-padded, and where db is set the partial column sums [strips]
+// [N2], which the products' launch adds up there.
 struct GradSource {
-  size_t extra_bytes;
-  bool fits;
+  bool fits;    // its grid is launchable
+  float* db;
+  int strips;
 };
 
 template <class Grad>
@@ -370,16 +371,18 @@ int run_backward(const char* what, char ta, char tb, int64_t M, int64_t N2, int6
   const int tile = gated_bwd_plan(&px, &pw);
   PackRows ca = {A, lda, is_n(ta), (int)M, (int)K, nullptr, (int)rows, Kp};
   PackRows cb = {B, ldb, !is_n(tb), (int)N2, (int)K, nullptr, (int)N2, Kp};
-  if (!gated_bwd_fits(px, pw) || !src.fits || (packA && !pack_rows_fits(ca, 2)) ||
+  const bool sums = src.db != nullptr;
+  if (!gated_bwd_fits(px, pw, sums ? N2 : 0) || !src.fits || (packA && !pack_rows_fits(ca, 2)) ||
       (packB && !pack_rows_fits(cb, 2)))
     return TGEMM_ERR_UNSUPPORTED;
   const size_t bytesX =
       px.splitk > 1 ? round256((size_t)px.splitk * px.M * px.N * sizeof(float)) : 0;
   const size_t bytesW =
       pw.splitk > 1 ? round256((size_t)pw.splitk * pw.M * pw.N * sizeof(float)) : 0;
+  const size_t bytesS = sums ? (size_t)src.strips * N2 * sizeof(float) : 0;
   Workspace w;
   const int st =
-      take_workspace(space, s, bytesG + bytesA + bytesB + bytesX + bytesW + src.extra_bytes, &w);
+      take_workspace(space, s, bytesG + bytesA + bytesB + bytesX + bytesW + bytesS, &w);
   if (st != TGEMM_OK) return st;
   if (verbose())
     fprintf(stderr,
@@ -389,7 +392,9 @@ int run_backward(const char* what, char ta, char tb, int64_t M, int64_t N2, int6
   char* ws = static_cast<char*>(w.ptr);
   uint16_t* const G = reinterpret_cast<uint16_t*>(ws);
   ws += bytesG;
-  hipError_t e = grad(G, ldg, (int)rows, ws + bytesA + bytesB + bytesX + bytesW);
+  float* const part =
+      sums ? reinterpret_cast<float*>(ws + bytesA + bytesB + bytesX + bytesW) : nullptr;
+  hipError_t e = grad(G, ldg, (int)rows, part);
   const void *Ar = A, *Br = B;  // [M][K], [2F][K] rows
   if (packA && e == hipSuccess) {
     ca.out = ws;
@@ -414,7 +419,7 @@ int run_backward(const char* what, char ta, char tb, int64_t M, int64_t N2, int6
   pw.B = swap ? G : static_cast<const uint16_t*>(Ar);
   pw.ldb = swap ? ldg : lda;
   pw.ws = reinterpret_cast<float*>(ws + bytesX);
-  if (e == hipSuccess) e = launch_gated_bwd(tile, px, pw, false, f32, s);
+  if (e == hipSuccess) e = launch_gated_bwd(tile, px, pw, false, f32, {part, src.strips, N2, src.db}, s);
   release_workspace(w);
   return status_of(e);
 }
@@ -426,8 +431,8 @@ int run_gated_backward(char ta, char tb, int64_t M, int64_t F, int64_t K, const 
                        void* dB, int64_t lddb, bool f32, const CallSpace& space, hipStream_t s) {
   return run_backward(
       "gated", ta, tb, M, 2 * F, K, A, lda, B, ldb, dA, ldda, dB, lddb, f32,
-      {0, gated_grad_fits(round_up(M, 64), F)},
-      [&](uint16_t* G, int64_t ldg, int rows, char*) {
+      {gated_grad_fits(round_up(M, 64), F), nullptr, 0},
+      [&](uint16_t* G, int64_t ldg, int rows, float*) {
         return launch_gated_grad(static_cast<const uint16_t*>(dH), lddh, GU, ldgu, gu_f32, (int)M,
                                  F, act, G, ldg, rows, ldg, s);
       },
@@ -441,14 +446,12 @@ int run_linear_backward(char ta, char tb, int64_t M, int64_t N, int64_t K, const
                         void* dB, int64_t lddb, bool f32, float* db, const CallSpace& space,
                         hipStream_t s) {
   const int64_t rows = round_up(M, 64), cols = round_up(N, 64);
-  const size_t sums = db != nullptr ? (size_t)linear_grad_strips(rows) * N * sizeof(float) : 0;
   return run_backward(
       "linear", ta, tb, M, N, K, A, lda, B, ldb, dA, ldda, dB, lddb, f32,
-      {sums, linear_grad_fits(rows, cols)},
-      [&](uint16_t* G, int64_t ldg, int r, char* extra) {
+      {linear_grad_fits(rows, cols), db, ceil_div(rows, linear_grad_strip(rows, cols))},
+      [&](uint16_t* G, int64_t ldg, int r, float* part) {
         return launch_linear_grad(static_cast<const uint16_t*>(dY), lddy, Z, ldz, z_f32, (int)M, N,
-                                  act, G, ldg, r, ldg,
-                                  db != nullptr ? reinterpret_cast<float*>(extra) : nullptr, db, s);
+                                  act, G, ldg, r, ldg, part, s);
       },
       space, s);
 }

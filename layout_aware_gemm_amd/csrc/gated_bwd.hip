@@ -113,15 +113,35 @@ __device__ __forceinline__ void grad_tile(const GemmParams& p, int bid, bool f32
                   m0 + wm * (kT / 2), n0 + wn * (kT / 2), lane);
 }
 
+// 64 columns of a sum over rows: four groups of rows, added in order.
+__device__ __forceinline__ void column_sum(const ColumnSum& j, int b, float* s) {
+  const int l = (int)threadIdx.x & 63, g = (int)threadIdx.x >> 6;
+  const int64_t c = (int64_t)b * 64 + l;
+  const int per = (j.rows + 3) / 4, end = min(j.rows, (g + 1) * per);
+  float a = 0.f;
+  if (c < j.cols) {
+#pragma unroll 4
+    for (int i = g * per; i < end; ++i) a += j.part[i * j.cols + c];
+  }
+  s[g * 64 + l] = a;
+  __syncthreads();
+  if (g == 0 && c < j.cols) j.out[c] = s[l] + s[64 + l] + s[128 + l] + s[192 + l];
+}
+
 // Workgroups 0 .. nfirst - 1 (a multiple of 8, so that a product's tiles
 // keep their XCDs) take the product with the longer tiles, dW if wfirst.
-// f32x, f32w: the output types (K chunks are fp32).
+// f32x, f32w: the output types (K chunks are fp32).  The workgroups after the
+// products' ntiles take the column sums, in the compute units' last gaps.
 template <int kT>
 __global__ void __launch_bounds__(kThreads, kT == 128 ? 2 : 1) gated_bwd_kernel(GemmParams px, GemmParams pw,
                                                                 int nfirst, int wfirst, int f32x,
-                                                                int f32w) {
+                                                                int f32w, int ntiles, ColumnSum sum) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[5 * kT * kBK];
   const int b = blockIdx.x;
+  if (b >= ntiles) {
+    column_sum(sum, b - ntiles, reinterpret_cast<float*>(lds));
+    return;
+  }
   const bool w = (b < nfirst) == (wfirst != 0);
   const int l = b < nfirst ? b : b - nfirst;
   // (workgroups past a product's last tile are the padding to a multiple of 8)
@@ -222,18 +242,20 @@ namespace {
 int64_t grid_of(const GemmParams& p) { return (int64_t)p.tilesM * p.tilesN * p.splitk; }
 }  // namespace
 
-bool gated_bwd_fits(const GemmParams& px, const GemmParams& pw) {
-  return grid_of(px) + grid_of(pw) + 8 <= kMaxWorkgroups;
+bool gated_bwd_fits(const GemmParams& px, const GemmParams& pw, int64_t sum_cols) {
+  return grid_of(px) + grid_of(pw) + 8 + ceil_div(sum_cols, 64) <= kMaxWorkgroups;
 }
 
 hipError_t launch_gated_bwd(int tile, const GemmParams& px, const GemmParams& pw, bool f32x,
-                            bool f32w, hipStream_t s) {
+                            bool f32w, const ColumnSum& sum, hipStream_t s) {
   const int64_t nx = grid_of(px), nw = grid_of(pw);
   const int wfirst = pw.kchunk > px.kchunk;
   const int nfirst = (int)(((wfirst ? nw : nx) + 7) / 8 * 8);
-  const dim3 grid((unsigned)(nfirst + (wfirst ? nx : nw))), block(kThreads);
+  const int ntiles = (int)(nfirst + (wfirst ? nx : nw));
+  const int sums = sum.part != nullptr ? ceil_div(sum.cols, 64) : 0;
+  const dim3 grid((unsigned)(ntiles + sums)), block(kThreads);
   const hipError_t e = enqueue(tile == 128 ? gated_bwd_kernel<128> : gated_bwd_kernel<256>, grid,
-                               block, s, px, pw, nfirst, wfirst, f32x ? 1 : 0, f32w ? 1 : 0);
+                               block, s, px, pw, nfirst, wfirst, f32x ? 1 : 0, f32w ? 1 : 0, ntiles, sum);
   // Only a product of at most 341 tiles is split (its K is 1.5 shares or
   // more), so the sums' grid stays under 2^16 workgroups.
   SumJob jx, jw;

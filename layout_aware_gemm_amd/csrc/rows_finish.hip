@@ -215,17 +215,16 @@ __global__ void __launch_bounds__(kThr) gated_grad_kernel(
 
 // The linear product's dz = dy act'(z), rounded once to bf16, the type the
 // gradient products read, and the column sums of dz before that rounding.  A
-// workgroup takes 256 columns (8 per thread) of a strip of kStrip rows, eight
-// rows at a time; its sums over the strip meet in LDS, in row order, and a
-// second kernel adds the strips in order: nothing depends on timing.  Rows
-// M .. rows - 1 and columns N .. cols - 1 of dz are set to zero.
-constexpr int kStrip = 64;
-
+// workgroup takes 256 columns (8 per thread) of a strip of rows, eight rows at a
+// time; its sums over the strip meet in LDS, in row order, and workgroups of
+// the gradient products' launch (gated_bwd.hip) add the strips in order: nothing
+// depends on timing.  Rows M .. rows - 1 and columns N .. cols - 1 of dz are set
+// to zero.
 template <class T>  // the type of z
 __global__ void __launch_bounds__(kThr) linear_grad_kernel(
     const uint16_t* __restrict__ dy, int64_t lddy, const T* __restrict__ z, int64_t ldz, int M,
     int64_t N, int act, uint16_t* __restrict__ dz, int64_t lddz, int rows, int64_t cols,
-    float* __restrict__ part, int cblocks) {
+    float* __restrict__ part, int cblocks, int strip_rows) {
   __shared__ float sums[8][256 + 8];
   const int strip = (int)(blockIdx.x / cblocks);
   const int64_t c0 = (int64_t)(blockIdx.x % cblocks) * 256;
@@ -234,8 +233,8 @@ __global__ void __launch_bounds__(kThr) linear_grad_kernel(
   const int n = (int)min((int64_t)8, N - c);  // values this thread computes
   float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 2
-  for (int i = 0; i < kStrip; i += 8) {
-    const int row = strip * kStrip + i + rl;
+  for (int i = 0; i < strip_rows; i += 8) {
+    const int row = strip * strip_rows + i + rl;
     if (row >= rows || c >= cols) continue;
     float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (row < M) {
@@ -273,23 +272,6 @@ __global__ void __launch_bounds__(kThr) linear_grad_kernel(
 #pragma unroll
   for (int r = 0; r < 8; ++r) s += sums[r][threadIdx.x];
   if (c0 + (int)threadIdx.x < N) part[strip * N + c0 + (int)threadIdx.x] = s;
-}
-
-// Columns of part [strips][N] added up: 64 columns by 4 groups of strips per
-// workgroup, the groups in order.
-__global__ void __launch_bounds__(kThr) column_sum_kernel(const float* __restrict__ part,
-                                                          int strips, int64_t N,
-                                                          float* __restrict__ out) {
-  __shared__ float s[4][64];
-  const int l = (int)threadIdx.x & 63, g = (int)threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + l;
-  const int per = (strips + 3) / 4, end = min(strips, (g + 1) * per);
-  float a = 0.f;
-  if (c < N)
-    for (int i = g * per; i < end; ++i) a += part[i * N + c];
-  s[g][l] = a;
-  __syncthreads();
-  if (g == 0 && c < N) out[c] = s[0][l] + s[1][l] + s[2][l] + s[3][l];
 }
 
 int64_t finish_blocks(const RowsParams& p, bool gate) {
@@ -363,28 +345,31 @@ hipError_t launch_gated_grad(const uint16_t* dh, int64_t lddh, const void* gu, i
                  static_cast<const uint16_t*>(gu), ldgu, M, F, act, dgu, lddgu, cols, per_row);
 }
 
-int linear_grad_strips(int64_t rows) { return ceil_div(rows, kStrip); }
+// Rows per strip: 64, or fewer until there are two workgroups per compute unit
+// (333 x 1000: strips of 64 rows, 24 workgroups, 11.9 us).
+int linear_grad_strip(int64_t rows, int64_t cols) {
+  int strip = 64;
+  while (strip > 8 && (int64_t)ceil_div(rows, strip) * ceil_div(cols, 256) < 512) strip /= 2;
+  return strip;
+}
 
 bool linear_grad_fits(int64_t rows, int64_t cols) {
-  return (int64_t)linear_grad_strips(rows) * ceil_div(cols, 256) <= kMaxWorkgroups;
+  return (int64_t)ceil_div(rows, linear_grad_strip(rows, cols)) * ceil_div(cols, 256) <=
+         kMaxWorkgroups;
 }
 
 hipError_t launch_linear_grad(const uint16_t* dy, int64_t lddy, const void* z, int64_t ldz,
                               bool z_f32, int M, int64_t N, int act, uint16_t* dz, int64_t lddz,
-                              int rows, int64_t cols, float* part, float* db, hipStream_t s) {
-  const int strips = linear_grad_strips(rows), cblocks = ceil_div(cols, 256);
-  const dim3 grid((unsigned)((int64_t)strips * cblocks)), block(kThr);
-  hipError_t e;
+                              int rows, int64_t cols, float* part, hipStream_t s) {
+  const int strip = linear_grad_strip(rows, cols), cblocks = ceil_div(cols, 256);
+  const dim3 grid((unsigned)((int64_t)ceil_div(rows, strip) * cblocks)), block(kThr);
   if (z_f32)
-    e = enqueue(linear_grad_kernel<float>, grid, block, s, dy, lddy, static_cast<const float*>(z),
-                ldz, M, N, act, dz, lddz, rows, cols, part, cblocks);
-  else
-    e = enqueue(linear_grad_kernel<uint16_t>, grid, block, s, dy, lddy,
-                static_cast<const uint16_t*>(z), ldz, M, N, act, dz, lddz, rows, cols, part,
-                cblocks);
-  if (e != hipSuccess || part == nullptr) return e;
-  return enqueue(column_sum_kernel, dim3(ceil_div(N, 64)), block, s,
-                 static_cast<const float*>(part), strips, N, db);
+    return enqueue(linear_grad_kernel<float>, grid, block, s, dy, lddy,
+                   static_cast<const float*>(z), ldz, M, N, act, dz, lddz, rows, cols, part,
+                   cblocks, strip);
+  return enqueue(linear_grad_kernel<uint16_t>, grid, block, s, dy, lddy,
+                 static_cast<const uint16_t*>(z), ldz, M, N, act, dz, lddz, rows, cols, part,
+                 cblocks, strip);
 }
 
 }  // namespace tgemm

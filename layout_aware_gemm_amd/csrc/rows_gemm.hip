@@ -401,13 +401,29 @@ __device__ __forceinline__ void linear_epilogue(const RowsParams& p,
       }
     } else {
 #pragma unroll 1
-      for (int q = 0; q < NQ; ++q) {
-        const float4 v = *reinterpret_cast<const float4*>(src + q * RPI * LD);
-        if (row + q * RPI >= p.M || n <= 0) continue;
-        const float e[4] = {v.x, v.y, v.z, v.w};
-        float r[4];
-        linear_res4<false>(p, row + q * RPI, c, n, r);
-        linear_put4<false>(p, row + q * RPI, c, n, e, b, r);
+      for (int q = 0; q < NQ; q += U) {
+        float r[U][4];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int at = row + (q + u) * RPI;
+          linear_res4<false>(p, at, c, at < p.M ? n : 0, r[u]);
+        }
+#pragma unroll 1
+        for (int u = 0; u < U; ++u) {
+          const int at = row + (q + u) * RPI;
+          const float4 v = *reinterpret_cast<const float4*>(src + (q + u) * RPI * LD);
+          if (at >= p.M || n <= 0) continue;
+          const float e[4] = {v.x, v.y, v.z, v.w};
+          // (r[u], which only constants can index)
+          float ru[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            ru[i] = r[0][i];
+#pragma unroll
+            for (int k = 1; k < U; ++k) ru[i] = u == k ? r[k][i] : ru[i];
+          }
+          linear_put4<false>(p, at, c, n, e, b, ru);
+        }
       }
     }
     wave_lds_order();

@@ -572,6 +572,15 @@ def _act(act, known=_ACTS):
     return int(act)
 
 
+_PACKED = torch.contiguous_format
+
+
+def _like(x):
+    """An uninitialised tensor of x's shape and type, contiguous.  (Half the
+    time of torch.empty: a small call is host time.)"""
+    return torch.empty_like(x, memory_format=_PACKED)
+
+
 def _store(dtype, what):
     """The epilogue that stores ``dtype``."""
     if dtype == torch.bfloat16:
@@ -882,9 +891,9 @@ def linear(x, w, bias=None, act="none", residual=None, out_dtype=torch.bfloat16,
     a = _act(act, _LINEAR_ACTS)
     dev = _same_device(x, w, bias, residual)
     with _on(dev, stream):
-        y = torch.empty(shape, dtype=out_dtype, device=dev)
+        y = x.new_empty(shape, dtype=out_dtype)
         if save is not False:
-            z = torch.empty(shape, dtype=save, device=dev)
+            z = x.new_empty(shape, dtype=save)
         _call_ws("tgemm_run_linear", dev, ta, tb, M, N, K, _ptr(x2), lda, _ptr(w), ldb, _ptr(bias),
                  a, _ptr(r2), ldr, _ptr(y), N, epi, _ptr(z), N, zt)
     return y if z is None else (y, z)
@@ -914,9 +923,9 @@ def linear_backward(dy, x, w, z=None, act="none", bias=False, dw_dtype=torch.bfl
         z2, ldz = _rows(z, "z", z.dtype)
     dev = _same_device(dy, x, w, z2)
     with _on(dev, stream):
-        dx = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
-        dw = torch.empty((N, K) if tb == b"T" else (K, N), dtype=dw_dtype, device=dev)
-        db = torch.empty(N, dtype=torch.float32, device=dev) if bias else None
+        dx = _like(x)
+        dw = x.new_empty((N, K) if tb == b"T" else (K, N), dtype=dw_dtype)
+        db = x.new_empty(N, dtype=torch.float32) if bias else None
         _call_ws("tgemm_run_linear_backward", dev, ta, tb, M, N, K, _ptr(x2), lda, _ptr(w), ldb,
                  _ptr(d2), ldd, _ptr(z2), ldz, zt, a, _ptr(dx), K, _ptr(dw), dw.shape[1], epi,
                  _ptr(db), sure=True)
@@ -930,10 +939,13 @@ def _gate(gate, M, K):
     """(gate rows, row stride) of a gate [K] or [G, K], G a divisor of M."""
     if gate is None:
         return 0, 0
-    g2 = gate.view(1, -1) if gate.dim() == 1 else gate
-    if g2.dim() != 2 or g2.shape[1] != K or g2.shape[0] < 1 or M % g2.shape[0]:
+    if gate.dim() == 1 and gate.dtype == torch.bfloat16:
+        _vector(gate, K, "gate", torch.bfloat16)
+        return 1, K
+    if gate.dim() not in (1, 2) or gate.shape[-1] != K or \
+            (gate.dim() == 2 and (gate.shape[0] < 1 or M % gate.shape[0])):
         raise ValueError("gate must be [K] or [G, K], G a divisor of the rows")
-    return g2.shape[0], _rows(g2, "gate", torch.bfloat16)[1]
+    return gate.shape[0], _rows(gate, "gate", torch.bfloat16)[1]
 
 
 def _norm_operands(y, residual, weight, post_weight, gate):
@@ -969,12 +981,14 @@ def block_norm(y, residual, weight, post_weight=None, gate=None, scale=1.0, eps=
     dev = _same_device(y, residual, weight, post_weight, gate, out_residual)
     with _on(dev, stream):
         if out_residual is None:
-            out_residual = torch.empty(y.shape, dtype=residual.dtype, device=dev)
-        if out_residual.shape != y.shape:
-            raise ValueError("y and out_residual differ in shape")
-        s2, lds = _rows(out_residual, "out_residual", residual.dtype)
-        n = torch.empty(y.shape, dtype=torch.bfloat16, device=dev)
-        rstd = (torch.empty(1 if post_weight is None else 2, M, dtype=torch.float32, device=dev)
+            s2 = out_residual = _like(residual)
+            lds = K
+        else:
+            if out_residual.shape != y.shape:
+                raise ValueError("y and out_residual differ in shape")
+            s2, lds = _rows(out_residual, "out_residual", residual.dtype)
+        n = _like(y)
+        rstd = (y.new_empty((1 if post_weight is None else 2, M), dtype=torch.float32)
                 if save else None)
         _call("tgemm_block_norm", dev, _ptr(y2), ldy, _ptr(r2), ldr, st, _ptr(post_weight),
               _ptr(gate), ldg, G, float(scale), _ptr(weight), float(eps), M, K, _ptr(s2), lds,
@@ -999,14 +1013,12 @@ def block_norm_backward(dn, y, residual, rstd, weight, post_weight=None, gate=No
         raise ValueError("rstd must be the contiguous fp32 tensor that block_norm saved")
     dev = _same_device(dn, y, residual, rstd, weight, post_weight, gate, ds)
     with _on(dev, stream):
-        f32 = {"dtype": torch.float32, "device": dev}
-        dh = torch.empty(y.shape, dtype=residual.dtype, device=dev)
-        dy = torch.empty(y.shape, dtype=torch.bfloat16, device=dev)
-        dw = torch.empty(K, **f32)
-        dp = torch.empty(K, **f32) if post else None
-        dg = torch.empty(gate.shape, **f32) if G else None
+        dh, dy = _like(residual), _like(y)
+        dw = rstd.new_empty(K)
+        dp = rstd.new_empty(K) if post else None
+        dg = rstd.new_empty(gate.shape) if G else None
         need = lib().tgemm_block_norm_backward_workspace_bytes(M, K, post, G)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
+        ws = rstd.new_empty(need // 4) if need > 0 else None
         _call("tgemm_block_norm_backward", dev, _ptr(d2), ldd, _ptr(s2), lds, _ptr(y2), ldy,
               _ptr(r2), ldr, st, _ptr(post_weight), _ptr(gate), ldg, G, float(scale), _ptr(weight),
               _ptr(rstd), M, K, _ptr(dh), K, _ptr(dy), K, _ptr(dw), _ptr(dp), _ptr(dg), _ptr(ws),
@@ -1046,9 +1058,9 @@ def _run_moe(x, router, ids, weights, w_gate_up, w_down, top, act, renormalize, 
             raise ValueError("router must be [K, E]")
         rt = _store(router.dtype, "router")
         r2, ldr = _rows(router.t(), "router (stored [E, K])", router.dtype)
-    y = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
+    y = _like(x)
     need = lib().tgemm_moe_workspace_bytes(M, K, F, E, top, 0 if router is None else 1)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
+    ws = x.new_empty((need + 1) // 2) if need > 0 else None
     _call("tgemm_run_moe", dev, M, K, F, E, top, _ptr(x2), ldx, _ptr(r2), ldr, rt,
           1 if renormalize else 0, float(scale), _ptr(ids), _ptr(weights), _ptr(w_gate_up), ld1, s1,
           _ptr(w_down), ld2, s2, _act(act), _ptr(y), K, _ptr(ws), max(need, 0))
@@ -1070,8 +1082,8 @@ def moe(x, router, w_gate_up, w_down, top_k, act="silu", renormalize=True, scale
     """
     dev = _same_device(x, router, w_gate_up, w_down)
     with _on(dev, stream):
-        ids = torch.empty(x.shape[:-1] + (top_k,), dtype=torch.int32, device=dev)
-        p = torch.empty(ids.shape, dtype=torch.float32, device=dev)
+        ids = x.new_empty(x.shape[:-1] + (top_k,), dtype=torch.int32)
+        p = x.new_empty(x.shape[:-1] + (top_k,), dtype=torch.float32)
         y = _run_moe(x, router, ids, p, w_gate_up, w_down, top_k, act, renormalize, scale, dev)
     return (y, ids, p) if routing else y
 
