@@ -45,28 +45,58 @@ __device__ __forceinline__ f32x4_t mma16(const i32x4_t& a, const i32x4_t& b, con
 
 // ---- routing -----------------------------------------------------------------
 
-template <class R>
+// A wave's sums of T = 1 or 8 values per lane; lane l returns that of value
+// l * T / 64.  (Eight values: each exchange halves what a lane still holds.)
+template <int T>
+__device__ __forceinline__ double wave_sums(double (&s)[T]) {
+  const int lane = threadIdx.x & 63;
+  double v = s[0];
+  if constexpr (T == 8) {
+    double h[4], q[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool up = (lane & 32) != 0;
+      h[i] = (up ? s[4 + i] : s[i]) + __shfl_xor(up ? s[i] : s[4 + i], 32, 64);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool up = (lane & 16) != 0;
+      q[i] = (up ? h[2 + i] : h[i]) + __shfl_xor(up ? h[i] : h[2 + i], 16, 64);
+    }
+    const bool up = (lane & 8) != 0;
+    v = (up ? q[1] : q[0]) + __shfl_xor(up ? q[0] : q[1], 8, 64);
+  }
+#pragma unroll
+  for (int o = 32 / T; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// T = 1 or 8 tokens per workgroup.
+template <class R, int T>
 __global__ void __launch_bounds__(256) moe_logits_kernel(MoeParams p) {
-  __shared__ double buf[16][8];
-  const int e = blockIdx.x, t0 = (int)blockIdx.y * 8;
+  __shared__ double buf[4][T];
+  const int e = blockIdx.x, t0 = (int)blockIdx.y * T;
   const R* const r = static_cast<const R*>(p.router) + (int64_t)e * p.ldr;
-  double s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  double s[T];
+#pragma unroll
+  for (int t = 0; t < T; ++t) s[t] = 0.0;
   for (int64_t c = (int64_t)threadIdx.x * 8; c < p.K; c += 2048) {
     const typename Vec8<R>::type w = load8(r, c, p.K);
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
+    for (int t = 0; t < T; ++t) {
       if (t0 + t >= p.M) break;
       const u16x8_any x = load8(p.x + (int64_t)(t0 + t) * p.ldx, c, p.K);
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[t] = fma((double)value(x, i), (double)value(w, i), s[t]);
     }
   }
-  group_sum(s, buf);
-  if (threadIdx.x == 0) {
-#pragma unroll
-    for (int t = 0; t < 8; ++t)
-      if (t0 + t < p.M) p.logits[(int64_t)(t0 + t) * p.E + e] = s[t];
-  }
+  const double v = wave_sums<T>(s);
+  const int lane = threadIdx.x & 63, t = lane * T / 64;
+  if ((lane & (64 / T - 1)) == 0) buf[threadIdx.x >> 6][t] = v;
+  __syncthreads();
+  const int i = threadIdx.x;
+  if (i < T && t0 + i < p.M)
+    p.logits[(int64_t)(t0 + i) * p.E + e] = ((buf[0][i] + buf[1][i]) + buf[2][i]) + buf[3][i];
 }
 
 // Ordered like the logits, NaN above all.
@@ -76,6 +106,11 @@ __device__ __forceinline__ uint64_t logit_key(double l) {
   // (-0 is +0)
   if (b == 0x8000000000000000ull) return 0x8000000000000000ull;
   return b >> 63 ? ~b : b | 0x8000000000000000ull;
+}
+
+// The logit of a key (a NaN for every NaN, 0 for -0).
+__device__ __forceinline__ double key_logit(uint64_t k) {
+  return __longlong_as_double((long long)(k >> 63 ? k ^ 0x8000000000000000ull : ~k));
 }
 
 // One workgroup per token, one thread per expert.
@@ -161,44 +196,77 @@ struct ChunkRows {
   }
 };
 
-// The experts' numbers as the workgroups of the products count them: with
-// fewer choices than experts, slot s stands for the expert of choice s, and
-// is idle if an earlier choice has the same; else for expert s.
-__device__ __forceinline__ int slot_expert(const MoeParams& p, int slot) {
-  const int A = p.M * p.top;
-  return A < p.E ? p.ids[slot] : slot;
-}
-
 // ---- gate and up -------------------------------------------------------------
 
-// TB groups of 8 tokens at a time, 16 NO outputs, W waves.
-template <int TB, int NO, int W, bool AL, bool NT>
+// The choice of up to kRouteSmall experts' logits (all tokens together) by the
+// workgroup itself, in the place of moe_choose_kernel: ids into LDS, and by one
+// workgroup, with the weights, into memory.
+constexpr int kRouteSmall = 1024;
+
+struct SmallRoute {
+  __attribute__((aligned(16))) uint64_t key[kRouteSmall];
+  double chosen[8 * kMoeTop];
+  int ids[8 * kMoeTop];
+};
+
+__device__ __forceinline__ void choose_here(const MoeParams& p, SmallRoute& r, int threads,
+                                            bool write) {
+  const int n = p.M * p.E, A = p.M * p.top;
+  for (int i = threadIdx.x; i < n; i += threads) r.key[i] = logit_key(p.logits[i]);
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += threads) {
+    const int t = i / p.E, e = i - t * p.E;
+    const uint64_t mine = r.key[i];
+    const uint64_t* const row = r.key + t * p.E;
+    int rank = 0;
+#pragma unroll 8
+    for (int j = 0; j < p.E; ++j) rank += (row[j] > mine || (row[j] == mine && j < e)) ? 1 : 0;
+    if (rank < p.top) {
+      r.ids[t * p.top + rank] = e;
+      r.chosen[t * p.top + rank] = key_logit(mine);
+    }
+  }
+  __syncthreads();
+  if (!write) return;
+  for (int a = threadIdx.x; a < A; a += threads) {
+    const int t = a / p.top;
+    const double top = r.chosen[t * p.top];
+    float total = 0.f;
+    if (p.renormalize)
+      for (int j = 0; j < p.top; ++j) total += expf((float)(r.chosen[t * p.top + j] - top));
+    else
+      for (int j = 0; j < p.E; ++j) total += expf((float)(key_logit(r.key[t * p.E + j]) - top));
+    p.ids[a] = r.ids[a];
+    p.weights[a] = p.scale * (expf((float)(r.chosen[a] - top)) / total);
+  }
+}
+
+// With fewer choices than experts, blockIdx.y stands for the expert of that
+// choice, and the workgroup is idle if an earlier choice has the same; else for
+// that expert.  TB groups of 8 tokens at a time, 16 outputs, W waves.  ROUTE: the
+// workgroup makes the choice itself.
+template <int TB, int W, bool ROUTE, bool AL, bool NT>
 __global__ void __launch_bounds__(W * 64) moe_up_kernel(MoeParams p) {
-  constexpr int NB = 2 * NO, MB = (TB + 1) / 2;
+  constexpr int NB = 2, MB = (TB + 1) / 2;  // blocks of 16 weight rows: gate, up
   constexpr int ROWS = NB * 16 + TB * 8, STAGE = ROWS * 8, RED = NB * MB * 64;
   __shared__ i32x4_t lds[W * (STAGE > RED ? STAGE : RED)];
   __shared__ uint16_t list[kMoeAssign];
   __shared__ int s_n, s_first;
+  static_assert(!ROUTE || sizeof(SmallRoute) <= sizeof(lds), "the choice fits");
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int slot = blockIdx.y, A = p.M * p.top;
-  const int e = __builtin_amdgcn_readfirstlane(slot_expert(p, slot));
-  if (e < 0 || e >= p.E) return;
-  if (threadIdx.x == 0) s_n = 0, s_first = A;
-  __syncthreads();
-  // this expert's choices (their order decides nothing: each token's sums are
-  // its own)
-  for (int a = threadIdx.x; a < A; a += W * 64) {
-    if (p.ids[a] != e) continue;
-    list[atomicAdd(&s_n, 1)] = (uint16_t)a;
-    atomicMin(&s_first, a);
+  const int32_t* ids = p.ids;
+  if constexpr (ROUTE) {
+    SmallRoute& r = *reinterpret_cast<SmallRoute*>(lds);
+    choose_here(p, r, W * 64, blockIdx.x == 0 && slot == 0);
+    ids = r.ids;
   }
-  __syncthreads();
-  const int n = __builtin_amdgcn_readfirstlane(s_n);
-  if (n == 0 || (A < p.E && s_first != slot)) return;
+  const int e = __builtin_amdgcn_readfirstlane(A < p.E ? ids[slot] : slot);
+  if (e < 0 || e >= p.E) return;
 
-  const int n0 = blockIdx.x * 16 * NO;
+  const int n0 = blockIdx.x * 16;
   const int kb = (int)p.K * 2, steps = (kb + kStep - 1) / kStep;
   const int lc = lane & 7, lr = lane >> 3;
   const char* const w1 = reinterpret_cast<const char*>(p.w1 + (int64_t)e * p.sw1);
@@ -210,10 +278,31 @@ __global__ void __launch_bounds__(W * 64) moe_up_kernel(MoeParams p) {
   rw[0].init(w1 + (int64_t)b0 * ld, kb);
   rw[1].init(w1 + ((int64_t)p.F + b0) * ld, kb);
   rx.init(reinterpret_cast<const char*>(p.x), kb);
-  uint32_t woff[2 * NO];
+  uint32_t woff[2];
 #pragma unroll
-  for (int b = 0; b < 2 * NO; ++b)
-    woff[b] = (uint32_t)((min(n0 + b * 8 + lr, p.F - 1) - b0) * ld);
+  for (int b = 0; b < 2; ++b) woff[b] = (uint32_t)((min(n0 + b * 8 + lr, p.F - 1) - b0) * ld);
+  i32x4_t wv[2 * NB], av[TB];
+  auto load_w = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int b = 0; b < 2 * NB; ++b) wv[b] = rw[b / 2].load(woff[b % 2], s * kStep + lc * 16);
+  };
+  // a single token's workgroups all have work: the weight's first steps need
+  // not wait for the list
+  const bool early = p.M == 1 && wave < steps;
+  if (early) load_w(wave);
+
+  if (threadIdx.x == 0) s_n = 0, s_first = A;
+  __syncthreads();
+  // this expert's choices (their order decides nothing: each token's sums are
+  // its own)
+  for (int a = threadIdx.x; a < A; a += W * 64) {
+    if (ids[a] != e) continue;
+    list[atomicAdd(&s_n, 1)] = (uint16_t)a;
+    atomicMin(&s_first, a);
+  }
+  __syncthreads();
+  const int n = __builtin_amdgcn_readfirstlane(s_n);
+  if (n == 0 || (A < p.E && s_first != slot)) return;
 
   // staged row R holds its chunk c at c ^ swz(R)
   i32x4_t* const st = lds + wave * STAGE;
@@ -240,16 +329,15 @@ __global__ void __launch_bounds__(W * 64) moe_up_kernel(MoeParams p) {
 #pragma unroll
     for (int t = 0; t < TB; ++t)
       aoff[t] = (uint32_t)((list[min(t0 + t * 8 + lr, n - 1)] / p.top) * ((int)p.ldx * 2));
-    i32x4_t wv[2 * NB], av[TB];
-    auto load = [&](int s) __attribute__((always_inline)) {
-      const int k = s * kStep + lc * 16;
-#pragma unroll
-      for (int b = 0; b < 2 * NB; ++b) wv[b] = rw[b / (2 * NO)].load(woff[b % (2 * NO)], k);
+    auto load_x = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
       for (int t = 0; t < TB; ++t)
-        if (t < tb) av[t] = rx.load(aoff[t], k);
+        if (t < tb) av[t] = rx.load(aoff[t], s * kStep + lc * 16);
     };
-    if (wave < steps) load(wave);
+    if (wave < steps) {
+      if (t0 > 0 || !early) load_w(wave);
+      load_x(wave);
+    }
     for (int s = wave; s < steps; s += W) {
 #pragma unroll
       for (int b = 0; b < 2 * NB; ++b) st[b * 64 + wr[b & 1]] = wv[b];
@@ -257,7 +345,10 @@ __global__ void __launch_bounds__(W * 64) moe_up_kernel(MoeParams p) {
       for (int t = 0; t < TB; ++t)
         if (t < tb) st[NB * 128 + t * 64 + wr[t & 1]] = av[t];
       wave_lds_order();
-      if (s + W < steps) load(s + W);
+      if (s + W < steps) {
+        load_w(s + W);
+        load_x(s + W);
+      }
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         i32x4_t wf[NB];
@@ -280,19 +371,17 @@ __global__ void __launch_bounds__(W * 64) moe_up_kernel(MoeParams p) {
 #pragma unroll
       for (int b = 0; b < NB; ++b) red[wave * RED + (m * NB + b) * 64 + lane] = acc[m][b];
     __syncthreads();
-    for (int t = threadIdx.x; t < MB * NO * 64; t += W * 64) {
-      const int l = t & 63, q = t >> 6;
-      const int m = q / NO, b = q % NO;
+    for (int t = threadIdx.x; t < MB * 64; t += W * 64) {
+      const int l = t & 63, m = t >> 6;
       const int col = m * 16 + (l & 15);  // which of the tokens
       if (t0 + col >= n || (TB == 1 && col >= 8)) continue;
-      f32x4_t a = red[(m * NB + b) * 64 + l], u = red[(m * NB + NO + b) * 64 + l];
+      f32x4_t a = red[m * NB * 64 + l], u = red[(m * NB + 1) * 64 + l];
 #pragma unroll
       for (int w = 1; w < W; ++w) {
-        a += red[w * RED + (m * NB + b) * 64 + l];
-        u += red[w * RED + (m * NB + NO + b) * 64 + l];
+        a += red[w * RED + m * NB * 64 + l];
+        u += red[w * RED + (m * NB + 1) * 64 + l];
       }
-      const int c0 = n0 + b * 16 + 4 * (l >> 4);
-      if (c0 >= p.ldh) continue;
+      const int c0 = n0 + 4 * (l >> 4);
       float v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = c0 + i < p.F ? act_times(a[i], u[i], p.act) : 0.f;
@@ -499,27 +588,47 @@ __global__ void __launch_bounds__(256) moe_add_kernel(MoeParams p, int shares, i
 
 int slots_of(const MoeParams& p) { return p.M * p.top < p.E ? p.M * p.top : p.E; }
 
+// The down product of few weights (48 MB) for up to 8 tokens runs on workgroups
+// of 16 waves and one share of the experts where that gives 128 workgroups:
+// what half the compute units lose is less than a launch to add shares (8
+// experts 2048 x 1024: 11.5 us whole; 8 waves 16.1 whole, in 4 shares 9.4 and
+// 3.3 for the sums).
+bool down_small(const MoeParams& p) {
+  return p.M <= 8 && (int64_t)slots_of(p) * p.F * p.K * 2 <= int64_t(48) << 20;
+}
+
 // Shares of the experts in the down product: enough workgroups of 16 columns
-// for two per compute unit.
+// for two per compute unit (128 experts 2048 x 768, 64 tokens, 1 / 2 / 4 / 8
+// shares: 161 / 94 / 68 / 75 us).
 int shares_of(const MoeParams& p) {
-  const int blocks = ceil_div(p.K, 16), want = ceil_div(512, blocks), slots = slots_of(p);
+  const int blocks = ceil_div(p.K, 16), slots = slots_of(p);
+  const int want = ceil_div(down_small(p) ? 128 : 512, blocks);
   return want < slots ? want : slots;
+}
+
+// The up product's workgroups make the choice of experts themselves where there
+// are few logits, and few workgroups to repeat it.
+bool routes_in_up(const MoeParams& p) {
+  return p.router != nullptr && p.M <= 8 && p.M * p.E <= kRouteSmall &&
+         p.ldh / 16 * slots_of(p) <= 1024;
 }
 
 template <int TB, int W, bool AL, bool NT>
 hipError_t launch_up(const MoeParams& p, hipStream_t s) {
-  const dim3 block(W * 64);
-  const int slots = slots_of(p);
-  return enqueue(moe_up_kernel<TB, 1, W, AL, NT>, dim3((unsigned)(p.ldh / 16), slots), block, s, p);
+  const dim3 grid((unsigned)(p.ldh / 16), slots_of(p)), block(W * 64);
+  if constexpr (TB == 1) {
+    if (routes_in_up(p)) return enqueue(moe_up_kernel<TB, W, true, AL, NT>, grid, block, s, p);
+  }
+  return enqueue(moe_up_kernel<TB, W, false, AL, NT>, grid, block, s, p);
 }
 
-template <int TB, int TMAX, bool AL, bool NT>
+template <int TB, int TMAX, int W, bool AL, bool NT>
 hipError_t launch_down(MoeParams p, hipStream_t s) {
-  constexpr int W = 8;
   const int steps = ceil_div((int64_t)p.F * 2, kStep), shares = shares_of(p);
-  // runs of up to 8 K steps, fewer where they would not go round the waves
+  // runs of up to 8 K steps, fewer where they would not go round the waves, and
+  // even ones: a wave takes every W-th (12 steps as 8 + 4 74 us, as 6 + 6 68)
   const int even = ceil_div((int64_t)slots_of(p) * steps, shares * W);
-  p.run = even < 8 ? even : 8;
+  p.run = ceil_div(steps, ceil_div(steps, even < 8 ? even : 8));
   const dim3 grid(ceil_div(p.K, 16), shares), block(W * 64);
   return enqueue(moe_down_kernel<TB, TMAX, W, AL, NT>, grid, block, s, p);
 }
@@ -529,12 +638,24 @@ hipError_t launch_products(const MoeParams& p, hipStream_t s) {
   // Tokens at a time: an expert with more than that reads its weights again
   // (from the cache), so a few experts that are hit often do not decide.
   const bool few = p.M <= 8, many = (int64_t)p.M * p.top > (int64_t)12 * p.E;
-  hipError_t e = few ? launch_up<1, 8, AL, NT>(p, s)
-                     : many ? launch_up<8, 4, AL, NT>(p, s) : launch_up<2, 8, AL, NT>(p, s);
+  // Waves per workgroup of the up product: four for up to 32 K steps, which
+  // have less to add up (2048 x 768, 64 tokens of 128 experts: 8 / 4 waves 136 /
+  // 128 us; 4096 x 13824, 13 tokens of 8 experts: 266 / 276).
+  const bool narrow = p.K <= 32 * kStep / 2;
+  hipError_t e;
+  if (few)
+    e = narrow ? launch_up<1, 4, AL, NT>(p, s) : launch_up<1, 8, AL, NT>(p, s);
+  else if (many)
+    e = launch_up<8, 4, AL, NT>(p, s);
+  else
+    e = narrow ? launch_up<2, 4, AL, NT>(p, s) : launch_up<2, 8, AL, NT>(p, s);
   if (e != hipSuccess) return e;
-  e = few ? launch_down<1, 16, AL, NT>(p, s)
-          : p.M <= 16 ? launch_down<2, 16, AL, NT>(p, s)
-                      : many ? launch_down<8, 64, AL, NT>(p, s) : launch_down<2, 64, AL, NT>(p, s);
+  if (few)
+    e = down_small(p) ? launch_down<1, 16, 16, AL, NT>(p, s) : launch_down<1, 16, 8, AL, NT>(p, s);
+  else if (p.M <= 16)
+    e = launch_down<2, 16, 8, AL, NT>(p, s);
+  else
+    e = many ? launch_down<8, 64, 8, AL, NT>(p, s) : launch_down<2, 64, 8, AL, NT>(p, s);
   const int shares = shares_of(p);
   if (e != hipSuccess || shares == 1) return e;
   const int per_row = ceil_div(p.K, 1024);
@@ -558,10 +679,15 @@ MoeSpace moe_space(const MoeParams& p) {
 
 hipError_t launch_moe(const MoeParams& p, hipStream_t s) {
   if (p.router != nullptr) {
-    const dim3 grid(p.E, ceil_div(p.M, 8));
-    hipError_t e = enqueue(p.router_f32 ? moe_logits_kernel<float> : moe_logits_kernel<uint16_t>,
-                           grid, dim3(256), s, p);
-    if (e == hipSuccess)
+    const bool one = p.M == 1;
+    const dim3 grid(p.E, one ? 1 : ceil_div(p.M, 8)), block(256);
+    hipError_t e =
+        p.router_f32
+            ? enqueue(one ? moe_logits_kernel<float, 1> : moe_logits_kernel<float, 8>, grid, block,
+                      s, p)
+            : enqueue(one ? moe_logits_kernel<uint16_t, 1> : moe_logits_kernel<uint16_t, 8>, grid,
+                      block, s, p);
+    if (e == hipSuccess && !routes_in_up(p))
       e = enqueue(moe_choose_kernel, dim3(p.M), dim3(ceil_div(p.E, 64) * 64), s, p);
     if (e != hipSuccess) return e;
   }
