@@ -686,8 +686,9 @@ TGEMM_API int tgemm_validate_block_norm_backward(
  * ---- Mixture-of-experts layers for few tokens -----------------------------
  *
  *   Y[m] = sum_j weights[m, j] * H[m, j] . W2[ids[m, j]]^T          bf16 [M, K]
- *   H[m, j] = bf16(act(g) * u),  [g | u] = X[m] . W1[ids[m, j]]^T
- * with fp32 sums: `top` of E gated experts for each token.  With a router the
+ *   H[m, j] = act(g) * u,  [g | u] = X[m] . W1[ids[m, j]]^T
+ * with fp32 sums, and H in 16 bits of mantissa (the sum of two bf16 values):
+ * `top` of E gated experts for each token.  With a router the
  * call chooses them: the top largest of the logits X[m] . router^T (sums in 64
  * bits, so that the choice depends on no order of summation; the lowest index
  * first among equals; NaN counts as largest), with the weights

@@ -272,8 +272,8 @@ struct MoeParams {
   int act;
   uint16_t* y;        // [M][ldy]
   int64_t ldy;
-  // workspace: 64-bit logits [M][E], h [M * top][ldh] (ldh a multiple of 64),
-  // the shares' sums [shares][M][K]
+  // workspace: 64-bit logits [M][E], h [2][M * top][ldh] (its two parts; ldh a
+  // multiple of 64), each choice's row [M * top][K]
   double* logits;
   uint16_t* h;
   int64_t ldh;

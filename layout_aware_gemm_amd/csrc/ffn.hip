@@ -265,10 +265,14 @@ int run_bf16(char ta, char tb, int64_t K, const void* A, int64_t lda, const void
   // (the stride of a single row is never used)
   if (is_n(ta) && p.M == 1) lda = Kp;
   if (!is_n(tb) && p.N == 1) ldb = Kp;
-  const bool packA = !is_n(ta) || !rows_aligned(A, 2 * lda, 2 * K) || !stride_fits(2 * lda);
-  const bool packB = is_n(tb) || !rows_aligned(B, 2 * ldb, 2 * K) || !stride_fits(2 * ldb);
+  // (a linear product of few rows reads rows of any alignment, if the weight is
+  // K-contiguous)
+  const bool any = !gate && p.M <= kSkinnyRows && !is_n(tb) && stride_fits(2 * ldb);
+  const bool packA =
+      !is_n(ta) || !(any || rows_aligned(A, 2 * lda, 2 * K)) || !stride_fits(2 * lda);
+  const bool packB = is_n(tb) || !(any || rows_aligned(B, 2 * ldb, 2 * K)) || !stride_fits(2 * ldb);
   if ((packA || packB) && !stride_fits(2 * Kp)) return TGEMM_ERR_UNSUPPORTED;
-  p.K = (int)(2 * Kp);
+  p.K = (int)(2 * (any ? K : Kp));
   const RowsPlan r = plan_rows(&p, gate, epi == kRowsLinear);
   PackRows ca = {A, lda, is_n(ta), p.M, (int)K, nullptr, p.M, Kp};
   PackRows cb = {B, ldb, !is_n(tb), p.N, (int)K, nullptr, p.N, Kp};
@@ -461,7 +465,13 @@ int run_linear_backward(char ta, char tb, int64_t M, int64_t N, int64_t K, const
 int run_moe(MoeParams p, int64_t M, const CallSpace& space, hipStream_t s) {
   p.ldh = round_up(p.F, 64);
   p.M = (int)(M < kMoeTokens ? M : kMoeTokens);
-  const MoeSpace need = moe_space(p);
+  MoeSpace need = moe_space(p);
+  if (M > kMoeTokens && M % kMoeTokens != 0) {  // (the last rows, which may run otherwise)
+    p.M = (int)(M % kMoeTokens);
+    const MoeSpace last = moe_space(p);
+    need = {need.logits > last.logits ? need.logits : last.logits, need.h > last.h ? need.h : last.h,
+            need.part > last.part ? need.part : last.part};
+  }
   const size_t bytesL = round256(need.logits), bytesH = round256(need.h);
   Workspace w;
   const int st = take_workspace(space, s, bytesL + bytesH + need.part, &w);

@@ -15,12 +15,20 @@
 // The products are those of the few-row kernel (rows_skinny.hip): the weight's
 // rows take the matrix instruction's row side, the tokens its columns; a wave
 // loads whole 128-byte runs of its rows and turns them around in LDS words of
-// its own.  Gate and up: a workgroup takes 16 or 32 outputs of one expert, its
-// waves share the K steps.  Down: a workgroup takes 16 columns of y and goes
-// through the experts, each wave through runs of K steps of its own; a token's
-// sums collect in LDS words of the wave, and the waves' sums are added in
-// order.  Few columns: the experts are split over workgroups, and a last
-// kernel adds their sums.  Nothing depends on timing.
+// its own.  A workgroup takes 16 outputs of one expert (gate and up) or 32 to 64
+// columns (down), its waves share the K steps, their sums meet in LDS in wave
+// order, and a last kernel adds a token's choices by their weights, in order.
+// Nothing depends on timing.
+//
+// h = act(g) u is kept as the sum of two bf16 values, 16 bits in all: rounded to
+// one it would be half of y's error.  The matrix instruction's 16 columns hold
+// eight tokens' high and low parts, so that for up to 8 tokens the second part
+// is free, and the weights are read once in any case.
+//
+// Measured (MI355X): 13 tokens on 2 of 8 experts 4096 x 13824 (2.7 GB of weights)
+// 418 us, 6.5 TB/s; 64 tokens on 8 of 128 experts 2048 x 768 (1.2 GB) 214 us; one
+// token on 8 of 64 experts 2048 x 1024 (100 MB) 31 us, three launches.
+#include "chunk_rows.h"
 #include "ffn.h"
 #include "gemm_kernel.h"
 #include "row_vec.h"
@@ -28,7 +36,6 @@
 namespace tgemm {
 namespace {
 
-typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kStep = 128;  // bytes of K per row and step
@@ -149,53 +156,6 @@ __global__ void __launch_bounds__(kMoeExperts) moe_choose_kernel(MoeParams p) {
         p.scale * (expf((float)(chosen[i] - top)) / total[0]);
 }
 
-// ---- weights' rows -----------------------------------------------------------
-
-// Rows of K elements from which lanes read 16-byte chunks, zeros past K.
-// AL: base and strides on 16-byte boundaries and K a multiple of 8; NT:
-// non-temporal.
-template <bool AL, bool NT>
-struct ChunkRows {
-  const char* base;
-  int kb;  // bytes of K
-#if defined(__HIP_DEVICE_COMPILE__)
-  __amdgpu_buffer_rsrc_t rs;
-#endif
-  __device__ __forceinline__ void init(const char* b, int k_bytes) {
-    base = b;
-    kb = k_bytes;
-#if defined(__HIP_DEVICE_COMPILE__)
-    // (2^31 - 1 bytes, which no row of a workgroup passes: the host checks
-    // the strides; a chunk past K takes an offset past it and reads as zero)
-    if constexpr (AL)
-      rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(b), (short)0, 0x7fffffff, 0x00020000);
-#endif
-  }
-  __device__ __forceinline__ i32x4_t load(uint32_t row_off, int k) const {
-    i32x4_t v = {0, 0, 0, 0};
-#if defined(__HIP_DEVICE_COMPILE__)
-    if constexpr (AL) {
-      const uint32_t ko = k < kb ? (uint32_t)k : 0x80000000u;
-      v = __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                          rs, (int)(row_off + ko), 0, NT ? kNonTemporal : 0));
-    } else {
-      const char* const s = base + row_off + k;
-      if (k + 16 <= kb) {
-        const u16x8_any a = *reinterpret_cast<const u16x8_any*>(s);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = (int)a.w[i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (k + 2 * i < kb)
-            v[i >> 1] |= (int)((uint32_t)reinterpret_cast<const uint16_t*>(s)[i] << (16 * (i & 1)));
-      }
-    }
-#endif
-    return v;
-  }
-};
-
 // ---- gate and up -------------------------------------------------------------
 
 // The choice of up to kRouteSmall experts' logits (all tokens together) by the
@@ -239,6 +199,23 @@ __device__ __forceinline__ void choose_here(const MoeParams& p, SmallRoute& r, i
     p.ids[a] = r.ids[a];
     p.weights[a] = p.scale * (expf((float)(r.chosen[a] - top)) / total);
   }
+}
+
+// The choices of expert e into list, by the whole workgroup; their number, and in
+// s_first the first of them.  (Their order there decides nothing: each choice's
+// sums are its own.)
+__device__ __forceinline__ int expert_tokens(const MoeParams& p, const int32_t* ids, int e,
+                                             int threads, uint16_t* list, int& s_n, int& s_first) {
+  const int A = p.M * p.top;
+  if (threadIdx.x == 0) s_n = 0, s_first = A;
+  __syncthreads();
+  for (int a = threadIdx.x; a < A; a += threads) {
+    if (ids[a] != e) continue;
+    list[atomicAdd(&s_n, 1)] = (uint16_t)a;
+    atomicMin(&s_first, a);
+  }
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(s_n);
 }
 
 // With fewer choices than experts, blockIdx.y stands for the expert of that
@@ -291,17 +268,7 @@ __global__ void __launch_bounds__(W * 64) moe_up_kernel(MoeParams p) {
   const bool early = p.M == 1 && wave < steps;
   if (early) load_w(wave);
 
-  if (threadIdx.x == 0) s_n = 0, s_first = A;
-  __syncthreads();
-  // this expert's choices (their order decides nothing: each token's sums are
-  // its own)
-  for (int a = threadIdx.x; a < A; a += W * 64) {
-    if (ids[a] != e) continue;
-    list[atomicAdd(&s_n, 1)] = (uint16_t)a;
-    atomicMin(&s_first, a);
-  }
-  __syncthreads();
-  const int n = __builtin_amdgcn_readfirstlane(s_n);
+  const int n = expert_tokens(p, ids, e, W * 64, list, s_n, s_first);
   if (n == 0 || (A < p.E && s_first != slot)) return;
 
   // staged row R holds its chunk c at c ^ swz(R)
@@ -382,11 +349,19 @@ __global__ void __launch_bounds__(W * 64) moe_up_kernel(MoeParams p) {
         u += red[w * RED + (m * NB + 1) * 64 + l];
       }
       const int c0 = n0 + 4 * (l >> 4);
-      float v[4];
+      float v[4], low[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = c0 + i < p.F ? act_times(a[i], u[i], p.act) : 0.f;
-      // (rows of h are padded with zeros to ldh, a multiple of 64)
-      put4(p.h + (int64_t)list[t0 + col] * p.ldh + c0, v, 4);
+      for (int i = 0; i < 4; ++i) {
+        v[i] = c0 + i < p.F ? act_times(a[i], u[i], p.act) : 0.f;
+        low[i] = v[i] - from_bf16(to_bf16(v[i]));
+        // (an infinite or NaN h has no second part)
+        if (!(fabsf(low[i]) <= 3.402823466e38f)) low[i] = 0.f;
+      }
+      // (rows of h are padded with zeros to ldh, a multiple of 64; the second
+      // parts follow the first ones)
+      uint16_t* const o = p.h + (int64_t)list[t0 + col] * p.ldh + c0;
+      put4(o, v, 4);
+      put4(o + (int64_t)A * p.ldh, low, 4);
     }
     if (t0 + TB * 8 < n) __syncthreads();  // the buffer becomes staged rows again
   }
@@ -394,16 +369,20 @@ __global__ void __launch_bounds__(W * 64) moe_up_kernel(MoeParams p) {
 
 // ---- down --------------------------------------------------------------------
 
-// 16 columns of y, TB groups of 8 tokens of an expert at a time, TMAX tokens in
-// all, W waves.  blockIdx.y: which share of the experts that are hit.
-template <int TB, int TMAX, int W, bool AL, bool NT>
-__global__ void __launch_bounds__(W * 64) moe_down_kernel(MoeParams p) {
-  constexpr int MB = (TB + 1) / 2, STAGE = (16 + TB * 8) * 8;
+// Few weights and up to 8 tokens: a workgroup takes 16 columns of y and goes
+// through all the experts that are hit, each of its 16 waves through runs of K
+// steps of its own; a token's sums collect in LDS words of the wave, and the
+// waves' sums are added in order.
+constexpr int kSmallWaves = 16;
+
+template <bool AL, bool NT>
+__global__ void __launch_bounds__(kSmallWaves * 64) moe_down_small_kernel(MoeParams p) {
+  constexpr int W = kSmallWaves, STAGE = 16 * 8;
   constexpr int LD = 17;  // floats per token's 16 sums
   __shared__ i32x4_t lds[W * STAGE];
-  __shared__ float sums[W * TMAX * LD];
-  __shared__ uint16_t order[kMoeAssign];           // choices, by expert
-  __shared__ uint16_t first[kMoeExperts], count[kMoeExperts], hit[kMoeExperts];
+  __shared__ float sums[W * 8 * LD];
+  __shared__ uint16_t order[8 * kMoeTop];          // choices, by expert
+  __shared__ uint16_t first[kMoeExperts], count[kMoeExperts], hit[8 * kMoeTop];
   __shared__ int cnt[kMoeExperts];
   __shared__ int s_hits;
 
@@ -411,7 +390,7 @@ __global__ void __launch_bounds__(W * 64) moe_down_kernel(MoeParams p) {
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int A = p.M * p.top;
   for (int i = threadIdx.x; i < p.E; i += W * 64) cnt[i] = 0;
-  for (int i = threadIdx.x; i < W * TMAX * LD; i += W * 64) sums[i] = 0.f;
+  for (int i = threadIdx.x; i < W * 8 * LD; i += W * 64) sums[i] = 0.f;
   __syncthreads();
   for (int a = threadIdx.x; a < A; a += W * 64) {
     const int e = p.ids[a];
@@ -447,9 +426,6 @@ __global__ void __launch_bounds__(W * 64) moe_down_kernel(MoeParams p) {
     if (e >= 0 && e < p.E) order[atomicAdd(&cnt[e], 1)] = (uint16_t)a;
   }
   __syncthreads();
-  const int hits = __builtin_amdgcn_readfirstlane(s_hits);
-  const int h0 = (int)((int64_t)hits * blockIdx.y / gridDim.y);
-  const int h1 = (int)((int64_t)hits * (blockIdx.y + 1) / gridDim.y);
 
   const int n0 = blockIdx.x * 16;
   const int kb = (int)p.F * 2, steps = (kb + kStep - 1) / kStep;
@@ -460,29 +436,29 @@ __global__ void __launch_bounds__(W * 64) moe_down_kernel(MoeParams p) {
 #pragma unroll
   for (int b = 0; b < 2; ++b) woff[b] = (uint32_t)((min(n0 + b * 8 + lr, (int)p.K - 1) - n0) * ld);
   i32x4_t* const st = lds + wave * STAGE;
-  float* const own = sums + wave * TMAX * LD;
+  float* const own = sums + wave * 8 * LD;
   int wr[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) wr[q] = lr * 8 + (lc ^ swz(8 * q + lr));
   const int r = lane & 15, g = lane >> 4;
-  const int ar = TB == 1 ? (r & 7) : r;
-  int fo[2], ao[2];
+  int fo[2];
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    fo[s] = r * 8 + ((4 * s + g) ^ swz(r));
-    ao[s] = 128 + ar * 8 + ((4 * s + g) ^ swz(ar));
-  }
+  for (int s = 0; s < 2; ++s) fo[s] = r * 8 + ((4 * s + g) ^ swz(r));
+  // the lane's part of h: token r & 7 of a group, its first or second part
+  const char* const hp = reinterpret_cast<const char*>(p.h) +
+                         ((r >> 3) ? (int64_t)A * p.ldh * 2 : 0) + g * 16;
 
-  // The wave's place: run `it` of the share's (expert, run) pairs, step s of
-  // it, tokens from t0 of the expert's n.
+  // The wave's place: (expert, run) pair `it`, step s of it, tokens from t0 of
+  // the expert's n (past 8 only where a token lists an expert twice).
+  const int items = __builtin_amdgcn_readfirstlane(s_hits) * runs;
   struct Place {
     int it, s, send, t0, n, base, e;
   };
   auto begin = [&](Place& q, int it) __attribute__((always_inline)) {
     q.it = it;
-    if (it >= (h1 - h0) * runs) return;
+    if (it >= items) return;
     const int i = it / runs, c = it - i * runs;
-    const int e = __builtin_amdgcn_readfirstlane((int)hit[h0 + i]);
+    const int e = __builtin_amdgcn_readfirstlane((int)hit[i]);
     q.e = e;
     q.s = c * p.run;
     q.send = min(steps, q.s + p.run);
@@ -490,69 +466,53 @@ __global__ void __launch_bounds__(W * 64) moe_down_kernel(MoeParams p) {
     q.n = __builtin_amdgcn_readfirstlane((int)count[e]);
     q.base = __builtin_amdgcn_readfirstlane((int)first[e]);
   };
-  i32x4_t wv[2], av[TB];
+  i32x4_t wv[2], av[2];
   auto load = [&](const Place& q) __attribute__((always_inline)) {
     const int k = q.s * kStep + lc * 16;
     ChunkRows<AL, NT> rw;
     rw.init(reinterpret_cast<const char*>(p.w2 + (int64_t)q.e * p.sw2) + (int64_t)n0 * ld, kb);
 #pragma unroll
     for (int b = 0; b < 2; ++b) wv[b] = rw.load(woff[b], k);
-#pragma unroll
-    for (int t = 0; t < TB; ++t) {
-      if (q.t0 + t * 8 >= q.n) continue;
-      const int a = order[q.base + min(q.t0 + t * 8 + lr, q.n - 1)];
-      av[t] = *reinterpret_cast<const i32x4_t*>(reinterpret_cast<const char*>(p.h) +
-                                                ((int64_t)a * p.ldh * 2 + k));
-    }
+    // (straight into the matrix instruction's layout: these lines are shared by
+    // all workgroups, and come from the cache)
+    const int a = order[q.base + min(q.t0 + (r & 7), q.n - 1)];
+    const char* const s = hp + ((int64_t)a * p.ldh * 2 + q.s * kStep);
+    av[0] = *reinterpret_cast<const i32x4_t*>(s);
+    av[1] = *reinterpret_cast<const i32x4_t*>(s + 64);
   };
-  f32x4_t acc[MB];
-#pragma unroll
-  for (int m = 0; m < MB; ++m) acc[m] = f32x4_t{0, 0, 0, 0};
-  const int items = (h1 - h0) * runs;
+  f32x4_t acc = {0, 0, 0, 0};
   Place cur = {};
   begin(cur, wave);
   if (cur.it < items) load(cur);
   while (cur.it < items) {
 #pragma unroll
     for (int b = 0; b < 2; ++b) st[b * 64 + wr[b]] = wv[b];
-#pragma unroll
-    for (int t = 0; t < TB; ++t)
-      if (cur.t0 + t * 8 < cur.n) st[128 + t * 64 + wr[t & 1]] = av[t];
+    const i32x4_t af[2] = {av[0], av[1]};
     wave_lds_order();
     Place nxt = cur;
     if (++nxt.s == nxt.send) {
       nxt.s = (cur.it % runs) * p.run;
-      nxt.t0 += TB * 8;
+      nxt.t0 += 8;
       if (nxt.t0 >= nxt.n) begin(nxt, cur.it + W);
     }
     if (nxt.it < items) load(nxt);
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const i32x4_t wf = st[fo[q]];
-#pragma unroll
-      for (int m = 0; m < MB; ++m) {
-        if (cur.t0 + m * 16 >= cur.n) continue;
-        acc[m] = mma16(wf, st[m * 128 + ao[q]], acc[m]);
-      }
-    }
+    for (int q = 0; q < 2; ++q) acc = mma16(st[fo[q]], af[q], acc);
     wave_lds_order();
     if (nxt.it != cur.it || nxt.t0 != cur.t0) {
-      // these tokens' sums of the run
+      // these tokens' sums of the run, of both parts
 #pragma unroll
-      for (int m = 0; m < MB; ++m) {
-        const int col = m * 16 + (lane & 15);
-        if (cur.t0 + col < cur.n && !(TB == 1 && col >= 8)) {
-          const int a = order[cur.base + cur.t0 + col];
-          const float w = p.weights[a];
-          float* const o = own + (a / p.top) * LD + 4 * (lane >> 4);
-          // (added, not set: a token may have chosen an expert twice)
+      for (int i = 0; i < 4; ++i) acc[i] += __shfl_xor(acc[i], 8, 64);
+      if (r < 8 && cur.t0 + r < cur.n) {
+        const int a = order[cur.base + cur.t0 + r];
+        const float w = p.weights[a];
+        float* const o = own + (a / p.top) * LD + 4 * g;
+        // (added, not set: a token may have chosen an expert twice)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            __hip_atomic_fetch_add(o + i, w * acc[m][i], __ATOMIC_RELAXED,
-                                   __HIP_MEMORY_SCOPE_WORKGROUP);
-        }
-        acc[m] = f32x4_t{0, 0, 0, 0};
+        for (int i = 0; i < 4; ++i)
+          __hip_atomic_fetch_add(o + i, w * acc[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
       }
+      acc = f32x4_t{0, 0, 0, 0};
     }
     cur = nxt;
   }
@@ -562,48 +522,150 @@ __global__ void __launch_bounds__(W * 64) moe_down_kernel(MoeParams p) {
     if (n0 + c >= p.K) continue;
     float v = sums[t * LD + c];
 #pragma unroll
-    for (int w = 1; w < W; ++w) v += sums[(w * TMAX + t) * LD + c];
-    if (gridDim.y == 1)
-      p.y[(int64_t)t * p.ldy + n0 + c] = to_bf16(v);
-    else
-      p.part[((int64_t)blockIdx.y * p.M + t) * p.K + n0 + c] = v;
+    for (int w = 1; w < W; ++w) v += sums[(w * 8 + t) * LD + c];
+    p.y[(int64_t)t * p.ldy + n0 + c] = to_bf16(v);
   }
 }
 
-// y = the shares' sums, in order, four columns per thread.
-__global__ void __launch_bounds__(256) moe_add_kernel(MoeParams p, int shares, int per_row) {
+// Other calls: a workgroup takes 16 NB columns of one expert, its waves share the
+// K steps, and each choice's row of sums goes to memory, [M * top][K], for
+// moe_weigh_kernel.  TB groups of 8 tokens at a time; blockIdx.y as in
+// moe_up_kernel.
+template <int TB, int NB, int W, bool AL, bool NT>
+__global__ void __launch_bounds__(W * 64) moe_down_rows_kernel(MoeParams p) {
+  constexpr int STAGE = NB * 16 * 8, RED = TB * NB * 64;
+  __shared__ i32x4_t lds[W * (STAGE > RED ? STAGE : RED)];
+  __shared__ uint16_t list[kMoeAssign];
+  __shared__ int s_n, s_first;
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int slot = blockIdx.y, A = p.M * p.top;
+  const int e = __builtin_amdgcn_readfirstlane(A < p.E ? p.ids[slot] : slot);
+  if (e < 0 || e >= p.E) return;
+  const int n = expert_tokens(p, p.ids, e, W * 64, list, s_n, s_first);
+  if (n == 0 || (A < p.E && s_first != slot)) return;
+
+  const int n0 = blockIdx.x * 16 * NB;
+  const int kb = (int)p.F * 2, steps = (kb + kStep - 1) / kStep;
+  const int lc = lane & 7, lr = lane >> 3;
+  const int ld = (int)p.ldw2 * 2;
+  ChunkRows<AL, NT> rw;
+  rw.init(reinterpret_cast<const char*>(p.w2 + (int64_t)e * p.sw2) + (int64_t)n0 * ld, kb);
+  uint32_t woff[2 * NB];
+#pragma unroll
+  for (int b = 0; b < 2 * NB; ++b)
+    woff[b] = (uint32_t)((min(n0 + b * 8 + lr, (int)p.K - 1) - n0) * ld);
+  i32x4_t* const st = lds + wave * STAGE;
+  int wr[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) wr[q] = lr * 8 + (lc ^ swz(8 * q + lr));
+  const int r = lane & 15, g = lane >> 4;
+  int fo[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) fo[s] = r * 8 + ((4 * s + g) ^ swz(r));
+  const char* const hp = reinterpret_cast<const char*>(p.h) +
+                         ((r >> 3) ? (int64_t)A * p.ldh * 2 : 0) + g * 16;
+
+  for (int t0 = 0; t0 < n; t0 += TB * 8) {
+    f32x4_t acc[TB][NB];
+    int64_t hoff[TB];
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+      hoff[t] = (int64_t)list[min(t0 + t * 8 + (r & 7), n - 1)] * p.ldh * 2;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) acc[t][b] = f32x4_t{0, 0, 0, 0};
+    }
+    i32x4_t wv[2 * NB], av[TB][2];
+    auto load = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+      for (int b = 0; b < 2 * NB; ++b) wv[b] = rw.load(woff[b], s * kStep + lc * 16);
+#pragma unroll
+      for (int t = 0; t < TB; ++t) {
+        if (t0 + t * 8 >= n) continue;
+        const char* const a = hp + (hoff[t] + s * kStep);
+        av[t][0] = *reinterpret_cast<const i32x4_t*>(a);
+        av[t][1] = *reinterpret_cast<const i32x4_t*>(a + 64);
+      }
+    };
+    if (wave < steps) load(wave);
+    for (int s = wave; s < steps; s += W) {
+#pragma unroll
+      for (int b = 0; b < 2 * NB; ++b) st[b * 64 + wr[b & 1]] = wv[b];
+      i32x4_t af[TB][2];
+#pragma unroll
+      for (int t = 0; t < TB; ++t) af[t][0] = av[t][0], af[t][1] = av[t][1];
+      wave_lds_order();
+      if (s + W < steps) load(s + W);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        i32x4_t wf[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) wf[b] = st[b * 128 + fo[q]];
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+          if (t0 + t * 8 >= n) continue;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) acc[t][b] = mma16(wf[b], af[t][q], acc[t][b]);
+        }
+      }
+      wave_lds_order();
+    }
+    __syncthreads();  // the staged rows become the sums' buffer
+    f32x4_t* const red = reinterpret_cast<f32x4_t*>(lds);
+#pragma unroll
+    for (int t = 0; t < TB; ++t)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        f32x4_t v = acc[t][b];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += __shfl_xor(v[i], 8, 64);
+        red[wave * RED + (t * NB + b) * 64 + lane] = v;
+      }
+    __syncthreads();
+    for (int i = threadIdx.x; i < RED; i += W * 64) {
+      const int l = i & 63, q = i >> 6, t = q / NB, b = q % NB;
+      const int col = t * 8 + (l & 15), c0 = n0 + b * 16 + 4 * (l >> 4);
+      const int m = min(4, (int)p.K - c0);
+      if ((l & 15) >= 8 || t0 + col >= n || m <= 0) continue;
+      f32x4_t a = red[i];
+#pragma unroll
+      for (int w = 1; w < W; ++w) a += red[w * RED + i];
+      const float v[4] = {a[0], a[1], a[2], a[3]};
+      put4(p.part + (int64_t)list[t0 + col] * p.K + c0, v, m);
+    }
+    if (t0 + TB * 8 < n) __syncthreads();  // the buffer becomes staged rows again
+  }
+}
+
+// y = the choices' rows by their weights, in order, four columns per thread.
+__global__ void __launch_bounds__(256) moe_weigh_kernel(MoeParams p, int per_row) {
   const int t = (int)(blockIdx.x / per_row);
   const int c = ((int)(blockIdx.x % per_row) * 256 + (int)threadIdx.x) * 4;
   const int n = min(4, (int)p.K - c);
   if (n <= 0) return;
   float a[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < shares; ++s) {
+  for (int j = t * p.top; j < (t + 1) * p.top; ++j) {
+    const int e = p.ids[j];
+    if (e < 0 || e >= p.E) continue;
+    const float w = p.weights[j];
     float v[4] = {0.f, 0.f, 0.f, 0.f};
-    get4(p.part + ((int64_t)s * p.M + t) * p.K + c, v, n);
+    get4(p.part + (int64_t)j * p.K + c, v, n);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] += v[i];
+    for (int i = 0; i < 4; ++i) a[i] = fmaf(w, v[i], a[i]);
   }
   put4(p.y + (int64_t)t * p.ldy + c, a, n);
 }
 
 int slots_of(const MoeParams& p) { return p.M * p.top < p.E ? p.M * p.top : p.E; }
 
-// The down product of few weights (48 MB) for up to 8 tokens runs on workgroups
-// of 16 waves and one share of the experts where that gives 128 workgroups:
-// what half the compute units lose is less than a launch to add shares (8
-// experts 2048 x 1024: 11.5 us whole; 8 waves 16.1 whole, in 4 shares 9.4 and
-// 3.3 for the sums).
+// The down product of few weights (48 MB) for up to 8 tokens, on at least 128
+// workgroups: what half the compute units and the short runs lose is less than a
+// launch to add up the choices (us, small kernel / the other and the sums: one
+// token, 8 experts 2048 x 1024 11.9 / 8.6 + 4.1; 8 tokens, 8 experts 2048 x 768
+// 8.4 / 6.7 + 3.2).
 bool down_small(const MoeParams& p) {
-  return p.M <= 8 && (int64_t)slots_of(p) * p.F * p.K * 2 <= int64_t(48) << 20;
-}
-
-// Shares of the experts in the down product: enough workgroups of 16 columns
-// for two per compute unit (128 experts 2048 x 768, 64 tokens, 1 / 2 / 4 / 8
-// shares: 161 / 94 / 68 / 75 us).
-int shares_of(const MoeParams& p) {
-  const int blocks = ceil_div(p.K, 16), slots = slots_of(p);
-  const int want = ceil_div(down_small(p) ? 128 : 512, blocks);
-  return want < slots ? want : slots;
+  return p.M <= 8 && p.K >= 2048 && (int64_t)slots_of(p) * p.F * p.K * 2 <= int64_t(48) << 20;
 }
 
 // The up product's workgroups make the choice of experts themselves where there
@@ -622,15 +684,20 @@ hipError_t launch_up(const MoeParams& p, hipStream_t s) {
   return enqueue(moe_up_kernel<TB, W, false, AL, NT>, grid, block, s, p);
 }
 
-template <int TB, int TMAX, int W, bool AL, bool NT>
-hipError_t launch_down(MoeParams p, hipStream_t s) {
-  const int steps = ceil_div((int64_t)p.F * 2, kStep), shares = shares_of(p);
-  // runs of up to 8 K steps, fewer where they would not go round the waves, and
-  // even ones: a wave takes every W-th (12 steps as 8 + 4 74 us, as 6 + 6 68)
-  const int even = ceil_div((int64_t)slots_of(p) * steps, shares * W);
+template <bool AL, bool NT>
+hipError_t launch_down_small(MoeParams p, hipStream_t s) {
+  const int steps = ceil_div((int64_t)p.F * 2, kStep);
+  // even runs of up to 8 K steps, fewer where they would not go round the waves
+  const int even = ceil_div((int64_t)slots_of(p) * steps, kSmallWaves);
   p.run = ceil_div(steps, ceil_div(steps, even < 8 ? even : 8));
-  const dim3 grid(ceil_div(p.K, 16), shares), block(W * 64);
-  return enqueue(moe_down_kernel<TB, TMAX, W, AL, NT>, grid, block, s, p);
+  return enqueue(moe_down_small_kernel<AL, NT>, dim3(ceil_div(p.K, 16)), dim3(kSmallWaves * 64), s,
+                 p);
+}
+
+template <int TB, int NB, int W, bool AL, bool NT>
+hipError_t launch_down_rows(const MoeParams& p, hipStream_t s) {
+  return enqueue(moe_down_rows_kernel<TB, NB, W, AL, NT>,
+                 dim3(ceil_div(p.K, 16 * NB), slots_of(p)), dim3(W * 64), s, p);
 }
 
 template <bool AL, bool NT>
@@ -650,16 +717,18 @@ hipError_t launch_products(const MoeParams& p, hipStream_t s) {
   else
     e = narrow ? launch_up<2, 4, AL, NT>(p, s) : launch_up<2, 8, AL, NT>(p, s);
   if (e != hipSuccess) return e;
-  if (few)
-    e = down_small(p) ? launch_down<1, 16, 16, AL, NT>(p, s) : launch_down<1, 16, 8, AL, NT>(p, s);
-  else if (p.M <= 16)
-    e = launch_down<2, 16, 8, AL, NT>(p, s);
-  else
-    e = many ? launch_down<8, 64, 8, AL, NT>(p, s) : launch_down<2, 64, 8, AL, NT>(p, s);
-  const int shares = shares_of(p);
-  if (e != hipSuccess || shares == 1) return e;
+  if (down_small(p)) return launch_down_small<AL, NT>(p, s);
+  // Tokens at a time and columns (in 16s) of the down product: h costs a
+  // workgroup as much as NB / 2 times its columns of weights for each group of
+  // tokens.  Us, 1 x 2 (8 waves) / 1 x 4 / 2 x 4 / 4 x 4: one token, 2 of 8 experts
+  // 4096 x 13824 36 / 51; 13 tokens, the same 137 / 133 / 135 / 136; 64 tokens, 8
+  // of 128 2048 x 768 75 / 68 / 70 / 84; 40 tokens, 2 of 8 4096 x 4096 86 / 82 / 54
+  // / 55; 32 tokens, 8 of 8 208 / 197 / 101 / 66.
+  e = few ? launch_down_rows<1, 2, 8, AL, NT>(p, s)
+          : many ? launch_down_rows<4, 4, 4, AL, NT>(p, s) : launch_down_rows<2, 4, 4, AL, NT>(p, s);
+  if (e != hipSuccess) return e;
   const int per_row = ceil_div(p.K, 1024);
-  return enqueue(moe_add_kernel, dim3((unsigned)((int64_t)p.M * per_row)), dim3(256), s, p, shares,
+  return enqueue(moe_weigh_kernel, dim3((unsigned)((int64_t)p.M * per_row)), dim3(256), s, p,
                  per_row);
 }
 
@@ -671,9 +740,8 @@ inline bool aligned16(const void* p, int64_t a, int64_t b) {
 
 MoeSpace moe_space(const MoeParams& p) {
   const size_t logits = p.router != nullptr ? (size_t)p.M * p.E * sizeof(double) : 0;
-  const size_t h = (size_t)p.M * p.top * p.ldh * 2;
-  const int shares = shares_of(p);
-  const size_t part = shares > 1 ? (size_t)shares * p.M * p.K * sizeof(float) : 0;
+  const size_t h = (size_t)p.M * p.top * p.ldh * 4;
+  const size_t part = down_small(p) ? 0 : (size_t)p.M * p.top * p.K * sizeof(float);
   return {logits, h, part};
 }
 

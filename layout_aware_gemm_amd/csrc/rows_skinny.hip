@@ -19,13 +19,13 @@
 // Measured (MI355X) for one token: cold weights of 71 to 283 MB 4.8 to 5.9
 // TB/s, where a large copy reaches 4.7; a 71 MB weight that stayed in part in
 // the last-level cache 5.7.
+#include "chunk_rows.h"
 #include "ffn.h"
 #include "gemm_kernel.h"
 
 namespace tgemm {
 namespace {
 
-typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 struct SkI8 {
@@ -54,8 +54,10 @@ constexpr int kStep = 128;  // bytes of K per row and step
 
 // TB groups of 8 tokens, NB blocks of 16 weight rows per wave (GATE: the
 // first half gate rows, the second half the up rows of the same outputs),
-// W waves.  ONCE: non-temporal weight loads.
-template <class Op, int TB, int NB, int W, bool GATE, int EPI, bool ONCE>
+// W waves.  ONCE: non-temporal weight loads.  AL: rows on 16-byte boundaries; a
+// linear product reads others in place, too (a copy would move the weight three
+// times).
+template <class Op, int TB, int NB, int W, bool GATE, int EPI, bool ONCE, bool AL>
 __global__ void __launch_bounds__(W * 64) skinny_kernel(RowsParams p) {
   constexpr bool I8 = std::is_same<Op, SkI8>::value;
   constexpr int NO = GATE ? NB / 2 : NB;  // blocks of 16 outputs
@@ -99,9 +101,21 @@ __global__ void __launch_bounds__(W * 64) skinny_kernel(RowsParams p) {
     rw[1] = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<char*>(p.B + ((int64_t)p.F + n0) * p.ldb), (short)0, 0x7fffffff,
         0x00020000);
+  ChunkRows<AL, false> uw, ua;  // (AL false)
+  if constexpr (!AL) {
+    uw.init(p.B + (int64_t)n0 * p.ldb, p.K);
+    ua.init(p.A, p.K);
+  }
   i32x4_t wv[2 * NB], av[TB];
   auto load = [&](int s) __attribute__((always_inline)) {
     const int k = s * kStep + lc * 16;
+    if constexpr (!AL) {
+#pragma unroll
+      for (int b = 0; b < 2 * NB; ++b) wv[b] = uw.load(woff[b], k);
+#pragma unroll
+      for (int t = 0; t < TB; ++t) av[t] = ua.load(aoff[t], k);
+      return;
+    }
     const uint32_t ko = k < p.K ? (uint32_t)k : 0x80000000u;
 #pragma unroll
     for (int b = 0; b < 2 * NB; ++b)
@@ -223,9 +237,13 @@ hipError_t launch_one(const RowsParams& p, hipStream_t s) {
   constexpr int NO = GATE ? NB / 2 : NB;
   const int nblk = ceil_div(GATE ? p.F : p.N, 16 * NO);
   const dim3 grid(nblk), block(W * 64);
+  if constexpr (EPI == kRowsLinear) {
+    if (!rows_aligned(p.A, p.lda, p.K) || !rows_aligned(p.B, p.ldb, p.K))
+      return enqueue(skinny_kernel<Op, TB, NB, W, GATE, EPI, false, false>, grid, block, s, p);
+  }
   if (streams_past_cache(p))
-    return enqueue(skinny_kernel<Op, TB, NB, W, GATE, EPI, true>, grid, block, s, p);
-  return enqueue(skinny_kernel<Op, TB, NB, W, GATE, EPI, false>, grid, block, s, p);
+    return enqueue(skinny_kernel<Op, TB, NB, W, GATE, EPI, true, true>, grid, block, s, p);
+  return enqueue(skinny_kernel<Op, TB, NB, W, GATE, EPI, false, true>, grid, block, s, p);
 }
 
 // up to 32 tokens

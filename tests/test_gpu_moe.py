@@ -6,7 +6,9 @@ Bounds (u = 2^-24, ub = 2^-8: half a step of fp32, of bf16):
   come from small integers, whose sums are exact).
 * weights: the logits' difference rounds to fp32 once, exp, the sum of n terms,
   the quotient and the scale follow: (|l - l_0| + n + 10) 2 u relative.
-* H: as the gated product (act_bounds of its test, ub included).
+* H: the gated product's fp32 errors (act_bounds of its test, its rounding to
+  bf16 taken off), and 2^-16 for its two parts (each rounds to half a step of
+  2^-8 of what it holds).
 * y: the errors of H and of the F-term sums through |W2| and the weights, their
   sum over the choices, and ub for the store.
 """
@@ -65,6 +67,8 @@ def check_layer(y, x, ids, p, w1, w2, act):
         gu, size = X[m] @ W1.T, np.abs(X[m]) @ np.abs(W1).T
         eg = K * 1.01 * U32 * size
         h, eh = act_bounds(gu, eg[:, :F], eg[:, F:], act)
+        e = (eh - 1.01 * UB * np.abs(h)) / (1 + 1.01 * UB)
+        eh = e + 2.0 ** -16 * (np.abs(h) + e) + 1e-38
         q = P[m, j][:, None]
         np.add.at(out, m, q * (h @ W2.T))
         np.add.at(err, m, np.abs(q) * (eh * 1.01 + (F + 2 * top + 12) * 1.01 * U32 * np.abs(h))
@@ -80,7 +84,8 @@ CASES = [(1, 64, 64, 4, 2), (1, 2048, 96, 64, 8), (1, 1, 1, 1, 1), (3, 40, 33, 5
          (16, 136, 65, 3, 3), (17, 520, 128, 4, 2), (33, 72, 1000, 30, 1), (64, 256, 96, 128, 8),
          (64, 72, 40, 2, 1), (64, 136, 200, 4, 4), (64, 64, 64, 1, 1), (65, 48, 16, 6, 2),
          (130, 200, 24, 9, 4), (2, 8200, 64, 3, 2), (40, 64, 16, 1024, 16), (3, 31, 7, 300, 2),
-         (4, 2048, 1024, 8, 4), (64, 520, 24, 70, 8), (20, 33, 2049, 2, 2)]
+         (4, 2048, 1024, 8, 4), (64, 520, 24, 70, 8), (20, 33, 2049, 2, 2), (8, 2049, 513, 20, 6),
+         (7, 2048, 2048, 9, 1), (33, 200, 136, 33, 3)]
 
 
 @pytest.mark.parametrize("M,K,F,E,top", CASES)
@@ -145,11 +150,11 @@ def test_ties_and_infinite_logits():
         assert torch.isnan(y2[3]).any()
 
 
-@pytest.mark.parametrize("M,E", [(6, 40), (30, 4)])
-def test_routing_of_the_callers(M, E):
+@pytest.mark.parametrize("M,E,K", [(6, 40, 72), (30, 4, 72), (6, 40, 2056), (5, 4, 2049)])
+def test_routing_of_the_callers(M, E, K):
     """Experts listed twice by a token, out of range, negative, none at all;
     weights of either sign and zero."""
-    K, F, top = 72, 40, 5
+    F, top = 40, 5
     x, _, w1, w2 = layer(M, K, F, E)
     u, d = w1.transpose(1, 2), w2.transpose(1, 2)
     g = torch.Generator().manual_seed(2)

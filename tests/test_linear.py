@@ -87,8 +87,11 @@ def test_validate_linear_backward(kw, expect):
 def test_workspace_queries():
     L, N, T = tgemm.lib(), b"N", b"T"
     assert L.tgemm_linear_workspace_bytes(N, T, 4, 4096, 4096, P, 4096, P, 4096) == 0
-    assert L.tgemm_linear_workspace_bytes(N, T, 4, 40, 33, P, 33, P, 33) >= (4 + 40) * 40 * 2
-    assert L.tgemm_linear_workspace_bytes(N, T, 4, 40, 64, P + 2, 64, P, 64) >= 4 * 64 * 2
+    # few rows of a K-contiguous weight are read at any alignment, others copied
+    assert L.tgemm_linear_workspace_bytes(N, T, 4, 40, 33, P, 33, P + 2, 35) == 0
+    assert L.tgemm_linear_workspace_bytes(N, T, 70, 40, 33, P, 33, P, 33) >= (70 + 40) * 40 * 2
+    assert L.tgemm_linear_workspace_bytes(N, T, 70, 40, 64, P + 2, 64, P, 64) >= 70 * 64 * 2
+    assert L.tgemm_linear_workspace_bytes(N, N, 4, 40, 64, P, 64, P, 40) >= 40 * 64 * 2
     assert L.tgemm_linear_workspace_bytes(N, T, 128, 128, 8192, P, 8192, P, 8192) >= 2 * 4 * 128 * 128
     assert L.tgemm_linear_workspace_bytes(N, T, 0, 40, 64, P, 64, P, 64) == INV
     assert L.tgemm_linear_backward_workspace_bytes(N, T, 4, 40, 64, P, 64, P, 64) >= (256 * 64 * 2
