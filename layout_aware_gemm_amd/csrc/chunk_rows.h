@@ -41,11 +41,15 @@ struct ChunkRows {
         const u16x8_any a = *reinterpret_cast<const u16x8_any*>(s);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = (int)a.w[i];
-      } else {
+      } else if (k < kb) {
+        // (loads that do not wait for each other)
+        uint32_t e[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (k + 2 * i < kb)
-            v[i >> 1] |= (int)((uint32_t)reinterpret_cast<const uint16_t*>(s)[i] << (16 * (i & 1)));
+          e[i] = *reinterpret_cast<const uint16_t*>(s + (k + 2 * i < kb ? 2 * i : kb - 2 - k));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (k + 2 * i < kb) v[i >> 1] |= (int)(e[i] << (16 * (i & 1)));
       }
     }
 #endif

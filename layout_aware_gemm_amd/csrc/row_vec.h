@@ -11,19 +11,24 @@ namespace tgemm {
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// 8 elements from column c of a row of n (zeros past the end).
+// 8 elements from column c of a row of n (zeros past the end).  The end of a row
+// is read as its last 8 elements, one load as elsewhere, and moved down: loaded
+// one by one, each would wait for the one before.
 __device__ __forceinline__ u16x8_any load8(const uint16_t* p, int64_t c, int64_t n) {
-  u16x8_any v;
+  u16x8_any v = {{0, 0, 0, 0}};
   if (c + 8 <= n) {
     v = *reinterpret_cast<const u16x8_any*>(p + c);
-  } else {
+  } else if (c < n && n >= 8) {
+    v = *reinterpret_cast<const u16x8_any*>(p + n - 8);
+    const int s = 16 * (int)(c + 8 - n);  // bits, 16 to 112
+    const uint64_t lo = v.w[0] | ((uint64_t)v.w[1] << 32), hi = v.w[2] | ((uint64_t)v.w[3] << 32);
+    const uint64_t l = s < 64 ? (lo >> s) | (hi << (64 - s)) : hi >> (s - 64);
+    const uint64_t h = s < 64 ? hi >> s : 0;
+    v = u16x8_any{{(uint32_t)l, (uint32_t)(l >> 32), (uint32_t)h, (uint32_t)(h >> 32)}};
+  } else if (c < n) {  // (a row of less than 8)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t w = 0;
-      if (c + 2 * i < n) w = p[c + 2 * i];
-      if (c + 2 * i + 1 < n) w |= (uint32_t)p[c + 2 * i + 1] << 16;
-      v.w[i] = w;
-    }
+    for (int i = 0; i < 7; ++i)
+      if (c + i < n) v.w[i >> 1] |= (uint32_t)p[c + i] << (16 * (i & 1));
   }
   return v;
 }
@@ -43,15 +48,27 @@ struct f32x8_any {
 };
 
 __device__ __forceinline__ f32x8_any load8(const float* p, int64_t c, int64_t n) {
-  f32x8_any v;
+  f32x8_any v = {};
   if (c + 8 <= n) {
     v.a = *reinterpret_cast<const x4_any<float>*>(p + c);
     v.b = *reinterpret_cast<const x4_any<float>*>(p + c + 4);
-  } else {
+  } else if (c < n && n >= 8) {
+    v.a = *reinterpret_cast<const x4_any<float>*>(p + n - 8);
+    v.b = *reinterpret_cast<const x4_any<float>*>(p + n - 4);
+    const int s = (int)(c + 8 - n);  // elements, 1 to 7
+    float f[8] = {v.a.v[0], v.a.v[1], v.a.v[2], v.a.v[3], v.b.v[0], v.b.v[1], v.b.v[2], v.b.v[3]};
+#pragma unroll
+    for (int m = 1; m < 8; m *= 2) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = (s & m) ? (i + m < 8 ? f[i + m] : 0.f) : f[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v.a.v[i] = f[i], v.b.v[i] = f[4 + i];
+  } else if (c < n) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v.a.v[i] = c + i < n ? p[c + i] : 0.f;
-      v.b.v[i] = c + 4 + i < n ? p[c + 4 + i] : 0.f;
+      if (c + i < n) v.a.v[i] = p[c + i];
+      if (c + 4 + i < n) v.b.v[i] = p[c + 4 + i];
     }
   }
   return v;

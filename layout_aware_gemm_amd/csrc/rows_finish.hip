@@ -77,6 +77,23 @@ __global__ void __launch_bounds__(kThr) finish_kernel(RowsParams p) {
   }
 }
 
+// The first n of a vector's 16 / ES elements at src, zeros behind them.  Every
+// load is made, past n from the last element on: in a loop each would wait for
+// the one before (13 us for a copy of a megabyte).
+template <int ES>
+__device__ __forceinline__ b16_any part_vector(const char* src, int n) {
+  using E = std::conditional_t<ES == 1, uint8_t, uint16_t>;
+  constexpr int V = 16 / ES, PER = 4 / ES;
+  uint32_t e[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) e[i] = reinterpret_cast<const E*>(src)[i < n ? i : n - 1];
+  b16_any v = {{0, 0, 0, 0}};
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    v.w[i / PER] |= i < n ? e[i] << (i % PER * 8 * ES) : 0;
+  return v;
+}
+
 // Copy a K-contiguous operand: 16 output bytes per thread, from any
 // alignment.  ES: bytes per element.
 template <int ES>
@@ -87,12 +104,10 @@ __global__ void __launch_bounds__(kThr) pack_rows_kernel(PackRows p, int chunks)
   b16_any v = {{0, 0, 0, 0}};
   if (r < p.R && k < p.K) {
     const char* src = static_cast<const char*>(p.X) + ((int64_t)r * p.ld + k) * ES;
-    if (k + 16 / ES <= p.K) {
+    if (k + 16 / ES <= p.K)
       v = *reinterpret_cast<const b16_any*>(src);
-    } else {
-      for (int i = 0; i < (p.K - k) * ES; ++i)
-        v.w[i >> 2] |= (uint32_t)(uint8_t)src[i] << ((i & 3) * 8);
-    }
+    else
+      v = part_vector<ES>(src, p.K - k);
   }
   *reinterpret_cast<b16_any*>(static_cast<char*>(p.out) + ((int64_t)r * p.ldo + k) * ES) = v;
 }
@@ -112,12 +127,10 @@ __global__ void __launch_bounds__(kThr) pack_cols_kernel(PackRows p, int kblocks
     b16_any v = {{0, 0, 0, 0}};
     if (k < p.K && r < p.R) {
       const char* src = static_cast<const char*>(p.X) + ((int64_t)k * p.ld + r) * ES;
-      if (r + V <= p.R) {
+      if (r + V <= p.R)
         v = *reinterpret_cast<const b16_any*>(src);
-      } else {
-        for (int e = 0; e < (p.R - r) * ES; ++e)
-          v.w[e >> 2] |= (uint32_t)(uint8_t)src[e] << ((e & 3) * 8);
-      }
+      else
+        v = part_vector<ES>(src, p.R - r);
     }
 #pragma unroll
     for (int e = 0; e < V; ++e)
