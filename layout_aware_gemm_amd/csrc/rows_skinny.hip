@@ -285,21 +285,42 @@ hipError_t launch_few(const RowsParams& p, hipStream_t s) {
 // loses at the band's upper end for long K (bf16 8192 x 5120 29.4 / 29.3 / 30.3
 // / 32.8, 29.0 / 30.2 / 31.4 / 35.9).  Below the band whole blocks win (bf16
 // 5504 x 4096 20.6 / 21.5 / 23.4 at 1 / 16 / 32 tokens, half 21.4 / 23.2 / 24.9),
-// as they do for plain products (int8 8192 x 4096 9.3 / 9.6 / 10.2, 9.1 / 9.9 /
-// 11.3).
+// as they do for plain int8 products (8192 x 4096 9.3 / 9.6 / 10.2, 9.1 / 9.9 /
+// 11.3); bf16 linear products are as heavy as gated int8 ones (one token 8192 x
+// 4096 19.0, half 13.2; 5120 x 5120 10.8; 5120 x 13824 24.6, half 24.7).
+// 33 to 64 tokens of a linear product (bf16), in 6 or 8 groups of 8.  A workgroup
+// holds 57 KB (two blocks, four waves) to 131 KB (four blocks, eight waves) of
+// LDS, so the grid is kept to one round where it can be (us, 48 tokens, cold
+// weights, two blocks 8 waves / four blocks 4 waves / four blocks 8 waves: 5120 x
+// 5120 14.5 / 19.4 / 19.4, 8192 x 8192 34.8 / 41.3 / 39.6, 11008 x 4096 27.5 / - /
+// 18.7, 16384 x 4096 34.6 / 29.0 / 26.8, 32000 x 4096 - / 48.2 / 51.8; 6 groups
+// take 1 to 2 us less than 8).
+template <int TB>
+hipError_t launch_linear_tokens(const RowsParams& p, hipStream_t s) {
+  if (ceil_div(p.N, 32) <= 128) return launch_one<SkBf16, TB, 1, 8, false, kRowsLinear>(p, s);
+  if (ceil_div(p.N, 32) <= 256) return launch_one<SkBf16, TB, 2, 8, false, kRowsLinear>(p, s);
+  if (ceil_div(p.N, 64) <= 256) return launch_one<SkBf16, TB, 4, 8, false, kRowsLinear>(p, s);
+  return launch_one<SkBf16, TB, 4, 4, false, kRowsLinear>(p, s);
+}
+
 template <class Op, bool GATE, int EPI>
 hipError_t launch_blocks(const RowsParams& p, hipStream_t s) {
   constexpr int NB = GATE ? 4 : 2;
   const int nout = GATE ? p.F : p.N;
   const int blocks = ceil_div(nout, 32);
-  const bool half = blocks <= 128 || (GATE && blocks > 208 && blocks <= 256);
+  const bool half =
+      blocks <= 128 || ((GATE || EPI == kRowsLinear) && blocks > 208 && blocks <= 256);
   if (p.M <= 32)
     return half ? launch_few<Op, NB / 2, GATE, EPI>(p, s) : launch_few<Op, NB, GATE, EPI>(p, s);
-  if (blocks <= 128) return launch_one<Op, 8, NB / 2, 8, GATE, EPI>(p, s);
-  if constexpr (!GATE) {
-    if (ceil_div(nout, 64) >= 256) return launch_one<Op, 8, 4, 4, GATE, EPI>(p, s);
+  if constexpr (EPI == kRowsLinear) {
+    return p.M <= 48 ? launch_linear_tokens<6>(p, s) : launch_linear_tokens<8>(p, s);
+  } else {
+    if (blocks <= 128) return launch_one<Op, 8, NB / 2, 8, GATE, EPI>(p, s);
+    if constexpr (!GATE) {
+      if (ceil_div(nout, 64) >= 256) return launch_one<Op, 8, 4, 4, GATE, EPI>(p, s);
+    }
+    return launch_one<Op, 8, NB, 4, GATE, EPI>(p, s);
   }
-  return launch_one<Op, 8, NB, 4, GATE, EPI>(p, s);
 }
 
 }  // namespace

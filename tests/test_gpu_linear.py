@@ -77,7 +77,8 @@ SHAPES = [(1, 1, 1), (1, 16, 8), (1, 5120, 512), (3, 17, 40), (8, 4200, 72), (9,
           (64, 4200, 40), (65, 64, 64), (100, 20001, 72), (127, 255, 136), (129, 130, 4096),
           (300, 520, 4104), (257, 513, 504), (513, 1000, 520), (130, 5003, 10248),
           (1030, 2100, 72), (2100, 4100, 40), (2300, 7268, 520), (2300, 9698, 520),
-          (5, 6151, 8200), (5, 9, 7), (70, 33, 65), (1, 1, 300), (200, 1, 64)]
+          (35, 9001, 40), (64, 16001, 40), (50, 33001, 24), (9, 7001, 136), (30, 8190, 72),
+          (41, 130, 2049), (5, 6151, 8200), (5, 9, 7), (70, 33, 65), (1, 1, 300), (200, 1, 64)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
