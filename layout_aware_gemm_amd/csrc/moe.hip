@@ -372,7 +372,8 @@ __global__ void __launch_bounds__(W * 64) moe_up_kernel(MoeParams p) {
 // Few weights and up to 8 tokens: a workgroup takes 16 columns of y and goes
 // through all the experts that are hit, each of its 16 waves through runs of K
 // steps of its own; a token's sums collect in LDS words of the wave, and the
-// waves' sums are added in order.
+// waves' sums are added in order.  A token that lists an expert more than once
+// takes one column of that expert, multiplied by its weights one by one.
 constexpr int kSmallWaves = 16;
 
 template <bool AL, bool NT>
@@ -381,7 +382,10 @@ __global__ void __launch_bounds__(kSmallWaves * 64) moe_down_small_kernel(MoePar
   constexpr int LD = 17;  // floats per token's 16 sums
   __shared__ i32x4_t lds[W * STAGE];
   __shared__ float sums[W * 8 * LD];
-  __shared__ uint16_t order[8 * kMoeTop];          // choices, by expert
+  __shared__ uint16_t order[8 * kMoeTop];          // a token's first choice of an expert, by expert
+  __shared__ uint16_t same[8 * kMoeTop];           // bit j: the token's choice j is that expert
+  __shared__ int32_t ids[8 * kMoeTop];
+  __shared__ float weight[8 * kMoeTop];
   __shared__ uint16_t first[kMoeExperts], count[kMoeExperts], hit[8 * kMoeTop];
   __shared__ int cnt[kMoeExperts];
   __shared__ int s_hits;
@@ -391,10 +395,23 @@ __global__ void __launch_bounds__(kSmallWaves * 64) moe_down_small_kernel(MoePar
   const int A = p.M * p.top;
   for (int i = threadIdx.x; i < p.E; i += W * 64) cnt[i] = 0;
   for (int i = threadIdx.x; i < W * 8 * LD; i += W * 64) sums[i] = 0.f;
+  static_assert(8 * kMoeTop <= W * 64, "a thread per choice");
+  const int own_a = threadIdx.x;
+  if (own_a < A) {
+    ids[own_a] = p.ids[own_a];
+    weight[own_a] = p.weights[own_a];
+  }
   __syncthreads();
-  for (int a = threadIdx.x; a < A; a += W * 64) {
-    const int e = p.ids[a];
-    if (e >= 0 && e < p.E) atomicAdd(&cnt[e], 1);
+  int own_e = -1;  // the expert, if this is the token's first choice of it
+  if (own_a < A) {
+    const int e = ids[own_a], j0 = own_a / p.top * p.top;
+    uint32_t m = 0;
+    for (int j = 0; j < p.top; ++j) m |= ids[j0 + j] == e ? 1u << j : 0u;
+    same[own_a] = (uint16_t)m;
+    if (e >= 0 && e < p.E && (m & ((1u << (own_a - j0)) - 1)) == 0) {
+      own_e = e;
+      atomicAdd(&cnt[e], 1);
+    }
   }
   __syncthreads();
   if (wave == 0) {
@@ -421,10 +438,7 @@ __global__ void __launch_bounds__(kSmallWaves * 64) moe_down_small_kernel(MoePar
     }
   }
   __syncthreads();
-  for (int a = threadIdx.x; a < A; a += W * 64) {
-    const int e = p.ids[a];
-    if (e >= 0 && e < p.E) order[atomicAdd(&cnt[e], 1)] = (uint16_t)a;
-  }
+  if (own_e >= 0) order[atomicAdd(&cnt[own_e], 1)] = (uint16_t)own_a;
   __syncthreads();
 
   const int n0 = blockIdx.x * 16;
@@ -448,11 +462,11 @@ __global__ void __launch_bounds__(kSmallWaves * 64) moe_down_small_kernel(MoePar
   const char* const hp = reinterpret_cast<const char*>(p.h) +
                          ((r >> 3) ? (int64_t)A * p.ldh * 2 : 0) + g * 16;
 
-  // The wave's place: (expert, run) pair `it`, step s of it, tokens from t0 of
-  // the expert's n (past 8 only where a token lists an expert twice).
+  // The wave's place: (expert, run) pair `it`, step s of it; the expert's tokens,
+  // n <= 8 of them, from `base` in the order.
   const int items = __builtin_amdgcn_readfirstlane(s_hits) * runs;
   struct Place {
-    int it, s, send, t0, n, base, e;
+    int it, s, send, n, base, e;
   };
   auto begin = [&](Place& q, int it) __attribute__((always_inline)) {
     q.it = it;
@@ -462,7 +476,6 @@ __global__ void __launch_bounds__(kSmallWaves * 64) moe_down_small_kernel(MoePar
     q.e = e;
     q.s = c * p.run;
     q.send = min(steps, q.s + p.run);
-    q.t0 = 0;
     q.n = __builtin_amdgcn_readfirstlane((int)count[e]);
     q.base = __builtin_amdgcn_readfirstlane((int)first[e]);
   };
@@ -475,7 +488,7 @@ __global__ void __launch_bounds__(kSmallWaves * 64) moe_down_small_kernel(MoePar
     for (int b = 0; b < 2; ++b) wv[b] = rw.load(woff[b], k);
     // (straight into the matrix instruction's layout: these lines are shared by
     // all workgroups, and come from the cache)
-    const int a = order[q.base + min(q.t0 + (r & 7), q.n - 1)];
+    const int a = order[q.base + min(r & 7, q.n - 1)];
     const char* const s = hp + ((int64_t)a * p.ldh * 2 + q.s * kStep);
     av[0] = *reinterpret_cast<const i32x4_t*>(s);
     av[1] = *reinterpret_cast<const i32x4_t*>(s + 64);
@@ -490,27 +503,23 @@ __global__ void __launch_bounds__(kSmallWaves * 64) moe_down_small_kernel(MoePar
     const i32x4_t af[2] = {av[0], av[1]};
     wave_lds_order();
     Place nxt = cur;
-    if (++nxt.s == nxt.send) {
-      nxt.s = (cur.it % runs) * p.run;
-      nxt.t0 += 8;
-      if (nxt.t0 >= nxt.n) begin(nxt, cur.it + W);
-    }
+    if (++nxt.s == nxt.send) begin(nxt, cur.it + W);
     if (nxt.it < items) load(nxt);
 #pragma unroll
     for (int q = 0; q < 2; ++q) acc = mma16(st[fo[q]], af[q], acc);
     wave_lds_order();
-    if (nxt.it != cur.it || nxt.t0 != cur.t0) {
+    if (nxt.it != cur.it) {
       // these tokens' sums of the run, of both parts
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i] += __shfl_xor(acc[i], 8, 64);
-      if (r < 8 && cur.t0 + r < cur.n) {
-        const int a = order[cur.base + cur.t0 + r];
-        const float w = p.weights[a];
-        float* const o = own + (a / p.top) * LD + 4 * g;
-        // (added, not set: a token may have chosen an expert twice)
+      if (r < 8 && r < cur.n) {
+        const int a = order[cur.base + r], t = a / p.top;
+        float* const o = own + t * LD + 4 * g;
+        f32x4_t v = {o[0], o[1], o[2], o[3]};
+        for (uint32_t m = same[a]; m != 0; m &= m - 1)
+          v += weight[t * p.top + __builtin_ctz(m)] * acc;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          __hip_atomic_fetch_add(o + i, w * acc[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        for (int i = 0; i < 4; ++i) o[i] = v[i];
       }
       acc = f32x4_t{0, 0, 0, 0};
     }

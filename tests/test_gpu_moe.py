@@ -175,6 +175,24 @@ def test_routing_of_the_callers(M, E, K):
     check_layer(tgemm.moe_experts(x, one, p, u, d), x, one, p, w1, w2, "silu")
 
 
+@pytest.mark.parametrize("M,K,F,E,top", [(8, 264, 520, 5, 11), (7, 72, 2100, 3, 13),
+                                         (2, 33, 40, 2, 16), (20, 264, 72, 5, 11)])
+def test_experts_listed_again(M, K, F, E, top):
+    """Every token lists its experts more than once, with weights of their own:
+    the same bits every time."""
+    x, _, w1, w2 = layer(M, K, F, E, seed=30)
+    u, d = w1.transpose(1, 2), w2.transpose(1, 2)
+    g = torch.Generator().manual_seed(3)
+    ids = torch.randint(0, E, (M, top), generator=g, dtype=torch.int32).to(dev())
+    p = torch.randn(M, top, generator=g).to(dev())
+    y = tgemm.moe_experts(x, ids, p, u, d)
+    check_layer(y, x, ids, p, w1, w2, "silu")
+    for _ in range(8):
+        assert torch.equal(tgemm.moe_experts(x, ids, p, u, d), y)
+    one = ids[:, :1].expand(M, top).contiguous()
+    check_layer(tgemm.moe_experts(x, one, p, u, d), x, one, p, w1, w2, "silu")
+
+
 @pytest.mark.parametrize("M,K,F,E,top", [(1, 64, 64, 4, 2), (5, 33, 17, 10, 3), (64, 72, 40, 6, 2),
                                          (70, 40, 9, 100, 16), (1, 1, 1, 1, 1)])
 @pytest.mark.parametrize("routed", [0, 1])
