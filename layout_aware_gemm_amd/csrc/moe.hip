@@ -27,7 +27,7 @@
 //
 // Measured (MI355X): 13 tokens on 2 of 8 experts 4096 x 13824 (2.7 GB of weights)
 // 418 us, 6.5 TB/s; 64 tokens on 8 of 128 experts 2048 x 768 (1.2 GB) 214 us; one
-// token on 8 of 64 experts 2048 x 1024 (100 MB) 31 us, three launches.
+// token on 8 of 64 experts 2048 x 1024 (100 MB) 30 us, three launches.
 #include "chunk_rows.h"
 #include "ffn.h"
 #include "gemm_kernel.h"
@@ -382,63 +382,54 @@ __global__ void __launch_bounds__(kSmallWaves * 64) moe_down_small_kernel(MoePar
   constexpr int LD = 17;  // floats per token's 16 sums
   __shared__ i32x4_t lds[W * STAGE];
   __shared__ float sums[W * 8 * LD];
-  __shared__ uint16_t order[8 * kMoeTop];          // a token's first choice of an expert, by expert
-  __shared__ uint16_t same[8 * kMoeTop];           // bit j: the token's choice j is that expert
-  __shared__ int32_t ids[8 * kMoeTop];
-  __shared__ float weight[8 * kMoeTop];
-  __shared__ uint16_t first[kMoeExperts], count[kMoeExperts], hit[8 * kMoeTop];
-  __shared__ int cnt[kMoeExperts];
-  __shared__ int s_hits;
+  constexpr int kChoices = 8 * kMoeTop;
+  __shared__ int32_t ids[kChoices];
+  __shared__ float weight[kChoices];
+  // A token's first choice of an expert stands for all of them (same: bit j for
+  // its choice j).  The first of these of all tokens is the expert's leader: its
+  // tokens are the `count` entries of order from 8 leader on.
+  __shared__ uint16_t same[kChoices], count[kChoices], order[kChoices * 8], hit[kChoices];
+  __shared__ uint8_t leads[kChoices];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int A = p.M * p.top;
-  for (int i = threadIdx.x; i < p.E; i += W * 64) cnt[i] = 0;
+  const int A = p.M * p.top, a = threadIdx.x;
+  static_assert(kChoices == 128 && kChoices <= W * 64, "a thread per choice, in two waves");
+  if (a < A) {
+    ids[a] = p.ids[a];
+    weight[a] = p.weights[a];
+  }
   for (int i = threadIdx.x; i < W * 8 * LD; i += W * 64) sums[i] = 0.f;
-  static_assert(8 * kMoeTop <= W * 64, "a thread per choice");
-  const int own_a = threadIdx.x;
-  if (own_a < A) {
-    ids[own_a] = p.ids[own_a];
-    weight[own_a] = p.weights[own_a];
+  __syncthreads();
+  if (a < kChoices) {
+    bool lead = false;
+    if (a < A) {
+      const int e = ids[a], own = a / p.top;
+      int leader = A, before = 0, n = 0;
+      uint32_t mask = 0;
+      for (int t = 0; t < p.M; ++t) {
+        uint32_t m = 0;
+        for (int k = 0; k < p.top; ++k) m |= ids[t * p.top + k] == e ? 1u << k : 0u;
+        if (m == 0) continue;
+        if (n++ == 0) leader = t * p.top + __builtin_ctz(m);
+        before += t < own ? 1 : 0;
+        if (t == own) mask = m;
+      }
+      if (e >= 0 && e < p.E && (mask & ((1u << (a - own * p.top)) - 1)) == 0) {
+        lead = leader == a;
+        same[a] = (uint16_t)mask;
+        order[leader * 8 + before] = (uint16_t)a;
+        if (lead) count[a] = (uint16_t)n;
+      }
+    }
+    leads[a] = lead;
   }
   __syncthreads();
-  int own_e = -1;  // the expert, if this is the token's first choice of it
-  if (own_a < A) {
-    const int e = ids[own_a], j0 = own_a / p.top * p.top;
-    uint32_t m = 0;
-    for (int j = 0; j < p.top; ++j) m |= ids[j0 + j] == e ? 1u << j : 0u;
-    same[own_a] = (uint16_t)m;
-    if (e >= 0 && e < p.E && (m & ((1u << (own_a - j0)) - 1)) == 0) {
-      own_e = e;
-      atomicAdd(&cnt[e], 1);
-    }
-  }
-  __syncthreads();
-  if (wave == 0) {
-    // 16 experts per lane at most: sums of counts and of hits before them
-    const int per = (p.E + 63) / 64, i0 = lane * per;
-    int c = 0, h = 0;
-    for (int i = i0; i < min(p.E, i0 + per); ++i) c += cnt[i], h += cnt[i] > 0;
-    int cs = c, hs = h;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int cu = __shfl_up(cs, o, 64), hu = __shfl_up(hs, o, 64);
-      if (lane >= o) cs += cu, hs += hu;
-    }
-    if (lane == 63) s_hits = hs;
-    cs -= c;
-    hs -= h;
-    for (int i = i0; i < min(p.E, i0 + per); ++i) {
-      const int k = cnt[i];
-      first[i] = (uint16_t)cs;
-      count[i] = (uint16_t)k;
-      if (k > 0) hit[hs++] = (uint16_t)i;
-      cnt[i] = cs;
-      cs += k;
-    }
-  }
-  __syncthreads();
-  if (own_e >= 0) order[atomicAdd(&cnt[own_e], 1)] = (uint16_t)own_a;
+  // the leaders in order (each wave counts them, the first two list them)
+  const uint64_t lead0 = __ballot(leads[lane] != 0), lead1 = __ballot(leads[lane + 64] != 0);
+  const int hits0 = __popcll(lead0), hits = hits0 + __popcll(lead1);
+  if (a < kChoices && leads[a])
+    hit[(wave ? hits0 : 0) + __popcll((wave ? lead1 : lead0) & ((1ull << lane) - 1))] = (uint16_t)a;
   __syncthreads();
 
   const int n0 = blockIdx.x * 16;
@@ -464,7 +455,7 @@ __global__ void __launch_bounds__(kSmallWaves * 64) moe_down_small_kernel(MoePar
 
   // The wave's place: (expert, run) pair `it`, step s of it; the expert's tokens,
   // n <= 8 of them, from `base` in the order.
-  const int items = __builtin_amdgcn_readfirstlane(s_hits) * runs;
+  const int items = hits * runs;
   struct Place {
     int it, s, send, n, base, e;
   };
@@ -472,12 +463,12 @@ __global__ void __launch_bounds__(kSmallWaves * 64) moe_down_small_kernel(MoePar
     q.it = it;
     if (it >= items) return;
     const int i = it / runs, c = it - i * runs;
-    const int e = __builtin_amdgcn_readfirstlane((int)hit[i]);
-    q.e = e;
+    const int l = __builtin_amdgcn_readfirstlane((int)hit[i]);
+    q.e = __builtin_amdgcn_readfirstlane(ids[l]);
     q.s = c * p.run;
     q.send = min(steps, q.s + p.run);
-    q.n = __builtin_amdgcn_readfirstlane((int)count[e]);
-    q.base = __builtin_amdgcn_readfirstlane((int)first[e]);
+    q.n = __builtin_amdgcn_readfirstlane((int)count[l]);
+    q.base = l * 8;
   };
   i32x4_t wv[2], av[2];
   auto load = [&](const Place& q) __attribute__((always_inline)) {

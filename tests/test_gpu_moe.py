@@ -176,7 +176,9 @@ def test_routing_of_the_callers(M, E, K):
 
 
 @pytest.mark.parametrize("M,K,F,E,top", [(8, 264, 520, 5, 11), (7, 72, 2100, 3, 13),
-                                         (2, 33, 40, 2, 16), (20, 264, 72, 5, 11)])
+                                         (2, 33, 40, 2, 16), (20, 264, 72, 5, 11),
+                                         (8, 2056, 520, 5, 11), (7, 2049, 72, 300, 16),
+                                         (8, 2048, 40, 6, 16), (1, 2048, 200, 3, 7)])
 def test_experts_listed_again(M, K, F, E, top):
     """Every token lists its experts more than once, with weights of their own:
     the same bits every time."""
