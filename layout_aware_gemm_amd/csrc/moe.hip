@@ -662,8 +662,8 @@ int slots_of(const MoeParams& p) { return p.M * p.top < p.E ? p.M * p.top : p.E;
 // The down product of few weights (48 MB) for up to 8 tokens, on at least 128
 // workgroups: what half the compute units and the short runs lose is less than a
 // launch to add up the choices (us, small kernel / the other and the sums: one
-// token, 8 experts 2048 x 1024 11.9 / 8.6 + 4.1; 8 tokens, 8 experts 2048 x 768
-// 8.4 / 6.7 + 3.2).
+// token, 8 experts 2048 x 1024 11.4 / 8.6 + 4.1; 8 tokens, 8 experts 2048 x 768
+// 9.2 / 6.7 + 3.2).
 bool down_small(const MoeParams& p) {
   return p.M <= 8 && p.K >= 2048 && (int64_t)slots_of(p) * p.F * p.K * 2 <= int64_t(48) << 20;
 }
