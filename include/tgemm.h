@@ -627,7 +627,8 @@ TGEMM_API int tgemm_validate_linear_backward(char transA, char transB, int64_t M
  *                    divides M; each row of it serves M / gates consecutive
  *                    rows: 1 for a learned gate per channel, the number of
  *                    sequences for one per sequence, M for one per token.
- *   scale, eps       finite; eps >= 0.
+ *   scale, eps       finite; eps >= 0.  With eps 0 a row whose rms is below 2^-128
+ *                    gives infinities or NaN, as one of zeros does.
  *   rstd             fp32 [M] of rs, then with a post_weight [M] of ry, for the
  *                    backward call; or NULL.
  * K up to 16384, M times the threads of a row below 2^32, else
@@ -656,7 +657,8 @@ TGEMM_API int tgemm_validate_block_norm(const void* y, int64_t ldy, const void* 
  *   dpost      fp32 [K], with a post_weight
  *   dgate      fp32 [gates, K], contiguous, with a gate
  * The other arguments as in the forward call; rstd as it left them.  s is
- * computed again from y and residual, in fp32.  The sums over rows are fp32,
+ * computed again from y and residual, in fp32; rows of any size that the
+ * forward takes keep their gradient.  The sums over rows are fp32,
  * in an order that depends on the sizes alone.  K up to 16384, else
  * TGEMM_ERR_UNSUPPORTED.  Workspace (as for the feed-forward calls): partial
  * sums of at most 512 groups of rows, at most 16 * 512 * K bytes.

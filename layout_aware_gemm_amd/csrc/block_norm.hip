@@ -6,23 +6,26 @@
 // rounded.  Means of squares are summed in 64 bits: squares of bf16 values
 // overflow fp32 from 1.8e19 on.
 //
-// Gradient, for dn and ds (of s from its other uses), with e = dn wn:
-//   t   = ds + rs e - s (rs^3 / K) sum(e s)      dh = t
-//   dwn = sum_m dn s rs
+// Gradient, for dn and ds (of s from its other uses), with e = dn wn and the
+// normed rows s' = s rs, y' = y ry:
+//   t   = ds + rs (e - s' sum(e s') / K)         dh = t
+//   dwn = sum_m dn s'
 //   dgate = sum over the gate's rows of scale t p
-//   f   = a t wp,  dy = ry f - y (ry^3 / K) sum(f y),  dwp = sum_m a t y ry
-// s is computed again from y, h and the kept factors, in fp32, as the forward
-// had it: read back in bf16 its rounding would be the error of dwn.  sum(f y)
-// follows from sums of known terms,
-//   sum(f y) = sum(q (ds + rs e)) - (rs^3 / K) sum(e s) sum(q s),  q = a wp y,
+//   f   = a t wp,  dy = ry (f - y' sum(f y') / K),  dwp = sum_m a t y'
+// Only s' and y' enter sums and products (their squares are at most K): rs^3, ry^3
+// or y s would leave fp32 for rows whose squares do.  s is computed again from
+// y, h and the kept factors, in fp32, as the forward had it: read back in bf16 its
+// rounding would be the error of dwn.  sum(f y') follows from sums of known terms,
+//   sum(f y') = sum(q (ds + rs e)) - (rs / K) sum(e s') sum(q s'),  q = a wp y',
 // so a row takes one reduction, not two in a chain.
 //
 // Bound: HBM bandwidth.  A row stays in registers between its reduction and
 // its results, so each element moves once: 8 bytes forward (bf16), 12
-// backward.  Measured: 8192 x 4096 51 us forward (5.3 TB/s, a large copy's
-// rate), 89 us backward (4.5 TB/s) and 7 us for the sums.  The gradients of the weights are kept per column in registers
-// while a workgroup works through its rows; the workgroups' sums are added
-// in order by a second kernel (no atomics: the same bits every time).
+// backward.  Measured: 8192 x 4096 53 us forward (5.1 TB/s, a large copy's
+// rate), 87 us backward (4.6 TB/s) and 7 us for the sums.  The gradients of the
+// weights are kept per column in registers while a workgroup works through its
+// rows; the workgroups' sums are added in order by a second kernel (no atomics:
+// the same bits every time).
 #include "ffn.h"
 #include "row_vec.h"
 
@@ -285,7 +288,7 @@ __global__ void __launch_bounds__(bwd_threads<V>()) block_norm_bwd_kernel(BlockN
     } else {
       load(cur, row);
     }
-    float s[V][8], t[V][8];
+    float s[V][8], t[V][8];        // s: s rs
     float q[3] = {0.f, 0.f, 0.f};  // sum e s, sum q (ds + rs e), sum q s
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -303,10 +306,10 @@ __global__ void __launch_bounds__(bwd_threads<V>()) block_norm_bwd_kernel(BlockN
       gate8<GATE>(gv[GATE ? v : 0], p.scale, a);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float yi = value(cur.y[v], i);
+        const float yi = POST ? value(cur.y[v], i) * ry : value(cur.y[v], i);
         float pi = yi;
-        if constexpr (POST) pi = yi * ry * value(wp[v], i);
-        s[v][i] = fmaf(a[i], pi, value(cur.h[v], i));
+        if constexpr (POST) pi = yi * value(wp[v], i);
+        s[v][i] = fmaf(a[i], pi, value(cur.h[v], i)) * rs;
         const float e = value(cur.dn[v], i) * value(wn[v], i);
         t[v][i] = fmaf(rs, e, value(cur.ds[v], i));
         q[0] = fmaf(e, s[v][i], q[0]);
@@ -318,8 +321,8 @@ __global__ void __launch_bounds__(bwd_threads<V>()) block_norm_bwd_kernel(BlockN
       }
     }
     group_sum(q, sums[row & 1]);
-    const float k = rs * (rs * q[0] * rk) * rs;                   // of s in t
-    const float ky = ry * (ry * fmaf(-k, q[2], q[1]) * rk) * ry;  // of y in dy
+    const float k = rs * (q[0] * rk);            // of s in t
+    const float ky = fmaf(-k, q[2], q[1]) * rk;  // of y ry in f
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const uint32_t c = col(v);
@@ -338,15 +341,15 @@ __global__ void __launch_bounds__(bwd_threads<V>()) block_norm_bwd_kernel(BlockN
       gate8<GATE>(gv[GATE ? v : 0], p.scale, a);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float yi = value(cur.y[v], i);
+        const float yi = POST ? value(cur.y[v], i) * ry : value(cur.y[v], i);
         t[v][i] = fmaf(-k, s[v][i], t[v][i]);
-        an.fma_to(v, i, value(cur.dn[v], i), s[v][i] * rs);
+        an.fma_to(v, i, value(cur.dn[v], i), s[v][i]);
         const float u = a[i] * t[v][i];
         if constexpr (POST) {
           const float w = value(wp[v], i);
-          ap.fma_to(v, i, u, yi * ry);
-          if constexpr (GATE) ag.fma_to(v, i, p.scale * t[v][i], yi * ry * w);
-          o[i] = fmaf(-ky, yi, ry * (u * w));
+          ap.fma_to(v, i, u, yi);
+          if constexpr (GATE) ag.fma_to(v, i, p.scale * t[v][i], yi * w);
+          o[i] = ry * fmaf(-ky, yi, u * w);
         } else {
           if constexpr (GATE) ag.fma_to(v, i, p.scale * t[v][i], yi);
           o[i] = u;
