@@ -391,12 +391,15 @@ __global__ void __launch_bounds__(bwd_threads<V>()) block_norm_bwd_kernel(BlockN
 
 // The workgroups' partial sums added, 64 columns per workgroup: job 0 dwn, then
 // dwp, then the gate's groups that more than one workgroup shared (a group's
-// first workgroup holds it as its tail, the others as their heads).
+// first workgroup holds it as its tail, the others as their heads).  These have
+// a job per group, or (by_end: more groups than workgroups) one for each
+// workgroup but the last, which takes the group that begins there and goes on.
 constexpr int kSumThreads = 1024;
 
 __global__ void __launch_bounds__(kSumThreads) block_norm_sum_kernel(BlockNormGradParams p,
                                                                      int groups, int cblocks,
-                                                                     int post, int gate) {
+                                                                     int post, int gate,
+                                                                     int by_end) {
   constexpr int NG = kSumThreads / 64;
   __shared__ float s[NG][64];
   const PartRows R = part_rows(post != 0, gate != 0);
@@ -407,7 +410,12 @@ __global__ void __launch_bounds__(kSumThreads) block_norm_sum_kernel(BlockNormGr
   int row = job, row0 = job;  // their row of partials, and the first one's
   float* out = job == 0 ? p.dweight : p.dpost;
   if (job > post) {
-    const int64_t grp = job - 1 - post;
+    int64_t grp = job - 1 - post;
+    if (by_end) {
+      const int64_t end = (grp + 1) * p.per_group, begin = end - p.per_group;
+      grp = (end - 1) / p.rows_per_gate;
+      if (grp * p.rows_per_gate < begin) return;  // (an earlier workgroup's)
+    }
     w0 = (int)(grp * p.rows_per_gate / p.per_group);
     w1 = (int)(((grp + 1) * p.rows_per_gate - 1) / p.per_group) + 1;
     if (w1 - w0 == 1) return;  // (written whole)
@@ -509,9 +517,8 @@ bool block_norm_fits(int64_t M, int64_t K) {
          M * (chunks < 1024 ? (chunks + 63) / 64 * 64 : 1024) < (int64_t(1) << 32);
 }
 
-bool block_norm_bwd_fits(int64_t M, int64_t K, int64_t gates) {
-  return K <= kNormMaxK && (2 + gates) * ceil_div(K, 64) <= kMaxWorkgroups / 4;
-}
+// (the sums have at most 2 + 511 jobs of 256 workgroups)
+bool block_norm_bwd_fits(int64_t K) { return K <= kNormMaxK; }
 
 size_t block_norm_bwd_bytes(int64_t M, int64_t K, bool post, bool gate) {
   const int64_t groups = ceil_div(M, per_group(M, K));
@@ -532,9 +539,10 @@ hipError_t launch_block_norm_bwd(BlockNormGradParams p, bool f32, hipStream_t s)
   const int cblocks = ceil_div(p.K, 64);
   // groups of whole rows of one workgroup need no second pass
   const bool shared = gate && p.per_group % p.rows_per_gate != 0;
-  const int64_t jobs = 1 + post + (shared ? p.M / p.rows_per_gate : 0);
+  const int gates = p.M / p.rows_per_gate, by_end = gates >= groups;
+  const int jobs = 1 + post + (!shared ? 0 : by_end ? groups - 1 : gates);
   return enqueue(block_norm_sum_kernel, dim3((unsigned)(jobs * cblocks)), dim3(kSumThreads), s, p,
-                 groups, cblocks, post, gate);
+                 groups, cblocks, post, gate, by_end);
 }
 
 }  // namespace tgemm

@@ -247,7 +247,7 @@ struct BlockNormGradParams {
   float* part;
   int per_group;   // set by the launcher
 };
-bool block_norm_bwd_fits(int64_t M, int64_t K, int64_t gates);
+bool block_norm_bwd_fits(int64_t K);
 size_t block_norm_bwd_bytes(int64_t M, int64_t K, bool post, bool gate);
 hipError_t launch_block_norm_bwd(BlockNormGradParams p, bool f32, hipStream_t s);
 

@@ -806,7 +806,7 @@ extern "C" int tgemm_block_norm(const void* y, int64_t ldy, const void* residual
 extern "C" int64_t tgemm_block_norm_backward_workspace_bytes(int64_t M, int64_t K, int post,
                                                              int64_t gates) {
   if (M < 1 || K < 1 || gates < 0 || (gates > 0 && M % gates != 0)) return TGEMM_ERR_INVALID_ARG;
-  if (M >= int64_t(1) << 31 || !block_norm_bwd_fits(M, K, gates)) return TGEMM_ERR_UNSUPPORTED;
+  if (M >= int64_t(1) << 31 || !block_norm_bwd_fits(K)) return TGEMM_ERR_UNSUPPORTED;
   return (int64_t)block_norm_bwd_bytes(M, K, post != 0, gates > 0);
 }
 
@@ -823,7 +823,7 @@ extern "C" int tgemm_block_norm_backward(const void* dn, int64_t lddn, const voi
       dn, lddn, ds, ldds, y, ldy, residual, ldr, stream_type, post_weight, gate, ldgate, gates,
       scale, weight, rstd, M, K, dresidual, lddr, dy, lddy, dweight, dpost, dgate);
   if (st != TGEMM_OK) return st;
-  if (!block_norm_bwd_fits(M, K, gate != nullptr ? gates : 0)) return TGEMM_ERR_UNSUPPORTED;
+  if (!block_norm_bwd_fits(K)) return TGEMM_ERR_UNSUPPORTED;
   return no_throw([&] {
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     Workspace w;
