@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 1024) block_norm_kernel(BlockNo
   }
   if (p.rstd != nullptr && threadIdx.x == 0) {
     p.rstd[row] = rs;
-    if constexpr (POST) p.rstd[p.M + row] = ry;
+    if constexpr (POST) p.rstd[(int64_t)p.M + row] = ry;
   }
 }
 
@@ -232,7 +232,8 @@ __global__ void __launch_bounds__(bwd_threads<V>()) block_norm_bwd_kernel(BlockN
   const int W = blockDim.x;
   const int64_t K = p.K;
   const float rk = 1.f / (float)K;
-  const int first = (int)blockIdx.x * p.per_group, end = min(p.M, first + p.per_group);
+  // (up to 2^31 - 1 rows: the last group's end and the rows of rstd pass 32 bits)
+  const int first = (int)blockIdx.x * p.per_group, end = first + min(p.per_group, p.M - first);
   constexpr PartRows R = {1, 1 + (POST ? 1 : 0), 2 + (POST ? 1 : 0),
                           1 + (POST ? 1 : 0) + (GATE ? 2 : 0)};
   float* const part = p.part + (int64_t)blockIdx.x * R.count * K;
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(bwd_threads<V>()) block_norm_bwd_kernel(BlockN
   for (int row = first; row < end; ++row) {
     const int grp = GATE ? row / p.rows_per_gate : 0;
     const uint16_t* const gate = GATE ? p.gate + (int64_t)grp * p.ldgate : nullptr;
-    const float rs = p.rstd[row], ry = POST ? p.rstd[p.M + row] : 1.f;
+    const float rs = p.rstd[row], ry = POST ? p.rstd[(int64_t)p.M + row] : 1.f;
     if constexpr (GATE && AHEAD) {
       if (grp != held) {
         held = grp;
