@@ -47,12 +47,16 @@ void set_tile(RowsParams* p, bool gate, int tile, int col0, int end) {
 // 0.8 (64x128), 1.33 (128x256) and 1.95 (256x256) of it (gated 13824 x 5120,
 // us for 64x128 / 128x128 / 128x256 / 256x256 tiles: 256 rows 101 / 66.9 /
 // 51.4 / 65.0 int8, 170 / 114 / 89 / 121 bf16; 512 rows 163 / 123 / 92 / 70
-// and 272 / 211 / 158 / 125).  256x192 tiles (linear products) take 0.77 of a
-// 256x256 round: 2047 x 5120 x 13824, one round of either, 278 us against 307
-// (216 workgroups instead of 160, cold operands; rows off 128-byte lines 360
-// against 431).
+// and 272 / 211 / 158 / 125).  256x192 tiles (linear products) take 0.89 of a
+// 256x256 round (us, cold operands, as many rounds of either: 2047 x 5120 x
+// 13824 262 / 294, one; 4096 x 6144 x 4096 184 / 204, two; 4096 x 9216 x 4096 277
+// / 310, three).  A round more than 256x256 tiles, or than these and smaller
+// ones in their last round, take is a loss (us, the smaller tiles first: 4096 x
+// 15360 x 4096 451 / 436, five and four; 8192 x 9216 x 1024 211 / 202, six and
+// five; 1979 x 9280 x 1024 74 / 60 and 1437 x 13120 x 4096 172 / 158, two and one
+// with a tail).
 double grid_cost(RowsParams* p, bool gate, int tile, int split, int col0, int end) {
-  constexpr double cost[5] = {1.95, 1.33, 1.0, 0.8, 1.5};
+  constexpr double cost[5] = {1.95, 1.33, 1.0, 0.8, 1.74};
   set_tile(p, gate, tile, col0, end);
   const double round = cost[tile] * (6 + 2.9e-3 * p->K / split);
   const double sums = split > 1 ? 4 + 1.7e-6 * split * p->M * p->N : 0;
