@@ -286,15 +286,25 @@ hipError_t launch_few(const RowsParams& p, hipStream_t s) {
 // / 32.8, 29.0 / 30.2 / 31.4 / 35.9).  Below the band whole blocks win (bf16
 // 5504 x 4096 20.6 / 21.5 / 23.4 at 1 / 16 / 32 tokens, half 21.4 / 23.2 / 24.9),
 // as they do for plain int8 products (8192 x 4096 9.3 / 9.6 / 10.2, 9.1 / 9.9 /
-// 11.3); bf16 linear products are as heavy as gated int8 ones (one token 8192 x
-// 4096 19.0, half 13.2; 5120 x 5120 10.8; 5120 x 13824 24.6, half 24.7).
+// 11.3).  bf16 linear products take half blocks there and past it for up to 8
+// tokens (us, whole / half, of 1, 8, 16 and 32 tokens; in the band 8192 x 4096 16.3
+// / 15.4, 16.7 / 15.2, 16.9 / 15.9, 17.6 / 19.8; 8192 x 13824 34.8 / 35.4, 34.8 /
+// 35.6, 36.3 / 43.2, 42.3 / 58.6; past it 11008 x 4096 23.7 / 19.1, 24.4 / 20.5,
+// 25.8 / 21.5, 27.0 / 26.4; 16384 x 13824 68.5 / 69.7, 69.7 / 70.6, 73.7 / 82.3,
+// 82.5 / 108; 32000 x 4096 49.2 / 43.8, 49.5 / 42.4, 48.7 / 46.4, 53.0 / 61.0;
+// before it 5120 x 4096 12.3 / 10.6, 13.1 / 11.4, 13.4 / 13.4, 14.6 / 17.9; 5120 x
+// 13824 25.2 / 25.6, 27.4 / 30.5, 31.0 / 39.3, 38.4 / 55.0).
 // 33 to 64 tokens of a linear product (bf16), in 6 or 8 groups of 8.  A workgroup
 // holds 57 KB (two blocks, four waves) to 131 KB (four blocks, eight waves) of
 // LDS, so the grid is kept to one round where it can be (us, 48 tokens, cold
 // weights, two blocks 8 waves / four blocks 4 waves / four blocks 8 waves: 5120 x
 // 5120 14.5 / 19.4 / 19.4, 8192 x 8192 34.8 / 41.3 / 39.6, 11008 x 4096 27.5 / - /
 // 18.7, 16384 x 4096 34.6 / 29.0 / 26.8, 32000 x 4096 - / 48.2 / 51.8; 6 groups
-// take 1 to 2 us less than 8).
+// take 1 to 2 us less than 8).  At the edges of a round (40 tokens, K = 4096; one
+// block / two / four, 8 waves / four, 4 waves): 4096 rows 11.9 / 14.8 / 19.9 /
+// 20.0, 4128 18.9 / 14.8 / 20.0 / 20.2; 8192 21.4 / 18.3 / 21.7 / 22.0, 8224 27.4
+// / 25.5 / 21.9 / 22.3; 16384 37.3 / 30.9 / 26.3 / 28.4, 16416 43.1 / 37.2 / 36.9
+// / 36.8, 24576 57.4 / 43.6 / 45.7 / 43.8.
 template <int TB>
 hipError_t launch_linear_tokens(const RowsParams& p, hipStream_t s) {
   if (ceil_div(p.N, 32) <= 128) return launch_one<SkBf16, TB, 1, 8, false, kRowsLinear>(p, s);
@@ -309,7 +319,8 @@ hipError_t launch_blocks(const RowsParams& p, hipStream_t s) {
   const int nout = GATE ? p.F : p.N;
   const int blocks = ceil_div(nout, 32);
   const bool half =
-      blocks <= 128 || ((GATE || EPI == kRowsLinear) && blocks > 208 && blocks <= 256);
+      blocks <= 128 ||
+      (blocks > 208 && (EPI == kRowsLinear ? p.M <= 8 : GATE && blocks <= 256));
   if (p.M <= 32)
     return half ? launch_few<Op, NB / 2, GATE, EPI>(p, s) : launch_few<Op, NB, GATE, EPI>(p, s);
   if constexpr (EPI == kRowsLinear) {
