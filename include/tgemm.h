@@ -710,9 +710,9 @@ TGEMM_API int tgemm_validate_block_norm_backward(
  *   activation  TGEMM_ACT_SILU or TGEMM_ACT_GELU_TANH.
  * E up to 1024, top up to 16, rows of X, W1 and W2 less than 2^22 elements
  * apart, else TGEMM_ERR_UNSUPPORTED.  The layer is made for few tokens: 64 rows
- * run at a time, and each pass reads the experts it hits.  Weights on 16-byte
- * boundaries (bases and strides; F a multiple of 8) are read at full rate,
- * others in place too, more slowly.  Workspace as for the feed-forward calls;
+ * run at a time, and each pass reads the experts it hits.  With X, W1 and W2 all
+ * on 16-byte boundaries (bases and strides; K and F multiples of 8) the weights
+ * are read at full rate, else in place too, more slowly.  Workspace as for the feed-forward calls;
  * nearly every call needs some.
  */
 TGEMM_API int tgemm_run_moe(int64_t M, int64_t K, int64_t F, int64_t E, int64_t top, const void* X,

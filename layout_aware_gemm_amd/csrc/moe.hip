@@ -7,18 +7,21 @@
 //
 // Logits: one workgroup per expert and eight tokens, products and sums in 64
 // bits, so that which experts a token takes depends on no order of summation.
-// Choice: one workgroup per token; an expert's place is the number of experts
-// before it (larger logit, or equal and lower index), counted from LDS.
-// No list of experts is built in memory: a workgroup of the products finds its
-// expert's tokens by a scan of the ids (at most 1024).
+// Choice: an expert's place is the number of experts before it (larger logit, or
+// equal and lower index), counted from LDS: by a workgroup per token, or for few
+// logits by each workgroup of the up product itself, a launch less.  No list of
+// experts is built in memory: a workgroup of the products finds its expert's
+// tokens by a scan of the ids (at most 1024).
 //
 // The products are those of the few-row kernel (rows_skinny.hip): the weight's
 // rows take the matrix instruction's row side, the tokens its columns; a wave
 // loads whole 128-byte runs of its rows and turns them around in LDS words of
-// its own.  A workgroup takes 16 outputs of one expert (gate and up) or 32 to 64
-// columns (down), its waves share the K steps, their sums meet in LDS in wave
-// order, and a last kernel adds a token's choices by their weights, in order.
-// Nothing depends on timing.
+// its own.  Up: a workgroup takes 16 outputs (gate and up) of one expert, its
+// waves share the K steps, and their sums meet in LDS in wave order.  Down, two
+// ways: a workgroup takes 16 columns of y and all experts that are hit, its waves
+// runs of K steps of them (few tokens and weights); or 32 to 64 columns of one
+// expert, as up, a row of sums per choice in memory, and a last kernel adds a
+// token's choices by their weights, in order.  Nothing depends on timing.
 //
 // h = act(g) u is kept as the sum of two bf16 values, 16 bits in all: rounded to
 // one it would be half of y's error.  The matrix instruction's 16 columns hold
@@ -659,13 +662,20 @@ __global__ void __launch_bounds__(256) moe_weigh_kernel(MoeParams p, int per_row
 
 int slots_of(const MoeParams& p) { return p.M * p.top < p.E ? p.M * p.top : p.E; }
 
-// The down product of few weights (48 MB) for up to 8 tokens, on at least 128
-// workgroups: what half the compute units and the short runs lose is less than a
-// launch to add up the choices (us, small kernel / the other and the sums: one
-// token, 8 experts 2048 x 1024 11.4 / 8.6 + 4.1; 8 tokens, 8 experts 2048 x 768
-// 9.2 / 6.7 + 3.2).
+// The down product of few weights (48 MB) for up to 8 tokens, on at least 32
+// workgroups per token: what idle compute units and the short runs lose is then
+// less than a launch to add up the choices.  Whole layer in us in a graph, small
+// kernel / the other and the sums, F = 768, 2 of 16 experts unless noted.  At the
+// edge: 1 token K = 1024 14.3 / 16.7, 2 tokens 1024 18.2 / 19.5, 3 tokens 1536 23.5
+// / 24.0, 4 tokens 2048 (all of 8 experts) 31.3 / 32.3, 8 tokens 4096 (F = 512, all
+// of 8) 36.1 / 39.4.  Before it: 3 tokens 1024 21.6 / 20.9, 6 tokens 2048 (all of 8)
+// 33.9 / 33.1, 8 tokens 2048 (all of 8) 37.1 / 35.0, 8 tokens 2048 (2 of 64) 47.6 /
+// 42.2.  Past 48 MB the sides change with the shape (8 tokens 8192 x 2048, 2 of 8
+// 140 / 146; 4 tokens 4096 x 1408 51.6 / 50.4; 8 tokens 2048 x 1024, 8 of 64 117 /
+// 106).
 bool down_small(const MoeParams& p) {
-  return p.M <= 8 && p.K >= 2048 && (int64_t)slots_of(p) * p.F * p.K * 2 <= int64_t(48) << 20;
+  return p.M <= 8 && p.K >= 512 * p.M &&
+         (int64_t)slots_of(p) * p.F * p.K * 2 <= int64_t(48) << 20;
 }
 
 // The up product's workgroups make the choice of experts themselves where there
@@ -707,7 +717,11 @@ hipError_t launch_products(const MoeParams& p, hipStream_t s) {
   const bool few = p.M <= 8, many = (int64_t)p.M * p.top > (int64_t)12 * p.E;
   // Waves per workgroup of the up product: four for up to 32 K steps, which
   // have less to add up (2048 x 768, 64 tokens of 128 experts: 8 / 4 waves 136 /
-  // 128 us; 4096 x 13824, 13 tokens of 8 experts: 266 / 276).
+  // 128 us; 4096 x 13824, 13 tokens of 8 experts: 266 / 276).  Whole layers between
+  // these, 8 of 64 experts, 8 / 4 waves: 8 tokens, F = 1024, K = 1024 64.0 / 64.9,
+  // 1536 76.0 / 75.0, 2048 102 / 103, 2560 117 / 120, 4096 184 / 190; 24 tokens, F =
+  // 768, 1024 67.3 / 65.2, 2048 113 / 113, 2560 131 / 133, 4096 196 / 199; one token
+  // even to 4096, 62.9 / 69.4 at 6144.
   const bool narrow = p.K <= 32 * kStep / 2;
   hipError_t e;
   if (few)
